@@ -67,7 +67,11 @@ typedef enum {
   COLI_Q_INT8_PC = 1
 } coli_qtype;
 
-typedef enum { COLI_X_BF16 = 0, COLI_X_F32 = 1 } coli_xtype;
+typedef enum {
+  COLI_X_BF16 = 0,
+  COLI_X_F32 = 1,
+  COLI_X_F16 = 2 /* router logits, cached rows and attention queries; not a layer input */
+} coli_xtype;
 
 /*
  * One quantised matrix W[N][K] (N output rows, K inputs), device pointers.
@@ -224,6 +228,10 @@ COLI_API coli_status colibri_moe_debug_routing(const coli_moe_plan_t* plan, cons
 #define COLI_DEV_BAD_EXPERT_ID 1   /* a router index outside [0, E) reached the grouping step */
 #define COLI_DEV_WAIT_TIMEOUT 2    /* a pipeline wait gave up after its time limit (~1 s) */
 #define COLI_DEV_SELECT_ROUNDS 4   /* the key selection's rounds did not narrow to one value (not expected) */
+#define COLI_DEV_KV_NO_PAGES 8     /* colibri_kv_step: too few free pages for every request */
+#define COLI_DEV_KV_TABLE_FULL 16  /* colibri_kv_step: a request needs more than max_pages pages, or its lengths are not valid */
+#define COLI_DEV_KV_TOKENS 32      /* colibri_kv_step: the new tokens exceed n_tokens */
+#define COLI_DEV_KV_BAD_PAGE 64    /* a page id outside [0, n_pages) where a page of the request was expected */
 COLI_API coli_status colibri_moe_check_status(const coli_moe_plan_t* plan, const void* workspace, int32_t* device_status,
                                      void* stream);
 
@@ -427,6 +435,176 @@ COLI_API coli_status colibri_indexer_scores(int T, int L, int pos0, int H, int d
                                             const void* keys, void* workspace, size_t workspace_bytes, void* stream);
 COLI_API coli_status colibri_indexer_select(int T, int L, int pos0, int topk, int32_t* topk_idx, void* workspace,
                                             size_t workspace_bytes, void* stream);
+
+/*
+ * Routing to experts from given logits, in the general form of which the
+ * layer's own router (step 1 at the top of this header) is the case
+ * {sigmoid, one group, renormalised}.  "25GB RAM runs 744B GLM-5.2" page,
+ * section 3.1: the router is DeepSeek-V3 style; that family also limits a
+ * token to some groups of experts and has softmax-scored members.
+ *   score        s = sigmoid(z), or s = softmax(z) over the E logits.
+ *   bias         float [E] or NULL: u = s + bias (u = s without one) decides
+ *                which experts are chosen, s gives their weights.
+ *   n_group      the experts form n_group groups of E / n_group consecutive
+ *                ids.  A group's score is the sum of its two largest u
+ *                (COLI_GROUP_TOP2) or its largest u (COLI_GROUP_MAX); the
+ *                topk_group best groups are kept (a tie to the lower group).
+ *   k            the k largest u of the kept groups (a tie to the lower id),
+ *                reported in ascending id.
+ *   weights      scale * s, divided by the sum of the chosen s if renorm.
+ * The choice is that of the exact scores: scores that fp32 cannot tell apart
+ * are computed again in 64 bits before they are compared.  A NaN logit counts
+ * as -infinity; a NaN u ranks as -infinity; +infinity logits share a softmax
+ * equally; where every chosen s is 0 the weights are 0.
+ * 1 <= k <= min(32, topk_group * E / n_group), E <= 1024, n_group <= 32 a
+ * divisor of E, 2 <= E / n_group for COLI_GROUP_TOP2 with topk_group < n_group.
+ */
+typedef enum { COLI_SCORE_SIGMOID = 0, COLI_SCORE_SOFTMAX = 1 } coli_score;
+typedef enum { COLI_GROUP_TOP2 = 0, COLI_GROUP_MAX = 1 } coli_group_score;
+typedef struct {
+  int E, k;
+  int score;       /* coli_score */
+  int n_group;     /* 1: no groups */
+  int topk_group;  /* groups kept, 1 <= topk_group <= n_group */
+  int group_score; /* coli_group_score; not used when topk_group == n_group */
+  int renorm;      /* 0 or 1 */
+  float scale;
+} coli_route_desc;
+/*
+ * T tokens (T = 0 does nothing).  logits: device [T][logit_stride >= E] of
+ * ltype (bf16, fp16 or fp32); topk_idx int32 [T][k], topk_w float [T][k].
+ * Asynchronous on stream.  Errors: COLI_EINVAL, COLI_EALIGN, COLI_EUNSUPPORTED,
+ * COLI_ECUDA.
+ */
+COLI_API coli_status colibri_moe_route(const coli_route_desc* desc, int T, const void* logits, int ltype,
+                                       long long logit_stride, const float* bias, int32_t* topk_idx, float* topk_w,
+                                       void* stream);
+/*
+ * The routing of this plan's following forward calls (resident, cached and
+ * static-scratch) and of a pilot that runs its router.  desc->E and desc->k
+ * must be the plan's; desc->scale takes the place of the plan's routed_scale.
+ * NULL restores the plan's own routing.  colibri_moe_debug_routing's near_tie
+ * then also marks tokens whose last kept and first dropped group scores differ
+ * by less than 1e-5.  Errors: COLI_EINVAL, COLI_EUNSUPPORTED.
+ */
+COLI_API coli_status colibri_moe_set_route(coli_moe_plan_t* plan, const coli_route_desc* desc);
+
+/*
+ * Paged cache of compressed keys ("25GB RAM runs 744B GLM-5.2" page, section
+ * 3.2: MLA attention keeps 576 values a token; section 3.3: sparse attention
+ * reads the 2048 keys selected by the indexer).  A cached row holds
+ * COLI_KV_WIDTH = 576 values, the 512 of the latent first (they are the
+ * attention's values) and then the 64 rotary ones (with the latent, its key).
+ *   cache        device [n_pages][page_stride] elements of dtype (bf16 or
+ *                fp16), 16-byte aligned; a page's page_size rows of 576 come
+ *                first.  page_stride is a multiple of 576, at least
+ *                page_size * 576 (larger where the pages of several layers
+ *                interleave).
+ *   block_table  device int32 [B][max_pages]: the pages of each request, key
+ *                j in page j / page_size at row j % page_size.
+ * A slot is page * page_size + row.  n_pages * page_size < 2^31.
+ */
+#define COLI_KV_WIDTH 576
+#define COLI_KV_VALUE 512
+typedef struct {
+  int page_size;         /* >= 1 */
+  int max_pages;         /* columns of the block table */
+  int n_pages;           /* pages of the cache */
+  int dtype;             /* COLI_X_BF16 or COLI_X_F16 */
+  long long page_stride; /* elements from a page to the next */
+} coli_kv_desc;
+/*
+ * One step of the cache's bookkeeping for B requests (1 <= B <= 8192), on the
+ * GPU: pages for the new tokens, the requests' first rows in the step's token
+ * batch, and each new token's position and slot.
+ *   new_len      int32 [B]: new tokens of each request (0: none); negative: the
+ *                request has finished, its pages return to the free pages.
+ *   seq_len      int32 [B]: tokens in the cache before the step (fewer than the
+ *                held pages have room for where drafted tokens were taken back).
+ *   held         int32 [B]: pages the request holds, block_table[b][0 .. held).
+ *   free_pages   int32 [n_pages], a stack of which the first *free_count are
+ *                free.  Pages of finished requests are pushed in request order
+ *                (a request's first page first); then new pages are popped, in
+ *                request order and ascending position.
+ *   seq_len_out, held_out, free_count_out: their values after the step (0, 0 for a
+ *                finished request); each may be the input array itself.
+ *   block_table  new pages are entered at block_table[b][held ..]; nothing else
+ *                is written.
+ *   q_start      int32 [B + 1]: exclusive sums of the served requests' new
+ *                tokens.
+ *   position, slot  int32 [n_tokens]: of row q_start[b] + i, seq_len[b] + i and
+ *                its slot.  Rows from q_start[B] on are left as they were.
+ *   status       int32: COLI_DEV_KV_* bits are OR-ed into it (the caller
+ *                clears it).
+ * A request is not served (no tokens, nothing changed, a status bit) when its
+ * lengths are not valid or exceed max_pages, or when the pages or the token
+ * rows that it and the requests before it ask for exceed those there are
+ * (requests that ask for none of what ran out are still served).
+ * A held page id outside [0, n_pages) gives slot -1 (COLI_DEV_KV_BAD_PAGE).
+ * Asynchronous on stream; one launch.  Errors: COLI_EINVAL, COLI_EALIGN,
+ * COLI_EUNSUPPORTED, COLI_ECUDA.
+ */
+COLI_API coli_status colibri_kv_step(const coli_kv_desc* desc, int B, int n_tokens, const int32_t* new_len,
+                                     const int32_t* seq_len, const int32_t* held, int32_t* block_table,
+                                     int32_t* free_pages, const int32_t* free_count, int32_t* seq_len_out,
+                                     int32_t* held_out, int32_t* free_count_out, int32_t* q_start, int32_t* position,
+                                     int32_t* slot, int32_t* status, void* stream);
+/*
+ * Write n_tokens new rows into the cache: row i, its latent (512 values at
+ * latent + i * latent_stride) and rotary part (64 at rope + i * rope_stride),
+ * goes to slot[i].  n_valid: device int32 or NULL; rows from *n_valid on are
+ * not written (q_start + B of colibri_kv_step: slots behind the last request
+ * are older steps').  Slots outside the cache are left out.  Slots of one call
+ * are distinct.  Elements are copied as they are (desc->dtype is not read).
+ * latent, rope, cache 16-byte aligned, the strides multiples of 8.
+ * max_pages is not read.  Asynchronous on stream.  Errors: COLI_EINVAL,
+ * COLI_EALIGN, COLI_EUNSUPPORTED, COLI_ECUDA.
+ */
+COLI_API coli_status colibri_kv_append(const coli_kv_desc* desc, int n_tokens, const int32_t* n_valid,
+                                       const void* latent, long long latent_stride, const void* rope,
+                                       long long rope_stride, const int32_t* slot, void* cache, void* stream);
+/*
+ * Attention of the step's new tokens over the cache, after their rows were
+ * appended.  Row n of request b (q_start[b] <= n < q_start[b+1]) is at position
+ * seq_len[b] - (q_start[b+1] - q_start[b]) + n - q_start[b]; seq_len counts the
+ * new tokens (seq_len_out of colibri_kv_step).  With k[j] the cached row of
+ * key j and v[j] its first 512 values, head h of row n gets
+ *   out[n][h] = sum_j softmax_j(scale * q[n][h] . k[j]) v[j]
+ * over the keys j up to the row's position, or, with topk_idx, over
+ * the keys topk_idx[n][0 .. topk) (colibri_indexer_topk's output: entries that
+ * are negative or beyond the row's position are left out, an entry that occurs
+ * twice counts twice).  Queries are in the latent space (the up-projection of
+ * the keys absorbed): 512 latent values, then 64 rotary.
+ *   q            device [n_tokens][H][576] of desc->dtype with the strides (in
+ *                elements) given; 16-byte aligned; the strides multiples of 8
+ *                whose greatest common divisor is at least 576.  1 <= H <= 1024.
+ *   q_start      int32 [B + 1] ascending, seq_len int32 [B].
+ *   topk_idx     device int32 [n_tokens][topk], or NULL (topk is then not read).
+ *   out          device [n_tokens][H][512] of desc->dtype, 16-byte aligned.
+ *   lse          device float [n_tokens][H] or NULL: log of the softmax's sum.
+ *   workspace    device, >= colibri_kv_attention_workspace_size bytes, 256-byte
+ *                aligned; its first int32 is the status word
+ *                (colibri_kv_check_status).  Two calls that overlap on the GPU
+ *                need two workspaces.
+ * A row that sees no key gets 0 and lse -infinity.  Rows outside
+ * [q_start[0], q_start[B]) are left as they were.  Keys that a row does not see
+ * do not reach its output, whatever values (infinities, NaN) they hold.  A
+ * key whose page id is outside [0, n_pages) is left out and reported
+ * (COLI_DEV_KV_BAD_PAGE).  Softmax and sums in fp32; the weights are rounded
+ * to dtype for the product with the values.  The result does not depend on
+ * timing.
+ * Asynchronous on stream, three launches.  n_tokens = 0 does nothing.  Errors: COLI_EINVAL, COLI_EALIGN,
+ * COLI_EWORKSPACE, COLI_EUNSUPPORTED, COLI_ECUDA.
+ */
+COLI_API coli_status colibri_kv_attention_workspace_size(int B, int n_tokens, int H, size_t* bytes);
+COLI_API coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, int H, float scale,
+                                          const void* q, long long q_token_stride, long long q_head_stride,
+                                          const void* cache, const int32_t* block_table, const int32_t* q_start,
+                                          const int32_t* seq_len, const int32_t* topk_idx, int topk, void* out,
+                                          float* lse, void* workspace, size_t workspace_bytes, void* stream);
+/* The status word of an attention workspace (synchronises `stream`): 0, or
+ * COLI_DEV_KV_BAD_PAGE, COLI_DEV_WAIT_TIMEOUT (then COLI_EDEVICE). */
+COLI_API coli_status colibri_kv_check_status(const void* workspace, int32_t* device_status, void* stream);
 
 /* Number of kernel launches the last forward call of this plan issued. */
 COLI_API int colibri_moe_last_launch_count(const coli_moe_plan_t* plan);

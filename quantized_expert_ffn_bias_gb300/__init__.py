@@ -18,8 +18,12 @@ from . import build as _build
 
 COLI_OK, COLI_EINVAL, COLI_EALIGN, COLI_EUNSUPPORTED, COLI_EWORKSPACE, COLI_ECUDA, COLI_EDEVICE, COLI_ESTATE = range(8)
 COLI_Q_INT4_G128, COLI_Q_INT8_PC = 0, 1
-COLI_X_BF16, COLI_X_F32 = 0, 1
-COLI_DEV_BAD_EXPERT_ID, COLI_DEV_WAIT_TIMEOUT = 1, 2
+COLI_X_BF16, COLI_X_F32, COLI_X_F16 = 0, 1, 2
+COLI_SCORE_SIGMOID, COLI_SCORE_SOFTMAX = 0, 1
+COLI_GROUP_TOP2, COLI_GROUP_MAX = 0, 1
+COLI_KV_WIDTH, COLI_KV_VALUE = 576, 512
+COLI_DEV_BAD_EXPERT_ID, COLI_DEV_WAIT_TIMEOUT, COLI_DEV_SELECT_ROUNDS = 1, 2, 4
+COLI_DEV_KV_NO_PAGES, COLI_DEV_KV_TABLE_FULL, COLI_DEV_KV_TOKENS, COLI_DEV_KV_BAD_PAGE = 8, 16, 32, 64
 COLI_INJECT_WITHHOLD_STAGE, COLI_INJECT_BAD_EXPERT_ID = 1, 2
 
 # the in-tree build, the only library this binding loads
@@ -50,6 +54,17 @@ class coli_moe_desc(ctypes.Structure):
 
 class coli_kernel_time(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("total_ms", ctypes.c_double), ("launches", ctypes.c_int)]
+
+
+class coli_route_desc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("k", ctypes.c_int), ("score", ctypes.c_int), ("n_group", ctypes.c_int),
+                ("topk_group", ctypes.c_int), ("group_score", ctypes.c_int), ("renorm", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class coli_kv_desc(ctypes.Structure):
+    _fields_ = [("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("page_stride", ctypes.c_longlong)]
 
 
 def build(force: bool = False) -> str:
@@ -122,6 +137,23 @@ def lib():
             L.colibri_moe_cache_pilot.restype = st
             L.colibri_moe_cache_simulate.argtypes = [i32, i32, ctypes.c_double, vp, vp, i32, vp, vp]
             L.colibri_moe_cache_simulate.restype = st
+            i64 = ctypes.c_longlong
+            rdesc, kdesc = ctypes.POINTER(coli_route_desc), ctypes.POINTER(coli_kv_desc)
+            L.colibri_moe_route.argtypes = [rdesc, i32, vp, i32, i64, vp, vp, vp, vp]
+            L.colibri_moe_route.restype = st
+            L.colibri_moe_set_route.argtypes = [vp, rdesc]
+            L.colibri_moe_set_route.restype = st
+            L.colibri_kv_step.argtypes = [kdesc, i32, i32] + [vp] * 14
+            L.colibri_kv_step.restype = st
+            L.colibri_kv_append.argtypes = [kdesc, i32, vp, vp, i64, vp, i64, vp, vp, vp]
+            L.colibri_kv_append.restype = st
+            L.colibri_kv_attention_workspace_size.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+            L.colibri_kv_attention_workspace_size.restype = st
+            L.colibri_kv_attention.argtypes = [kdesc, i32, i32, i32, ctypes.c_float, vp, i64, i64, vp, vp, vp, vp, vp,
+                                               i32, vp, vp, vp, sz, vp]
+            L.colibri_kv_attention.restype = st
+            L.colibri_kv_check_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), vp]
+            L.colibri_kv_check_status.restype = st
             L.colibri_moe_last_launch_count.argtypes = [vp]
             L.colibri_moe_last_launch_count.restype = i32
             L.colibri_moe_last_error.argtypes = []
@@ -189,6 +221,54 @@ def colibri_indexer_select(T: int, L: int, pos0: int, topk: int, topk_idx, works
 def colibri_indexer_check_status(workspace, stream=None) -> int:
     v = ctypes.c_int32()
     rc = lib().colibri_indexer_check_status(_ptr(workspace), ctypes.byref(v), _stream(stream))
+    if rc not in (COLI_OK, COLI_EDEVICE):
+        _check(rc)
+    return v.value
+
+
+def colibri_moe_route(desc: coli_route_desc, T: int, logits, ltype: int, logit_stride: int, bias, topk_idx, topk_w,
+                      stream=None):
+    """Routing to experts from given logits (see the header): ids in topk_idx, weights in topk_w."""
+    _check(lib().colibri_moe_route(ctypes.byref(desc), T, _ptr(logits), ltype, logit_stride, _ptr(bias),
+                                   _ptr(topk_idx), _ptr(topk_w), _stream(stream)))
+
+
+def colibri_kv_step(desc: coli_kv_desc, B: int, n_tokens: int, new_len, seq_len, held, block_table, free_pages,
+                    free_count, seq_len_out, held_out, free_count_out, q_start, position, slot, status, stream=None):
+    """One step of the paged cache's bookkeeping (see the header): pages, q_start, positions and slots."""
+    _check(lib().colibri_kv_step(ctypes.byref(desc), B, n_tokens, _ptr(new_len), _ptr(seq_len), _ptr(held),
+                                 _ptr(block_table), _ptr(free_pages), _ptr(free_count), _ptr(seq_len_out),
+                                 _ptr(held_out), _ptr(free_count_out), _ptr(q_start), _ptr(position), _ptr(slot),
+                                 _ptr(status), _stream(stream)))
+
+
+def colibri_kv_append(desc: coli_kv_desc, n_tokens: int, n_valid, latent, latent_stride: int, rope, rope_stride: int,
+                      slot, cache, stream=None):
+    """Write n_tokens new rows (latent and rotary part) into the paged cache at their slots."""
+    _check(lib().colibri_kv_append(ctypes.byref(desc), n_tokens, _ptr(n_valid), _ptr(latent), latent_stride,
+                                   _ptr(rope), rope_stride, _ptr(slot), _ptr(cache), _stream(stream)))
+
+
+def colibri_kv_attention_workspace_size(B: int, n_tokens: int, H: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().colibri_kv_attention_workspace_size(B, n_tokens, H, ctypes.byref(n)))
+    return n.value
+
+
+def colibri_kv_attention(desc: coli_kv_desc, B: int, n_tokens: int, H: int, scale: float, q, q_token_stride: int,
+                         q_head_stride: int, cache, block_table, q_start, seq_len, topk_idx, topk: int, out, lse,
+                         workspace, workspace_bytes: int, stream=None):
+    """Attention of the new tokens over the paged cache, over every key up to a token's position or over the keys
+    topk_idx names (see the header)."""
+    _check(lib().colibri_kv_attention(ctypes.byref(desc), B, n_tokens, H, scale, _ptr(q), q_token_stride,
+                                      q_head_stride, _ptr(cache), _ptr(block_table), _ptr(q_start), _ptr(seq_len),
+                                      _ptr(topk_idx), topk, _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes,
+                                      _stream(stream)))
+
+
+def colibri_kv_check_status(workspace, stream=None) -> int:
+    v = ctypes.c_int32()
+    rc = lib().colibri_kv_check_status(_ptr(workspace), ctypes.byref(v), _stream(stream))
     if rc not in (COLI_OK, COLI_EDEVICE):
         _check(rc)
     return v.value
@@ -377,6 +457,12 @@ class Plan:
         _check(lib().colibri_moe_set_idot(self.handle, 1 if enable else 0))
 
     set_idot = colibri_moe_set_idot
+
+    def colibri_moe_set_route(self, desc: coli_route_desc | None):
+        """Routing of the following forward calls (None: the plan's own)."""
+        _check(lib().colibri_moe_set_route(self.handle, ctypes.byref(desc) if desc is not None else None))
+
+    set_route = colibri_moe_set_route
 
     def colibri_moe_debug_hidden(self, workspace, T: int, h_out, stream=None):
         """The down projection's input of the last forward (device float [rows, Fmax], grouped row order)."""

@@ -316,6 +316,8 @@ coli_status coli::forward_impl(coli_moe_plan* plan, const ExpertTables& tb, Betw
   a.wait_ns = plan->wait_ns;
   a.inject = plan->inject;
   a.idot = plan->idot;
+  a.routed = plan->routed;
+  a.route = plan->route;
 
   const bool prof = plan->prof_calls < plan->prof_max_calls;
   int launches = 0;

@@ -1,0 +1,869 @@
+// Attention of new tokens over the paged compressed cache ("25GB RAM runs 744B
+// GLM-5.2" page (pwwt.cn), section 3.2: 576 cached values a token; section 3.3:
+// sparse attention over the selected keys):
+//   out[n][h] = sum_j p_j v[j],  p = softmax_j(scale * q[n][h] . k[j]),
+// k[j] the cached row of key j (576 values), v[j] its first 512.
+//
+// Every head of a token shares the cached row, so a tile of 64 (token, head)
+// rows and 128 keys is two dense contractions of the same 128 cached rows, and
+// the tile is loaded once for both (tcgen05, operands in shared memory, fp32
+// accumulators in tensor memory):
+//   S^T[128 keys][64 rows]  = K Q^T    (K as it lies: keys are the MMA's M)
+//   O^T[512][64 rows]      += V^T P^T  (V^T is the same tile read transposed)
+// The transposed form is what makes it fit: O^T takes 256 of the 512 TMEM
+// columns, where 128 rows of O would take all of them, and each thread of the
+// softmax holds one key's 64 scores, so that its weights are one 128-byte row
+// of the P^T operand.  Shared memory: 144 KB of cached rows, 72 KB of queries;
+// P^T takes the place of the rotary part, which only S^T reads.
+//
+// Softmax: per row a reference m (log2 units) that is raised, with the sums and
+// O^T rescaled, only when a score exceeds it by 8: weights stay below 2^8, and
+// a tile needs no reduction over its keys (they lie across lanes).  References
+// are whole numbers, so that raising one rounds nothing.  Each thread sums its
+// own key's weights; the sums are reduced once at the end.
+//
+// Work: the plan kernel lists the units (64 rows of one request, or of one
+// token where keys are selected) with their key tiles and deals the tiles in
+// equal runs to one CTA per SM.  A unit cut by a border leaves partial results
+// in the workspace, which the join kernel adds up in order.
+#include <numeric>
+
+#include "plan.h"
+
+namespace coli {
+
+constexpr int kAtW = COLI_KV_WIDTH, kAtV = COLI_KV_VALUE;
+constexpr int kAtKeys = 128;                       // keys a tile (MMA M of S^T, TMEM lanes)
+constexpr int kAtRows = 64;                        // (token, head) rows a unit (MMA N)
+constexpr int kAtBoxBytes = kAtKeys * 128;         // 64 columns of a key tile, 128-byte swizzle
+constexpr int kAtQBoxBytes = kAtRows * 128;        // 64 columns of the queries
+constexpr int kAtBoxes = kAtW / 64;                // 9: eight of values, one rotary
+constexpr int kAtThreads = 6 * 32;
+constexpr int kAtMaxCtas = 160;                    // CTAs the workspace has room for
+constexpr size_t kAtSmem = (size_t)kAtBoxes * (kAtBoxBytes + kAtQBoxBytes) + 1024;
+constexpr int kAtPart = kAtRows * kAtV;            // floats of a partial O
+constexpr float kAtUnset = -1e30f;                 // reference of a part whose row has seen no key
+constexpr float kAtGrow = 8.f;                     // growth (log2) that raises a reference
+constexpr uint32_t kAtSCol = 256;                  // TMEM column of S^T (O^T: 0..255)
+
+struct AtUnit {
+  int b;        // request
+  int row0;     // first (token * H + head) row
+  int first;    // key tiles of the units before it
+  int tiles;    // its key tiles
+};
+
+struct AtArgs {
+  coli_kv_desc d;
+  int B, n_tokens, H, topk;
+  float scale_log2;
+  int rows_per_page;                 // cached rows from a page to the next (page_stride / 576)
+  int q_tok, q_head;                 // query tensor rows from a token (a head) to the next
+  const int32_t *table, *q_start, *seq_len, *sel;
+  uint16_t* out;
+  float* lse;
+  int32_t* status;
+  int* head;                         // [0] units, [1] CTAs, [2] key tiles, [4 ..) first unit of each CTA
+  AtUnit* units;
+  float* part;                       // [2 kAtMaxCtas][64][512]
+  float2* part_ml;                   // [2 kAtMaxCtas][64] reference, sum
+  unsigned long long wait_ns;
+};
+
+// The token rows of request b, kept inside the batch whatever q_start holds.
+__device__ __forceinline__ void at_span(const AtArgs& p, int b, int& q0, int& q1) {
+  const int lo = max(0, min(p.q_start[0], p.n_tokens)), hi = max(lo, min(p.q_start[p.B], p.n_tokens));
+  q0 = max(lo, min(p.q_start[b], hi));
+  q1 = max(q0, min(p.q_start[b + 1], hi));
+}
+
+// Border j of G equal runs of the W key tiles.
+__device__ __forceinline__ int at_cut(int W, int j, int G) { return (int)((long long)W * j / G); }
+
+// ------------------------------------------------------------------ plan
+// One CTA.  Dense: request b has T H rows, units of 64; a unit's keys end with its last row's position.
+// Selected keys: a token's heads in units of 64, all topk entries.
+constexpr int kAtPlanThreads = 1024;
+
+__global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(const AtArgs p, int max_units, int max_ctas) {
+  extern __shared__ int base_sm[];   // [B + 1] first unit of each request
+  __shared__ int warp_tot[32], total;
+  const int tid = threadIdx.x;
+  griddep_launch_dependents();
+  int carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kAtPlanThreads) {
+    const int b = b0 + tid;
+    int u = 0;
+    if (b < p.B) {
+      int q0, q1;
+      at_span(p, b, q0, q1);
+      u = p.sel ? (q1 - q0) * ((p.H + kAtRows - 1) / kAtRows)
+                : (int)(((long long)(q1 - q0) * p.H + kAtRows - 1) / kAtRows);
+    }
+    const int e = block_exclusive_scan(u, warp_tot, &total);
+    if (b < p.B) base_sm[b] = carry + e;
+    carry += total;
+    __syncthreads();
+  }
+  const int n_units = min(carry, max_units);       // (more only from a q_start that is not ascending)
+  if (tid == 0) base_sm[p.B] = carry;
+  __syncthreads();
+  int tiles = 0;
+  for (int u0 = 0; u0 < n_units; u0 += kAtPlanThreads) {
+    const int u = u0 + tid;
+    int c = 0;
+    AtUnit un{};
+    if (u < n_units) {
+      int l = 0, h = p.B;                          // last b with base[b] <= u
+      while (h - l > 1) {
+        const int mid = (l + h) >> 1;
+        if (base_sm[mid] <= u) l = mid;
+        else h = mid;
+      }
+      int q0, q1;
+      at_span(p, l, q0, q1);
+      un.b = l;
+      if (p.sel) {
+        const int ht = (p.H + kAtRows - 1) / kAtRows, i = u - base_sm[l];
+        un.row0 = (q0 + i / ht) * p.H + (i % ht) * kAtRows;
+        c = (p.topk + kAtKeys - 1) / kAtKeys;
+      } else {
+        un.row0 = q0 * p.H + (u - base_sm[l]) * kAtRows;
+        const int last_tok = min(q1 - 1, (un.row0 + kAtRows - 1) / p.H);
+        const long long keys = (long long)p.seq_len[l] - (q1 - q0) + (last_tok - q0) + 1;
+        const long long most = (long long)p.d.max_pages * p.d.page_size;
+        c = (int)((max(0ll, min(keys, most)) + kAtKeys - 1) / kAtKeys);
+      }
+      c = max(c, 1);                               // a unit without keys still writes its rows
+    }
+    const int e = block_exclusive_scan(c, warp_tot, &total);
+    if (u < n_units) {
+      un.first = tiles + e;
+      un.tiles = c;
+      p.units[u] = un;
+    }
+    tiles += total;
+    __syncthreads();
+  }
+  const int G = min(max_ctas, tiles);
+  if (tid == 0) {
+    p.head[0] = n_units;
+    p.head[1] = G;
+    p.head[2] = tiles;
+    *p.status = 0;
+  }
+  // the unit that holds each run's first tile
+  for (int j = tid; j < G; j += kAtPlanThreads) {
+    const int cut = at_cut(tiles, j, G);
+    int l = 0, h = n_units;
+    while (h - l > 1) {
+      const int mid = (l + h) >> 1;
+      if (p.units[mid].first <= cut) l = mid;
+      else h = mid;
+    }
+    p.head[4 + j] = l;
+  }
+}
+
+// ------------------------------------------------------------------ main kernel
+
+// Four rows of a tensor (rows y0..y3, 64 columns from x) into four consecutive 128-byte rows of shared memory.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int x, int4 y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Operand read transposed (MN-major), 128-byte swizzle: the operand's M (or N) runs along the 128-byte rows,
+// 64 elements an atom, the next 64 `mn_bytes` further; K runs down the rows, 8 an atom of 1024 bytes.
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t mn_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(mn_bytes >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+__device__ __forceinline__ float at_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t at_pack(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Barrier of the four softmax warps; with `or`: whether any thread's pred is true.
+__device__ __forceinline__ void sm_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool sm_any(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred)
+      : "memory");
+  return r != 0;
+}
+
+// Reduce v[64] over the warp's lanes; lane l ends with the results of columns 2 l and 2 l + 1.
+template <typename F>
+__device__ __forceinline__ float2 warp_columns(const float (&v)[64], F op) {
+  const int lane = threadIdx.x & 31;
+  float w[32];
+  // fold: a lane keeps the half of the columns that its bit chooses and gives the other half away
+  {
+    const bool up = lane & 16;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float keep = up ? v[32 + i] : v[i], give = up ? v[i] : v[32 + i];
+      w[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 16));
+    }
+  }
+#pragma unroll
+  for (int o = 8, n = 16; o >= 1; o >>= 1, n >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = up ? w[n + i] : w[i], give = up ? w[i] : w[n + i];
+      w[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  return make_float2(w[0], w[1]);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kAtThreads, 1)
+    kv_attention_kernel(const AtArgs p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ uint64_t full[5], empty[4], q_full, q_empty, s_full, p_ready, o_full;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  __shared__ uint32_t key_ok[2][4];                    // bit i of word w: key 32 w + i of the tile is there
+  __shared__ __align__(16) float ref[kAtRows], fac[kAtRows], red[4][kAtRows];
+  __shared__ __align__(16) int lim[kAtRows];           // last key position each row sees (dense)
+  __shared__ int has_ref[kAtRows];                     // the row has seen a key
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qs = smem + kAtBoxes * kAtBoxBytes;
+  uint8_t* rot = smem + 8 * kAtBoxBytes;               // rotary part of the keys, then P^T
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_v = &abort_flag;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 5; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&empty[i], 1);
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&s_full, 1);
+    mbar_init(&p_ready, 4);
+    mbar_init(&o_full, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  griddep_wait();                                      // the plan kernel's lists
+  griddep_launch_dependents();
+  const int G = p.head[1], W = p.head[2];
+  const int cta = blockIdx.x;
+  const int beg = cta < G ? at_cut(W, cta, G) : 0, end = cta < G ? at_cut(W, cta + 1, G) : 0;
+  const int unit0 = cta < G ? p.head[4 + cta] : 0;
+  auto fail_wait = [&]() {
+    atomicOr(p.status, COLI_DEV_WAIT_TIMEOUT);
+    atomicExch(&abort_flag, 1);
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loader: each lane gathers four keys' rows
+    bool ok = true;
+    int it = 0, un = 0;
+    const long long n_rows = (long long)p.d.n_pages * p.rows_per_page;
+    for (int at = beg, u = unit0; ok && at < end; ++u, ++un) {
+      const AtUnit ut = p.units[u];
+      const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
+      const int tok = ut.row0 / p.H;
+      int q0, q1;
+      at_span(p, ut.b, q0, q1);
+      const int seq = p.seq_len[ut.b];
+      const int row_end = p.sel ? (tok + 1) * p.H : q1 * p.H;
+      const int seen = p.sel ? min(seq, seq - (q1 - q0) + (tok - q0) + 1) : seq;   // keys before this are there
+      // the cached rows of this lane's four keys of tile t, and which of them are there
+      auto rows_of = [&](int t, int4& y, unsigned& there) {
+        int r[4];
+        there = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int key = t * kAtKeys + lane * 4 + i;
+          if (p.sel) key = key < p.topk ? p.sel[(size_t)tok * p.topk + key] : -1;
+          r[i] = 0;
+          if (key < 0 || key >= seen) continue;
+          const int col = key / p.d.page_size;
+          const int page = col < p.d.max_pages ? p.table[(size_t)ut.b * p.d.max_pages + col] : -1;
+          if (page < 0 || page >= p.d.n_pages) {
+            atomicOr(p.status, COLI_DEV_KV_BAD_PAGE);
+            continue;
+          }
+          const long long row = (long long)page * p.rows_per_page + (key - col * p.d.page_size);
+          if (row < n_rows) {
+            r[i] = (int)row;
+            there |= 1u << i;
+          }
+        }
+        y = make_int4(r[0], r[1], r[2], r[3]);
+      };
+      int4 y;
+      unsigned there;
+      rows_of(t0, y, there);
+      // queries
+      if (un > 0 && !mbar_wait(&q_empty, (un - 1) & 1, p.wait_ns)) { ok = false; break; }
+      if (lane == 0) mbar_arrive_expect_tx(&q_full, (uint32_t)(kAtBoxes * kAtQBoxBytes));
+      __syncwarp();
+      if (lane < 16) {
+        int r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int row = ut.row0 + lane * 4 + i;
+          if (row >= row_end) row = ut.row0;           // rows past the unit's last: computed, not written
+          r[i] = (row / p.H) * p.q_tok + (row % p.H) * p.q_head;
+        }
+#pragma unroll 1
+        for (int x = 0; x < kAtBoxes; ++x)
+          tma_gather4(qs + x * kAtQBoxBytes + lane * 512, &qmap, x * 64, make_int4(r[0], r[1], r[2], r[3]), &q_full);
+      }
+      for (int t = t0; t < t1; ++t, ++it) {
+        if (*abort_v) { ok = false; break; }
+        // pairs of value boxes as the previous tile's products free them, then the rotary box
+#pragma unroll 1
+        for (int d = 0; d < 4 && ok; ++d) {
+          if (it > 0 && !mbar_wait(&empty[d], (it - 1) & 1, p.wait_ns)) { ok = false; break; }
+          if (d == 0) {
+            // which keys are there, as bits in key order: lane l holds keys 4 l .. 4 l + 3
+            unsigned word = there << ((lane & 7) * 4);
+            word |= __shfl_xor_sync(0xffffffffu, word, 1);
+            word |= __shfl_xor_sync(0xffffffffu, word, 2);
+            word |= __shfl_xor_sync(0xffffffffu, word, 4);
+            if ((lane & 7) == 0) key_ok[it & 1][lane >> 3] = word;
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&full[d], (uint32_t)(2 * kAtBoxBytes));
+          __syncwarp();
+          tma_gather4(smem + (2 * d) * kAtBoxBytes + lane * 512, &kmap, (2 * d) * 64, y, &full[d]);
+          tma_gather4(smem + (2 * d + 1) * kAtBoxBytes + lane * 512, &kmap, (2 * d + 1) * 64, y, &full[d]);
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&full[4], (uint32_t)kAtBoxBytes);
+        __syncwarp();
+        tma_gather4(rot + lane * 512, &kmap, 8 * 64, y, &full[4]);
+        if (t + 1 < t1) rows_of(t + 1, y, there);
+      }
+      at = ut.first + t1;
+    }
+    if (!ok) {
+      fail_wait();
+      // copies in flight land before the CTA leaves
+      if (lane == 0) {
+        mbar_wait(&q_full, un & 1, 1000000ull);
+        for (int d = 0; d < 5; ++d) {
+          mbar_wait(&full[d], it & 1, 1000000ull);
+          if (it > 0) mbar_wait(&full[d], (it - 1) & 1, 1000000ull);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t fmt = BF16 ? (1u << 7) | (1u << 10) : 0u;
+      const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)(kAtRows >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+      const uint32_t idesc_t = idesc | (1u << 15) | (1u << 16);          // both operands MN-major
+      const uint64_t kd = umma_desc_sw128(smem_u32(smem)), qd = umma_desc_sw128(smem_u32(qs));
+      const uint64_t vd = umma_desc_sw128_mn(smem_u32(smem), kAtBoxBytes);
+      const uint64_t pd = umma_desc_sw128_mn(smem_u32(rot), kAtBoxBytes);
+      bool ok = true;
+      int it = 0, un = 0;
+      for (int at = beg, u = unit0; ok && at < end; ++u, ++un) {
+        const AtUnit ut = p.units[u];
+        const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
+        if (!mbar_wait_spin(&q_full, un & 1, p.wait_ns)) { ok = false; break; }
+        for (int t = t0; t < t1; ++t, ++it) {
+          if (*abort_v) { ok = false; break; }
+          // S^T: nine boxes of 64 columns, four steps of 16 each
+          for (int x = 0; x < kAtBoxes; ++x) {
+            if ((x & 1) == 0 && !mbar_wait_spin(&full[x >> 1], it & 1, p.wait_ns)) { ok = false; break; }
+            if ((x & 1) == 0) tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              umma_ss(tmem + kAtSCol, kd + (uint64_t)(x * (kAtBoxBytes >> 4) + s * 2),
+                      qd + (uint64_t)(x * (kAtQBoxBytes >> 4) + s * 2), idesc, (x | s) ? 1u : 0u);
+          }
+          if (!ok) break;
+          umma_commit(&s_full);
+          if (t + 1 == t1) umma_commit(&q_empty);
+          if (!mbar_wait_spin(&p_ready, it & 1, p.wait_ns)) { ok = false; break; }
+          tc_fence_after();
+          // O^T: four blocks of 128 values, eight steps of 16 keys each
+#pragma unroll 1
+          for (int d = 0; d < 4; ++d) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              umma_ss(tmem + (uint32_t)(d * kAtRows), vd + (uint64_t)(2 * d * (kAtBoxBytes >> 4) + s * 128),
+                      pd + (uint64_t)(s * 128), idesc_t, (t > t0 || s) ? 1u : 0u);
+            umma_commit(&empty[d]);
+          }
+        }
+        if (!ok) break;
+        umma_commit(&o_full);
+        at = ut.first + t1;
+      }
+      if (!ok) {
+        fail_wait();
+        // what was issued ends before tensor memory is freed
+        umma_commit(&o_full);
+        mbar_wait(&o_full, un & 1, p.wait_ns);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax and output (warps 2..5)
+    const int sp = warp & 3;                           // TMEM sub-partition: keys 32 sp .. 32 sp + 31 of a tile
+    const int me = sp * 32 + lane;                     // this thread's key of a tile, value of a block of O^T
+    const uint32_t trow = tmem + ((uint32_t)(sp * 32) << 16);
+    int it = 0, un = 0;
+    for (int at = beg, u = unit0; at < end; ++u, ++un) {
+      const AtUnit ut = p.units[u];
+      const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
+      const bool whole = t0 == 0 && t1 == ut.tiles;
+      const int slot = 2 * cta + (u == unit0 ? 0 : 1);
+      const int tok0 = ut.row0 / p.H;
+      int q0, q1;
+      at_span(p, ut.b, q0, q1);
+      const int row_end = p.sel ? (tok0 + 1) * p.H : q1 * p.H;
+      const int past = p.seq_len[ut.b] - (q1 - q0);     // position of the request's first new token
+      if (me < kAtRows) {
+        const int row = min(ut.row0 + me, row_end - 1);
+        lim[me] = p.sel ? 0x7fffffff : past + row / p.H - q0;
+        ref[me] = 0.f;
+        has_ref[me] = 0;
+      }
+      const int seen_all = past + tok0 - q0;            // every row of the unit sees the keys up to this one
+      float l[kAtRows];
+#pragma unroll
+      for (int c = 0; c < kAtRows; ++c) l[c] = 0.f;
+      sm_sync();
+      bool ok = true, unset = true;                    // unset: some row has no reference yet
+      for (int t = t0; t < t1; ++t, ++it) {
+        // (the rotary box's barrier orders the loader's key_ok before this read)
+        ok = mbar_wait(&full[4], it & 1, p.wait_ns) && mbar_wait(&s_full, it & 1, p.wait_ns);
+        tc_fence_after();
+        float x[kAtRows];
+        {
+          uint32_t r[4][16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld16_issue(trow + kAtSCol + c * 16, r[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < kAtRows; ++c) x[c] = __uint_as_float(r[c >> 4][c & 15]);
+        }
+        const uint32_t kw = key_ok[it & 1][sp];
+        const bool there = (kw >> lane) & 1u;
+        const int key = t * kAtKeys + me;
+        bool bad_key = false;
+        const bool masked = p.sel ? kw != 0xffffffffu : (t * kAtKeys + sp * 32 + 31 > seen_all || kw != 0xffffffffu);
+        if (masked) {                                  // warp-uniform
+          // a key whose every score is not finite holds an infinity or a NaN: its values must not meet the
+          // zero weights of the rows that do not see it
+          bool fin = false;
+#pragma unroll
+          for (int c = 0; c < kAtRows; ++c) fin |= fabsf(x[c]) < INFINITY;
+          bad_key = !fin;
+#pragma unroll
+          for (int c = 0; c < kAtRows; c += 4) {
+            const int4 lm = *reinterpret_cast<const int4*>(&lim[c]);
+            if (!there || (!p.sel && key > lm.x)) x[c] = -INFINITY;
+            if (!there || (!p.sel && key > lm.y)) x[c + 1] = -INFINITY;
+            if (!there || (!p.sel && key > lm.z)) x[c + 2] = -INFINITY;
+            if (!there || (!p.sel && key > lm.w)) x[c + 3] = -INFINITY;
+          }
+        }
+        // distance to the references; does any score exceed its row's by more than kAtGrow?
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kAtRows; c += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&ref[c]);
+          x[c] = fmaf(x[c], p.scale_log2, -m.x);
+          x[c + 1] = fmaf(x[c + 1], p.scale_log2, -m.y);
+          x[c + 2] = fmaf(x[c + 2], p.scale_log2, -m.z);
+          x[c + 3] = fmaf(x[c + 3], p.scale_log2, -m.w);
+          top = fmaxf(fmaxf(fmaxf(top, x[c]), fmaxf(x[c + 1], x[c + 2])), x[c + 3]);
+        }
+        if (sm_any(top > kAtGrow || unset || !ok)) {
+          if (sm_any(!ok)) { ok = false; break; }
+          const float2 cm = warp_columns(x, [](float a, float b) { return fmaxf(a, b); });
+          *reinterpret_cast<float2*>(&red[sp][2 * lane]) = cm;
+          sm_sync();
+          bool none = false;
+          if (me < kAtRows) {
+            const float g = ceilf(fmaxf(fmaxf(red[0][me], red[1][me]), fmaxf(red[2][me], red[3][me])));
+            const bool raise = g > kAtGrow || (!has_ref[me] && g > -INFINITY);
+            fac[me] = raise ? g : 0.f;                 // by how much
+            if (raise) {
+              ref[me] += g;
+              has_ref[me] = 1;
+            }
+            none = !has_ref[me];
+          }
+          unset = sm_any(none);
+#pragma unroll
+          for (int c = 0; c < kAtRows; ++c) {
+            const float g = fac[c];
+            x[c] -= g;
+            l[c] *= at_exp2(-g);
+          }
+          if (t > t0) {                                // (the first tile's products overwrite O^T)
+#pragma unroll 1
+            for (int d = 0; d < 4; ++d) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t r[16];
+                tmem_ld16_issue(trow + d * kAtRows + c * 16, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  r[i] = __float_as_uint(__uint_as_float(r[i]) * at_exp2(-fac[c * 16 + i]));
+                tmem_st16(trow + d * kAtRows + c * 16, r);
+              }
+            }
+            tmem_st_wait();
+          }
+        }
+        // weights, their sums, and the key's row of P^T (64 weights = 128 bytes, swizzled)
+        uint8_t* prow = rot + me * 128;
+#pragma unroll
+        for (int c = 0; c < kAtRows; c += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = at_exp2(x[c + 2 * i]), b = at_exp2(x[c + 2 * i + 1]);
+            l[c + 2 * i] += a;
+            l[c + 2 * i + 1] += b;
+            w[i] = at_pack<BF16>(a, b);
+          }
+          *reinterpret_cast<uint4*>(prow + (((c >> 3) ^ (me & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (bad_key) {
+#pragma unroll 1
+          for (int i = 0; i < 64; ++i)
+            *reinterpret_cast<uint4*>(smem + (i >> 3) * kAtBoxBytes + me * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_ready);
+      }
+      if (!ok) {
+        fail_wait();
+        break;
+      }
+      // -------------------------------------------------------------- the unit's rows
+      ok = mbar_wait(&o_full, un & 1, p.wait_ns);
+      tc_fence_after();
+      const float2 ls = warp_columns(l, [](float a, float b) { return a + b; });
+      *reinterpret_cast<float2*>(&red[sp][2 * lane]) = ls;
+      if (sm_any(!ok)) {
+        fail_wait();
+        break;
+      }
+      if (me < kAtRows) {
+        const float sum = (red[0][me] + red[1][me]) + (red[2][me] + red[3][me]);
+        if (whole) {
+          fac[me] = sum == 0.f ? 0.f : 1.0f / sum;
+          const int row = ut.row0 + me;
+          if (p.lse && row < row_end)
+            p.lse[row] = sum == 0.f ? -INFINITY : (ref[me] + log2f(sum)) * 0.693147180559945309f;
+        } else {
+          p.part_ml[(size_t)slot * kAtRows + me] = make_float2(has_ref[me] ? ref[me] : kAtUnset, sum);
+        }
+      }
+      sm_sync();
+      const int rows = min(kAtRows, row_end - ut.row0);
+      float* part = p.part + (size_t)slot * kAtPart;
+#pragma unroll 1
+      for (int d = 0; d < 4; ++d) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[16];
+          tmem_ld16_issue(trow + d * kAtRows + c * 16, r);
+          tmem_ld_wait();
+          if (whole) {
+            // lanes 2 i and 2 i + 1 hold neighbouring values of a row: they trade halves of two rows
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const int c0 = c * 16 + i;
+              const float a = __uint_as_float(r[i]) * fac[c0], b = __uint_as_float(r[i + 1]) * fac[c0 + 1];
+              const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
+              const int cc = c0 + (lane & 1);
+              const uint32_t two = (lane & 1) ? at_pack<BF16>(got, b) : at_pack<BF16>(a, got);
+              if (cc < rows)
+                *reinterpret_cast<uint32_t*>(p.out + (size_t)(ut.row0 + cc) * kAtV + d * 128 + (me & ~1)) = two;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c * 16 + i < rows) part[(c * 16 + i) * kAtV + d * 128 + me] = __uint_as_float(r[i]);
+          }
+        }
+      }
+      tc_fence_before();
+      sm_sync();                                       // everyone is done with ref, fac, red
+      at = ut.first + t1;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  }
+}
+
+// ------------------------------------------------------------------ join
+// Block (j - 1, row): the unit cut by border j, if j is the first border inside it.  Its parts lie in
+// the workspace in CTA order; they are added up in that order.
+constexpr int kAtJoinThreads = 128;
+
+template <bool BF16>
+__global__ void __launch_bounds__(kAtJoinThreads) kv_attention_join_kernel(const AtArgs p) {
+  __shared__ float wgt[kAtMaxCtas];
+  __shared__ float s_m, s_l;
+  griddep_wait();
+  const int G = p.head[1], W = p.head[2];
+  const int j = blockIdx.x + 1, r = blockIdx.y;
+  if (j >= G) return;
+  const int cut = at_cut(W, j, G);
+  const AtUnit ut = p.units[p.head[4 + j]];
+  if (ut.first >= cut) return;                          // a border between units
+  if (at_cut(W, j - 1, G) > ut.first) return;           // not the unit's first border
+  const int row = ut.row0 + r;
+  int q0, q1;
+  at_span(p, ut.b, q0, q1);
+  const int row_end = p.sel ? (ut.row0 / p.H + 1) * p.H : q1 * p.H;
+  if (row >= row_end) return;
+  int n = 1;                                            // parts: CTAs j - 1, j, ...
+  while (j - 1 + n < G && at_cut(W, j - 1 + n, G) < ut.first + ut.tiles) ++n;
+  auto slot = [&](int i) { return 2 * (j - 1 + i) + (i == 0 && at_cut(W, j - 1, G) < ut.first ? 1 : 0); };
+  const int tid = threadIdx.x;
+  if (tid < 32) {
+    float m = kAtUnset;
+    for (int i = tid; i < n; i += 32) m = fmaxf(m, p.part_ml[(size_t)slot(i) * kAtRows + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.f;
+    for (int i = tid; i < n; i += 32) {
+      const float2 ml = p.part_ml[(size_t)slot(i) * kAtRows + r];
+      const float w = at_exp2(ml.x - m);
+      wgt[i] = w;
+      l += w * ml.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (tid == 0) {
+      s_m = m;
+      s_l = l;
+    }
+  }
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float4 v = *reinterpret_cast<const float4*>(p.part + (size_t)slot(i) * kAtPart + r * kAtV + tid * 4);
+    const float w = wgt[i];
+    acc.x = fmaf(w, v.x, acc.x);
+    acc.y = fmaf(w, v.y, acc.y);
+    acc.z = fmaf(w, v.z, acc.z);
+    acc.w = fmaf(w, v.w, acc.w);
+  }
+  const float inv = s_l == 0.f ? 0.f : 1.0f / s_l;
+  uint2 o;
+  o.x = at_pack<BF16>(acc.x * inv, acc.y * inv);
+  o.y = at_pack<BF16>(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(p.out + (size_t)row * kAtV + tid * 4) = o;
+  if (p.lse && tid == 0) p.lse[row] = s_l == 0.f ? -INFINITY : (s_m + log2f(s_l)) * 0.693147180559945309f;
+}
+
+// ------------------------------------------------------------------ host side
+
+struct AtWs {
+  size_t head, units, part, part_ml, total;
+  long long max_units;
+};
+
+static AtWs at_ws(int B, int n_tokens, int H) {
+  AtWs w;
+  // dense: sum over requests of ceil(T H / 64); selected keys: n_tokens * ceil(H / 64)
+  const long long dense = (long long)n_tokens * H / kAtRows + B + 1;
+  const long long sel = (long long)n_tokens * ((H + kAtRows - 1) / kAtRows);
+  w.max_units = dense > sel ? dense : sel;
+  size_t off = 256;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, 256);
+    return o;
+  };
+  w.head = take((4 + kAtMaxCtas) * sizeof(int));
+  w.units = take((size_t)w.max_units * sizeof(AtUnit));
+  w.part = take((size_t)2 * kAtMaxCtas * kAtPart * sizeof(float));
+  w.part_ml = take((size_t)2 * kAtMaxCtas * kAtRows * sizeof(float2));
+  w.total = off;
+  return w;
+}
+
+static CUresult at_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, bool bf16, const void* base,
+                       long long rows, long long stride) {
+  const cuuint64_t gdim[2] = {(cuuint64_t)kAtW, (cuuint64_t)rows};
+  const cuuint64_t gstr[1] = {(cuuint64_t)stride * 2};
+  const cuuint32_t box[2] = {64, 1};                   // gathers take one row a coordinate
+  const cuuint32_t es[2] = {1, 1};
+  return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                const_cast<void*>(base), gdim, gstr, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+template <bool BF16>
+static cudaError_t at_launch(const AtArgs& a, const CUtensorMap& kmap, const CUtensorMap& qmap, int max_units,
+                             int ctas, cudaStream_t st) {
+  kv_attention_plan_kernel<<<1, kAtPlanThreads, (a.B + 1) * sizeof(int), st>>>(a, max_units, ctas);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(kv_attention_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kv_attention_kernel<BF16>, dim3(ctas), dim3(kAtThreads), kAtSmem, st, a, kmap, qmap);
+  if (e != cudaSuccess || ctas < 2) return e;
+  return launch_pdl(kv_attention_join_kernel<BF16>, dim3(ctas - 1, kAtRows), dim3(kAtJoinThreads), 0, st, a);
+}
+
+}  // namespace coli
+
+using namespace coli;
+
+extern "C" {
+
+coli_status colibri_kv_attention_workspace_size(int B, int n_tokens, int H, size_t* bytes) {
+  if (!bytes || B < 1 || n_tokens < 0 || H < 1) return fail(COLI_EINVAL, "kv_attention_workspace_size: bad argument");
+  if ((long long)n_tokens * H > 0x7fffffffLL)
+    return fail(COLI_EUNSUPPORTED, "kv_attention_workspace_size: n_tokens * H exceeds 2^31 - 1 rows");
+  *bytes = at_ws(B, n_tokens, H).total;
+  return COLI_OK;
+}
+
+coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, int H, float scale, const void* q,
+                                 long long q_token_stride, long long q_head_stride, const void* cache,
+                                 const int32_t* block_table, const int32_t* q_start, const int32_t* seq_len,
+                                 const int32_t* topk_idx, int topk, void* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const coli_status rc = check_kv_desc(desc, "kv_attention");
+  if (rc != COLI_OK) return rc;
+  if (B < 1 || n_tokens < 0 || H < 1) return fail(COLI_EINVAL, "kv_attention: need B, H >= 1 and n_tokens >= 0");
+  if (B > 8192 || H > 1024) return fail(COLI_EUNSUPPORTED, "kv_attention: at most 8192 requests of 1024 heads");
+  if (desc->dtype != COLI_X_BF16 && desc->dtype != COLI_X_F16)
+    return fail(COLI_EUNSUPPORTED, "kv_attention: the cache holds bf16 or fp16 (dtype %d)", desc->dtype);
+  if (!(scale == scale) || scale - scale != 0.f) return fail(COLI_EINVAL, "kv_attention: scale is not finite");
+  if (topk_idx && topk < 1) return fail(COLI_EINVAL, "kv_attention: topk must be positive with topk_idx");
+  if ((long long)n_tokens * H > 0x7fffffffLL - 64)
+    return fail(COLI_EUNSUPPORTED, "kv_attention: n_tokens * H exceeds 2^31 rows");
+  const long long per_page = desc->page_stride / COLI_KV_WIDTH;
+  const long long cached = (desc->n_pages - 1LL) * per_page + desc->page_size;
+  if (cached > 0x7fffffffLL) return fail(COLI_EUNSUPPORTED, "kv_attention: the cache exceeds 2^31 - 1 rows");
+  if (n_tokens == 0) return COLI_OK;
+  if (!q || !cache || !block_table || !q_start || !seq_len || !out || !workspace)
+    return fail(COLI_EINVAL, "kv_attention: null pointer");
+  if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(out, 16) || !aligned(workspace, 256))
+    return fail(COLI_EALIGN, "kv_attention: q, cache and out 16-byte, workspace 256-byte alignment");
+  if (!aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(seq_len, 4) || !aligned(topk_idx, 4) || !aligned(lse, 4))
+    return fail(COLI_EALIGN, "kv_attention: a pointer is not 4-byte aligned");
+  // queries as rows of one stride: the common divisor of the token and head strides
+  const long long ts = n_tokens > 1 ? q_token_stride : 0, hs = H > 1 ? q_head_stride : 0;
+  if (ts < 0 || hs < 0 || (n_tokens > 1 && ts == 0) || (H > 1 && hs == 0))
+    return fail(COLI_EINVAL, "kv_attention: query strides must be positive");
+  const long long g0 = std::gcd(ts, hs), g = g0 ? g0 : kAtW;
+  if (g % 8) return fail(COLI_EALIGN, "kv_attention: query strides must be multiples of 8 elements");
+  if (g < kAtW) return fail(COLI_EUNSUPPORTED, "kv_attention: the query strides' common divisor is below %d", kAtW);
+  const long long q_rows = (n_tokens - 1LL) * (ts / g) + (H - 1LL) * (hs / g) + 1;
+  if (q_rows > 0x7fffffffLL) return fail(COLI_EUNSUPPORTED, "kv_attention: the queries span more than 2^31 - 1 rows");
+  const AtWs w = at_ws(B, n_tokens, H);
+  if (workspace_bytes < w.total)
+    return fail(COLI_EWORKSPACE, "kv_attention: workspace %zu bytes < required %zu", workspace_bytes, w.total);
+  const long long tiles = topk_idx ? (topk + kAtKeys - 1LL) / kAtKeys
+                                   : ((long long)desc->max_pages * desc->page_size + kAtKeys - 1) / kAtKeys;
+  if (w.max_units * tiles > 0x7fffffffLL)
+    return fail(COLI_EUNSUPPORTED, "kv_attention: %lld units of up to %lld key tiles exceed 2^31 - 1",
+                w.max_units, tiles);
+  auto encode = get_encode();
+  if (!encode) return fail(COLI_ECUDA, "kv_attention: cuTensorMapEncodeTiled is not available");
+  int dev = 0, sms = 0;
+  cudaError_t ce = cudaGetDevice(&dev);
+  if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (ce != cudaSuccess) return cuda_fail(ce, "kv_attention: device query");
+  const bool bf16 = desc->dtype == COLI_X_BF16;
+  CUtensorMap kmap, qmap;
+  CUresult r = at_map(encode, &kmap, bf16, cache, cached, kAtW);
+  if (r != CUDA_SUCCESS) return fail(COLI_ECUDA, "kv_attention: cache tensor map (%d)", (int)r);
+  r = at_map(encode, &qmap, bf16, q, q_rows, g);
+  if (r != CUDA_SUCCESS) return fail(COLI_ECUDA, "kv_attention: query tensor map (%d)", (int)r);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AtArgs a;
+  a.d = *desc;
+  a.B = B;
+  a.n_tokens = n_tokens;
+  a.H = H;
+  a.topk = topk_idx ? topk : 0;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.rows_per_page = (int)per_page;
+  a.q_tok = (int)(ts / g);
+  a.q_head = (int)(hs / g);
+  a.table = block_table;
+  a.q_start = q_start;
+  a.seq_len = seq_len;
+  a.sel = topk_idx;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.head = reinterpret_cast<int*>(ws + w.head);
+  a.units = reinterpret_cast<AtUnit*>(ws + w.units);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  a.wait_ns = kWaitLimitNs;
+  const int ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ce = bf16 ? at_launch<true>(a, kmap, qmap, (int)w.max_units, ctas, st)
+            : at_launch<false>(a, kmap, qmap, (int)w.max_units, ctas, st);
+  return ce == cudaSuccess ? COLI_OK : cuda_fail(ce, "kv_attention: launch");
+}
+
+coli_status colibri_kv_check_status(const void* workspace, int32_t* device_status, void* stream) {
+  if (!workspace || !device_status) return fail(COLI_EINVAL, "kv_check_status: null argument");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int32_t v = 0;
+  cudaError_t ce = cudaMemcpyAsync(&v, workspace, 4, cudaMemcpyDeviceToHost, st);
+  if (ce == cudaSuccess) ce = cudaStreamSynchronize(st);
+  if (ce != cudaSuccess) return cuda_fail(ce, "kv_check_status");
+  *device_status = v;
+  if (v) return fail(COLI_EDEVICE, "kv_attention device status 0x%x (wait timeout = 2, bad page = 64)", v);
+  return COLI_OK;
+}
+
+}  // extern "C"

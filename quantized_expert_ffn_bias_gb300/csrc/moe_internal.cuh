@@ -123,6 +123,8 @@ struct FwdArgs {
   unsigned long long wait_ns; // limit of every pipeline wait (kWaitLimitNs unless a test shortens it)
   int inject;                 // COLI_INJECT_* bits of a failure-path test, 0 in normal use
   int idot;                   // 1: integer-dot inputs (int8 codes per block of 32, power-of-two scale)
+  int routed;                 // 1: `route` decides the routing (colibri_moe_set_route)
+  coli_route_desc route;
 };
 
 // ---------------------------------------------------------------- launchers (one .cu file each)

@@ -57,10 +57,17 @@ struct coli_moe_plan {
   int inject = 0;
   // integer-dot expert inputs (colibri_moe_set_idot)
   int idot = 0;
+  // routing given by colibri_moe_set_route (routed = 0: the plan's own)
+  int routed = 0;
+  coli_route_desc route = {};
   unsigned long long wait_ns = coli::kWaitLimitNs;
 };
 
 namespace coli {
+// Ranges of a routing description (route.cu); `who` begins the message.
+coli_status check_route_desc(const coli_route_desc& r, const char* who);
+// Ranges of a paged cache description (kv_cache.cu).
+coli_status check_kv_desc(const coli_kv_desc* d, const char* who);
 coli_status forward_impl(coli_moe_plan* plan, const ExpertTables& tb, BetweenFn between, void* ctx, int T,
                          const void* x, const float* router_w, const float* bias, const float* residual, float* out,
                          void* workspace, size_t workspace_bytes, void* stream);

@@ -6,7 +6,7 @@
 // selection and scaling must be reproduced exactly).  Logits stay in fp32 on
 // CUDA cores: a TF32 contraction would move scores by ~1e-3 and break exact
 // top-k agreement.
-#include "moe_internal.cuh"
+#include "route_select.cuh"
 
 namespace coli {
 
@@ -312,6 +312,39 @@ __device__ void topk_token(const FwdArgs& a, int t, float* u, float* s) {
   if ((a.inject & COLI_INJECT_BAD_EXPERT_ID) && t == 0 && lane == 0) a.topk_idx[0] = -1;
 }
 
+// Routing given by colibri_moe_set_route: the token's logits (K-split partial sums in split order) in
+// registers, chosen by route_token.
+template <int NV>
+__device__ __forceinline__ void routed_token_nv(const FwdArgs& a, int t, int* sel_out) {
+  const int lane = threadIdx.x & 31;
+  float z[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 32 * i;
+    z[i] = -INFINITY;
+    if (e < a.E) {
+      float v = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < kRouterKSplit; ++ks) v += __ldcg(a.logits + ((size_t)ks * a.T + t) * a.E + e);
+      if (v == v) z[i] = v;
+    }
+  }
+  route_token<NV>(a.route, z, a.bias, a.topk_idx + (size_t)t * a.k, a.topk_w + (size_t)t * a.k, sel_out,
+                  a.near_tie + t);
+}
+
+__device__ __forceinline__ void routed_token(const FwdArgs& a, int t, int* sel_out) {
+  if (a.E <= 256) routed_token_nv<8>(a, t, sel_out);
+  else routed_token_nv<32>(a, t, sel_out);
+}
+
+__global__ void __launch_bounds__(kTopkWarps * 32) routed_topk_kernel(FwdArgs a) {
+  const int t = blockIdx.x * kTopkWarps + (threadIdx.x >> 5);
+  if (t >= a.T) return;
+  routed_token(a, t, nullptr);
+  if ((a.inject & COLI_INJECT_BAD_EXPERT_ID) && t == 0 && (threadIdx.x & 31) == 0) a.topk_idx[0] = -1;
+}
+
 __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(FwdArgs a) {
   extern __shared__ float sm[];
   const int warp = threadIdx.x >> 5;
@@ -324,7 +357,8 @@ __global__ void __launch_bounds__(kTopkWarps * 32) router_topk_kernel(FwdArgs a)
 cudaError_t launch_router_topk(const FwdArgs& a, cudaStream_t st) {
   const int blocks = (a.T + kTopkWarps - 1) / kTopkWarps;
   const size_t smem = (size_t)kTopkWarps * 2 * a.E * sizeof(float);
-  router_topk_kernel<<<blocks, kTopkWarps * 32, smem, st>>>(a);
+  if (a.routed) routed_topk_kernel<<<blocks, kTopkWarps * 32, 0, st>>>(a);
+  else router_topk_kernel<<<blocks, kTopkWarps * 32, smem, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -337,7 +371,9 @@ cudaError_t launch_router_topk(const FwdArgs& a, cudaStream_t st) {
 //   T*k <= 256 pairs.
 constexpr int kRouteThreads = 256;
 
-template <int NT, int XT>
+// RG: the routing is the one given by colibri_moe_set_route (an instantiation of its own, so that the
+// plan's own routing keeps its code).
+template <int NT, int XT, bool RG>
 __global__ void __launch_bounds__(kRouteThreads) route_decode_kernel(FwdArgs a) {
   // dynamic shared memory (last CTA): per token (u[E], s[E])
   extern __shared__ float sm[];
@@ -456,13 +492,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_decode_kernel(FwdArgs a) 
   __threadfence();
 
   // (4) top-k: every thread loads scores (all loads independent), then one warp per token selects
-  for (int i = tid; i < a.T * a.E; i += kRouteThreads) {
-    const int t = i / a.E, e = i - t * a.E;
-    float* u = topk_sm + (size_t)t * 2 * a.E;
-    router_scores(a, t, e, u[a.E + e], u[e]);
-  }
-  __syncthreads();
-  {
+  if constexpr (RG) {
+    for (int t = tid >> 5; t < a.T; t += kRouteThreads / 32) routed_token(a, t, sidx + t * a.k);
+  } else {
+    for (int i = tid; i < a.T * a.E; i += kRouteThreads) {
+      const int t = i / a.E, e = i - t * a.E;
+      float* u = topk_sm + (size_t)t * 2 * a.E;
+      router_scores(a, t, e, u[a.E + e], u[e]);
+    }
+    __syncthreads();
     const int warp = tid >> 5;
     for (int t = warp; t < a.T; t += kRouteThreads / 32) {
       float* u = topk_sm + (size_t)t * 2 * a.E;
@@ -556,7 +594,10 @@ cudaError_t launch_route_decode(const FwdArgs& a, cudaStream_t st) {
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
 #define COLI_ROUTE(NT)                                                                                    \
   {                                                                                                       \
-    auto kern = a.xtype == COLI_X_BF16 ? route_decode_kernel<NT, COLI_X_BF16> : route_decode_kernel<NT, COLI_X_F32>; \
+    auto kern = a.routed ? (a.xtype == COLI_X_BF16 ? route_decode_kernel<NT, COLI_X_BF16, true>                      \
+                                                   : route_decode_kernel<NT, COLI_X_F32, true>)                      \
+                         : (a.xtype == COLI_X_BF16 ? route_decode_kernel<NT, COLI_X_BF16, false>                     \
+                                                   : route_decode_kernel<NT, COLI_X_F32, false>);                    \
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);   \
     if (e != cudaSuccess) return e;                                                                       \
     kern<<<blocks, kRouteThreads, smem, st>>>(a);                                                         \
