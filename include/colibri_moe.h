@@ -577,7 +577,7 @@ COLI_API coli_status colibri_kv_append(const coli_kv_desc* desc, int n_tokens, c
  * the keys absorbed): 512 latent values, then 64 rotary.
  *   q            device [n_tokens][H][576] of desc->dtype with the strides (in
  *                elements) given; 16-byte aligned; the strides multiples of 8
- *                whose greatest common divisor is at least 576.  1 <= H <= 1024.
+ *                (a stride along an axis of one is not read).  1 <= H <= 1024.
  *   q_start      int32 [B + 1] ascending, seq_len int32 [B].
  *   topk_idx     device int32 [n_tokens][topk], or NULL (topk is then not read).
  *   out          device [n_tokens][H][512] of desc->dtype, 16-byte aligned.

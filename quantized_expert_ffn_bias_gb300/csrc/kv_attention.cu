@@ -26,8 +26,6 @@
 // token where keys are selected) with their key tiles and deals the tiles in
 // equal runs to one CTA per SM.  A unit cut by a border leaves partial results
 // in the workspace, which the join kernel adds up in order.
-#include <numeric>
-
 #include "plan.h"
 
 namespace coli {
@@ -38,7 +36,10 @@ constexpr int kAtRows = 64;                        // (token, head) rows a unit 
 constexpr int kAtBoxBytes = kAtKeys * 128;         // 64 columns of a key tile, 128-byte swizzle
 constexpr int kAtQBoxBytes = kAtRows * 128;        // 64 columns of the queries
 constexpr int kAtBoxes = kAtW / 64;                // 9: eight of values, one rotary
-constexpr int kAtThreads = 6 * 32;
+constexpr int kAtLoadWarps = 2;                    // loader warps that copy rows themselves (one issues TMA loads)
+constexpr int kAtLaneKeys = kAtKeys / (32 * kAtLoadWarps);   // keys of a tile a copying lane looks up
+constexpr int at_threads(bool tma) { return (5 + (tma ? 1 : kAtLoadWarps)) * 32; }
+constexpr int kAtMinBox = 8;                       // fewest key rows a TMA box has
 constexpr int kAtMaxCtas = 160;                    // CTAs the workspace has room for
 constexpr size_t kAtSmem = (size_t)kAtBoxes * (kAtBoxBytes + kAtQBoxBytes) + 1024;
 constexpr int kAtPart = kAtRows * kAtV;            // floats of a partial O
@@ -58,7 +59,9 @@ struct AtArgs {
   int B, n_tokens, H, topk;
   float scale_log2;
   int rows_per_page;                 // cached rows from a page to the next (page_stride / 576)
-  int q_tok, q_head;                 // query tensor rows from a token (a head) to the next
+  int box;                           // TMA loads: key rows of a box (divides the page size and 128)
+  long long q_tok, q_head;           // query strides, bytes
+  const uint8_t *q, *cache;
   const int32_t *table, *q_start, *seq_len, *sel;
   uint16_t* out;
   float* lse;
@@ -167,13 +170,12 @@ __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(co
 
 // ------------------------------------------------------------------ main kernel
 
-// Four rows of a tensor (rows y0..y3, 64 columns from x) into four consecutive 128-byte rows of shared memory.
-__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, int x, int4 y, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(smem_u32(bar))
-      : "memory");
+// 16 bytes of global memory into shared memory, asynchronously; `bar` counts this thread once its copies so far have landed.
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Operand read transposed (MN-major), 128-byte swizzle: the operand's M (or N) runs along the 128-byte rows,
@@ -241,8 +243,12 @@ __device__ __forceinline__ float2 warp_columns(const float (&v)[64], F op) {
   return make_float2(w[0], w[1]);
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kAtThreads, 1)
+// TMA: key tiles arrive as TMA boxes of p.box rows (pages of a multiple of eight rows, every key up to the
+// position) and the queries as one box a 64 columns (token and head rows evenly spaced); otherwise two warps
+// copy row by row (cp.async), from pages of any size, for selected keys and for queries of any strides.  A
+// gathering TMA load of four rows a coordinate measured 83 cycles for 512 bytes, 12.5 us a tile of 128 keys.
+template <bool BF16, bool TMA>
+__global__ void __launch_bounds__(at_threads(TMA), 1)
     kv_attention_kernel(const AtArgs p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint64_t full[5], empty[4], q_full, q_empty, s_full, p_ready, o_full;
@@ -259,9 +265,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
   volatile int* abort_v = &abort_flag;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 5; ++i) mbar_init(&full[i], 1);
+    // copying warps: one arrival a thread, and one a warp for key_ok (with the rotary box)
+    for (int i = 0; i < 5; ++i) mbar_init(&full[i], TMA ? 1 : kAtLoadWarps * 32 + (i == 4 ? kAtLoadWarps : 0));
     for (int i = 0; i < 4; ++i) mbar_init(&empty[i], 1);
-    mbar_init(&q_full, 1);
+    mbar_init(&q_full, TMA ? 1 : kAtLoadWarps * 32);
     mbar_init(&q_empty, 1);
     mbar_init(&s_full, 1);
     mbar_init(&p_ready, 4);
@@ -289,11 +296,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     atomicExch(&abort_flag, 1);
   };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- loader: each lane gathers four keys' rows
+  if (warp == 0 || warp > 5) {
+    // ---------------------------------------------------------------- loader
+    const int lw = warp == 0 ? 0 : warp - 5;           // copying: this warp's keys of a tile start at 32 kAtLaneKeys lw
     bool ok = true;
     int it = 0, un = 0;
-    const long long n_rows = (long long)p.d.n_pages * p.rows_per_page;
+    const int n_box = TMA ? kAtKeys / p.box : 0;       // boxes of 64 columns a tile
     for (int at = beg, u = unit0; ok && at < end; ++u, ++un) {
       const AtUnit ut = p.units[u];
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
@@ -303,85 +311,137 @@ __global__ void __launch_bounds__(kAtThreads, 1)
       const int seq = p.seq_len[ut.b];
       const int row_end = p.sel ? (tok + 1) * p.H : q1 * p.H;
       const int seen = p.sel ? min(seq, seq - (q1 - q0) + (tok - q0) + 1) : seq;   // keys before this are there
-      // the cached rows of this lane's four keys of tile t, and which of them are there
-      auto rows_of = [&](int t, int4& y, unsigned& there) {
-        int r[4];
-        there = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          int key = t * kAtKeys + lane * 4 + i;
-          if (p.sel) key = key < p.topk ? p.sel[(size_t)tok * p.topk + key] : -1;
-          r[i] = 0;
-          if (key < 0 || key >= seen) continue;
-          const int col = key / p.d.page_size;
-          const int page = col < p.d.max_pages ? p.table[(size_t)ut.b * p.d.max_pages + col] : -1;
-          if (page < 0 || page >= p.d.n_pages) {
-            atomicOr(p.status, COLI_DEV_KV_BAD_PAGE);
-            continue;
-          }
-          const long long row = (long long)page * p.rows_per_page + (key - col * p.d.page_size);
-          if (row < n_rows) {
-            r[i] = (int)row;
-            there |= 1u << i;
-          }
+      // cached row of a key; false where there is none (then row 0, whose values meet weights of 0)
+      auto row_of = [&](int key, long long& row) {
+        row = 0;
+        if (key < 0 || key >= seen) return false;
+        const int col = key / p.d.page_size;
+        const int page = col < p.d.max_pages ? p.table[(size_t)ut.b * p.d.max_pages + col] : -1;
+        if (page < 0 || page >= p.d.n_pages) {
+          atomicOr(p.status, COLI_DEV_KV_BAD_PAGE);
+          return false;
         }
-        y = make_int4(r[0], r[1], r[2], r[3]);
+        row = (long long)page * p.rows_per_page + (key - col * p.d.page_size);
+        return true;
       };
-      int4 y;
-      unsigned there;
-      rows_of(t0, y, there);
+      // TMA: lane l has box l of a tile (lanes beyond the boxes repeat); copying: key 32 j + l of the warp's
+      constexpr int kRows = TMA ? 1 : kAtLaneKeys;
+      long long row[kRows];
+      bool there[kRows];
+      auto find = [&](int t) {
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          int key;
+          if constexpr (TMA) {
+            key = t * kAtKeys + (lane & (n_box - 1)) * p.box;
+          } else {
+            key = t * kAtKeys + (lw * kAtLaneKeys + j) * 32 + lane;
+            if (p.sel) key = key < p.topk ? p.sel[(size_t)tok * p.topk + key] : -1;
+          }
+          there[j] = row_of(key, row[j]);
+        }
+      };
+      find(t0);
       // queries
       if (un > 0 && !mbar_wait(&q_empty, (un - 1) & 1, p.wait_ns)) { ok = false; break; }
-      if (lane == 0) mbar_arrive_expect_tx(&q_full, (uint32_t)(kAtBoxes * kAtQBoxBytes));
-      __syncwarp();
-      if (lane < 16) {
-        int r[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          int row = ut.row0 + lane * 4 + i;
-          if (row >= row_end) row = ut.row0;           // rows past the unit's last: computed, not written
-          r[i] = (row / p.H) * p.q_tok + (row % p.H) * p.q_head;
-        }
+      if constexpr (TMA) {
+        if (lane == 0) mbar_arrive_expect_tx(&q_full, (uint32_t)(kAtBoxes * kAtQBoxBytes));
+        __syncwarp();
+        // rows past the unit's last are other rows' or, behind the tensor, zeros: computed, not written
+        if (lane < kAtBoxes) tma_load_2d_nohint(qs + lane * kAtQBoxBytes, &qmap, lane * 64, ut.row0, &q_full);
+      } else {
+        // eight lanes a row and box: 16 bytes each
+        const int c = lane & 7;
 #pragma unroll 1
-        for (int x = 0; x < kAtBoxes; ++x)
-          tma_gather4(qs + x * kAtQBoxBytes + lane * 512, &qmap, x * 64, make_int4(r[0], r[1], r[2], r[3]), &q_full);
+        for (int i = 0; i < kAtRows / (4 * kAtLoadWarps); ++i) {
+          const int r = (i * kAtLoadWarps + lw) * 4 + (lane >> 3);
+          const int gr = min(ut.row0 + r, row_end - 1);
+          const uint8_t* src = p.q + (gr / p.H) * p.q_tok + (gr % p.H) * p.q_head + c * 16;
+          uint8_t* dst = qs + r * 128 + ((c ^ (r & 7)) << 4);
+#pragma unroll
+          for (int x = 0; x < kAtBoxes; ++x) copy16(dst + x * kAtQBoxBytes, src + x * 128);
+        }
+        copies_arrive(&q_full);
       }
       for (int t = t0; t < t1; ++t, ++it) {
         if (*abort_v) { ok = false; break; }
+        // which keys are there, in key order
+        uint32_t mine[kRows] = {};
+        if constexpr (TMA) {
+          // box j holds keys j box .. (j + 1) box - 1, there up to `seen`
+          const unsigned boxes = __ballot_sync(0xffffffffu, there[0]);
+          const int per = p.box < 32 ? p.box : 32;     // keys of a word that one box decides
+          if (lane < 4) {
+#pragma unroll 1
+            for (int i = 0; i < 32; i += per)
+              if ((boxes >> ((lane * 32 + i) / p.box)) & 1u) mine[0] |= (per == 32 ? 0xffffffffu : ((1u << per) - 1u) << i);
+            const int left = seen - (t * kAtKeys + lane * 32);
+            if (left < 32) mine[0] &= left <= 0 ? 0u : (1u << left) - 1u;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kRows; ++j) mine[j] = __ballot_sync(0xffffffffu, there[j]);
+        }
         // pairs of value boxes as the previous tile's products free them, then the rotary box
 #pragma unroll 1
         for (int d = 0; d < 4 && ok; ++d) {
           if (it > 0 && !mbar_wait(&empty[d], (it - 1) & 1, p.wait_ns)) { ok = false; break; }
-          if (d == 0) {
-            // which keys are there, as bits in key order: lane l holds keys 4 l .. 4 l + 3
-            unsigned word = there << ((lane & 7) * 4);
-            word |= __shfl_xor_sync(0xffffffffu, word, 1);
-            word |= __shfl_xor_sync(0xffffffffu, word, 2);
-            word |= __shfl_xor_sync(0xffffffffu, word, 4);
-            if ((lane & 7) == 0) key_ok[it & 1][lane >> 3] = word;
+          if constexpr (TMA) {
+            if (d == 0 && lane < 4) key_ok[it & 1][lane] = mine[0];
+            if (lane == 0) mbar_arrive_expect_tx(&full[d], (uint32_t)(2 * kAtBoxBytes));
             __syncwarp();
+            // lanes 0 .. n_box - 1: the first 64 columns, the next n_box lanes: the other 64 (n_box <= 16)
+            if (lane < 2 * n_box) {
+              const int x = 2 * d + (lane >= n_box), j = lane & (n_box - 1);
+              tma_load_2d_nohint(smem + x * kAtBoxBytes + j * p.box * 128, &kmap, x * 64, (int)row[0], &full[d]);
+            }
+          } else {
+            if (d == 0 && lane == 0)
+#pragma unroll
+              for (int j = 0; j < kRows; ++j) key_ok[it & 1][lw * kRows + j] = mine[j];
+            const int c = lane & 7;
+#pragma unroll
+            for (int i = 0; i < 8 * kRows; ++i) {      // eight lanes a key
+              const int k = lw * 32 * kRows + i * 4 + (lane >> 3);
+              const uint8_t* src =
+                  p.cache + __shfl_sync(0xffffffffu, row[i >> 3], (i & 7) * 4 + (lane >> 3)) * (kAtW * 2) + c * 16;
+              uint8_t* dst = smem + k * 128 + ((c ^ (k & 7)) << 4);
+              copy16(dst + (2 * d) * kAtBoxBytes, src + (2 * d) * 128);
+              copy16(dst + (2 * d + 1) * kAtBoxBytes, src + (2 * d + 1) * 128);
+            }
+            copies_arrive(&full[d]);
           }
-          if (lane == 0) mbar_arrive_expect_tx(&full[d], (uint32_t)(2 * kAtBoxBytes));
-          __syncwarp();
-          tma_gather4(smem + (2 * d) * kAtBoxBytes + lane * 512, &kmap, (2 * d) * 64, y, &full[d]);
-          tma_gather4(smem + (2 * d + 1) * kAtBoxBytes + lane * 512, &kmap, (2 * d + 1) * 64, y, &full[d]);
         }
         if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&full[4], (uint32_t)kAtBoxBytes);
-        __syncwarp();
-        tma_gather4(rot + lane * 512, &kmap, 8 * 64, y, &full[4]);
-        if (t + 1 < t1) rows_of(t + 1, y, there);
+        if constexpr (TMA) {
+          if (lane == 0) mbar_arrive_expect_tx(&full[4], (uint32_t)kAtBoxBytes);
+          __syncwarp();
+          if (lane < n_box) tma_load_2d_nohint(rot + lane * p.box * 128, &kmap, 8 * 64, (int)row[0], &full[4]);
+        } else {
+          const int c = lane & 7;
+#pragma unroll
+          for (int i = 0; i < 8 * kRows; ++i) {
+            const int k = lw * 32 * kRows + i * 4 + (lane >> 3);
+            copy16(rot + k * 128 + ((c ^ (k & 7)) << 4),
+                   p.cache + __shfl_sync(0xffffffffu, row[i >> 3], (i & 7) * 4 + (lane >> 3)) * (kAtW * 2) + 8 * 128 +
+                       c * 16);
+          }
+          copies_arrive(&full[4]);
+          if (lane == 0) mbar_arrive(&full[4]);        // key_ok is written
+        }
+        if (t + 1 < t1) find(t + 1);
       }
       at = ut.first + t1;
     }
     if (!ok) {
       fail_wait();
       // copies in flight land before the CTA leaves
-      if (lane == 0) {
+      if constexpr (!TMA) asm volatile("cp.async.wait_all;" ::: "memory");
+      if (TMA && lane == 0) {
         mbar_wait(&q_full, un & 1, 1000000ull);
         for (int d = 0; d < 5; ++d) {
-          mbar_wait(&full[d], it & 1, 1000000ull);
           if (it > 0) mbar_wait(&full[d], (it - 1) & 1, 1000000ull);
+          mbar_wait(&full[d], it & 1, 1000000ull);
         }
       }
       __syncwarp();
@@ -401,12 +461,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const AtUnit ut = p.units[u];
         const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
         if (!mbar_wait_spin(&q_full, un & 1, p.wait_ns)) { ok = false; break; }
+        if (!TMA) fence_proxy_async_smem();            // the copies are ordinary writes; the MMA reads by the async proxy
         for (int t = t0; t < t1; ++t, ++it) {
           if (*abort_v) { ok = false; break; }
           // S^T: nine boxes of 64 columns, four steps of 16 each
           for (int x = 0; x < kAtBoxes; ++x) {
             if ((x & 1) == 0 && !mbar_wait_spin(&full[x >> 1], it & 1, p.wait_ns)) { ok = false; break; }
-            if ((x & 1) == 0) tc_fence_after();
+            if ((x & 1) == 0) {
+              if (!TMA) fence_proxy_async_smem();
+              tc_fence_after();
+            }
 #pragma unroll
             for (int s = 0; s < 4; ++s)
               umma_ss(tmem + kAtSCol, kd + (uint64_t)(x * (kAtBoxBytes >> 4) + s * 2),
@@ -732,26 +796,27 @@ static AtWs at_ws(int B, int n_tokens, int H) {
   return w;
 }
 
+// Rows of 576 elements, boxes of 64 columns and `box` rows, 128-byte swizzle.
 static CUresult at_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, bool bf16, const void* base,
-                       long long rows, long long stride) {
+                       long long rows, int box_rows) {
   const cuuint64_t gdim[2] = {(cuuint64_t)kAtW, (cuuint64_t)rows};
-  const cuuint64_t gstr[1] = {(cuuint64_t)stride * 2};
-  const cuuint32_t box[2] = {64, 1};                   // gathers take one row a coordinate
+  const cuuint64_t gstr[1] = {(cuuint64_t)kAtW * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
   const cuuint32_t es[2] = {1, 1};
   return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                 const_cast<void*>(base), gdim, gstr, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-template <bool BF16>
+template <bool BF16, bool TMA>
 static cudaError_t at_launch(const AtArgs& a, const CUtensorMap& kmap, const CUtensorMap& qmap, int max_units,
                              int ctas, cudaStream_t st) {
   kv_attention_plan_kernel<<<1, kAtPlanThreads, (a.B + 1) * sizeof(int), st>>>(a, max_units, ctas);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kv_attention_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem);
+  e = cudaFuncSetAttribute(kv_attention_kernel<BF16, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kv_attention_kernel<BF16>, dim3(ctas), dim3(kAtThreads), kAtSmem, st, a, kmap, qmap);
+  e = launch_pdl(kv_attention_kernel<BF16, TMA>, dim3(ctas), dim3(at_threads(TMA)), kAtSmem, st, a, kmap, qmap);
   if (e != cudaSuccess || ctas < 2) return e;
   return launch_pdl(kv_attention_join_kernel<BF16>, dim3(ctas - 1, kAtRows), dim3(kAtJoinThreads), 0, st, a);
 }
@@ -795,15 +860,10 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
     return fail(COLI_EALIGN, "kv_attention: q, cache and out 16-byte, workspace 256-byte alignment");
   if (!aligned(block_table, 4) || !aligned(q_start, 4) || !aligned(seq_len, 4) || !aligned(topk_idx, 4) || !aligned(lse, 4))
     return fail(COLI_EALIGN, "kv_attention: a pointer is not 4-byte aligned");
-  // queries as rows of one stride: the common divisor of the token and head strides
   const long long ts = n_tokens > 1 ? q_token_stride : 0, hs = H > 1 ? q_head_stride : 0;
   if (ts < 0 || hs < 0 || (n_tokens > 1 && ts == 0) || (H > 1 && hs == 0))
     return fail(COLI_EINVAL, "kv_attention: query strides must be positive");
-  const long long g0 = std::gcd(ts, hs), g = g0 ? g0 : kAtW;
-  if (g % 8) return fail(COLI_EALIGN, "kv_attention: query strides must be multiples of 8 elements");
-  if (g < kAtW) return fail(COLI_EUNSUPPORTED, "kv_attention: the query strides' common divisor is below %d", kAtW);
-  const long long q_rows = (n_tokens - 1LL) * (ts / g) + (H - 1LL) * (hs / g) + 1;
-  if (q_rows > 0x7fffffffLL) return fail(COLI_EUNSUPPORTED, "kv_attention: the queries span more than 2^31 - 1 rows");
+  if (ts % 8 || hs % 8) return fail(COLI_EALIGN, "kv_attention: query strides must be multiples of 8 elements");
   const AtWs w = at_ws(B, n_tokens, H);
   if (workspace_bytes < w.total)
     return fail(COLI_EWORKSPACE, "kv_attention: workspace %zu bytes < required %zu", workspace_bytes, w.total);
@@ -812,18 +872,24 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   if (w.max_units * tiles > 0x7fffffffLL)
     return fail(COLI_EUNSUPPORTED, "kv_attention: %lld units of up to %lld key tiles exceed 2^31 - 1",
                 w.max_units, tiles);
-  auto encode = get_encode();
-  if (!encode) return fail(COLI_ECUDA, "kv_attention: cuTensorMapEncodeTiled is not available");
   int dev = 0, sms = 0;
   cudaError_t ce = cudaGetDevice(&dev);
   if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (ce != cudaSuccess) return cuda_fail(ce, "kv_attention: device query");
   const bool bf16 = desc->dtype == COLI_X_BF16;
-  CUtensorMap kmap, qmap;
-  CUresult r = at_map(encode, &kmap, bf16, cache, cached, kAtW);
-  if (r != CUDA_SUCCESS) return fail(COLI_ECUDA, "kv_attention: cache tensor map (%d)", (int)r);
-  r = at_map(encode, &qmap, bf16, q, q_rows, g);
-  if (r != CUDA_SUCCESS) return fail(COLI_ECUDA, "kv_attention: query tensor map (%d)", (int)r);
+  // TMA boxes where pages are whole boxes and query rows evenly spaced; else the copying kernel
+  int box = kAtKeys;
+  while (desc->page_size % box) box /= 2;
+  const bool tma = !topk_idx && box >= kAtMinBox && (H == 1 || hs == kAtW) && (n_tokens == 1 || ts == (long long)H * kAtW);
+  CUtensorMap kmap = {}, qmap = {};
+  if (tma) {
+    auto encode = get_encode();
+    if (!encode) return fail(COLI_ECUDA, "kv_attention: cuTensorMapEncodeTiled is not available");
+    CUresult r = at_map(encode, &kmap, bf16, cache, cached, box);
+    if (r != CUDA_SUCCESS) return fail(COLI_ECUDA, "kv_attention: cache tensor map (%d)", (int)r);
+    r = at_map(encode, &qmap, bf16, q, (long long)n_tokens * H, kAtRows);
+    if (r != CUDA_SUCCESS) return fail(COLI_ECUDA, "kv_attention: query tensor map (%d)", (int)r);
+  }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   AtArgs a;
   a.d = *desc;
@@ -833,8 +899,11 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   a.topk = topk_idx ? topk : 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.rows_per_page = (int)per_page;
-  a.q_tok = (int)(ts / g);
-  a.q_head = (int)(hs / g);
+  a.box = box;
+  a.q_tok = ts * 2;
+  a.q_head = hs * 2;
+  a.q = static_cast<const uint8_t*>(q);
+  a.cache = static_cast<const uint8_t*>(cache);
   a.table = block_table;
   a.q_start = q_start;
   a.seq_len = seq_len;
@@ -849,8 +918,9 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   a.wait_ns = kWaitLimitNs;
   const int ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  ce = bf16 ? at_launch<true>(a, kmap, qmap, (int)w.max_units, ctas, st)
-            : at_launch<false>(a, kmap, qmap, (int)w.max_units, ctas, st);
+  const int mu = (int)w.max_units;
+  if (tma) ce = bf16 ? at_launch<true, true>(a, kmap, qmap, mu, ctas, st) : at_launch<false, true>(a, kmap, qmap, mu, ctas, st);
+  else ce = bf16 ? at_launch<true, false>(a, kmap, qmap, mu, ctas, st) : at_launch<false, false>(a, kmap, qmap, mu, ctas, st);
   return ce == cudaSuccess ? COLI_OK : cuda_fail(ce, "kv_attention: launch");
 }
 

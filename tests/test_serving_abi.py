@@ -134,8 +134,7 @@ def test_append_arguments():
     (dict(ws=None), coli.COLI_EINVAL), (dict(q=P + 8), coli.COLI_EALIGN), (dict(cache=P + 2), coli.COLI_EALIGN),
     (dict(out=P + 4), coli.COLI_EALIGN), (dict(ws=P + 128), coli.COLI_EALIGN), (dict(lse=P + 2), coli.COLI_EALIGN),
     (dict(sel=P + 2, topk=4), coli.COLI_EALIGN), (dict(ts=0), coli.COLI_EINVAL), (dict(hs=-576), coli.COLI_EINVAL),
-    (dict(ts=64 * 576 + 4, hs=580), coli.COLI_EALIGN), (dict(ts=64 * 576 + 8), coli.COLI_EUNSUPPORTED),
-    (dict(hs=512, ts=64 * 512), coli.COLI_EUNSUPPORTED), (dict(nbytes=1000), coli.COLI_EWORKSPACE),
+    (dict(ts=64 * 576 + 4), coli.COLI_EALIGN), (dict(hs=580), coli.COLI_EALIGN), (dict(nbytes=1000), coli.COLI_EWORKSPACE),
 ])
 def test_attention_arguments(bad, status):
     refused(status, lambda: attn(kv(), **bad))
