@@ -38,7 +38,10 @@ constexpr int kAtQBoxBytes = kAtRows * 128;        // 64 columns of the queries
 constexpr int kAtBoxes = kAtW / 64;                // 9: eight of values, one rotary
 constexpr int kAtLoadWarps = 2;                    // loader warps that copy rows themselves (one issues TMA loads)
 constexpr int kAtLaneKeys = kAtKeys / (32 * kAtLoadWarps);   // keys of a tile a copying lane looks up
-constexpr int at_threads(bool tma) { return (5 + (tma ? 1 : kAtLoadWarps)) * 32; }
+constexpr int kAtSmWarps = 8;                      // softmax warps: two per TMEM sub-partition, 32 rows each
+constexpr int kAtSmThreads = kAtSmWarps * 32, kAtHalf = kAtRows / 2;
+constexpr int kAtFirstLoad = 2 + kAtSmWarps;       // warp 0 loads; copying loaders go on from here
+constexpr int at_threads(bool tma) { return (1 + kAtSmWarps + (tma ? 1 : kAtLoadWarps)) * 32; }
 constexpr int kAtMinBox = 8;                       // fewest key rows a TMA box has
 constexpr int kAtMaxCtas = 160;                    // CTAs the workspace has room for
 constexpr size_t kAtSmem = (size_t)kAtBoxes * (kAtBoxBytes + kAtQBoxBytes) + 1024;
@@ -204,43 +207,84 @@ __device__ __forceinline__ uint32_t at_pack(float lo, float hi) {
   return r;
 }
 
-// Barrier of the four softmax warps; with `or`: whether any thread's pred is true.
-__device__ __forceinline__ void sm_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barrier of the softmax warps; with `or`: whether any thread's pred is true.
+__device__ __forceinline__ void sm_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kAtSmThreads) : "memory"); }
 __device__ __forceinline__ bool sm_any(bool pred) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)pred)
+      : "r"((uint32_t)pred), "n"(kAtSmThreads)
       : "memory");
   return r != 0;
 }
 
-// Reduce v[64] over the warp's lanes; lane l ends with the results of columns 2 l and 2 l + 1.
+// Reduce v[32] over the warp's lanes; lane l ends with the result of column l.
 template <typename F>
-__device__ __forceinline__ float2 warp_columns(const float (&v)[64], F op) {
+__device__ __forceinline__ float warp_columns(const float (&v)[32], F op) {
   const int lane = threadIdx.x & 31;
   float w[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) w[i] = v[i];
   // fold: a lane keeps the half of the columns that its bit chooses and gives the other half away
-  {
-    const bool up = lane & 16;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float keep = up ? v[32 + i] : v[i], give = up ? v[i] : v[32 + i];
-      w[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 16));
-    }
-  }
-#pragma unroll
-  for (int o = 8, n = 16; o >= 1; o >>= 1, n >>= 1) {
-    const bool up = lane & o;
+  for (int n = 16; n >= 1; n >>= 1) {
+    const bool up = lane & n;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const float keep = up ? w[n + i] : w[i], give = up ? w[i] : w[n + i];
-      w[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+      w[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, n));
     }
   }
-  return make_float2(w[0], w[1]);
+  return w[0];
+}
+
+// MMAs of a K-step sequence, both operands in shared memory, issued by one elected lane of a converged warp
+// (descriptors then stay in uniform registers: 36 MMAs took 4,900 cycles to issue from a single-lane branch).
+// Step s adds s * sa (sb) to the descriptor of A (B), in units of 16 bytes; acc = 0: the first overwrites.
+template <int STEPS, int SA, int SB>
+__device__ __forceinline__ void umma_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  static_assert(STEPS == 4 || STEPS == 8, "");
+  if constexpr (STEPS == 8) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+        "add.u64 a1, %1, %5;\n\tadd.u64 a2, a1, %5;\n\tadd.u64 a3, a2, %5;\n\tadd.u64 a4, a3, %5;\n\t"
+        "add.u64 a5, a4, %5;\n\tadd.u64 a6, a5, %5;\n\tadd.u64 a7, a6, %5;\n\t"
+        "add.u64 b1, %2, %6;\n\tadd.u64 b2, b1, %6;\n\tadd.u64 b3, b2, %6;\n\tadd.u64 b4, b3, %6;\n\t"
+        "add.u64 b5, b4, %6;\n\tadd.u64 b6, b5, %6;\n\tadd.u64 b7, b6, %6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(SA), "n"(SB)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+        "add.u64 a1, %1, %5;\n\tadd.u64 a2, a1, %5;\n\tadd.u64 a3, a2, %5;\n\t"
+        "add.u64 b1, %2, %6;\n\tadd.u64 b2, b1, %6;\n\tadd.u64 b3, b2, %6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(SA), "n"(SB)
+        : "memory");
+  }
+}
+
+// Arrive on `bar` when the MMAs issued so far are complete (one elected lane of a converged warp).
+__device__ __forceinline__ void umma_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 // TMA: key tiles arrive as TMA boxes of p.box rows (pages of a multiple of eight rows, every key up to the
@@ -255,6 +299,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ uint32_t key_ok[2][4];                    // bit i of word w: key 32 w + i of the tile is there
+  __shared__ uint32_t key_fin[2][4];                   // bit i of word w of a half: key 32 w + i has a finite score there
   __shared__ __align__(16) float ref[kAtRows], fac[kAtRows], red[4][kAtRows];
   __shared__ __align__(16) int lim[kAtRows];           // last key position each row sees (dense)
   __shared__ int has_ref[kAtRows];                     // the row has seen a key
@@ -271,7 +316,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     mbar_init(&q_full, TMA ? 1 : kAtLoadWarps * 32);
     mbar_init(&q_empty, 1);
     mbar_init(&s_full, 1);
-    mbar_init(&p_ready, 4);
+    mbar_init(&p_ready, kAtSmWarps);
     mbar_init(&o_full, 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -296,9 +341,9 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     atomicExch(&abort_flag, 1);
   };
 
-  if (warp == 0 || warp > 5) {
+  if (warp == 0 || warp >= kAtFirstLoad) {
     // ---------------------------------------------------------------- loader
-    const int lw = warp == 0 ? 0 : warp - 5;           // copying: this warp's keys of a tile start at 32 kAtLaneKeys lw
+    const int lw = warp == 0 ? 0 : warp - kAtFirstLoad + 1;           // copying: this warp's keys of a tile start at 32 kAtLaneKeys lw
     bool ok = true;
     int it = 0, un = 0;
     const int n_box = TMA ? kAtKeys / p.box : 0;       // boxes of 64 columns a tile
@@ -447,66 +492,66 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       __syncwarp();
     }
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t fmt = BF16 ? (1u << 7) | (1u << 10) : 0u;
-      const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)(kAtRows >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-      const uint32_t idesc_t = idesc | (1u << 15) | (1u << 16);          // both operands MN-major
-      const uint64_t kd = umma_desc_sw128(smem_u32(smem)), qd = umma_desc_sw128(smem_u32(qs));
-      const uint64_t vd = umma_desc_sw128_mn(smem_u32(smem), kAtBoxBytes);
-      const uint64_t pd = umma_desc_sw128_mn(smem_u32(rot), kAtBoxBytes);
-      bool ok = true;
-      int it = 0, un = 0;
-      for (int at = beg, u = unit0; ok && at < end; ++u, ++un) {
-        const AtUnit ut = p.units[u];
-        const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
-        if (!mbar_wait_spin(&q_full, un & 1, p.wait_ns)) { ok = false; break; }
-        if (!TMA) fence_proxy_async_smem();            // the copies are ordinary writes; the MMA reads by the async proxy
-        for (int t = t0; t < t1; ++t, ++it) {
-          if (*abort_v) { ok = false; break; }
-          // S^T: nine boxes of 64 columns, four steps of 16 each
-          for (int x = 0; x < kAtBoxes; ++x) {
-            if ((x & 1) == 0 && !mbar_wait_spin(&full[x >> 1], it & 1, p.wait_ns)) { ok = false; break; }
-            if ((x & 1) == 0) {
-              if (!TMA) fence_proxy_async_smem();
-              tc_fence_after();
-            }
+    // ---------------------------------------------------------------- MMA issuer (the warp stays converged)
+    const uint32_t fmt = BF16 ? (1u << 7) | (1u << 10) : 0u;
+    const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)(kAtRows >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+    const uint32_t idesc_t = idesc | (1u << 15) | (1u << 16);            // both operands MN-major
+    const uint64_t kd = umma_desc_sw128(smem_u32(smem)), qd = umma_desc_sw128(smem_u32(qs));
+    const uint64_t vd = umma_desc_sw128_mn(smem_u32(smem), kAtBoxBytes);
+    const uint64_t pd = umma_desc_sw128_mn(smem_u32(rot), kAtBoxBytes);
+    bool ok = true;
+    int it = 0, un = 0;
+    for (int at = beg, u = unit0; ok && at < end; ++u, ++un) {
+      const int first = p.units[u].first, tiles = p.units[u].tiles;
+      const int t0 = at - first, t1 = min(end - first, tiles);
+      ok = __all_sync(0xffffffffu, mbar_wait_spin(&q_full, un & 1, p.wait_ns));
+      if (!TMA) fence_proxy_async_smem();              // the copies are ordinary writes; the MMA reads by the async proxy
+      for (int t = t0; ok && t < t1; ++t, ++it) {
+        ok = !__shfl_sync(0xffffffffu, *abort_v, 0);
+        // S^T: nine boxes of 64 columns, four steps of 16 each
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              umma_ss(tmem + kAtSCol, kd + (uint64_t)(x * (kAtBoxBytes >> 4) + s * 2),
-                      qd + (uint64_t)(x * (kAtQBoxBytes >> 4) + s * 2), idesc, (x | s) ? 1u : 0u);
+        for (int x = 0; x < kAtBoxes; ++x) {
+          if ((x & 1) == 0) {
+            ok = ok && mbar_wait_spin(&full[x >> 1], it & 1, p.wait_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!TMA) fence_proxy_async_smem();
+            tc_fence_after();
           }
-          if (!ok) break;
-          umma_commit(&s_full);
-          if (t + 1 == t1) umma_commit(&q_empty);
-          if (!mbar_wait_spin(&p_ready, it & 1, p.wait_ns)) { ok = false; break; }
-          tc_fence_after();
-          // O^T: four blocks of 128 values, eight steps of 16 keys each
-#pragma unroll 1
-          for (int d = 0; d < 4; ++d) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-              umma_ss(tmem + (uint32_t)(d * kAtRows), vd + (uint64_t)(2 * d * (kAtBoxBytes >> 4) + s * 128),
-                      pd + (uint64_t)(s * 128), idesc_t, (t > t0 || s) ? 1u : 0u);
-            umma_commit(&empty[d]);
-          }
+          if (ok)
+            umma_steps<4, 2, 2>(tmem + kAtSCol, kd + (uint64_t)(x * (kAtBoxBytes >> 4)),
+                                qd + (uint64_t)(x * (kAtQBoxBytes >> 4)), idesc, x ? 1u : 0u);
         }
+        umma_commit_elect(&s_full);
+        if (t + 1 == t1) umma_commit_elect(&q_empty);
+        ok = ok && mbar_wait_spin(&p_ready, it & 1, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        umma_commit(&o_full);
-        at = ut.first + t1;
+        tc_fence_after();
+        // O^T: four blocks of 128 values, eight steps of 16 keys each
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          umma_steps<8, 128, 128>(tmem + (uint32_t)(d * kAtRows), vd + (uint64_t)(2 * d * (kAtBoxBytes >> 4)), pd,
+                                  idesc_t, t > t0 ? 1u : 0u);
+          umma_commit_elect(&empty[d]);
+        }
       }
-      if (!ok) {
-        fail_wait();
-        // what was issued ends before tensor memory is freed
-        umma_commit(&o_full);
-        mbar_wait(&o_full, un & 1, p.wait_ns);
-      }
+      if (!ok) break;
+      umma_commit_elect(&o_full);
+      at = first + t1;
+    }
+    if (!ok) {
+      if (lane == 0) fail_wait();
+      // what was issued ends before tensor memory is freed
+      umma_commit_elect(&o_full);
+      mbar_wait(&o_full, un & 1, p.wait_ns);
     }
   } else {
-    // ---------------------------------------------------------------- softmax and output (warps 2..5)
+    // ---------------------------------------------------------------- softmax and output (warps 2 ..)
     const int sp = warp & 3;                           // TMEM sub-partition: keys 32 sp .. 32 sp + 31 of a tile
+    const int half = (warp - 2) >> 2, c0 = half * kAtHalf;   // this warp's 32 rows of the unit
     const int me = sp * 32 + lane;                     // this thread's key of a tile, value of a block of O^T
-    const uint32_t trow = tmem + ((uint32_t)(sp * 32) << 16);
+    const int id = threadIdx.x - 64;                   // thread among the softmax warps
+    const uint32_t trow = tmem + ((uint32_t)(sp * 32) << 16) + (uint32_t)c0;
     int it = 0, un = 0;
     for (int at = beg, u = unit0; at < end; ++u, ++un) {
       const AtUnit ut = p.units[u];
@@ -518,46 +563,45 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       at_span(p, ut.b, q0, q1);
       const int row_end = p.sel ? (tok0 + 1) * p.H : q1 * p.H;
       const int past = p.seq_len[ut.b] - (q1 - q0);     // position of the request's first new token
-      if (me < kAtRows) {
-        const int row = min(ut.row0 + me, row_end - 1);
-        lim[me] = p.sel ? 0x7fffffff : past + row / p.H - q0;
-        ref[me] = 0.f;
-        has_ref[me] = 0;
+      if (id < kAtRows) {
+        const int row = min(ut.row0 + id, row_end - 1);
+        lim[id] = p.sel ? 0x7fffffff : past + row / p.H - q0;
+        ref[id] = 0.f;
+        has_ref[id] = 0;
       }
       const int seen_all = past + tok0 - q0;            // every row of the unit sees the keys up to this one
-      float l[kAtRows];
+      float l[kAtHalf];
 #pragma unroll
-      for (int c = 0; c < kAtRows; ++c) l[c] = 0.f;
+      for (int c = 0; c < kAtHalf; ++c) l[c] = 0.f;
       sm_sync();
       bool ok = true, unset = true;                    // unset: some row has no reference yet
       for (int t = t0; t < t1; ++t, ++it) {
         // (the rotary box's barrier orders the loader's key_ok before this read)
         ok = mbar_wait(&full[4], it & 1, p.wait_ns) && mbar_wait(&s_full, it & 1, p.wait_ns);
         tc_fence_after();
-        float x[kAtRows];
+        float x[kAtHalf];
         {
-          uint32_t r[4][16];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld16_issue(trow + kAtSCol + c * 16, r[c]);
+          uint32_t r[2][16];
+          tmem_ld16_issue(trow + kAtSCol, r[0]);
+          tmem_ld16_issue(trow + kAtSCol + 16, r[1]);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < kAtRows; ++c) x[c] = __uint_as_float(r[c >> 4][c & 15]);
+          for (int c = 0; c < kAtHalf; ++c) x[c] = __uint_as_float(r[c >> 4][c & 15]);
         }
         const uint32_t kw = key_ok[it & 1][sp];
         const bool there = (kw >> lane) & 1u;
         const int key = t * kAtKeys + me;
-        bool bad_key = false;
+        // some row does not see some key of this warp (the same in both halves)
         const bool masked = p.sel ? kw != 0xffffffffu : (t * kAtKeys + sp * 32 + 31 > seen_all || kw != 0xffffffffu);
-        if (masked) {                                  // warp-uniform
-          // a key whose every score is not finite holds an infinity or a NaN: its values must not meet the
-          // zero weights of the rows that do not see it
+        if (masked) {
           bool fin = false;
 #pragma unroll
-          for (int c = 0; c < kAtRows; ++c) fin |= fabsf(x[c]) < INFINITY;
-          bad_key = !fin;
+          for (int c = 0; c < kAtHalf; ++c) fin |= fabsf(x[c]) < INFINITY;
+          const unsigned fw = __ballot_sync(0xffffffffu, fin);
+          if (lane == 0) key_fin[half][sp] = fw;
 #pragma unroll
-          for (int c = 0; c < kAtRows; c += 4) {
-            const int4 lm = *reinterpret_cast<const int4*>(&lim[c]);
+          for (int c = 0; c < kAtHalf; c += 4) {
+            const int4 lm = *reinterpret_cast<const int4*>(&lim[c0 + c]);
             if (!there || (!p.sel && key > lm.x)) x[c] = -INFINITY;
             if (!there || (!p.sel && key > lm.y)) x[c + 1] = -INFINITY;
             if (!there || (!p.sel && key > lm.z)) x[c + 2] = -INFINITY;
@@ -567,8 +611,8 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
         // distance to the references; does any score exceed its row's by more than kAtGrow?
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < kAtRows; c += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&ref[c]);
+        for (int c = 0; c < kAtHalf; c += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&ref[c0 + c]);
           x[c] = fmaf(x[c], p.scale_log2, -m.x);
           x[c + 1] = fmaf(x[c + 1], p.scale_log2, -m.y);
           x[c + 2] = fmaf(x[c + 2], p.scale_log2, -m.z);
@@ -577,48 +621,45 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
         }
         if (sm_any(top > kAtGrow || unset || !ok)) {
           if (sm_any(!ok)) { ok = false; break; }
-          const float2 cm = warp_columns(x, [](float a, float b) { return fmaxf(a, b); });
-          *reinterpret_cast<float2*>(&red[sp][2 * lane]) = cm;
+          red[sp][c0 + lane] = warp_columns(x, [](float a, float b) { return fmaxf(a, b); });
           sm_sync();
           bool none = false;
-          if (me < kAtRows) {
-            const float g = ceilf(fmaxf(fmaxf(red[0][me], red[1][me]), fmaxf(red[2][me], red[3][me])));
-            const bool raise = g > kAtGrow || (!has_ref[me] && g > -INFINITY);
-            fac[me] = raise ? g : 0.f;                 // by how much
+          if (id < kAtRows) {
+            const float g = ceilf(fmaxf(fmaxf(red[0][id], red[1][id]), fmaxf(red[2][id], red[3][id])));
+            const bool raise = g > kAtGrow || (!has_ref[id] && g > -INFINITY);
+            fac[id] = raise ? g : 0.f;                 // by how much
             if (raise) {
-              ref[me] += g;
-              has_ref[me] = 1;
+              ref[id] += g;
+              has_ref[id] = 1;
             }
-            none = !has_ref[me];
+            none = !has_ref[id];
           }
           unset = sm_any(none);
 #pragma unroll
-          for (int c = 0; c < kAtRows; ++c) {
-            const float g = fac[c];
+          for (int c = 0; c < kAtHalf; ++c) {
+            const float g = fac[c0 + c];
             x[c] -= g;
             l[c] *= at_exp2(-g);
           }
           if (t > t0) {                                // (the first tile's products overwrite O^T)
 #pragma unroll 1
-            for (int d = 0; d < 4; ++d) {
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t r[16];
-                tmem_ld16_issue(trow + d * kAtRows + c * 16, r);
-                tmem_ld_wait();
+            for (int i = 0; i < 8; ++i) {              // four blocks of O^T, 16 rows at a time
+              const uint32_t col = (uint32_t)((i >> 1) * kAtRows + (i & 1) * 16);
+              uint32_t r[16];
+              tmem_ld16_issue(trow + col, r);
+              tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  r[i] = __float_as_uint(__uint_as_float(r[i]) * at_exp2(-fac[c * 16 + i]));
-                tmem_st16(trow + d * kAtRows + c * 16, r);
-              }
+              for (int j = 0; j < 16; ++j)
+                r[j] = __float_as_uint(__uint_as_float(r[j]) * at_exp2(-fac[c0 + (i & 1) * 16 + j]));
+              tmem_st16(trow + col, r);
             }
             tmem_st_wait();
           }
         }
-        // weights, their sums, and the key's row of P^T (64 weights = 128 bytes, swizzled)
+        // weights, their sums, and the key's half of its row of P^T (64 weights = 128 bytes, swizzled)
         uint8_t* prow = rot + me * 128;
 #pragma unroll
-        for (int c = 0; c < kAtRows; c += 8) {
+        for (int c = 0; c < kAtHalf; c += 8) {
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -627,11 +668,13 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
             l[c + 2 * i + 1] += b;
             w[i] = at_pack<BF16>(a, b);
           }
-          *reinterpret_cast<uint4*>(prow + (((c >> 3) ^ (me & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(prow + ((((c0 + c) >> 3) ^ (me & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (bad_key) {
+        // a key whose every score is not finite holds an infinity or a NaN: its values must not meet the zero
+        // weights of the rows that do not see it
+        if (masked && !(((key_fin[0][sp] | key_fin[1][sp]) >> lane) & 1u)) {
 #pragma unroll 1
-          for (int i = 0; i < 64; ++i)
+          for (int i = half * 32; i < half * 32 + 32; ++i)
             *reinterpret_cast<uint4*>(smem + (i >> 3) * kAtBoxBytes + me * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
@@ -646,50 +689,47 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       // -------------------------------------------------------------- the unit's rows
       ok = mbar_wait(&o_full, un & 1, p.wait_ns);
       tc_fence_after();
-      const float2 ls = warp_columns(l, [](float a, float b) { return a + b; });
-      *reinterpret_cast<float2*>(&red[sp][2 * lane]) = ls;
+      red[sp][c0 + lane] = warp_columns(l, [](float a, float b) { return a + b; });
       if (sm_any(!ok)) {
         fail_wait();
         break;
       }
-      if (me < kAtRows) {
-        const float sum = (red[0][me] + red[1][me]) + (red[2][me] + red[3][me]);
+      if (id < kAtRows) {
+        const float sum = (red[0][id] + red[1][id]) + (red[2][id] + red[3][id]);
         if (whole) {
-          fac[me] = sum == 0.f ? 0.f : 1.0f / sum;
-          const int row = ut.row0 + me;
+          fac[id] = sum == 0.f ? 0.f : 1.0f / sum;
+          const int row = ut.row0 + id;
           if (p.lse && row < row_end)
-            p.lse[row] = sum == 0.f ? -INFINITY : (ref[me] + log2f(sum)) * 0.693147180559945309f;
+            p.lse[row] = sum == 0.f ? -INFINITY : (ref[id] + log2f(sum)) * 0.693147180559945309f;
         } else {
-          p.part_ml[(size_t)slot * kAtRows + me] = make_float2(has_ref[me] ? ref[me] : kAtUnset, sum);
+          p.part_ml[(size_t)slot * kAtRows + id] = make_float2(has_ref[id] ? ref[id] : kAtUnset, sum);
         }
       }
       sm_sync();
-      const int rows = min(kAtRows, row_end - ut.row0);
-      float* part = p.part + (size_t)slot * kAtPart;
+      const int rows = min(kAtRows, row_end - ut.row0) - c0;    // of this half
+      float* part = p.part + (size_t)slot * kAtPart + c0 * kAtV;
+      uint16_t* out = p.out + (size_t)(ut.row0 + c0) * kAtV;
 #pragma unroll 1
       for (int d = 0; d < 4; ++d) {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t r[16];
-          tmem_ld16_issue(trow + d * kAtRows + c * 16, r);
-          tmem_ld_wait();
-          if (whole) {
-            // lanes 2 i and 2 i + 1 hold neighbouring values of a row: they trade halves of two rows
+        uint32_t r[2][16];
+        tmem_ld16_issue(trow + d * kAtRows, r[0]);
+        tmem_ld16_issue(trow + d * kAtRows + 16, r[1]);
+        tmem_ld_wait();
+        if (whole) {
+          // lanes 2 i and 2 i + 1 hold neighbouring values of a row: they trade halves of two rows
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const int c0 = c * 16 + i;
-              const float a = __uint_as_float(r[i]) * fac[c0], b = __uint_as_float(r[i + 1]) * fac[c0 + 1];
-              const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
-              const int cc = c0 + (lane & 1);
-              const uint32_t two = (lane & 1) ? at_pack<BF16>(got, b) : at_pack<BF16>(a, got);
-              if (cc < rows)
-                *reinterpret_cast<uint32_t*>(p.out + (size_t)(ut.row0 + cc) * kAtV + d * 128 + (me & ~1)) = two;
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c * 16 + i < rows) part[(c * 16 + i) * kAtV + d * 128 + me] = __uint_as_float(r[i]);
+          for (int i = 0; i < kAtHalf; i += 2) {
+            const float a = __uint_as_float(r[i >> 4][i & 15]) * fac[c0 + i];
+            const float b = __uint_as_float(r[i >> 4][(i & 15) + 1]) * fac[c0 + i + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
+            const int c = i + (lane & 1);
+            const uint32_t two = (lane & 1) ? at_pack<BF16>(got, b) : at_pack<BF16>(a, got);
+            if (c < rows) *reinterpret_cast<uint32_t*>(out + (size_t)c * kAtV + d * 128 + (me & ~1)) = two;
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kAtHalf; ++i)
+            if (i < rows) part[i * kAtV + d * 128 + me] = __uint_as_float(r[i >> 4][i & 15]);
         }
       }
       tc_fence_before();
