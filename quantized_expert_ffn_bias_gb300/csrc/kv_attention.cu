@@ -57,6 +57,14 @@ struct AtUnit {
   int tiles;    // its key tiles
 };
 
+// A unit cut by borders: its parts are those of CTAs cta .. cta + parts - 1.
+struct AtJoin {
+  int row0, row_end;
+  int cta, parts;
+  int slot;     // of the first part (the others': 2 * their CTA)
+  int pad[3];
+};
+
 struct AtArgs {
   coli_kv_desc d;
   int B, n_tokens, H, topk;
@@ -69,9 +77,10 @@ struct AtArgs {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int* head;                         // [0] units, [1] CTAs, [2] key tiles, [4 ..) first unit of each CTA
+  int* head;                         // [0] units, [1] CTAs, [2] key tiles, [3] joins, [4 ..) first unit of each CTA
   AtUnit* units;
-  float* part;                       // [2 kAtMaxCtas][64][512]
+  AtJoin* joins;
+  float* part;                       // [2 kAtMaxCtas] partial O, in the order the main kernel's threads hold it (at_part)
   float2* part_ml;                   // [2 kAtMaxCtas][64] reference, sum
   unsigned long long wait_ns;
 };
@@ -83,6 +92,10 @@ __device__ __forceinline__ void at_span(const AtArgs& p, int b, int& q0, int& q1
   q1 = max(q0, min(p.q_start[b + 1], hi));
 }
 
+// Place of row c (a multiple of four: four rows follow one another) and value v in a partial O.  A thread of
+// the main kernel holds many rows of one value, so neighbouring values of four rows lie together.
+__host__ __device__ constexpr int at_part(int c, int v) { return ((c >> 2) * kAtV + v) * 4; }
+
 // Border j of G equal runs of the W key tiles.
 __device__ __forceinline__ int at_cut(int W, int j, int G) { return (int)((long long)W * j / G); }
 
@@ -90,10 +103,12 @@ __device__ __forceinline__ int at_cut(int W, int j, int G) { return (int)((long 
 // One CTA.  Dense: request b has T H rows, units of 64; a unit's keys end with its last row's position.
 // Selected keys: a token's heads in units of 64, all topk entries.
 constexpr int kAtPlanThreads = 1024;
+constexpr int kAtPlanNear = 2048;                  // units whose first tiles are kept in shared memory for the searches
 
 __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(const AtArgs p, int max_units, int max_ctas) {
   extern __shared__ int base_sm[];   // [B + 1] first unit of each request
   __shared__ int warp_tot[32], total;
+  __shared__ int first_sm[kAtPlanNear];
   const int tid = threadIdx.x;
   griddep_launch_dependents();
   int carry = 0;
@@ -147,27 +162,55 @@ __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(co
       un.first = tiles + e;
       un.tiles = c;
       p.units[u] = un;
+      if (u < kAtPlanNear) first_sm[u] = un.first;
     }
     tiles += total;
     __syncthreads();
   }
   const int G = min(max_ctas, tiles);
+  __syncthreads();
+  // the unit that holds each run's first tile
+  const bool near = n_units <= kAtPlanNear;
+  auto first_of = [&](int u) { return near ? first_sm[u] : p.units[u].first; };
+  int unit = 0, cut = 0;
+  bool opens = false;                              // border tid is the first inside its unit
+  if (tid < G) {
+    cut = at_cut(tiles, tid, G);
+    int l = 0, h = n_units;
+    while (h - l > 1) {
+      const int mid = (l + h) >> 1;
+      if (first_of(mid) <= cut) l = mid;
+      else h = mid;
+    }
+    unit = l;
+    p.head[4 + tid] = l;
+    const int first = first_of(l);
+    opens = tid > 0 && first < cut && at_cut(tiles, tid - 1, G) <= first;
+  }
+  const int at = block_exclusive_scan(opens ? 1 : 0, warp_tot, &total);
+  if (opens) {
+    const AtUnit un = p.units[unit];
+    int q0, q1;
+    at_span(p, un.b, q0, q1);
+    AtJoin jn{};
+    jn.row0 = un.row0;
+    jn.row_end = min(un.row0 + kAtRows, p.sel ? (un.row0 / p.H + 1) * p.H : q1 * p.H);
+    jn.cta = tid - 1;
+    // CTAs up to the one that holds the unit's last tile: borders below first + tiles
+    const int last = un.first + un.tiles;
+    int n = (int)(((long long)last * G + tiles - 1) / tiles);          // at_cut(j) < last for j < n (or one more)
+    while (n > 0 && at_cut(tiles, n - 1, G) >= last) --n;
+    while (n < G && at_cut(tiles, n, G) < last) ++n;
+    jn.parts = n - jn.cta;
+    jn.slot = 2 * jn.cta + (at_cut(tiles, tid - 1, G) < un.first ? 1 : 0);
+    p.joins[at] = jn;
+  }
   if (tid == 0) {
     p.head[0] = n_units;
     p.head[1] = G;
     p.head[2] = tiles;
+    p.head[3] = total;
     *p.status = 0;
-  }
-  // the unit that holds each run's first tile
-  for (int j = tid; j < G; j += kAtPlanThreads) {
-    const int cut = at_cut(tiles, j, G);
-    int l = 0, h = n_units;
-    while (h - l > 1) {
-      const int mid = (l + h) >> 1;
-      if (p.units[mid].first <= cut) l = mid;
-      else h = mid;
-    }
-    p.head[4 + j] = l;
   }
 }
 
@@ -707,7 +750,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       }
       sm_sync();
       const int rows = min(kAtRows, row_end - ut.row0) - c0;    // of this half
-      float* part = p.part + (size_t)slot * kAtPart + c0 * kAtV;
+      float* part = p.part + (size_t)slot * kAtPart;
       uint16_t* out = p.out + (size_t)(ut.row0 + c0) * kAtV;
 #pragma unroll 1
       for (int d = 0; d < 4; ++d) {
@@ -728,8 +771,11 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < kAtHalf; ++i)
-            if (i < rows) part[i * kAtV + d * 128 + me] = __uint_as_float(r[i >> 4][i & 15]);
+          for (int i = 0; i < kAtHalf; i += 4)
+            if (i < rows)
+              *reinterpret_cast<float4*>(part + at_part(c0 + i, d * 128 + me)) =
+                  make_float4(__uint_as_float(r[i >> 4][i & 15]), __uint_as_float(r[i >> 4][(i & 15) + 1]),
+                              __uint_as_float(r[i >> 4][(i & 15) + 2]), __uint_as_float(r[i >> 4][(i & 15) + 3]));
         }
       }
       tc_fence_before();
@@ -746,73 +792,86 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
 }
 
 // ------------------------------------------------------------------ join
-// Block (j - 1, row): the unit cut by border j, if j is the first border inside it.  Its parts lie in
-// the workspace in CTA order; they are added up in that order.
-constexpr int kAtJoinThreads = 128;
+// Adds up the parts of every cut unit, in order.  A task is four rows of a unit: 128 values a thread group
+// where the parts are many (four groups take every fourth part each, then meet in shared memory), all 512
+// where they are few.
+constexpr int kAtJoinThreads = 512, kAtJoinCtas = 456, kAtJoinFew = 12;
 
 template <bool BF16>
 __global__ void __launch_bounds__(kAtJoinThreads) kv_attention_join_kernel(const AtArgs p) {
-  __shared__ float wgt[kAtMaxCtas];
-  __shared__ float s_m, s_l;
+  __shared__ __align__(16) float wgt[kAtMaxCtas][4];
+  __shared__ float inv[4];
+  __shared__ float4 sums[3][128];
   griddep_wait();
-  const int G = p.head[1], W = p.head[2];
-  const int j = blockIdx.x + 1, r = blockIdx.y;
-  if (j >= G) return;
-  const int cut = at_cut(W, j, G);
-  const AtUnit ut = p.units[p.head[4 + j]];
-  if (ut.first >= cut) return;                          // a border between units
-  if (at_cut(W, j - 1, G) > ut.first) return;           // not the unit's first border
-  const int row = ut.row0 + r;
-  int q0, q1;
-  at_span(p, ut.b, q0, q1);
-  const int row_end = p.sel ? (ut.row0 / p.H + 1) * p.H : q1 * p.H;
-  if (row >= row_end) return;
-  int n = 1;                                            // parts: CTAs j - 1, j, ...
-  while (j - 1 + n < G && at_cut(W, j - 1 + n, G) < ut.first + ut.tiles) ++n;
-  auto slot = [&](int i) { return 2 * (j - 1 + i) + (i == 0 && at_cut(W, j - 1, G) < ut.first ? 1 : 0); };
-  const int tid = threadIdx.x;
-  if (tid < 32) {
-    float m = kAtUnset;
-    for (int i = tid; i < n; i += 32) m = fmaxf(m, p.part_ml[(size_t)slot(i) * kAtRows + r].x);
+  const int n_join = p.head[3];
+  const int tid = threadIdx.x, grp = tid >> 7, v = tid & 127, warp = tid >> 5, lane = tid & 31;
+  for (int task = blockIdx.x; task < n_join * 64; task += gridDim.x) {
+    const AtJoin jn = p.joins[task >> 6];
+    const int n = jn.parts, sub = task & 63;
+    const bool few = n <= kAtJoinFew;
+    if (few && sub >= 16) continue;
+    const int c = (few ? sub : sub >> 2) * 4, rows = jn.row_end - jn.row0 - c;
+    if (rows <= 0) continue;
+    auto slot = [&](int i) { return (size_t)(i ? 2 * (jn.cta + i) : jn.slot); };
+    __syncthreads();                                    // the previous task's weights are read
+    if (warp < 4) {                                     // warp w: the parts' weights for row c + w
+      float m = kAtUnset;
+      for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[slot(i) * kAtRows + c + warp].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.f;
-    for (int i = tid; i < n; i += 32) {
-      const float2 ml = p.part_ml[(size_t)slot(i) * kAtRows + r];
-      const float w = at_exp2(ml.x - m);
-      wgt[i] = w;
-      l += w * ml.y;
-    }
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float l = 0.f;
+      for (int i = lane; i < n; i += 32) {
+        const float2 ml = p.part_ml[slot(i) * kAtRows + c + warp];
+        const float w = at_exp2(ml.x - m);
+        wgt[i][warp] = w;
+        l += w * ml.y;
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (tid == 0) {
-      s_m = m;
-      s_l = l;
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      if (lane == 0) {
+        inv[warp] = l == 0.f ? 0.f : 1.0f / l;
+        if (p.lse && warp < rows && (few || (sub & 3) == 0))
+          p.lse[jn.row0 + c + warp] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+      }
     }
+    const int val = (few ? grp : sub & 3) * 128 + v;    // value of the row
+    const float* src = p.part + at_part(c, val);
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int step = few ? 1 : 4;
+#pragma unroll 8
+    for (int i = few ? 0 : grp; i < n; i += step) {
+      const float4 o = *reinterpret_cast<const float4*>(src + slot(i) * kAtPart);
+      const float4 w = *reinterpret_cast<const float4*>(wgt[i]);
+      acc.x = fmaf(w.x, o.x, acc.x);
+      acc.y = fmaf(w.y, o.y, acc.y);
+      acc.z = fmaf(w.z, o.z, acc.z);
+      acc.w = fmaf(w.w, o.w, acc.w);
+    }
+    if (!few) {
+      if (grp) sums[grp - 1][v] = acc;
+      __syncthreads();
+      if (grp) continue;
+#pragma unroll
+      for (int g = 0; g < 3; ++g) {
+        const float4 o = sums[g][v];
+        acc.x += o.x;
+        acc.y += o.y;
+        acc.z += o.z;
+        acc.w += o.w;
+      }
+    }
+    const float r[4] = {acc.x * inv[0], acc.y * inv[1], acc.z * inv[2], acc.w * inv[3]};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < rows) p.out[(size_t)(jn.row0 + c + i) * kAtV + val] = (uint16_t)at_pack<BF16>(r[i], 0.f);
   }
-  __syncthreads();
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float4 v = *reinterpret_cast<const float4*>(p.part + (size_t)slot(i) * kAtPart + r * kAtV + tid * 4);
-    const float w = wgt[i];
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
-  }
-  const float inv = s_l == 0.f ? 0.f : 1.0f / s_l;
-  uint2 o;
-  o.x = at_pack<BF16>(acc.x * inv, acc.y * inv);
-  o.y = at_pack<BF16>(acc.z * inv, acc.w * inv);
-  *reinterpret_cast<uint2*>(p.out + (size_t)row * kAtV + tid * 4) = o;
-  if (p.lse && tid == 0) p.lse[row] = s_l == 0.f ? -INFINITY : (s_m + log2f(s_l)) * 0.693147180559945309f;
 }
 
 // ------------------------------------------------------------------ host side
 
 struct AtWs {
-  size_t head, units, part, part_ml, total;
+  size_t head, units, joins, part, part_ml, total;
   long long max_units;
 };
 
@@ -830,6 +889,7 @@ static AtWs at_ws(int B, int n_tokens, int H) {
   };
   w.head = take((4 + kAtMaxCtas) * sizeof(int));
   w.units = take((size_t)w.max_units * sizeof(AtUnit));
+  w.joins = take((size_t)kAtMaxCtas * sizeof(AtJoin));
   w.part = take((size_t)2 * kAtMaxCtas * kAtPart * sizeof(float));
   w.part_ml = take((size_t)2 * kAtMaxCtas * kAtRows * sizeof(float2));
   w.total = off;
@@ -858,7 +918,7 @@ static cudaError_t at_launch(const AtArgs& a, const CUtensorMap& kmap, const CUt
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv_attention_kernel<BF16, TMA>, dim3(ctas), dim3(at_threads(TMA)), kAtSmem, st, a, kmap, qmap);
   if (e != cudaSuccess || ctas < 2) return e;
-  return launch_pdl(kv_attention_join_kernel<BF16>, dim3(ctas - 1, kAtRows), dim3(kAtJoinThreads), 0, st, a);
+  return launch_pdl(kv_attention_join_kernel<BF16>, dim3(kAtJoinCtas), dim3(kAtJoinThreads), 0, st, a);
 }
 
 }  // namespace coli
@@ -953,6 +1013,7 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   a.status = reinterpret_cast<int32_t*>(ws);
   a.head = reinterpret_cast<int*>(ws + w.head);
   a.units = reinterpret_cast<AtUnit*>(ws + w.units);
+  a.joins = reinterpret_cast<AtJoin*>(ws + w.joins);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   a.wait_ns = kWaitLimitNs;
