@@ -50,19 +50,24 @@ constexpr float kAtUnset = -1e30f;                 // reference of a part whose 
 constexpr float kAtGrow = 8.f;                     // growth (log2) that raises a reference
 constexpr uint32_t kAtSCol = 256;                  // TMEM column of S^T (O^T: 0..255)
 
-struct AtUnit {
-  int b;        // request
-  int row0;     // first (token * H + head) row
-  int first;    // key tiles of the units before it
-  int tiles;    // its key tiles
+// A unit: the work of one gang of CTAs, 64 rows each, over the same keys.
+struct __align__(16) AtUnit {
+  int b;              // request
+  int row0, row_end;  // (token * H + head) rows; member m of the gang has row0 + 64 m ..
+  int first;          // key tiles of the units before it
+  int tiles;          // its key tiles
+  int shift;          // position of a row's token: shift + row / H
+  int seq;            // tokens of the request in the cache
+  int pad;
 };
 
-// A unit cut by borders: its parts are those of CTAs cta .. cta + parts - 1.
-struct AtJoin {
+// 64 rows of a unit cut by borders: its parts are those of CTAs cta, cta + gang, ...
+struct __align__(16) AtJoin {
   int row0, row_end;
   int cta, parts;
   int slot;     // of the first part (the others': 2 * their CTA)
-  int pad[3];
+  int gang;
+  int pad[2];
 };
 
 struct AtArgs {
@@ -77,7 +82,7 @@ struct AtArgs {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int* head;                         // [0] units, [1] CTAs, [2] key tiles, [3] joins, [4 ..) first unit of each CTA
+  int* head;                         // [0] CTAs a gang, [1] gangs, [2] key tiles, [3] joins, [4 ..) first unit of each gang
   AtUnit* units;
   AtJoin* joins;
   float* part;                       // [2 kAtMaxCtas] partial O, in the order the main kernel's threads hold it (at_part)
@@ -100,26 +105,82 @@ __host__ __device__ constexpr int at_part(int c, int v) { return ((c >> 2) * kAt
 __device__ __forceinline__ int at_cut(int W, int j, int G) { return (int)((long long)W * j / G); }
 
 // ------------------------------------------------------------------ plan
-// One CTA.  Dense: request b has T H rows, units of 64; a unit's keys end with its last row's position.
-// Selected keys: a token's heads in units of 64, all topk entries.
+// One CTA.  Rows come in tiles of 64: a request's T H rows, or, where keys are selected, a token's heads.
+// Row tiles of the same keys may go to a gang of CTAs that take the same key tiles at about the same time, so
+// that a tile comes from memory once and from L2 for the others of the gang: 24 requests of three tokens read
+// 589 MB of 236 MB unique without gangs, their row tiles being dealt to CTAs at unrelated times.  A gang costs
+// CTAs (whole gangs only) and idle members (rows that do not fill it), so the size is chosen by an estimate:
+// time of the longest run of key tiles, or of the tiles' bytes from memory, whichever is longer.
 constexpr int kAtPlanThreads = 1024;
 constexpr int kAtPlanNear = 2048;                  // units whose first tiles are kept in shared memory for the searches
+constexpr int kAtGangs = 6;
+__constant__ int kAtGangSize[kAtGangs] = {1, 2, 3, 4, 6, 8};
+constexpr float kAtTileNs = 2700.f;                // a key tile on one SM (measured)
+constexpr float kAtTileMemNs = 23.f;               // 147 KB at the memory's measured copy rate
+constexpr int kAtL2Tiles = 400;                    // 59 MB: unique tiles that stay in L2 between row tiles
 
 __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(const AtArgs p, int max_units, int max_ctas) {
   extern __shared__ int base_sm[];   // [B + 1] first unit of each request
   __shared__ int warp_tot[32], total;
   __shared__ int first_sm[kAtPlanNear];
+  __shared__ unsigned long long sums[kAtGangs + 1];
+  __shared__ int s_gang;
   const int tid = threadIdx.x;
   griddep_launch_dependents();
+  if (tid <= kAtGangs) sums[tid] = 0;
+  __syncthreads();
+  const int heads = (p.H + kAtRows - 1) / kAtRows;
+  const long long most = (long long)p.d.max_pages * p.d.page_size;
+  const int sel_tiles = (p.topk + kAtKeys - 1) / kAtKeys;
+  // row tiles over the same keys (a row tile group) and how many such groups a request has
+  auto groups = [&](int b, int& n, int& rows) {
+    int q0, q1;
+    at_span(p, b, q0, q1);
+    n = p.sel ? q1 - q0 : (q1 > q0 ? 1 : 0);
+    rows = p.sel ? heads : (int)(((long long)(q1 - q0) * p.H + kAtRows - 1) / kAtRows);
+  };
+  {
+    unsigned long long s[kAtGangs + 1] = {};
+    for (int b = tid; b < p.B; b += kAtPlanThreads) {
+      int n, rows;
+      groups(b, n, rows);
+      const long long keys = max(0ll, min((long long)p.seq_len[b], most));
+      const unsigned long long c = n * (unsigned long long)(p.sel ? sel_tiles : max(1ll, (keys + kAtKeys - 1) / kAtKeys));
+#pragma unroll
+      for (int g = 0; g < kAtGangs; ++g) s[g] += c * ((rows + kAtGangSize[g] - 1) / kAtGangSize[g]);
+      s[kAtGangs] += c;
+    }
+#pragma unroll
+    for (int g = 0; g <= kAtGangs; ++g) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s[g] += __shfl_xor_sync(0xffffffffu, s[g], o);
+      if ((tid & 31) == 0 && s[g]) atomicAdd(&sums[g], s[g]);
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    float best = INFINITY;
+    for (int g = 0; g < kAtGangs && kAtGangSize[g] <= max_ctas; ++g) {
+      const float runs = (float)(max_ctas / kAtGangSize[g]);
+      const float mem = sums[kAtGangs] <= kAtL2Tiles ? (float)sums[kAtGangs] : (float)sums[g];
+      const float cost = fmaxf(ceilf((float)sums[g] / runs) * kAtTileNs, mem * kAtTileMemNs);
+      if (cost < best) {
+        best = cost;
+        s_gang = kAtGangSize[g];
+      }
+    }
+  }
+  __syncthreads();
+  const int gang = s_gang, gang_rows = gang * kAtRows;
+
   int carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += kAtPlanThreads) {
     const int b = b0 + tid;
     int u = 0;
     if (b < p.B) {
-      int q0, q1;
-      at_span(p, b, q0, q1);
-      u = p.sel ? (q1 - q0) * ((p.H + kAtRows - 1) / kAtRows)
-                : (int)(((long long)(q1 - q0) * p.H + kAtRows - 1) / kAtRows);
+      int n, rows;
+      groups(b, n, rows);
+      u = n * ((rows + gang - 1) / gang);
     }
     const int e = block_exclusive_scan(u, warp_tot, &total);
     if (b < p.B) base_sm[b] = carry + e;
@@ -144,15 +205,18 @@ __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(co
       int q0, q1;
       at_span(p, l, q0, q1);
       un.b = l;
+      un.seq = p.seq_len[l];
+      un.shift = un.seq - q1;                      // seq - (q1 - q0) - q0
       if (p.sel) {
-        const int ht = (p.H + kAtRows - 1) / kAtRows, i = u - base_sm[l];
-        un.row0 = (q0 + i / ht) * p.H + (i % ht) * kAtRows;
-        c = (p.topk + kAtKeys - 1) / kAtKeys;
+        const int per = (heads + gang - 1) / gang, i = u - base_sm[l], tok = q0 + i / per;
+        un.row0 = tok * p.H + (i % per) * gang_rows;
+        un.row_end = (tok + 1) * p.H;
+        c = sel_tiles;
       } else {
-        un.row0 = q0 * p.H + (u - base_sm[l]) * kAtRows;
-        const int last_tok = min(q1 - 1, (un.row0 + kAtRows - 1) / p.H);
-        const long long keys = (long long)p.seq_len[l] - (q1 - q0) + (last_tok - q0) + 1;
-        const long long most = (long long)p.d.max_pages * p.d.page_size;
+        un.row0 = q0 * p.H + (u - base_sm[l]) * gang_rows;
+        un.row_end = q1 * p.H;
+        const int last_tok = min(un.row_end - 1, un.row0 + gang_rows - 1) / p.H;
+        const long long keys = (long long)un.shift + last_tok + 1;
         c = (int)((max(0ll, min(keys, most)) + kAtKeys - 1) / kAtKeys);
       }
       c = max(c, 1);                               // a unit without keys still writes its rows
@@ -167,15 +231,14 @@ __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(co
     tiles += total;
     __syncthreads();
   }
-  const int G = min(max_ctas, tiles);
+  const int G = min(max_ctas / gang, tiles);
   __syncthreads();
   // the unit that holds each run's first tile
   const bool near = n_units <= kAtPlanNear;
   auto first_of = [&](int u) { return near ? first_sm[u] : p.units[u].first; };
-  int unit = 0, cut = 0;
-  bool opens = false;                              // border tid is the first inside its unit
+  int unit = 0, members = 0;
   if (tid < G) {
-    cut = at_cut(tiles, tid, G);
+    const int cut = at_cut(tiles, tid, G);
     int l = 0, h = n_units;
     while (h - l > 1) {
       const int mid = (l + h) >> 1;
@@ -185,28 +248,32 @@ __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(co
     unit = l;
     p.head[4 + tid] = l;
     const int first = first_of(l);
-    opens = tid > 0 && first < cut && at_cut(tiles, tid - 1, G) <= first;
+    // the first border inside its unit lists the unit's joins
+    if (tid > 0 && first < cut && at_cut(tiles, tid - 1, G) <= first) {
+      const AtUnit un = p.units[unit];
+      members = min(gang, (un.row_end - un.row0 + kAtRows - 1) / kAtRows);
+    }
   }
-  const int at = block_exclusive_scan(opens ? 1 : 0, warp_tot, &total);
-  if (opens) {
+  const int at = block_exclusive_scan(members, warp_tot, &total);
+  if (members) {
     const AtUnit un = p.units[unit];
-    int q0, q1;
-    at_span(p, un.b, q0, q1);
-    AtJoin jn{};
-    jn.row0 = un.row0;
-    jn.row_end = min(un.row0 + kAtRows, p.sel ? (un.row0 / p.H + 1) * p.H : q1 * p.H);
-    jn.cta = tid - 1;
-    // CTAs up to the one that holds the unit's last tile: borders below first + tiles
-    const int last = un.first + un.tiles;
-    int n = (int)(((long long)last * G + tiles - 1) / tiles);          // at_cut(j) < last for j < n (or one more)
+    const int last = un.first + un.tiles, run0 = tid - 1;
+    int n = (int)(((long long)last * G + tiles - 1) / tiles);           // runs 0 .. n - 1 begin before the unit's end
     while (n > 0 && at_cut(tiles, n - 1, G) >= last) --n;
     while (n < G && at_cut(tiles, n, G) < last) ++n;
-    jn.parts = n - jn.cta;
-    jn.slot = 2 * jn.cta + (at_cut(tiles, tid - 1, G) < un.first ? 1 : 0);
-    p.joins[at] = jn;
+    for (int m = 0; m < members; ++m) {
+      AtJoin jn{};
+      jn.row0 = un.row0 + m * kAtRows;
+      jn.row_end = min(jn.row0 + kAtRows, un.row_end);
+      jn.cta = run0 * gang + m;
+      jn.gang = gang;
+      jn.parts = n - run0;
+      jn.slot = 2 * jn.cta + (at_cut(tiles, run0, G) < un.first ? 1 : 0);
+      p.joins[at + m] = jn;
+    }
   }
   if (tid == 0) {
-    p.head[0] = n_units;
+    p.head[0] = gang;
     p.head[1] = G;
     p.head[2] = tiles;
     p.head[3] = total;
@@ -375,10 +442,11 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   const uint32_t tmem = tmem_base;
   griddep_wait();                                      // the plan kernel's lists
   griddep_launch_dependents();
-  const int G = p.head[1], W = p.head[2];
-  const int cta = blockIdx.x;
-  const int beg = cta < G ? at_cut(W, cta, G) : 0, end = cta < G ? at_cut(W, cta + 1, G) : 0;
-  const int unit0 = cta < G ? p.head[4 + cta] : 0;
+  const int gang = p.head[0], G = p.head[1], W = p.head[2];
+  const int cta = blockIdx.x, run = cta / gang;
+  const int my_rows = (cta - run * gang) * kAtRows;    // this member's rows of a unit begin there
+  const int beg = run < G ? at_cut(W, run, G) : 0, end = run < G ? at_cut(W, run + 1, G) : 0;
+  const int unit0 = run < G ? p.head[4 + run] : 0;
   auto fail_wait = [&]() {
     atomicOr(p.status, COLI_DEV_WAIT_TIMEOUT);
     atomicExch(&abort_flag, 1);
@@ -390,60 +458,72 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     bool ok = true;
     int it = 0, un = 0;
     const int n_box = TMA ? kAtKeys / p.box : 0;       // boxes of 64 columns a tile
-    for (int at = beg, u = unit0; ok && at < end; ++u, ++un) {
+    for (int at = beg, u = unit0; ok && at < end; ++u) {
       const AtUnit ut = p.units[u];
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
-      const int tok = ut.row0 / p.H;
-      int q0, q1;
-      at_span(p, ut.b, q0, q1);
-      const int seq = p.seq_len[ut.b];
-      const int row_end = p.sel ? (tok + 1) * p.H : q1 * p.H;
-      const int seen = p.sel ? min(seq, seq - (q1 - q0) + (tok - q0) + 1) : seq;   // keys before this are there
-      // cached row of a key; false where there is none (then row 0, whose values meet weights of 0)
-      auto row_of = [&](int key, long long& row) {
+      const int row0 = ut.row0 + my_rows;
+      if (row0 >= ut.row_end) {                        // this member has no rows of the unit
+        at = ut.first + t1;
+        continue;
+      }
+      const int tok = row0 / p.H;
+      const int seen = p.sel ? min(ut.seq, ut.shift + tok + 1) : ut.seq;   // keys before this are there
+      const int32_t* table = p.table + (size_t)ut.b * p.d.max_pages;
+      const int32_t* sel = p.sel + (size_t)tok * p.topk;
+      // Where a key's row is, in two steps a tile apart, so that their loads are on the way before a tile's
+      // copies queue up: the key (TMA: the first of box l; copying: key 32 j + l of the warp's), then its page.
+      constexpr int kRows = TMA ? 1 : kAtLaneKeys;
+      int key[kRows], next[kRows], page[kRows];       // tile t + 1's keys, tile t + 2's, tile t + 1's pages
+      auto find_key = [&](int t, int (&key)[kRows]) {
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          if constexpr (TMA) {
+            key[j] = t * kAtKeys + (lane & (n_box - 1)) * p.box;
+          } else {
+            key[j] = t * kAtKeys + (lw * kAtLaneKeys + j) * 32 + lane;
+            if (p.sel) key[j] = key[j] < p.topk ? sel[key[j]] : -1;
+          }
+        }
+      };
+      auto find_page = [&]() {
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+          const int col = key[j] / p.d.page_size;
+          page[j] = key[j] >= 0 && key[j] < seen && col < p.d.max_pages ? table[col] : -1;
+        }
+      };
+      // the row; false where there is none (then row 0, whose values meet weights of 0)
+      auto row_of = [&](int j, long long& row) {
         row = 0;
-        if (key < 0 || key >= seen) return false;
-        const int col = key / p.d.page_size;
-        const int page = col < p.d.max_pages ? p.table[(size_t)ut.b * p.d.max_pages + col] : -1;
-        if (page < 0 || page >= p.d.n_pages) {
+        if (key[j] < 0 || key[j] >= seen) return false;
+        if (page[j] < 0 || page[j] >= p.d.n_pages) {
           atomicOr(p.status, COLI_DEV_KV_BAD_PAGE);
           return false;
         }
-        row = (long long)page * p.rows_per_page + (key - col * p.d.page_size);
+        row = (long long)page[j] * p.rows_per_page + key[j] % p.d.page_size;
         return true;
       };
-      // TMA: lane l has box l of a tile (lanes beyond the boxes repeat); copying: key 32 j + l of the warp's
-      constexpr int kRows = TMA ? 1 : kAtLaneKeys;
       long long row[kRows];
       bool there[kRows];
-      auto find = [&](int t) {
+      find_key(t0, key);
+      find_page();
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-          int key;
-          if constexpr (TMA) {
-            key = t * kAtKeys + (lane & (n_box - 1)) * p.box;
-          } else {
-            key = t * kAtKeys + (lw * kAtLaneKeys + j) * 32 + lane;
-            if (p.sel) key = key < p.topk ? p.sel[(size_t)tok * p.topk + key] : -1;
-          }
-          there[j] = row_of(key, row[j]);
-        }
-      };
-      find(t0);
+      for (int j = 0; j < kRows; ++j) there[j] = row_of(j, row[j]);
+      find_key(t0 + 1, key);
       // queries
       if (un > 0 && !mbar_wait(&q_empty, (un - 1) & 1, p.wait_ns)) { ok = false; break; }
       if constexpr (TMA) {
         if (lane == 0) mbar_arrive_expect_tx(&q_full, (uint32_t)(kAtBoxes * kAtQBoxBytes));
         __syncwarp();
         // rows past the unit's last are other rows' or, behind the tensor, zeros: computed, not written
-        if (lane < kAtBoxes) tma_load_2d_nohint(qs + lane * kAtQBoxBytes, &qmap, lane * 64, ut.row0, &q_full);
+        if (lane < kAtBoxes) tma_load_2d_nohint(qs + lane * kAtQBoxBytes, &qmap, lane * 64, row0, &q_full);
       } else {
         // eight lanes a row and box: 16 bytes each
         const int c = lane & 7;
 #pragma unroll 1
         for (int i = 0; i < kAtRows / (4 * kAtLoadWarps); ++i) {
           const int r = (i * kAtLoadWarps + lw) * 4 + (lane >> 3);
-          const int gr = min(ut.row0 + r, row_end - 1);
+          const int gr = min(row0 + r, ut.row_end - 1);
           const uint8_t* src = p.q + (gr / p.H) * p.q_tok + (gr % p.H) * p.q_head + c * 16;
           uint8_t* dst = qs + r * 128 + ((c ^ (r & 7)) << 4);
 #pragma unroll
@@ -470,6 +550,17 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
 #pragma unroll
           for (int j = 0; j < kRows; ++j) mine[j] = __ballot_sync(0xffffffffu, there[j]);
         }
+        // copying: the rows of the eight lanes a key, once a tile
+        const uint8_t* src[TMA ? 1 : 8 * kRows];
+        if constexpr (!TMA) {
+#pragma unroll
+          for (int i = 0; i < 8 * kRows; ++i)
+            src[i] = p.cache + __shfl_sync(0xffffffffu, row[i >> 3], (i & 7) * 4 + (lane >> 3)) * (kAtW * 2) + (lane & 7) * 16;
+        }
+        if (t + 1 < t1) {
+          find_page();
+          find_key(t + 2, next);
+        }
         // pairs of value boxes as the previous tile's products free them, then the rotary box
 #pragma unroll 1
         for (int d = 0; d < 4 && ok; ++d) {
@@ -487,15 +578,12 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
             if (d == 0 && lane == 0)
 #pragma unroll
               for (int j = 0; j < kRows; ++j) key_ok[it & 1][lw * kRows + j] = mine[j];
-            const int c = lane & 7;
 #pragma unroll
             for (int i = 0; i < 8 * kRows; ++i) {      // eight lanes a key
               const int k = lw * 32 * kRows + i * 4 + (lane >> 3);
-              const uint8_t* src =
-                  p.cache + __shfl_sync(0xffffffffu, row[i >> 3], (i & 7) * 4 + (lane >> 3)) * (kAtW * 2) + c * 16;
-              uint8_t* dst = smem + k * 128 + ((c ^ (k & 7)) << 4);
-              copy16(dst + (2 * d) * kAtBoxBytes, src + (2 * d) * 128);
-              copy16(dst + (2 * d + 1) * kAtBoxBytes, src + (2 * d + 1) * 128);
+              uint8_t* dst = smem + k * 128 + (((lane & 7) ^ (k & 7)) << 4);
+              copy16(dst + (2 * d) * kAtBoxBytes, src[i] + (2 * d) * 128);
+              copy16(dst + (2 * d + 1) * kAtBoxBytes, src[i] + (2 * d + 1) * 128);
             }
             copies_arrive(&full[d]);
           }
@@ -506,20 +594,25 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
           __syncwarp();
           if (lane < n_box) tma_load_2d_nohint(rot + lane * p.box * 128, &kmap, 8 * 64, (int)row[0], &full[4]);
         } else {
-          const int c = lane & 7;
 #pragma unroll
           for (int i = 0; i < 8 * kRows; ++i) {
             const int k = lw * 32 * kRows + i * 4 + (lane >> 3);
-            copy16(rot + k * 128 + ((c ^ (k & 7)) << 4),
-                   p.cache + __shfl_sync(0xffffffffu, row[i >> 3], (i & 7) * 4 + (lane >> 3)) * (kAtW * 2) + 8 * 128 +
-                       c * 16);
+            copy16(rot + k * 128 + (((lane & 7) ^ (k & 7)) << 4), src[i] + 8 * 128);
           }
           copies_arrive(&full[4]);
           if (lane == 0) mbar_arrive(&full[4]);        // key_ok is written
         }
-        if (t + 1 < t1) find(t + 1);
+        if (t + 1 < t1) {
+#pragma unroll
+          for (int j = 0; j < kRows; ++j) {
+            there[j] = row_of(j, row[j]);
+            key[j] = next[j];
+          }
+        }
       }
+      if (!ok) break;
       at = ut.first + t1;
+      ++un;
     }
     if (!ok) {
       fail_wait();
@@ -544,9 +637,11 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     const uint64_t pd = umma_desc_sw128_mn(smem_u32(rot), kAtBoxBytes);
     bool ok = true;
     int it = 0, un = 0;
-    for (int at = beg, u = unit0; ok && at < end; ++u, ++un) {
-      const int first = p.units[u].first, tiles = p.units[u].tiles;
-      const int t0 = at - first, t1 = min(end - first, tiles);
+    for (int at = beg, u = unit0; ok && at < end; ++u) {
+      const AtUnit ut = p.units[u];
+      const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
+      at = ut.first + t1;
+      if (ut.row0 + my_rows >= ut.row_end) continue;
       ok = __all_sync(0xffffffffu, mbar_wait_spin(&q_full, un & 1, p.wait_ns));
       if (!TMA) fence_proxy_async_smem();              // the copies are ordinary writes; the MMA reads by the async proxy
       for (int t = t0; ok && t < t1; ++t, ++it) {
@@ -580,7 +675,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       }
       if (!ok) break;
       umma_commit_elect(&o_full);
-      at = first + t1;
+      ++un;
     }
     if (!ok) {
       if (lane == 0) fail_wait();
@@ -596,23 +691,20 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     const int id = threadIdx.x - 64;                   // thread among the softmax warps
     const uint32_t trow = tmem + ((uint32_t)(sp * 32) << 16) + (uint32_t)c0;
     int it = 0, un = 0;
-    for (int at = beg, u = unit0; at < end; ++u, ++un) {
+    for (int at = beg, u = unit0; at < end; ++u) {
       const AtUnit ut = p.units[u];
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
+      at = ut.first + t1;
+      const int row0 = ut.row0 + my_rows;
+      if (row0 >= ut.row_end) continue;
       const bool whole = t0 == 0 && t1 == ut.tiles;
       const int slot = 2 * cta + (u == unit0 ? 0 : 1);
-      const int tok0 = ut.row0 / p.H;
-      int q0, q1;
-      at_span(p, ut.b, q0, q1);
-      const int row_end = p.sel ? (tok0 + 1) * p.H : q1 * p.H;
-      const int past = p.seq_len[ut.b] - (q1 - q0);     // position of the request's first new token
       if (id < kAtRows) {
-        const int row = min(ut.row0 + id, row_end - 1);
-        lim[id] = p.sel ? 0x7fffffff : past + row / p.H - q0;
+        lim[id] = p.sel ? 0x7fffffff : ut.shift + min(row0 + id, ut.row_end - 1) / p.H;
         ref[id] = 0.f;
         has_ref[id] = 0;
       }
-      const int seen_all = past + tok0 - q0;            // every row of the unit sees the keys up to this one
+      const int seen_all = ut.shift + row0 / p.H;      // every row sees the keys up to this one
       float l[kAtHalf];
 #pragma unroll
       for (int c = 0; c < kAtHalf; ++c) l[c] = 0.f;
@@ -741,17 +833,17 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
         const float sum = (red[0][id] + red[1][id]) + (red[2][id] + red[3][id]);
         if (whole) {
           fac[id] = sum == 0.f ? 0.f : 1.0f / sum;
-          const int row = ut.row0 + id;
-          if (p.lse && row < row_end)
+          const int row = row0 + id;
+          if (p.lse && row < ut.row_end)
             p.lse[row] = sum == 0.f ? -INFINITY : (ref[id] + log2f(sum)) * 0.693147180559945309f;
         } else {
           p.part_ml[(size_t)slot * kAtRows + id] = make_float2(has_ref[id] ? ref[id] : kAtUnset, sum);
         }
       }
       sm_sync();
-      const int rows = min(kAtRows, row_end - ut.row0) - c0;    // of this half
+      const int rows = min(kAtRows, ut.row_end - row0) - c0;    // of this half
       float* part = p.part + (size_t)slot * kAtPart;
-      uint16_t* out = p.out + (size_t)(ut.row0 + c0) * kAtV;
+      uint16_t* out = p.out + (size_t)(row0 + c0) * kAtV;
 #pragma unroll 1
       for (int d = 0; d < 4; ++d) {
         uint32_t r[2][16];
@@ -780,7 +872,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       }
       tc_fence_before();
       sm_sync();                                       // everyone is done with ref, fac, red
-      at = ut.first + t1;
+      ++un;
     }
   }
   tc_fence_before();
@@ -812,7 +904,7 @@ __global__ void __launch_bounds__(kAtJoinThreads) kv_attention_join_kernel(const
     if (few && sub >= 16) continue;
     const int c = (few ? sub : sub >> 2) * 4, rows = jn.row_end - jn.row0 - c;
     if (rows <= 0) continue;
-    auto slot = [&](int i) { return (size_t)(i ? 2 * (jn.cta + i) : jn.slot); };
+    auto slot = [&](int i) { return (size_t)(i ? 2 * (jn.cta + i * jn.gang) : jn.slot); };
     __syncthreads();                                    // the previous task's weights are read
     if (warp < 4) {                                     // warp w: the parts' weights for row c + w
       float m = kAtUnset;
