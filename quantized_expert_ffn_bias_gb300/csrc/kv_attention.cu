@@ -44,6 +44,7 @@ constexpr int kAtFirstLoad = 2 + kAtSmWarps;       // warp 0 loads; copying load
 constexpr int at_threads(bool tma) { return (1 + kAtSmWarps + (tma ? 1 : kAtLoadWarps)) * 32; }
 constexpr int kAtMinBox = 8;                       // fewest key rows a TMA box has
 constexpr int kAtMaxCtas = 160;                    // CTAs the workspace has room for
+constexpr int kAtMaxB = 8192, kAtMaxH = 1024;
 constexpr size_t kAtSmem = (size_t)kAtBoxes * (kAtBoxBytes + kAtQBoxBytes) + 1024;
 constexpr int kAtPart = kAtRows * kAtV;            // floats of a partial O
 constexpr float kAtUnset = -1e30f;                 // reference of a part whose row has seen no key
@@ -101,8 +102,11 @@ __device__ __forceinline__ void at_span(const AtArgs& p, int b, int& q0, int& q1
 // the main kernel holds many rows of one value, so neighbouring values of four rows lie together.
 __host__ __device__ constexpr int at_part(int c, int v) { return ((c >> 2) * kAtV + v) * 4; }
 
-// Border j of G equal runs of the W key tiles.
-__device__ __forceinline__ int at_cut(int W, int j, int G) { return (int)((long long)W * j / G); }
+// Border j of G <= kAtMaxCtas equal runs of the W key tiles: floor(W j / G) without leaving 32 bits.
+__device__ __forceinline__ int at_cut(int W, int j, int G) {
+  const int q = W / G;
+  return q * j + (W - q * G) * j / G;
+}
 
 // ------------------------------------------------------------------ plan
 // One CTA.  Rows come in tiles of 64: a request's T H rows, or, where keys are selected, a token's heads.
@@ -111,43 +115,63 @@ __device__ __forceinline__ int at_cut(int W, int j, int G) { return (int)((long 
 // 589 MB of 236 MB unique without gangs, their row tiles being dealt to CTAs at unrelated times.  A gang costs
 // CTAs (whole gangs only) and idle members (rows that do not fill it), so the size is chosen by an estimate:
 // time of the longest run of key tiles, or of the tiles' bytes from memory, whichever is longer.
-constexpr int kAtPlanThreads = 1024;
+constexpr int kAtPlanThreads = 256;
 constexpr int kAtPlanNear = 2048;                  // units whose first tiles are kept in shared memory for the searches
 constexpr int kAtGangs = 6;
-__constant__ int kAtGangSize[kAtGangs] = {1, 2, 3, 4, 6, 8};
+constexpr int at_gang(int i) { return i < 4 ? i + 1 : i * 2 - 2; }   // 1, 2, 3, 4, 6, 8
 constexpr float kAtTileNs = 2700.f;                // a key tile on one SM (measured)
 constexpr float kAtTileMemNs = 23.f;               // 147 KB at the memory's measured copy rate
 constexpr int kAtL2Tiles = 400;                    // 59 MB: unique tiles that stay in L2 between row tiles
 
+constexpr size_t at_plan_smem(int B) { return (size_t)(3 * B + 2) * sizeof(int); }
+
 __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(const AtArgs p, int max_units, int max_ctas) {
-  extern __shared__ int base_sm[];   // [B + 1] first unit of each request
-  __shared__ int warp_tot[32], total;
+  extern __shared__ int plan_sm[];
+  int* qs = plan_sm;                 // [B + 1] q_start, kept inside the batch and ascending
+  int* base = qs + p.B + 1;          // [B + 1] first unit of each request
+  int* seq = base + p.B + 1;         // [B]
+  __shared__ int warp_tot[32], total, s_max;
   __shared__ int first_sm[kAtPlanNear];
   __shared__ unsigned long long sums[kAtGangs + 1];
-  __shared__ int s_gang;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, B = p.B;
   griddep_launch_dependents();
+  griddep_wait();                    // the launch may overlap the kernel before; its results (and workspace) not
   if (tid <= kAtGangs) sums[tid] = 0;
+  if (tid == 0) s_max = 0;
+  for (int b = tid; b < B; b += kAtPlanThreads) {
+    int q0, q1;
+    at_span(p, b, q0, q1);
+    qs[b] = q0;
+    seq[b] = p.seq_len[b];
+    if (b == B - 1) qs[B] = q1;
+  }
   __syncthreads();
   const int heads = (p.H + kAtRows - 1) / kAtRows;
-  const long long most = (long long)p.d.max_pages * p.d.page_size;
+  const int most = p.d.max_pages * p.d.page_size;      // (at most 2^31 - 1: checked by the host)
   const int sel_tiles = (p.topk + kAtKeys - 1) / kAtKeys;
   // row tiles over the same keys (a row tile group) and how many such groups a request has
   auto groups = [&](int b, int& n, int& rows) {
-    int q0, q1;
-    at_span(p, b, q0, q1);
-    n = p.sel ? q1 - q0 : (q1 > q0 ? 1 : 0);
-    rows = p.sel ? heads : (int)(((long long)(q1 - q0) * p.H + kAtRows - 1) / kAtRows);
+    const int T = max(0, qs[b + 1] - qs[b]);
+    n = p.sel ? T : min(T, 1);
+    rows = p.sel ? heads : (T * p.H + kAtRows - 1) / kAtRows;          // (n_tokens * H < 2^31 - 64)
   };
-  {
+  // a gang is of use where row tiles share keys
+  for (int b = tid; b < B; b += kAtPlanThreads) {
+    int n, rows;
+    groups(b, n, rows);
+    if (n && rows > 1) s_max = 1;
+  }
+  __syncthreads();
+  int gang = 1;
+  if (s_max) {
     unsigned long long s[kAtGangs + 1] = {};
-    for (int b = tid; b < p.B; b += kAtPlanThreads) {
+    for (int b = tid; b < B; b += kAtPlanThreads) {
       int n, rows;
       groups(b, n, rows);
-      const long long keys = max(0ll, min((long long)p.seq_len[b], most));
-      const unsigned long long c = n * (unsigned long long)(p.sel ? sel_tiles : max(1ll, (keys + kAtKeys - 1) / kAtKeys));
+      const int keys = max(0, min(seq[b], most));
+      const unsigned long long c = (unsigned long long)n * (p.sel ? sel_tiles : max(1, (keys + kAtKeys - 1) / kAtKeys));
 #pragma unroll
-      for (int g = 0; g < kAtGangs; ++g) s[g] += c * ((rows + kAtGangSize[g] - 1) / kAtGangSize[g]);
+      for (int g = 0; g < kAtGangs; ++g) s[g] += c * ((rows + at_gang(g) - 1) / at_gang(g));
       s[kAtGangs] += c;
     }
 #pragma unroll
@@ -156,68 +180,64 @@ __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(co
       for (int o = 16; o > 0; o >>= 1) s[g] += __shfl_xor_sync(0xffffffffu, s[g], o);
       if ((tid & 31) == 0 && s[g]) atomicAdd(&sums[g], s[g]);
     }
-  }
-  __syncthreads();
-  if (tid == 0) {
+    __syncthreads();
     float best = INFINITY;
-    for (int g = 0; g < kAtGangs && kAtGangSize[g] <= max_ctas; ++g) {
-      const float runs = (float)(max_ctas / kAtGangSize[g]);
+#pragma unroll
+    for (int g = 0; g < kAtGangs; ++g) {
+      if (at_gang(g) > max_ctas) continue;
+      const float runs = (float)(max_ctas / at_gang(g));
       const float mem = sums[kAtGangs] <= kAtL2Tiles ? (float)sums[kAtGangs] : (float)sums[g];
       const float cost = fmaxf(ceilf((float)sums[g] / runs) * kAtTileNs, mem * kAtTileMemNs);
       if (cost < best) {
         best = cost;
-        s_gang = kAtGangSize[g];
+        gang = at_gang(g);
       }
     }
   }
-  __syncthreads();
-  const int gang = s_gang, gang_rows = gang * kAtRows;
+  const int gang_rows = gang * kAtRows;
 
   int carry = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kAtPlanThreads) {
+  for (int b0 = 0; b0 < B; b0 += kAtPlanThreads) {
     const int b = b0 + tid;
     int u = 0;
-    if (b < p.B) {
+    if (b < B) {
       int n, rows;
       groups(b, n, rows);
       u = n * ((rows + gang - 1) / gang);
     }
     const int e = block_exclusive_scan(u, warp_tot, &total);
-    if (b < p.B) base_sm[b] = carry + e;
+    if (b < B) base[b] = carry + e;
     carry += total;
     __syncthreads();
   }
   const int n_units = min(carry, max_units);       // (more only from a q_start that is not ascending)
-  if (tid == 0) base_sm[p.B] = carry;
-  __syncthreads();
   int tiles = 0;
   for (int u0 = 0; u0 < n_units; u0 += kAtPlanThreads) {
     const int u = u0 + tid;
     int c = 0;
     AtUnit un{};
     if (u < n_units) {
-      int l = 0, h = p.B;                          // last b with base[b] <= u
+      int l = 0, h = B;                            // last b with base[b] <= u
       while (h - l > 1) {
         const int mid = (l + h) >> 1;
-        if (base_sm[mid] <= u) l = mid;
+        if (base[mid] <= u) l = mid;
         else h = mid;
       }
-      int q0, q1;
-      at_span(p, l, q0, q1);
+      const int q0 = qs[l], q1 = max(q0, qs[l + 1]);
       un.b = l;
-      un.seq = p.seq_len[l];
+      un.seq = seq[l];
       un.shift = un.seq - q1;                      // seq - (q1 - q0) - q0
       if (p.sel) {
-        const int per = (heads + gang - 1) / gang, i = u - base_sm[l], tok = q0 + i / per;
+        const int per = (heads + gang - 1) / gang, i = u - base[l], tok = q0 + i / per;
         un.row0 = tok * p.H + (i % per) * gang_rows;
         un.row_end = (tok + 1) * p.H;
         c = sel_tiles;
       } else {
-        un.row0 = q0 * p.H + (u - base_sm[l]) * gang_rows;
+        un.row0 = q0 * p.H + (u - base[l]) * gang_rows;
         un.row_end = q1 * p.H;
         const int last_tok = min(un.row_end - 1, un.row0 + gang_rows - 1) / p.H;
         const long long keys = (long long)un.shift + last_tok + 1;
-        c = (int)((max(0ll, min(keys, most)) + kAtKeys - 1) / kAtKeys);
+        c = (int)(max(0ll, min(keys, (long long)most)) + kAtKeys - 1) / kAtKeys;
       }
       c = max(c, 1);                               // a unit without keys still writes its rows
     }
@@ -232,7 +252,6 @@ __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(co
     __syncthreads();
   }
   const int G = min(max_ctas / gang, tiles);
-  __syncthreads();
   // the unit that holds each run's first tile
   const bool near = n_units <= kAtPlanNear;
   auto first_of = [&](int u) { return near ? first_sm[u] : p.units[u].first; };
@@ -258,9 +277,12 @@ __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(co
   if (members) {
     const AtUnit un = p.units[unit];
     const int last = un.first + un.tiles, run0 = tid - 1;
-    int n = (int)(((long long)last * G + tiles - 1) / tiles);           // runs 0 .. n - 1 begin before the unit's end
-    while (n > 0 && at_cut(tiles, n - 1, G) >= last) --n;
-    while (n < G && at_cut(tiles, n, G) < last) ++n;
+    int n = tid;                                   // runs run0 .. n - 1 begin before the unit's end
+    for (int h = G; n < h;) {
+      const int mid = (n + h) >> 1;
+      if (at_cut(tiles, mid, G) < last) n = mid + 1;
+      else h = mid;
+    }
     for (int m = 0; m < members; ++m) {
       AtJoin jn{};
       jn.row0 = un.row0 + m * kAtRows;
@@ -608,6 +630,18 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
             there[j] = row_of(j, row[j]);
             key[j] = next[j];
           }
+          // the next tile is on its way to L2 while this one is worked on (its place in shared memory is taken)
+          if constexpr (TMA) {
+            for (int i = lane; i < kAtBoxes * n_box; i += 32)      // (i and the lane have the same box of rows)
+              tma_prefetch_2d(&kmap, (i / n_box) * 64, (int)row[0]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kRows; ++j)
+              if (there[j])
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.cache + row[j] * (kAtW * 2)),
+                             "n"(kAtW * 2)
+                             : "memory");
+          }
         }
       }
       if (!ok) break;
@@ -894,6 +928,7 @@ __global__ void __launch_bounds__(kAtJoinThreads) kv_attention_join_kernel(const
   __shared__ __align__(16) float wgt[kAtMaxCtas][4];
   __shared__ float inv[4];
   __shared__ float4 sums[3][128];
+  griddep_launch_dependents();
   griddep_wait();
   const int n_join = p.head[3];
   const int tid = threadIdx.x, grp = tid >> 7, v = tid & 127, warp = tid >> 5, lane = tid & 31;
@@ -1003,8 +1038,12 @@ static CUresult at_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m,
 template <bool BF16, bool TMA>
 static cudaError_t at_launch(const AtArgs& a, const CUtensorMap& kmap, const CUtensorMap& qmap, int max_units,
                              int ctas, cudaStream_t st) {
-  kv_attention_plan_kernel<<<1, kAtPlanThreads, (a.B + 1) * sizeof(int), st>>>(a, max_units, ctas);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  if (at_plan_smem(a.B) > 32 * 1024)
+    e = cudaFuncSetAttribute(kv_attention_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)at_plan_smem(kAtMaxB));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kv_attention_plan_kernel, dim3(1), dim3(kAtPlanThreads), at_plan_smem(a.B), st, a, max_units, ctas);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kv_attention_kernel<BF16, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem);
   if (e != cudaSuccess) return e;
@@ -1035,7 +1074,7 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   const coli_status rc = check_kv_desc(desc, "kv_attention");
   if (rc != COLI_OK) return rc;
   if (B < 1 || n_tokens < 0 || H < 1) return fail(COLI_EINVAL, "kv_attention: need B, H >= 1 and n_tokens >= 0");
-  if (B > 8192 || H > 1024) return fail(COLI_EUNSUPPORTED, "kv_attention: at most 8192 requests of 1024 heads");
+  if (B > kAtMaxB || H > kAtMaxH) return fail(COLI_EUNSUPPORTED, "kv_attention: at most 8192 requests of 1024 heads");
   if (desc->dtype != COLI_X_BF16 && desc->dtype != COLI_X_F16)
     return fail(COLI_EUNSUPPORTED, "kv_attention: the cache holds bf16 or fp16 (dtype %d)", desc->dtype);
   if (!(scale == scale) || scale - scale != 0.f) return fail(COLI_EINVAL, "kv_attention: scale is not finite");
