@@ -230,7 +230,7 @@ COLI_API coli_status colibri_moe_debug_routing(const coli_moe_plan_t* plan, cons
 #define COLI_DEV_SELECT_ROUNDS 4   /* the key selection's rounds did not narrow to one value (not expected) */
 #define COLI_DEV_KV_NO_PAGES 8     /* colibri_kv_step: too few free pages for every request */
 #define COLI_DEV_KV_TABLE_FULL 16  /* colibri_kv_step: a request needs more than max_pages pages, or its lengths are not valid */
-#define COLI_DEV_KV_TOKENS 32      /* colibri_kv_step: the new tokens exceed n_tokens */
+#define COLI_DEV_KV_TOKENS 32      /* the new tokens exceed n_tokens, or q_start does not ascend */
 #define COLI_DEV_KV_BAD_PAGE 64    /* a page id outside [0, n_pages) where a page of the request was expected */
 COLI_API coli_status colibri_moe_check_status(const coli_moe_plan_t* plan, const void* workspace, int32_t* device_status,
                                      void* stream);
@@ -578,7 +578,8 @@ COLI_API coli_status colibri_kv_append(const coli_kv_desc* desc, int n_tokens, c
  *   q            device [n_tokens][H][576] of desc->dtype with the strides (in
  *                elements) given; 16-byte aligned; the strides multiples of 8
  *                (a stride along an axis of one is not read).  1 <= H <= 1024.
- *   q_start      int32 [B + 1] ascending, seq_len int32 [B].
+ *   q_start      int32 [B + 1] ascending (else nothing is computed and the
+ *                status word gets COLI_DEV_KV_TOKENS), seq_len int32 [B].
  *   topk_idx     device int32 [n_tokens][topk], or NULL (topk is then not read).
  *   out          device [n_tokens][H][512] of desc->dtype, 16-byte aligned.
  *   lse          device float [n_tokens][H] or NULL: log of the softmax's sum.
@@ -593,7 +594,7 @@ COLI_API coli_status colibri_kv_append(const coli_kv_desc* desc, int n_tokens, c
  * (COLI_DEV_KV_BAD_PAGE).  Softmax and sums in fp32; the weights are rounded
  * to dtype for the product with the values.  The result does not depend on
  * timing.
- * Asynchronous on stream, three launches.  n_tokens = 0 does nothing.  Errors: COLI_EINVAL, COLI_EALIGN,
+ * Asynchronous on stream, two launches.  n_tokens = 0 does nothing.  Errors: COLI_EINVAL, COLI_EALIGN,
  * COLI_EWORKSPACE, COLI_EUNSUPPORTED, COLI_ECUDA.
  */
 COLI_API coli_status colibri_kv_attention_workspace_size(int B, int n_tokens, int H, size_t* bytes);
@@ -603,7 +604,8 @@ COLI_API coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n
                                           const int32_t* seq_len, const int32_t* topk_idx, int topk, void* out,
                                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
 /* The status word of an attention workspace (synchronises `stream`): 0, or
- * COLI_DEV_KV_BAD_PAGE, COLI_DEV_WAIT_TIMEOUT (then COLI_EDEVICE). */
+ * COLI_DEV_KV_BAD_PAGE, COLI_DEV_KV_TOKENS, COLI_DEV_WAIT_TIMEOUT (then
+ * COLI_EDEVICE). */
 COLI_API coli_status colibri_kv_check_status(const void* workspace, int32_t* device_status, void* stream);
 
 /* Number of kernel launches the last forward call of this plan issued. */

@@ -22,10 +22,10 @@
 // are whole numbers, so that raising one rounds nothing.  Each thread sums its
 // own key's weights; the sums are reduced once at the end.
 //
-// Work: the plan kernel lists the units (64 rows of one request, or of one
-// token where keys are selected) with their key tiles and deals the tiles in
-// equal runs to one CTA per SM.  A unit cut by a border leaves partial results
-// in the workspace, which the join kernel adds up in order.
+// Work: units (row tiles of one request, or of one token where keys are
+// selected) with their key tiles, dealt in equal runs of key tiles to one CTA
+// per SM (or gang of CTAs).  A unit cut by a border leaves partial results in
+// the workspace, which the join kernel adds up in order.
 #include "plan.h"
 
 namespace coli {
@@ -83,20 +83,13 @@ struct AtArgs {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int* head;                         // [0] CTAs a gang, [1] gangs, [2] key tiles, [3] joins, [4 ..) first unit of each gang
-  AtUnit* units;
-  AtJoin* joins;
+  int32_t* cta_status;               // [kAtMaxCtas] what each CTA saw
+  AtUnit* units;                     // unit u of run r at u + r
+  AtJoin* joins;                     // [kAtMaxCtas] written by every CTA (parts = 0: none)
   float* part;                       // [2 kAtMaxCtas] partial O, in the order the main kernel's threads hold it (at_part)
   float2* part_ml;                   // [2 kAtMaxCtas][64] reference, sum
   unsigned long long wait_ns;
 };
-
-// The token rows of request b, kept inside the batch whatever q_start holds.
-__device__ __forceinline__ void at_span(const AtArgs& p, int b, int& q0, int& q1) {
-  const int lo = max(0, min(p.q_start[0], p.n_tokens)), hi = max(lo, min(p.q_start[p.B], p.n_tokens));
-  q0 = max(lo, min(p.q_start[b], hi));
-  q1 = max(q0, min(p.q_start[b + 1], hi));
-}
 
 // Place of row c (a multiple of four: four rows follow one another) and value v in a partial O.  A thread of
 // the main kernel holds many rows of one value, so neighbouring values of four rows lie together.
@@ -109,41 +102,42 @@ __device__ __forceinline__ int at_cut(int W, int j, int G) {
 }
 
 // ------------------------------------------------------------------ plan
-// One CTA.  Rows come in tiles of 64: a request's T H rows, or, where keys are selected, a token's heads.
+// Every CTA finds its own run of the work from the lengths (a kernel of its own took 7 us, most of it launch and
+// loads).  Rows come in tiles of 64: a request's T H rows, or, where keys are selected, a token's heads.
 // Row tiles of the same keys may go to a gang of CTAs that take the same key tiles at about the same time, so
 // that a tile comes from memory once and from L2 for the others of the gang: 24 requests of three tokens read
 // 589 MB of 236 MB unique without gangs, their row tiles being dealt to CTAs at unrelated times.  A gang costs
 // CTAs (whole gangs only) and idle members (rows that do not fill it), so the size is chosen by an estimate:
 // time of the longest run of key tiles, or of the tiles' bytes from memory, whichever is longer.
-constexpr int kAtPlanThreads = 256;
-constexpr int kAtPlanNear = 2048;                  // units whose first tiles are kept in shared memory for the searches
 constexpr int kAtGangs = 6;
 constexpr int at_gang(int i) { return i < 4 ? i + 1 : i * 2 - 2; }   // 1, 2, 3, 4, 6, 8
 constexpr float kAtTileNs = 2700.f;                // a key tile on one SM (measured)
 constexpr float kAtTileMemNs = 23.f;               // 147 KB at the memory's measured copy rate
 constexpr int kAtL2Tiles = 400;                    // 59 MB: unique tiles that stay in L2 between row tiles
 
-constexpr size_t at_plan_smem(int B) { return (size_t)(3 * B + 2) * sizeof(int); }
+struct AtRun {
+  int gang, run;         // CTAs a gang, this CTA's gang
+  int beg, end, unit0;   // its key tiles, the unit of the first
+  int prefetch;          // 1: the keys exceed what stays in L2
+  int wrong;             // 1: q_start does not ascend
+};
 
-__global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(const AtArgs p, int max_units, int max_ctas) {
-  extern __shared__ int plan_sm[];
-  int* qs = plan_sm;                 // [B + 1] q_start, kept inside the batch and ascending
+// `sm`: shared memory for 3 B + 2 ints, free again when the call returns.  Every thread of the CTA calls it.
+__device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm) {
+  int* qs = sm;                      // [B + 1] q_start, kept inside the batch
   int* base = qs + p.B + 1;          // [B + 1] first unit of each request
   int* seq = base + p.B + 1;         // [B]
-  __shared__ int warp_tot[32], total, s_max;
-  __shared__ int first_sm[kAtPlanNear];
+  __shared__ int warp_tot[32], total, s_many, s_unit0, s_wrong;
   __shared__ unsigned long long sums[kAtGangs + 1];
-  const int tid = threadIdx.x, B = p.B;
-  griddep_launch_dependents();
-  griddep_wait();                    // the launch may overlap the kernel before; its results (and workspace) not
+  const int tid = threadIdx.x, nthr = blockDim.x, B = p.B, max_ctas = gridDim.x;
   if (tid <= kAtGangs) sums[tid] = 0;
-  if (tid == 0) s_max = 0;
-  for (int b = tid; b < B; b += kAtPlanThreads) {
-    int q0, q1;
-    at_span(p, b, q0, q1);
-    qs[b] = q0;
-    seq[b] = p.seq_len[b];
-    if (b == B - 1) qs[B] = q1;
+  if (tid == 0) s_many = s_unit0 = s_wrong = 0;
+  {
+    const int lo = max(0, min(p.q_start[0], p.n_tokens)), hi = max(lo, min(p.q_start[B], p.n_tokens));
+    for (int b = tid; b <= B; b += nthr) {
+      qs[b] = max(lo, min(p.q_start[b], hi));
+      if (b < B) seq[b] = p.seq_len[b];
+    }
   }
   __syncthreads();
   const int heads = (p.H + kAtRows - 1) / kAtRows;
@@ -155,49 +149,56 @@ __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(co
     n = p.sel ? T : min(T, 1);
     rows = p.sel ? heads : (T * p.H + kAtRows - 1) / kAtRows;          // (n_tokens * H < 2^31 - 64)
   };
-  // a gang is of use where row tiles share keys
-  for (int b = tid; b < B; b += kAtPlanThreads) {
-    int n, rows;
-    groups(b, n, rows);
-    if (n && rows > 1) s_max = 1;
-  }
-  __syncthreads();
-  int gang = 1;
-  if (s_max) {
+  {
     unsigned long long s[kAtGangs + 1] = {};
-    for (int b = tid; b < B; b += kAtPlanThreads) {
+    bool many = false;                                 // a gang is of use where row tiles share keys
+    for (int b = tid; b < B; b += nthr) {
       int n, rows;
       groups(b, n, rows);
       const int keys = max(0, min(seq[b], most));
       const unsigned long long c = (unsigned long long)n * (p.sel ? sel_tiles : max(1, (keys + kAtKeys - 1) / kAtKeys));
+      many |= n && rows > 1;
+      if (qs[b + 1] < qs[b]) s_wrong = 1;              // not ascending: nothing is computed
 #pragma unroll
       for (int g = 0; g < kAtGangs; ++g) s[g] += c * ((rows + at_gang(g) - 1) / at_gang(g));
       s[kAtGangs] += c;
     }
+    many = __any_sync(0xffffffffu, many);
+    if (many && (tid & 31) == 0) s_many = 1;
 #pragma unroll
     for (int g = 0; g <= kAtGangs; ++g) {
+      if (g < kAtGangs && !many) continue;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s[g] += __shfl_xor_sync(0xffffffffu, s[g], o);
       if ((tid & 31) == 0 && s[g]) atomicAdd(&sums[g], s[g]);
     }
-    __syncthreads();
+    // (a warp none of whose requests shares keys adds the same to every sum)
+    if (!many && (tid & 31) == 0 && s[kAtGangs])
+#pragma unroll
+      for (int g = 0; g < kAtGangs; ++g) atomicAdd(&sums[g], s[kAtGangs]);
+  }
+  __syncthreads();
+  AtRun r;
+  r.gang = 1;
+  r.prefetch = sums[kAtGangs] > kAtL2Tiles;
+  if (s_many) {
     float best = INFINITY;
 #pragma unroll
     for (int g = 0; g < kAtGangs; ++g) {
       if (at_gang(g) > max_ctas) continue;
       const float runs = (float)(max_ctas / at_gang(g));
-      const float mem = sums[kAtGangs] <= kAtL2Tiles ? (float)sums[kAtGangs] : (float)sums[g];
+      const float mem = (float)(r.prefetch ? sums[g] : sums[kAtGangs]);
       const float cost = fmaxf(ceilf((float)sums[g] / runs) * kAtTileNs, mem * kAtTileMemNs);
       if (cost < best) {
         best = cost;
-        gang = at_gang(g);
+        r.gang = at_gang(g);
       }
     }
   }
-  const int gang_rows = gang * kAtRows;
+  const int gang = r.gang, gang_rows = gang * kAtRows;
 
   int carry = 0;
-  for (int b0 = 0; b0 < B; b0 += kAtPlanThreads) {
+  for (int b0 = 0; b0 < B; b0 += nthr) {
     const int b = b0 + tid;
     int u = 0;
     if (b < B) {
@@ -210,97 +211,99 @@ __global__ void __launch_bounds__(kAtPlanThreads, 1) kv_attention_plan_kernel(co
     carry += total;
     __syncthreads();
   }
-  const int n_units = min(carry, max_units);       // (more only from a q_start that is not ascending)
-  int tiles = 0;
-  for (int u0 = 0; u0 < n_units; u0 += kAtPlanThreads) {
-    const int u = u0 + tid;
-    int c = 0;
-    AtUnit un{};
-    if (u < n_units) {
-      int l = 0, h = B;                            // last b with base[b] <= u
-      while (h - l > 1) {
-        const int mid = (l + h) >> 1;
-        if (base[mid] <= u) l = mid;
-        else h = mid;
-      }
-      const int q0 = qs[l], q1 = max(q0, qs[l + 1]);
-      un.b = l;
-      un.seq = seq[l];
-      un.shift = un.seq - q1;                      // seq - (q1 - q0) - q0
-      if (p.sel) {
-        const int per = (heads + gang - 1) / gang, i = u - base[l], tok = q0 + i / per;
-        un.row0 = tok * p.H + (i % per) * gang_rows;
-        un.row_end = (tok + 1) * p.H;
-        c = sel_tiles;
-      } else {
-        un.row0 = q0 * p.H + (u - base[l]) * gang_rows;
-        un.row_end = q1 * p.H;
-        const int last_tok = min(un.row_end - 1, un.row0 + gang_rows - 1) / p.H;
-        const long long keys = (long long)un.shift + last_tok + 1;
-        c = (int)(max(0ll, min(keys, (long long)most)) + kAtKeys - 1) / kAtKeys;
-      }
-      c = max(c, 1);                               // a unit without keys still writes its rows
-    }
-    const int e = block_exclusive_scan(c, warp_tot, &total);
-    if (u < n_units) {
-      un.first = tiles + e;
-      un.tiles = c;
-      p.units[u] = un;
-      if (u < kAtPlanNear) first_sm[u] = un.first;
-    }
-    tiles += total;
-    __syncthreads();
-  }
-  const int G = min(max_ctas / gang, tiles);
-  // the unit that holds each run's first tile
-  const bool near = n_units <= kAtPlanNear;
-  auto first_of = [&](int u) { return near ? first_sm[u] : p.units[u].first; };
-  int unit = 0, members = 0;
-  if (tid < G) {
-    const int cut = at_cut(tiles, tid, G);
-    int l = 0, h = n_units;
+  const int n_units = s_wrong ? 0 : carry;
+  r.wrong = s_wrong;
+  auto unit = [&](int u) {
+    int l = 0, h = B;                                  // last b with base[b] <= u
     while (h - l > 1) {
       const int mid = (l + h) >> 1;
-      if (first_of(mid) <= cut) l = mid;
+      if (base[mid] <= u) l = mid;
       else h = mid;
     }
-    unit = l;
-    p.head[4 + tid] = l;
-    const int first = first_of(l);
-    // the first border inside its unit lists the unit's joins
-    if (tid > 0 && first < cut && at_cut(tiles, tid - 1, G) <= first) {
-      const AtUnit un = p.units[unit];
-      members = min(gang, (un.row_end - un.row0 + kAtRows - 1) / kAtRows);
+    AtUnit un;
+    const int q0 = qs[l], q1 = qs[l + 1];
+    un.b = l;
+    un.seq = seq[l];
+    un.shift = un.seq - q1;                            // seq - (q1 - q0) - q0
+    un.pad = un.first = 0;
+    if (p.sel) {
+      const int per = (heads + gang - 1) / gang, i = u - base[l], tok = q0 + i / per;
+      un.row0 = tok * p.H + (i % per) * gang_rows;
+      un.row_end = (tok + 1) * p.H;
+      un.tiles = sel_tiles;
+    } else {
+      un.row0 = q0 * p.H + (u - base[l]) * gang_rows;
+      un.row_end = q1 * p.H;
+      const int last_tok = min(un.row_end - 1, un.row0 + gang_rows - 1) / p.H;
+      const long long keys = (long long)un.shift + last_tok + 1;
+      un.tiles = (int)(max(0ll, min(keys, (long long)most)) + kAtKeys - 1) / kAtKeys;
+      un.tiles = max(un.tiles, 1);                     // a unit without keys still writes its rows
     }
+    return un;
+  };
+  // all key tiles, then the units of this run
+  int W = 0;
+  if (n_units > nthr) {
+    int mine = 0;
+    for (int u = tid; u < n_units; u += nthr) mine += unit(u).tiles;
+    block_exclusive_scan(mine, warp_tot, &total);
+    W = total;
+    __syncthreads();
   }
-  const int at = block_exclusive_scan(members, warp_tot, &total);
-  if (members) {
-    const AtUnit un = p.units[unit];
-    const int last = un.first + un.tiles, run0 = tid - 1;
-    int n = tid;                                   // runs run0 .. n - 1 begin before the unit's end
-    for (int h = G; n < h;) {
-      const int mid = (n + h) >> 1;
-      if (at_cut(tiles, mid, G) < last) n = mid + 1;
-      else h = mid;
+  r.run = blockIdx.x / gang;
+  const int member = blockIdx.x - r.run * gang;
+  int first = 0, G = 0;
+  r.beg = r.end = 0;
+  bool opens = false;
+  for (int u0 = 0; u0 < n_units; u0 += nthr) {
+    const int u = u0 + tid;
+    AtUnit un;
+    un.tiles = 0;
+    if (u < n_units) un = unit(u);
+    const int e = block_exclusive_scan(un.tiles, warp_tot, &total);
+    if (n_units <= nthr) W = total;
+    if (u0 == 0) {
+      G = min(max_ctas / gang, W);
+      if (r.run < G) {
+        r.beg = at_cut(W, r.run, G);
+        r.end = at_cut(W, r.run + 1, G);
+      }
     }
-    for (int m = 0; m < members; ++m) {
-      AtJoin jn{};
-      jn.row0 = un.row0 + m * kAtRows;
-      jn.row_end = min(jn.row0 + kAtRows, un.row_end);
-      jn.cta = run0 * gang + m;
-      jn.gang = gang;
-      jn.parts = n - run0;
-      jn.slot = 2 * jn.cta + (at_cut(tiles, run0, G) < un.first ? 1 : 0);
-      p.joins[at + m] = jn;
+    un.first = first + e;
+    const int last = un.first + un.tiles;
+    if (un.tiles && un.first < r.end && last > r.beg) {
+      p.units[u + r.run] = un;
+      if (un.first <= r.beg) {
+        s_unit0 = u;
+        // a run that begins with the first border inside its unit lists the join of its member's rows
+        const int row0 = un.row0 + member * kAtRows;
+        opens = r.run > 0 && un.first < r.beg && at_cut(W, r.run - 1, G) <= un.first && row0 < un.row_end;
+        if (opens) {
+          int n = r.run;                               // runs run - 1 .. n - 1 begin before the unit's end
+          for (int h = G; n < h;) {
+            const int mid = (n + h) >> 1;
+            if (at_cut(W, mid, G) < last) n = mid + 1;
+            else h = mid;
+          }
+          AtJoin jn;
+          jn.row0 = row0;
+          jn.row_end = min(row0 + kAtRows, un.row_end);
+          jn.cta = (r.run - 1) * gang + member;
+          jn.gang = gang;
+          jn.parts = n - (r.run - 1);
+          jn.slot = 2 * jn.cta + (at_cut(W, r.run - 1, G) < un.first ? 1 : 0);
+          jn.pad[0] = jn.pad[1] = 0;
+          p.joins[blockIdx.x] = jn;
+        }
+      }
     }
+    first += total;
+    __syncthreads();
+    if (first >= r.end && W > 0) break;                // (uniform: the units that follow are other runs')
   }
-  if (tid == 0) {
-    p.head[0] = gang;
-    p.head[1] = G;
-    p.head[2] = tiles;
-    p.head[3] = total;
-    *p.status = 0;
-  }
+  if (!__syncthreads_or(opens) && tid == 0) p.joins[blockIdx.x].parts = 0;
+  r.unit0 = s_unit0;
+  return r;
 }
 
 // ------------------------------------------------------------------ main kernel
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint64_t full[5], empty[4], q_full, q_empty, s_full, p_ready, o_full;
   __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, cta_status;
   __shared__ uint32_t key_ok[2][4];                    // bit i of word w: key 32 w + i of the tile is there
   __shared__ uint32_t key_fin[2][4];                   // bit i of word w of a half: key 32 w + i has a finite score there
   __shared__ __align__(16) float ref[kAtRows], fac[kAtRows], red[4][kAtRows];
@@ -462,15 +465,18 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  griddep_wait();                                      // the plan kernel's lists
   griddep_launch_dependents();
-  const int gang = p.head[0], G = p.head[1], W = p.head[2];
-  const int cta = blockIdx.x, run = cta / gang;
-  const int my_rows = (cta - run * gang) * kAtRows;    // this member's rows of a unit begin there
-  const int beg = run < G ? at_cut(W, run, G) : 0, end = run < G ? at_cut(W, run + 1, G) : 0;
-  const int unit0 = run < G ? p.head[4 + run] : 0;
+  griddep_wait();                                      // the launch may overlap the kernel before; its results not
+  const AtRun plan = at_plan(p, reinterpret_cast<int*>(smem));
+  const int cta = blockIdx.x, beg = plan.beg, end = plan.end, unit0 = plan.unit0;
+  const int my_rows = (cta - plan.run * plan.gang) * kAtRows;    // this member's rows of a unit begin there
+  const AtUnit* units = p.units + plan.run;
+  if (threadIdx.x == 0) cta_status = plan.wrong ? COLI_DEV_KV_TOKENS : 0;
+  // (the plan's use of shared memory ends before the TMA and MMA use of it)
+  fence_proxy_async_smem();
+  __syncthreads();
   auto fail_wait = [&]() {
-    atomicOr(p.status, COLI_DEV_WAIT_TIMEOUT);
+    atomicOr(&cta_status, COLI_DEV_WAIT_TIMEOUT);
     atomicExch(&abort_flag, 1);
   };
 
@@ -481,7 +487,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     int it = 0, un = 0;
     const int n_box = TMA ? kAtKeys / p.box : 0;       // boxes of 64 columns a tile
     for (int at = beg, u = unit0; ok && at < end; ++u) {
-      const AtUnit ut = p.units[u];
+      const AtUnit ut = units[u];
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
       const int row0 = ut.row0 + my_rows;
       if (row0 >= ut.row_end) {                        // this member has no rows of the unit
@@ -519,7 +525,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
         row = 0;
         if (key[j] < 0 || key[j] >= seen) return false;
         if (page[j] < 0 || page[j] >= p.d.n_pages) {
-          atomicOr(p.status, COLI_DEV_KV_BAD_PAGE);
+          atomicOr(&cta_status, COLI_DEV_KV_BAD_PAGE);
           return false;
         }
         row = (long long)page[j] * p.rows_per_page + key[j] % p.d.page_size;
@@ -631,7 +637,8 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
             key[j] = next[j];
           }
           // the next tile is on its way to L2 while this one is worked on (its place in shared memory is taken)
-          if constexpr (TMA) {
+          if (!plan.prefetch) {
+          } else if constexpr (TMA) {
             for (int i = lane; i < kAtBoxes * n_box; i += 32)      // (i and the lane have the same box of rows)
               tma_prefetch_2d(&kmap, (i / n_box) * 64, (int)row[0]);
           } else {
@@ -672,7 +679,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     bool ok = true;
     int it = 0, un = 0;
     for (int at = beg, u = unit0; ok && at < end; ++u) {
-      const AtUnit ut = p.units[u];
+      const AtUnit ut = units[u];
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
       at = ut.first + t1;
       if (ut.row0 + my_rows >= ut.row_end) continue;
@@ -726,7 +733,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     const uint32_t trow = tmem + ((uint32_t)(sp * 32) << 16) + (uint32_t)c0;
     int it = 0, un = 0;
     for (int at = beg, u = unit0; at < end; ++u) {
-      const AtUnit ut = p.units[u];
+      const AtUnit ut = units[u];
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
       at = ut.first + t1;
       const int row0 = ut.row0 + my_rows;
@@ -911,6 +918,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0) p.cta_status[cta] = cta_status;
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
@@ -924,16 +932,32 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
 constexpr int kAtJoinThreads = 512, kAtJoinCtas = 456, kAtJoinFew = 12;
 
 template <bool BF16>
-__global__ void __launch_bounds__(kAtJoinThreads) kv_attention_join_kernel(const AtArgs p) {
+__global__ void __launch_bounds__(kAtJoinThreads) kv_attention_join_kernel(const AtArgs p, int ctas) {
   __shared__ __align__(16) float wgt[kAtMaxCtas][4];
   __shared__ float inv[4];
   __shared__ float4 sums[3][128];
   griddep_launch_dependents();
   griddep_wait();
-  const int n_join = p.head[3];
   const int tid = threadIdx.x, grp = tid >> 7, v = tid & 127, warp = tid >> 5, lane = tid & 31;
+  // the cut units' rows, listed; the main kernel's CTAs' status
+  __shared__ int list[kAtMaxCtas], s_n;
+  if (warp == 0) {
+    int n = 0, bits = 0;
+    for (int c0 = 0; c0 < ctas; c0 += 32) {
+      const bool is = c0 + lane < ctas && p.joins[c0 + lane].parts > 0;
+      if (blockIdx.x == 0 && c0 + lane < ctas) bits |= p.cta_status[c0 + lane];
+      const unsigned m = __ballot_sync(0xffffffffu, is);
+      if (is) list[n + __popc(m & ((1u << lane) - 1u))] = c0 + lane;
+      n += __popc(m);
+    }
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (blockIdx.x == 0 && lane == 0) *p.status = bits;
+    if (lane == 0) s_n = n;
+  }
+  __syncthreads();
+  const int n_join = s_n;
   for (int task = blockIdx.x; task < n_join * 64; task += gridDim.x) {
-    const AtJoin jn = p.joins[task >> 6];
+    const AtJoin jn = p.joins[list[task >> 6]];
     const int n = jn.parts, sub = task & 63;
     const bool few = n <= kAtJoinFew;
     if (few && sub >= 16) continue;
@@ -998,7 +1022,7 @@ __global__ void __launch_bounds__(kAtJoinThreads) kv_attention_join_kernel(const
 // ------------------------------------------------------------------ host side
 
 struct AtWs {
-  size_t head, units, joins, part, part_ml, total;
+  size_t cta_status, units, joins, part, part_ml, total;
   long long max_units;
 };
 
@@ -1014,8 +1038,8 @@ static AtWs at_ws(int B, int n_tokens, int H) {
     off = align_up(off + bytes, 256);
     return o;
   };
-  w.head = take((4 + kAtMaxCtas) * sizeof(int));
-  w.units = take((size_t)w.max_units * sizeof(AtUnit));
+  w.cta_status = take(kAtMaxCtas * sizeof(int32_t));
+  w.units = take((size_t)(w.max_units + kAtMaxCtas) * sizeof(AtUnit));
   w.joins = take((size_t)kAtMaxCtas * sizeof(AtJoin));
   w.part = take((size_t)2 * kAtMaxCtas * kAtPart * sizeof(float));
   w.part_ml = take((size_t)2 * kAtMaxCtas * kAtRows * sizeof(float2));
@@ -1036,20 +1060,15 @@ static CUresult at_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m,
 }
 
 template <bool BF16, bool TMA>
-static cudaError_t at_launch(const AtArgs& a, const CUtensorMap& kmap, const CUtensorMap& qmap, int max_units,
-                             int ctas, cudaStream_t st) {
-  cudaError_t e = cudaSuccess;
-  if (at_plan_smem(a.B) > 32 * 1024)
-    e = cudaFuncSetAttribute(kv_attention_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)at_plan_smem(kAtMaxB));
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(kv_attention_plan_kernel, dim3(1), dim3(kAtPlanThreads), at_plan_smem(a.B), st, a, max_units, ctas);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kv_attention_kernel<BF16, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem);
+static cudaError_t at_launch(const AtArgs& a, const CUtensorMap& kmap, const CUtensorMap& qmap, int ctas,
+                             cudaStream_t st) {
+  static_assert((size_t)(3 * kAtMaxB + 2) * sizeof(int) + 1024 <= kAtSmem, "the plan's arrays");
+  cudaError_t e =
+      cudaFuncSetAttribute(kv_attention_kernel<BF16, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv_attention_kernel<BF16, TMA>, dim3(ctas), dim3(at_threads(TMA)), kAtSmem, st, a, kmap, qmap);
-  if (e != cudaSuccess || ctas < 2) return e;
-  return launch_pdl(kv_attention_join_kernel<BF16>, dim3(kAtJoinCtas), dim3(kAtJoinThreads), 0, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kv_attention_join_kernel<BF16>, dim3(kAtJoinCtas), dim3(kAtJoinThreads), 0, st, a, ctas);
 }
 
 }  // namespace coli
@@ -1142,7 +1161,7 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = reinterpret_cast<int32_t*>(ws);
-  a.head = reinterpret_cast<int*>(ws + w.head);
+  a.cta_status = reinterpret_cast<int32_t*>(ws + w.cta_status);
   a.units = reinterpret_cast<AtUnit*>(ws + w.units);
   a.joins = reinterpret_cast<AtJoin*>(ws + w.joins);
   a.part = reinterpret_cast<float*>(ws + w.part);
@@ -1150,9 +1169,8 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   a.wait_ns = kWaitLimitNs;
   const int ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int mu = (int)w.max_units;
-  if (tma) ce = bf16 ? at_launch<true, true>(a, kmap, qmap, mu, ctas, st) : at_launch<false, true>(a, kmap, qmap, mu, ctas, st);
-  else ce = bf16 ? at_launch<true, false>(a, kmap, qmap, mu, ctas, st) : at_launch<false, false>(a, kmap, qmap, mu, ctas, st);
+  if (tma) ce = bf16 ? at_launch<true, true>(a, kmap, qmap, ctas, st) : at_launch<false, true>(a, kmap, qmap, ctas, st);
+  else ce = bf16 ? at_launch<true, false>(a, kmap, qmap, ctas, st) : at_launch<false, false>(a, kmap, qmap, ctas, st);
   return ce == cudaSuccess ? COLI_OK : cuda_fail(ce, "kv_attention: launch");
 }
 

@@ -391,6 +391,18 @@ def test_attention_reports_bad_pages(torch_cuda):
     b.check(status=R.BAD_PAGE)
 
 
+def test_attention_refuses_a_wrong_q_start(torch_cuda):
+    """Not ascending: nothing is written and the status says so.  Beyond the batch: the rows that exist are computed."""
+    torch = torch_cuda
+    b = Batch(torch_cuda, [300, 100, 50], [2, 2, 2], 64, 32, seed=15)
+    b.q_start = np.array([0, 4, 2, 6], np.int32)
+    out, z = b.run(status=R.TOKENS)
+    assert (out == 3.0).all() and (z == 3.0).all()
+    b.q_start = np.array([0, 2, 4, 1 << 30], np.int32)
+    out, _ = b.run()
+    assert torch.isfinite(out).all()
+
+
 def test_attention_long_context_and_splits(torch_cuda):
     """One unit cut over every SM, uneven units cut at odd places: against the sum over thirds of the keys in 64 bits."""
     torch = torch_cuda
