@@ -75,6 +75,8 @@ def build(force: bool = False) -> str:
 def lib():
     """Load libcolibri_moe.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:            # every call passes here: no lock once it is loaded
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -165,23 +167,23 @@ def lib():
 
 
 def _ptr(v) -> int | None:
-    if v is None:
-        return None
+    if v is None or type(v) is int:
+        return v
     if isinstance(v, int):
         return v
-    return int(v.data_ptr())
+    return v.data_ptr()
 
 
 def _stream(s) -> int | None:
-    if s is None:
-        return None
+    if s is None or type(s) is int:
+        return s
     if isinstance(s, int):
         return s
-    return int(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _check(rc: int):
-    if rc != COLI_OK:
+    if rc:
         raise ColiError(rc, lib().colibri_moe_last_error().decode(errors="replace"))
 
 

@@ -110,7 +110,7 @@ __device__ __forceinline__ int at_cut(int W, int j, int G) {
 // CTAs (whole gangs only) and idle members (rows that do not fill it), so the size is chosen by an estimate:
 // time of the longest run of key tiles, or of the tiles' bytes from memory, whichever is longer.
 constexpr int kAtGangs = 6;
-constexpr int at_gang(int i) { return i < 4 ? i + 1 : i * 2 - 2; }   // 1, 2, 3, 4, 6, 8
+__host__ __device__ constexpr int at_gang(int i) { return i < 4 ? i + 1 : i * 2 - 2; }   // 1, 2, 3, 4, 6, 8
 constexpr float kAtTileNs = 2700.f;                // a key tile on one SM (measured)
 constexpr float kAtTileMemNs = 23.f;               // 147 KB at the memory's measured copy rate
 constexpr int kAtL2Tiles = 400;                    // 59 MB: unique tiles that stay in L2 between row tiles
@@ -123,17 +123,20 @@ struct AtRun {
 };
 
 // `sm`: shared memory for 3 B + 2 ints, free again when the call returns.  Every thread of the CTA calls it.
-__device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm) {
+// unit_sm receives the run's first unit.  The code runs once a launch, and what it costs is mostly fetching it:
+// loops are kept rolled and each step is written once.
+__device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_sm) {
   int* qs = sm;                      // [B + 1] q_start, kept inside the batch
   int* base = qs + p.B + 1;          // [B + 1] first unit of each request
   int* seq = base + p.B + 1;         // [B]
-  __shared__ int warp_tot[32], total, s_many, s_unit0, s_wrong;
-  __shared__ unsigned long long sums[kAtGangs + 1];
+  __shared__ int warp_tot[32], total, s_unit0, s_flags[2];
+  __shared__ unsigned sums[kAtGangs + 1];
   const int tid = threadIdx.x, nthr = blockDim.x, B = p.B, max_ctas = gridDim.x;
   if (tid <= kAtGangs) sums[tid] = 0;
-  if (tid == 0) s_many = s_unit0 = s_wrong = 0;
+  if (tid < 2) s_flags[tid] = 0;
   {
     const int lo = max(0, min(p.q_start[0], p.n_tokens)), hi = max(lo, min(p.q_start[B], p.n_tokens));
+#pragma unroll 1
     for (int b = tid; b <= B; b += nthr) {
       qs[b] = max(lo, min(p.q_start[b], hi));
       if (b < B) seq[b] = p.seq_len[b];
@@ -143,52 +146,49 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm) {
   const int heads = (p.H + kAtRows - 1) / kAtRows;
   const int most = p.d.max_pages * p.d.page_size;      // (at most 2^31 - 1: checked by the host)
   const int sel_tiles = (p.topk + kAtKeys - 1) / kAtKeys;
-  // row tiles over the same keys (a row tile group) and how many such groups a request has
-  auto groups = [&](int b, int& n, int& rows) {
-    const int T = max(0, qs[b + 1] - qs[b]);
-    n = p.sel ? T : min(T, 1);
-    rows = p.sel ? heads : (T * p.H + kAtRows - 1) / kAtRows;          // (n_tokens * H < 2^31 - 64)
+  // Requests: row tiles over the same keys (a row tile group), how many such groups, key tiles of each.  Sums of
+  // key tiles stay below 2^31 (checked by the host).
+  struct Req {
+    int n, rows;
+    unsigned tiles;
   };
-  {
-    unsigned long long s[kAtGangs + 1] = {};
-    bool many = false;                                 // a gang is of use where row tiles share keys
-    for (int b = tid; b < B; b += nthr) {
-      int n, rows;
-      groups(b, n, rows);
-      const int keys = max(0, min(seq[b], most));
-      const unsigned long long c = (unsigned long long)n * (p.sel ? sel_tiles : max(1, (keys + kAtKeys - 1) / kAtKeys));
-      many |= n && rows > 1;
-      if (qs[b + 1] < qs[b]) s_wrong = 1;              // not ascending: nothing is computed
-#pragma unroll
-      for (int g = 0; g < kAtGangs; ++g) s[g] += c * ((rows + at_gang(g) - 1) / at_gang(g));
-      s[kAtGangs] += c;
+  auto request = [&](int b) {
+    Req r;
+    const int T = max(0, qs[b + 1] - qs[b]);
+    r.n = p.sel ? T : min(T, 1);
+    r.rows = p.sel ? heads : (T * p.H + kAtRows - 1) / kAtRows;        // (n_tokens * H < 2^31 - 64)
+    const int keys = max(0, min(seq[b], most));
+    r.tiles = (unsigned)r.n * (unsigned)(p.sel ? sel_tiles : max(1, (int)(((unsigned)keys + kAtKeys - 1) / kAtKeys)));
+    return r;
+  };
+#pragma unroll 1
+  for (int b0 = 0; b0 < B; b0 += nthr) {               // (whole warps)
+    const int b = b0 + tid;
+    Req r{0, 0, 0};
+    if (b < B) {
+      r = request(b);
+      if (qs[b + 1] < qs[b]) s_flags[0] = 1;           // not ascending: nothing is computed
+      if (r.n && r.rows > 1) s_flags[1] = 1;           // a gang is of use where row tiles share keys
     }
-    many = __any_sync(0xffffffffu, many);
-    if (many && (tid & 31) == 0) s_many = 1;
-#pragma unroll
+#pragma unroll 1
     for (int g = 0; g <= kAtGangs; ++g) {
-      if (g < kAtGangs && !many) continue;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s[g] += __shfl_xor_sync(0xffffffffu, s[g], o);
-      if ((tid & 31) == 0 && s[g]) atomicAdd(&sums[g], s[g]);
+      const int size = g < kAtGangs ? at_gang(g) : r.rows + 1;
+      const unsigned s = __reduce_add_sync(0xffffffffu, r.tiles * (unsigned)((r.rows + size - 1) / size));
+      if ((tid & 31) == 0 && s) atomicAdd(&sums[g], s);
     }
-    // (a warp none of whose requests shares keys adds the same to every sum)
-    if (!many && (tid & 31) == 0 && s[kAtGangs])
-#pragma unroll
-      for (int g = 0; g < kAtGangs; ++g) atomicAdd(&sums[g], s[kAtGangs]);
   }
   __syncthreads();
   AtRun r;
+  r.wrong = s_flags[0];
   r.gang = 1;
-  r.prefetch = sums[kAtGangs] > kAtL2Tiles;
-  if (s_many) {
+  r.prefetch = sums[kAtGangs] > (unsigned)kAtL2Tiles;
+  if (s_flags[1]) {
     float best = INFINITY;
-#pragma unroll
-    for (int g = 0; g < kAtGangs; ++g) {
-      if (at_gang(g) > max_ctas) continue;
+#pragma unroll 1
+    for (int g = 0; g < kAtGangs && at_gang(g) <= max_ctas; ++g) {
       const float runs = (float)(max_ctas / at_gang(g));
       const float mem = (float)(r.prefetch ? sums[g] : sums[kAtGangs]);
-      const float cost = fmaxf(ceilf((float)sums[g] / runs) * kAtTileNs, mem * kAtTileMemNs);
+      const float cost = fmaxf(ceilf(__fdividef((float)sums[g], runs)) * kAtTileNs, mem * kAtTileMemNs);
       if (cost < best) {
         best = cost;
         r.gang = at_gang(g);
@@ -196,110 +196,103 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm) {
     }
   }
   const int gang = r.gang, gang_rows = gang * kAtRows;
-
-  int carry = 0;
-  for (int b0 = 0; b0 < B; b0 += nthr) {
-    const int b = b0 + tid;
-    int u = 0;
-    if (b < B) {
-      int n, rows;
-      groups(b, n, rows);
-      u = n * ((rows + gang - 1) / gang);
-    }
-    const int e = block_exclusive_scan(u, warp_tot, &total);
-    if (b < B) base[b] = carry + e;
-    carry += total;
-    __syncthreads();
-  }
-  const int n_units = s_wrong ? 0 : carry;
-  r.wrong = s_wrong;
-  auto unit = [&](int u) {
-    int l = 0, h = B;                                  // last b with base[b] <= u
-    while (h - l > 1) {
-      const int mid = (l + h) >> 1;
-      if (base[mid] <= u) l = mid;
-      else h = mid;
-    }
-    AtUnit un;
-    const int q0 = qs[l], q1 = qs[l + 1];
-    un.b = l;
-    un.seq = seq[l];
-    un.shift = un.seq - q1;                            // seq - (q1 - q0) - q0
-    un.pad = un.first = 0;
-    if (p.sel) {
-      const int per = (heads + gang - 1) / gang, i = u - base[l], tok = q0 + i / per;
-      un.row0 = tok * p.H + (i % per) * gang_rows;
-      un.row_end = (tok + 1) * p.H;
-      un.tiles = sel_tiles;
-    } else {
-      un.row0 = q0 * p.H + (u - base[l]) * gang_rows;
-      un.row_end = q1 * p.H;
-      const int last_tok = min(un.row_end - 1, un.row0 + gang_rows - 1) / p.H;
-      const long long keys = (long long)un.shift + last_tok + 1;
-      un.tiles = (int)(max(0ll, min(keys, (long long)most)) + kAtKeys - 1) / kAtKeys;
-      un.tiles = max(un.tiles, 1);                     // a unit without keys still writes its rows
-    }
-    return un;
-  };
-  // all key tiles, then the units of this run
-  int W = 0;
-  if (n_units > nthr) {
-    int mine = 0;
-    for (int u = tid; u < n_units; u += nthr) mine += unit(u).tiles;
-    block_exclusive_scan(mine, warp_tot, &total);
-    W = total;
-    __syncthreads();
-  }
   r.run = blockIdx.x / gang;
   const int member = blockIdx.x - r.run * gang;
-  int first = 0, G = 0;
   r.beg = r.end = 0;
+
+  // Two sums over the CTA's threads share this loop: pass 0, units of each request; pass 1, key tiles of each
+  // unit (only their total, needed where one round does not see every unit); pass 2, the run's own units.
+  int n_units = 0, W = 0, G = 0, n = B;
   bool opens = false;
-  for (int u0 = 0; u0 < n_units; u0 += nthr) {
-    const int u = u0 + tid;
-    AtUnit un;
-    un.tiles = 0;
-    if (u < n_units) un = unit(u);
-    const int e = block_exclusive_scan(un.tiles, warp_tot, &total);
-    if (n_units <= nthr) W = total;
-    if (u0 == 0) {
-      G = min(max_ctas / gang, W);
-      if (r.run < G) {
-        r.beg = at_cut(W, r.run, G);
-        r.end = at_cut(W, r.run + 1, G);
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    int carry = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += nthr) {
+      const int i = i0 + tid;
+      int v = 0;
+      AtUnit un;
+      if (i < n && pass == 0) {
+        const Req q = request(i);
+        v = q.n * ((q.rows + gang - 1) / gang);
+      } else if (i < n) {
+        int l = 0, h = B;                              // last b with base[b] <= i
+#pragma unroll 1
+        while (h - l > 1) {
+          const int mid = (l + h) >> 1;
+          if (base[mid] <= i) l = mid;
+          else h = mid;
+        }
+        const int q0 = qs[l], q1 = qs[l + 1];
+        un.b = l;
+        un.seq = seq[l];
+        un.shift = un.seq - q1;                        // seq - (q1 - q0) - q0
+        un.pad = 0;
+        if (p.sel) {
+          const int per = (heads + gang - 1) / gang, j = i - base[l], tok = q0 + j / per;
+          un.row0 = tok * p.H + (j % per) * gang_rows;
+          un.row_end = (tok + 1) * p.H;
+          v = sel_tiles;
+        } else {
+          un.row0 = q0 * p.H + (i - base[l]) * gang_rows;
+          un.row_end = q1 * p.H;
+          const long long keys = (long long)un.shift + min(un.row_end - 1, un.row0 + gang_rows - 1) / p.H + 1;
+          v = max(1, (int)(((unsigned)max(0ll, min(keys, (long long)most)) + kAtKeys - 1) / kAtKeys));
+        }                                              // (a unit without keys still writes its rows: one tile)
+        un.tiles = v;
       }
-    }
-    un.first = first + e;
-    const int last = un.first + un.tiles;
-    if (un.tiles && un.first < r.end && last > r.beg) {
-      p.units[u + r.run] = un;
-      if (un.first <= r.beg) {
-        s_unit0 = u;
-        // a run that begins with the first border inside its unit lists the join of its member's rows
-        const int row0 = un.row0 + member * kAtRows;
-        opens = r.run > 0 && un.first < r.beg && at_cut(W, r.run - 1, G) <= un.first && row0 < un.row_end;
-        if (opens) {
-          int n = r.run;                               // runs run - 1 .. n - 1 begin before the unit's end
-          for (int h = G; n < h;) {
-            const int mid = (n + h) >> 1;
-            if (at_cut(W, mid, G) < last) n = mid + 1;
-            else h = mid;
+      const int e = carry + block_exclusive_scan(v, warp_tot, &total);
+      carry += total;
+      if (pass == 0 && i < B) base[i] = e;
+      if (pass == 2) {
+        if (i0 == 0) {
+          if (W == 0) W = total;
+          G = min(max_ctas / gang, W);
+          if (r.run < G) {
+            r.beg = at_cut(W, r.run, G);
+            r.end = at_cut(W, r.run + 1, G);
           }
-          AtJoin jn;
-          jn.row0 = row0;
-          jn.row_end = min(row0 + kAtRows, un.row_end);
-          jn.cta = (r.run - 1) * gang + member;
-          jn.gang = gang;
-          jn.parts = n - (r.run - 1);
-          jn.slot = 2 * jn.cta + (at_cut(W, r.run - 1, G) < un.first ? 1 : 0);
-          jn.pad[0] = jn.pad[1] = 0;
-          p.joins[blockIdx.x] = jn;
+        }
+        un.first = e;
+        const int last = e + v;
+        if (v && e < r.end && last > r.beg) {
+          p.units[i + r.run] = un;
+          if (e <= r.beg) {
+            s_unit0 = i;
+            *unit_sm = un;
+            // a run that begins with the first border inside its unit lists the join of its member's rows
+            const int row0 = un.row0 + member * kAtRows;
+            opens = r.run > 0 && e < r.beg && at_cut(W, r.run - 1, G) <= e && row0 < un.row_end;
+            if (opens) {
+              int m = r.run;                           // runs run - 1 .. m - 1 begin before the unit's end
+#pragma unroll 1
+              for (int h = G; m < h;) {
+                const int mid = (m + h) >> 1;
+                if (at_cut(W, mid, G) < last) m = mid + 1;
+                else h = mid;
+              }
+              AtJoin jn;
+              jn.row0 = row0;
+              jn.row_end = min(row0 + kAtRows, un.row_end);
+              jn.cta = (r.run - 1) * gang + member;
+              jn.gang = gang;
+              jn.parts = m - (r.run - 1);
+              jn.slot = 2 * jn.cta + (at_cut(W, r.run - 1, G) < e ? 1 : 0);
+              jn.pad[0] = jn.pad[1] = 0;
+              p.joins[blockIdx.x] = jn;
+            }
+          }
         }
       }
+      __syncthreads();
+      if (pass == 2 && carry >= r.end) break;          // the units that follow are other runs'
     }
-    first += total;
-    __syncthreads();
-    if (first >= r.end && W > 0) break;                // (uniform: the units that follow are other runs')
+    if (pass == 0) {
+      n = n_units = r.wrong ? 0 : carry;
+      if (n_units <= nthr) pass = 1;                   // one round sees every unit: no need of pass 1
+    } else if (pass == 1) {
+      W = carry;
+    }
   }
   if (!__syncthreads_or(opens) && tid == 0) p.joins[blockIdx.x].parts = 0;
   r.unit0 = s_unit0;
@@ -433,6 +426,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   __shared__ uint64_t full[5], empty[4], q_full, q_empty, s_full, p_ready, o_full;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, cta_status;
+  __shared__ AtUnit unit_sm;                           // the run's first unit
   __shared__ uint32_t key_ok[2][4];                    // bit i of word w: key 32 w + i of the tile is there
   __shared__ uint32_t key_fin[2][4];                   // bit i of word w of a half: key 32 w + i has a finite score there
   __shared__ __align__(16) float ref[kAtRows], fac[kAtRows], red[4][kAtRows];
@@ -444,6 +438,10 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_v = &abort_flag;
 
+  if (TMA && warp == 0 && lane == 0) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&qmap);
+  }
   if (threadIdx.x == 0) {
     // copying warps: one arrival a thread, and one a warp for key_ok (with the rotary box)
     for (int i = 0; i < 5; ++i) mbar_init(&full[i], TMA ? 1 : kAtLoadWarps * 32 + (i == 4 ? kAtLoadWarps : 0));
@@ -467,7 +465,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   const uint32_t tmem = tmem_base;
   griddep_launch_dependents();
   griddep_wait();                                      // the launch may overlap the kernel before; its results not
-  const AtRun plan = at_plan(p, reinterpret_cast<int*>(smem));
+  const AtRun plan = at_plan(p, reinterpret_cast<int*>(smem), &unit_sm);
   const int cta = blockIdx.x, beg = plan.beg, end = plan.end, unit0 = plan.unit0;
   const int my_rows = (cta - plan.run * plan.gang) * kAtRows;    // this member's rows of a unit begin there
   const AtUnit* units = p.units + plan.run;
@@ -487,7 +485,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     int it = 0, un = 0;
     const int n_box = TMA ? kAtKeys / p.box : 0;       // boxes of 64 columns a tile
     for (int at = beg, u = unit0; ok && at < end; ++u) {
-      const AtUnit ut = units[u];
+      const AtUnit ut = u == unit0 ? unit_sm : units[u];
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
       const int row0 = ut.row0 + my_rows;
       if (row0 >= ut.row_end) {                        // this member has no rows of the unit
@@ -679,7 +677,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     bool ok = true;
     int it = 0, un = 0;
     for (int at = beg, u = unit0; ok && at < end; ++u) {
-      const AtUnit ut = units[u];
+      const AtUnit ut = u == unit0 ? unit_sm : units[u];
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
       at = ut.first + t1;
       if (ut.row0 + my_rows >= ut.row_end) continue;
@@ -733,7 +731,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     const uint32_t trow = tmem + ((uint32_t)(sp * 32) << 16) + (uint32_t)c0;
     int it = 0, un = 0;
     for (int at = beg, u = unit0; at < end; ++u) {
-      const AtUnit ut = units[u];
+      const AtUnit ut = u == unit0 ? unit_sm : units[u];
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
       at = ut.first + t1;
       const int row0 = ut.row0 + my_rows;
@@ -926,96 +924,123 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
 }
 
 // ------------------------------------------------------------------ join
-// Adds up the parts of every cut unit, in order.  A task is four rows of a unit: 128 values a thread group
-// where the parts are many (four groups take every fourth part each, then meet in shared memory), all 512
-// where they are few.
-constexpr int kAtJoinThreads = 512, kAtJoinCtas = 456, kAtJoinFew = 12;
+// Adds up the parts of every cut unit, in order.  A task is four rows of a unit and 64 values where the parts
+// are many (eight thread groups take every eighth part each, then meet in shared memory), eight rows and all
+// values where they are few.
+constexpr int kAtJoinThreads = 512, kAtJoinCtas = 608, kAtJoinFew = 12, kAtJoinTasks = 128;
 
 template <bool BF16>
 __global__ void __launch_bounds__(kAtJoinThreads) kv_attention_join_kernel(const AtArgs p, int ctas) {
-  __shared__ __align__(16) float wgt[kAtMaxCtas][4];
-  __shared__ float inv[4];
-  __shared__ float4 sums[3][128];
+  __shared__ __align__(16) float wgt[kAtMaxCtas][8];    // a part's reference, then its weight, for each row of the task
+  __shared__ float sum[kAtMaxCtas][8];
+  __shared__ float inv[8];
+  __shared__ float4 meet[7][64];
+  __shared__ int list[kAtMaxCtas], counts[8];
   griddep_launch_dependents();
   griddep_wait();
-  const int tid = threadIdx.x, grp = tid >> 7, v = tid & 127, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the cut units' rows, listed; the main kernel's CTAs' status
-  __shared__ int list[kAtMaxCtas], s_n;
-  if (warp == 0) {
-    int n = 0, bits = 0;
-    for (int c0 = 0; c0 < ctas; c0 += 32) {
-      const bool is = c0 + lane < ctas && p.joins[c0 + lane].parts > 0;
-      if (blockIdx.x == 0 && c0 + lane < ctas) bits |= p.cta_status[c0 + lane];
-      const unsigned m = __ballot_sync(0xffffffffu, is);
-      if (is) list[n + __popc(m & ((1u << lane) - 1u))] = c0 + lane;
-      n += __popc(m);
-    }
-    bits = __reduce_or_sync(0xffffffffu, bits);
-    if (blockIdx.x == 0 && lane == 0) *p.status = bits;
-    if (lane == 0) s_n = n;
+  static_assert(kAtMaxCtas <= 8 * 32, "a thread each");
+  const bool is = tid < ctas && p.joins[tid].parts > 0;
+  const unsigned mask = __ballot_sync(0xffffffffu, is);
+  if (lane == 0 && warp < 8) counts[warp] = __popc(mask);
+  const int bits = __reduce_or_sync(0xffffffffu, blockIdx.x == 0 && tid < ctas ? p.cta_status[tid] : 0);
+  if (blockIdx.x == 0 && lane == 0 && warp < 8) list[warp] = bits;
+  __syncthreads();
+  if (blockIdx.x == 0 && tid == 0) {
+    int all = 0;
+    for (int w = 0; w < 8; ++w) all |= list[w];
+    *p.status = all;
   }
   __syncthreads();
-  const int n_join = s_n;
-  for (int task = blockIdx.x; task < n_join * 64; task += gridDim.x) {
-    const AtJoin jn = p.joins[list[task >> 6]];
-    const int n = jn.parts, sub = task & 63;
+  int n_join = 0, before = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) before += counts[w];
+    n_join += counts[w];
+  }
+  if (is) list[before + __popc(mask & ((1u << lane) - 1u))] = tid;
+  __syncthreads();
+  for (int task = blockIdx.x; task < n_join * kAtJoinTasks; task += gridDim.x) {
+    const AtJoin jn = p.joins[list[task / kAtJoinTasks]];
+    const int n = jn.parts, sub = task % kAtJoinTasks;
     const bool few = n <= kAtJoinFew;
-    if (few && sub >= 16) continue;
-    const int c = (few ? sub : sub >> 2) * 4, rows = jn.row_end - jn.row0 - c;
+    if (few && sub >= 8) continue;
+    const int c = few ? sub * 8 : (sub >> 3) * 4, rows = jn.row_end - jn.row0 - c, nr = few ? 8 : 4;
     if (rows <= 0) continue;
     auto slot = [&](int i) { return (size_t)(i ? 2 * (jn.cta + i * jn.gang) : jn.slot); };
     __syncthreads();                                    // the previous task's weights are read
-    if (warp < 4) {                                     // warp w: the parts' weights for row c + w
+    for (int i = tid; i < n * nr; i += kAtJoinThreads) {
+      const int part = i / nr, r = i % nr;
+      const float2 ml = p.part_ml[slot(part) * kAtRows + c + r];
+      wgt[part][r] = ml.x;
+      sum[part][r] = ml.y;
+    }
+    __syncthreads();
+    if (warp < nr) {                                    // warp w: the parts' weights for row c + w
       float m = kAtUnset;
-      for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_ml[slot(i) * kAtRows + c + warp].x);
+      for (int i = lane; i < n; i += 32) m = fmaxf(m, wgt[i][warp]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       float l = 0.f;
       for (int i = lane; i < n; i += 32) {
-        const float2 ml = p.part_ml[slot(i) * kAtRows + c + warp];
-        const float w = at_exp2(ml.x - m);
+        const float w = at_exp2(wgt[i][warp] - m);
         wgt[i][warp] = w;
-        l += w * ml.y;
+        l += w * sum[i][warp];
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       if (lane == 0) {
         inv[warp] = l == 0.f ? 0.f : 1.0f / l;
-        if (p.lse && warp < rows && (few || (sub & 3) == 0))
+        if (p.lse && warp < rows && (few || (sub & 7) == 0))
           p.lse[jn.row0 + c + warp] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
       }
     }
-    const int val = (few ? grp : sub & 3) * 128 + v;    // value of the row
-    const float* src = p.part + at_part(c, val);
     __syncthreads();
+    auto add = [](float4& a, const float4 w, const float4 o) {
+      a.x = fmaf(w.x, o.x, a.x);
+      a.y = fmaf(w.y, o.y, a.y);
+      a.z = fmaf(w.z, o.z, a.z);
+      a.w = fmaf(w.w, o.w, a.w);
+    };
+    auto write = [&](const float4 a, int r0, int val) { // rows c + r0 .. + 3
+      const float r[4] = {a.x * inv[r0], a.y * inv[r0 + 1], a.z * inv[r0 + 2], a.w * inv[r0 + 3]};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (r0 + i < rows) p.out[(size_t)(jn.row0 + c + r0 + i) * kAtV + val] = (uint16_t)at_pack<BF16>(r[i], 0.f);
+    };
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int step = few ? 1 : 4;
+    if (few) {
+      float4 acc2 = acc;
+      const float* src = p.part + at_part(c, tid);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float* s = src + slot(i) * kAtPart;
+        const float4 o = *reinterpret_cast<const float4*>(s);
+        const float4 o2 = *reinterpret_cast<const float4*>(s + at_part(4, 0));
+        add(acc, *reinterpret_cast<const float4*>(&wgt[i][0]), o);
+        add(acc2, *reinterpret_cast<const float4*>(&wgt[i][4]), o2);
+      }
+      write(acc, 0, tid);
+      write(acc2, 4, tid);
+    } else {
+      const int grp = tid >> 6, v = tid & 63, val = (sub & 7) * 64 + v;
+      const float* src = p.part + at_part(c, val);
 #pragma unroll 8
-    for (int i = few ? 0 : grp; i < n; i += step) {
-      const float4 o = *reinterpret_cast<const float4*>(src + slot(i) * kAtPart);
-      const float4 w = *reinterpret_cast<const float4*>(wgt[i]);
-      acc.x = fmaf(w.x, o.x, acc.x);
-      acc.y = fmaf(w.y, o.y, acc.y);
-      acc.z = fmaf(w.z, o.z, acc.z);
-      acc.w = fmaf(w.w, o.w, acc.w);
-    }
-    if (!few) {
-      if (grp) sums[grp - 1][v] = acc;
+      for (int i = grp; i < n; i += 8)
+        add(acc, *reinterpret_cast<const float4*>(&wgt[i][0]), *reinterpret_cast<const float4*>(src + slot(i) * kAtPart));
+      if (grp) meet[grp - 1][v] = acc;
       __syncthreads();
       if (grp) continue;
 #pragma unroll
-      for (int g = 0; g < 3; ++g) {
-        const float4 o = sums[g][v];
+      for (int g = 0; g < 7; ++g) {
+        const float4 o = meet[g][v];
         acc.x += o.x;
         acc.y += o.y;
         acc.z += o.z;
         acc.w += o.w;
       }
+      write(acc, 0, val);
     }
-    const float r[4] = {acc.x * inv[0], acc.y * inv[1], acc.z * inv[2], acc.w * inv[3]};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < rows) p.out[(size_t)(jn.row0 + c + i) * kAtV + val] = (uint16_t)at_pack<BF16>(r[i], 0.f);
   }
 }
 
