@@ -71,12 +71,32 @@ struct __align__(16) AtJoin {
   int pad[2];
 };
 
+// Division of 0 <= x < 2^31 by a divisor known at the launch, as a multiplication and two shifts (Granlund and
+// Montgomery 1994): the loader divides on its way to every tile.
+struct FastDiv {
+  unsigned mul, s1, s2;
+  int d;
+  void set(int div) {
+    d = div;
+    int l = 0;
+    while ((1ll << l) < div) ++l;
+    mul = (unsigned)((((1ull << l) - (unsigned)div) << 32) / (unsigned)div + 1);
+    s1 = l < 1 ? l : 1;
+    s2 = l < 1 ? 0 : l - 1;
+  }
+  __device__ __forceinline__ int operator()(int x) const {
+    const unsigned t = __umulhi(mul, (unsigned)x);
+    return (int)((t + (((unsigned)x - t) >> s1)) >> s2);
+  }
+};
+
 struct AtArgs {
   coli_kv_desc d;
+  FastDiv by_page, by_heads;         // page_size, H
   int B, n_tokens, H, topk;
   float scale_log2;
   int rows_per_page;                 // cached rows from a page to the next (page_stride / 576)
-  int box;                           // TMA loads: key rows of a box (divides the page size and 128)
+  int box, box_log2;                 // TMA loads: key rows of a box (a power of two, divides the page size and 128)
   long long q_tok, q_head;           // query strides, bytes
   const uint8_t *q, *cache;
   const int32_t *table, *q_start, *seq_len, *sel;
@@ -95,11 +115,14 @@ struct AtArgs {
 // the main kernel holds many rows of one value, so neighbouring values of four rows lie together.
 __host__ __device__ constexpr int at_part(int c, int v) { return ((c >> 2) * kAtV + v) * 4; }
 
-// Border j of G <= kAtMaxCtas equal runs of the W key tiles: floor(W j / G) without leaving 32 bits.
-__device__ __forceinline__ int at_cut(int W, int j, int G) {
-  const int q = W / G;
-  return q * j + (W - q * G) * j / G;
-}
+// Borders of G <= kAtMaxCtas equal runs of the W key tiles: floor(W j / G), without leaving 32 bits.  The
+// remainder's part is below kAtMaxCtas^2, where the fp32 quotient of x + 1/2 is exact.
+struct AtCuts {
+  int q, r;
+  float inv;
+  __device__ __forceinline__ AtCuts(int W, int G) : q(W / G), r(W - q * G), inv(1.0f / (float)G) {}
+  __device__ __forceinline__ int operator()(int j) const { return q * j + (int)(((float)(r * j) + 0.5f) * inv); }
+};
 
 // ------------------------------------------------------------------ plan
 // Every CTA finds its own run of the work from the lengths (a kernel of its own took 7 us, most of it launch and
@@ -161,21 +184,25 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
     r.tiles = (unsigned)r.n * (unsigned)(p.sel ? sel_tiles : max(1, (int)(((unsigned)keys + kAtKeys - 1) / kAtKeys)));
     return r;
   };
+  // eight threads a request: one for each gang size, one for the unique key tiles, one idle
+  {
+    const int g = tid & 7, size = g < kAtGangs ? at_gang(g) : 1 << 30;
+    const unsigned third = size == 3 ? 0x55555556u : 0x2AAAAAABu;      // of x < 2^31: x / 3, x / 6
+    unsigned s = 0;
+    bool down = false, many = false;
 #pragma unroll 1
-  for (int b0 = 0; b0 < B; b0 += nthr) {               // (whole warps)
-    const int b = b0 + tid;
-    Req r{0, 0, 0};
-    if (b < B) {
-      r = request(b);
-      if (qs[b + 1] < qs[b]) s_flags[0] = 1;           // not ascending: nothing is computed
-      if (r.n && r.rows > 1) s_flags[1] = 1;           // a gang is of use where row tiles share keys
+    for (int b = tid >> 3; b < B; b += nthr >> 3) {
+      const Req q = request(b);
+      down |= qs[b + 1] < qs[b];                       // not ascending: nothing is computed
+      many |= q.n && q.rows > 1;                       // a gang is of use where row tiles share keys
+      const unsigned x = (unsigned)(q.rows + size - 1);
+      s += q.tiles * (g >= kAtGangs ? 1u : (size == 3 || size == 6) ? __umulhi(x, third) : x >> (31 - __clz(size)));
     }
-#pragma unroll 1
-    for (int g = 0; g <= kAtGangs; ++g) {
-      const int size = g < kAtGangs ? at_gang(g) : r.rows + 1;
-      const unsigned s = __reduce_add_sync(0xffffffffu, r.tiles * (unsigned)((r.rows + size - 1) / size));
-      if ((tid & 31) == 0 && s) atomicAdd(&sums[g], s);
-    }
+    s += __shfl_xor_sync(0xffffffffu, s, 8);
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    if ((tid & 31) <= kAtGangs && s) atomicAdd(&sums[tid & 7], s);
+    if (down) s_flags[0] = 1;
+    if (many) s_flags[1] = 1;
   }
   __syncthreads();
   AtRun r;
@@ -202,7 +229,7 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
 
   // Two sums over the CTA's threads share this loop: pass 0, units of each request; pass 1, key tiles of each
   // unit (only their total, needed where one round does not see every unit); pass 2, the run's own units.
-  int n_units = 0, W = 0, G = 0, n = B;
+  int n_units = 0, W = 0, G = 0, n = B, before = 0;   // before: where the run before this one begins
   bool opens = false;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
@@ -214,7 +241,7 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
       AtUnit un;
       if (i < n && pass == 0) {
         const Req q = request(i);
-        v = q.n * ((q.rows + gang - 1) / gang);
+        v = q.n * (gang == 1 ? q.rows : (q.rows + gang - 1) / gang);
       } else if (i < n) {
         int l = 0, h = B;                              // last b with base[b] <= i
 #pragma unroll 1
@@ -229,14 +256,14 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
         un.shift = un.seq - q1;                        // seq - (q1 - q0) - q0
         un.pad = 0;
         if (p.sel) {
-          const int per = (heads + gang - 1) / gang, j = i - base[l], tok = q0 + j / per;
-          un.row0 = tok * p.H + (j % per) * gang_rows;
+          const int per = (heads + gang - 1) / gang, j = i - base[l], tok = q0 + (per == 1 ? j : j / per);
+          un.row0 = tok * p.H + (per == 1 ? 0 : j % per) * gang_rows;
           un.row_end = (tok + 1) * p.H;
           v = sel_tiles;
         } else {
           un.row0 = q0 * p.H + (i - base[l]) * gang_rows;
           un.row_end = q1 * p.H;
-          const long long keys = (long long)un.shift + min(un.row_end - 1, un.row0 + gang_rows - 1) / p.H + 1;
+          const long long keys = (long long)un.shift + p.by_heads(min(un.row_end - 1, un.row0 + gang_rows - 1)) + 1;
           v = max(1, (int)(((unsigned)max(0ll, min(keys, (long long)most)) + kAtKeys - 1) / kAtKeys));
         }                                              // (a unit without keys still writes its rows: one tile)
         un.tiles = v;
@@ -249,8 +276,10 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
           if (W == 0) W = total;
           G = min(max_ctas / gang, W);
           if (r.run < G) {
-            r.beg = at_cut(W, r.run, G);
-            r.end = at_cut(W, r.run + 1, G);
+            const AtCuts cut(W, G);
+            before = r.run > 0 ? cut(r.run - 1) : 0;
+            r.beg = cut(r.run);
+            r.end = cut(r.run + 1);
           }
         }
         un.first = e;
@@ -262,13 +291,14 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
             *unit_sm = un;
             // a run that begins with the first border inside its unit lists the join of its member's rows
             const int row0 = un.row0 + member * kAtRows;
-            opens = r.run > 0 && e < r.beg && at_cut(W, r.run - 1, G) <= e && row0 < un.row_end;
+            opens = r.run > 0 && e < r.beg && before <= e && row0 < un.row_end;
             if (opens) {
+              const AtCuts cut(W, G);
               int m = r.run;                           // runs run - 1 .. m - 1 begin before the unit's end
 #pragma unroll 1
               for (int h = G; m < h;) {
                 const int mid = (m + h) >> 1;
-                if (at_cut(W, mid, G) < last) m = mid + 1;
+                if (cut(mid) < last) m = mid + 1;
                 else h = mid;
               }
               AtJoin jn;
@@ -277,7 +307,7 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
               jn.cta = (r.run - 1) * gang + member;
               jn.gang = gang;
               jn.parts = m - (r.run - 1);
-              jn.slot = 2 * jn.cta + (at_cut(W, r.run - 1, G) < e ? 1 : 0);
+              jn.slot = 2 * jn.cta + (before < e ? 1 : 0);
               jn.pad[0] = jn.pad[1] = 0;
               p.joins[blockIdx.x] = jn;
             }
@@ -483,7 +513,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     const int lw = warp == 0 ? 0 : warp - kAtFirstLoad + 1;           // copying: this warp's keys of a tile start at 32 kAtLaneKeys lw
     bool ok = true;
     int it = 0, un = 0;
-    const int n_box = TMA ? kAtKeys / p.box : 0;       // boxes of 64 columns a tile
+    const int n_box = TMA ? kAtKeys >> p.box_log2 : 0;       // boxes of 64 columns a tile
     for (int at = beg, u = unit0; ok && at < end; ++u) {
       const AtUnit ut = u == unit0 ? unit_sm : units[u];
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
@@ -492,7 +522,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
         at = ut.first + t1;
         continue;
       }
-      const int tok = row0 / p.H;
+      const int tok = p.by_heads(row0);
       const int seen = p.sel ? min(ut.seq, ut.shift + tok + 1) : ut.seq;   // keys before this are there
       const int32_t* table = p.table + (size_t)ut.b * p.d.max_pages;
       const int32_t* sel = p.sel + (size_t)tok * p.topk;
@@ -514,7 +544,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       auto find_page = [&]() {
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
-          const int col = key[j] / p.d.page_size;
+          const int col = p.by_page(max(key[j], 0));
           page[j] = key[j] >= 0 && key[j] < seen && col < p.d.max_pages ? table[col] : -1;
         }
       };
@@ -526,7 +556,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
           atomicOr(&cta_status, COLI_DEV_KV_BAD_PAGE);
           return false;
         }
-        row = (long long)page[j] * p.rows_per_page + key[j] % p.d.page_size;
+        row = (long long)page[j] * p.rows_per_page + (key[j] - p.by_page(key[j]) * p.d.page_size);
         return true;
       };
       long long row[kRows];
@@ -550,7 +580,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
         for (int i = 0; i < kAtRows / (4 * kAtLoadWarps); ++i) {
           const int r = (i * kAtLoadWarps + lw) * 4 + (lane >> 3);
           const int gr = min(row0 + r, ut.row_end - 1);
-          const uint8_t* src = p.q + (gr / p.H) * p.q_tok + (gr % p.H) * p.q_head + c * 16;
+          const uint8_t* src = p.q + p.by_heads(gr) * p.q_tok + (gr - p.by_heads(gr) * p.H) * p.q_head + c * 16;
           uint8_t* dst = qs + r * 128 + ((c ^ (r & 7)) << 4);
 #pragma unroll
           for (int x = 0; x < kAtBoxes; ++x) copy16(dst + x * kAtQBoxBytes, src + x * 128);
@@ -568,7 +598,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
           if (lane < 4) {
 #pragma unroll 1
             for (int i = 0; i < 32; i += per)
-              if ((boxes >> ((lane * 32 + i) / p.box)) & 1u) mine[0] |= (per == 32 ? 0xffffffffu : ((1u << per) - 1u) << i);
+              if ((boxes >> ((lane * 32 + i) >> p.box_log2)) & 1u) mine[0] |= (per == 32 ? 0xffffffffu : ((1u << per) - 1u) << i);
             const int left = seen - (t * kAtKeys + lane * 32);
             if (left < 32) mine[0] &= left <= 0 ? 0u : (1u << left) - 1u;
           }
@@ -638,7 +668,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
           if (!plan.prefetch) {
           } else if constexpr (TMA) {
             for (int i = lane; i < kAtBoxes * n_box; i += 32)      // (i and the lane have the same box of rows)
-              tma_prefetch_2d(&kmap, (i / n_box) * 64, (int)row[0]);
+              tma_prefetch_2d(&kmap, (i >> (7 - p.box_log2)) * 64, (int)row[0]);
           } else {
 #pragma unroll
             for (int j = 0; j < kRows; ++j)
@@ -739,11 +769,11 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       const bool whole = t0 == 0 && t1 == ut.tiles;
       const int slot = 2 * cta + (u == unit0 ? 0 : 1);
       if (id < kAtRows) {
-        lim[id] = p.sel ? 0x7fffffff : ut.shift + min(row0 + id, ut.row_end - 1) / p.H;
+        lim[id] = p.sel ? 0x7fffffff : ut.shift + p.by_heads(min(row0 + id, ut.row_end - 1));
         ref[id] = 0.f;
         has_ref[id] = 0;
       }
-      const int seen_all = ut.shift + row0 / p.H;      // every row sees the keys up to this one
+      const int seen_all = ut.shift + p.by_heads(row0);      // every row sees the keys up to this one
       float l[kAtHalf];
 #pragma unroll
       for (int c = 0; c < kAtHalf; ++c) l[c] = 0.f;
@@ -924,59 +954,97 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
 }
 
 // ------------------------------------------------------------------ join
-// Adds up the parts of every cut unit, in order.  A task is four rows of a unit and 64 values where the parts
-// are many (eight thread groups take every eighth part each, then meet in shared memory), eight rows and all
-// values where they are few.
-constexpr int kAtJoinThreads = 512, kAtJoinCtas = 608, kAtJoinFew = 12, kAtJoinTasks = 128;
+// Adds up the parts of every cut unit, in order.  A task is four rows of a unit: 64 values where the parts are
+// many (eight thread groups take every eighth part each, then meet in shared memory), all 512 where they are
+// few (every thread then finds the parts' weights by itself, while its values are on the way).
+constexpr int kAtJoinThreads = 512, kAtJoinCtas = 304, kAtJoinFew = 8;
+__host__ __device__ constexpr int at_join_tasks(int parts) { return parts <= 0 ? 0 : parts <= kAtJoinFew ? 16 : 128; }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kAtJoinThreads) kv_attention_join_kernel(const AtArgs p, int ctas) {
-  __shared__ __align__(16) float wgt[kAtMaxCtas][8];    // a part's reference, then its weight, for each row of the task
-  __shared__ float sum[kAtMaxCtas][8];
-  __shared__ float inv[8];
+__global__ void __launch_bounds__(kAtJoinThreads, 2) kv_attention_join_kernel(const AtArgs p, int ctas) {
+  __shared__ __align__(16) float wgt[kAtMaxCtas][4];    // a part's reference, then its weight, for each row of the task
+  __shared__ float sum[kAtMaxCtas][4];
+  __shared__ float inv[4];
   __shared__ float4 meet[7][64];
-  __shared__ int list[kAtMaxCtas], counts[8];
+  __shared__ int starts[8 * 32 + 1], warp_tot[32], total;  // first task of each CTA's join
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the cut units' rows, listed; the main kernel's CTAs' status
   static_assert(kAtMaxCtas <= 8 * 32, "a thread each");
-  const bool is = tid < ctas && p.joins[tid].parts > 0;
-  const unsigned mask = __ballot_sync(0xffffffffu, is);
-  if (lane == 0 && warp < 8) counts[warp] = __popc(mask);
-  const int bits = __reduce_or_sync(0xffffffffu, blockIdx.x == 0 && tid < ctas ? p.cta_status[tid] : 0);
-  if (blockIdx.x == 0 && lane == 0 && warp < 8) list[warp] = bits;
-  __syncthreads();
-  if (blockIdx.x == 0 && tid == 0) {
-    int all = 0;
-    for (int w = 0; w < 8; ++w) all |= list[w];
-    *p.status = all;
+  const int parts = tid < ctas ? p.joins[tid].parts : 0;
+  const int bits = blockIdx.x == 0 && tid < ctas ? p.cta_status[tid] : 0;
+  const int start = block_exclusive_scan(at_join_tasks(parts), warp_tot, &total);
+  if (tid < 8 * 32) starts[tid] = start;
+  if (blockIdx.x == 0) {
+    const int timed = __syncthreads_or(bits & COLI_DEV_WAIT_TIMEOUT), page = __syncthreads_or(bits & COLI_DEV_KV_BAD_PAGE);
+    const int order = __syncthreads_or(bits & COLI_DEV_KV_TOKENS);
+    if (tid == 0)
+      *p.status = (timed ? COLI_DEV_WAIT_TIMEOUT : 0) | (page ? COLI_DEV_KV_BAD_PAGE : 0) | (order ? COLI_DEV_KV_TOKENS : 0);
   }
   __syncthreads();
-  int n_join = 0, before = 0;
-  for (int w = 0; w < 8; ++w) {
-    if (w < warp) before += counts[w];
-    n_join += counts[w];
-  }
-  if (is) list[before + __popc(mask & ((1u << lane) - 1u))] = tid;
-  __syncthreads();
-  for (int task = blockIdx.x; task < n_join * kAtJoinTasks; task += gridDim.x) {
-    const AtJoin jn = p.joins[list[task / kAtJoinTasks]];
-    const int n = jn.parts, sub = task % kAtJoinTasks;
+  const int n_tasks = total;
+  for (int task = blockIdx.x; task < n_tasks; task += gridDim.x) {
+    int j = 0, h = 8 * 32;                              // last CTA whose join starts at or before the task
+    while (h - j > 1) {
+      const int mid = (j + h) >> 1;
+      if (starts[mid] <= task) j = mid;
+      else h = mid;
+    }
+    const AtJoin jn = p.joins[j];
+    const int sub = task - starts[j];
+    const int n = jn.parts;
     const bool few = n <= kAtJoinFew;
-    if (few && sub >= 8) continue;
-    const int c = few ? sub * 8 : (sub >> 3) * 4, rows = jn.row_end - jn.row0 - c, nr = few ? 8 : 4;
+    const int c = (few ? sub : sub >> 3) * 4, rows = jn.row_end - jn.row0 - c;
     if (rows <= 0) continue;
     auto slot = [&](int i) { return (size_t)(i ? 2 * (jn.cta + i * jn.gang) : jn.slot); };
+    auto add = [](float4& a, const float4 w, const float4 o) {
+      a.x = fmaf(w.x, o.x, a.x);
+      a.y = fmaf(w.y, o.y, a.y);
+      a.z = fmaf(w.z, o.z, a.z);
+      a.w = fmaf(w.w, o.w, a.w);
+    };
+    auto write = [&](const float4 a, const float4 by, int val) {
+      const float r[4] = {a.x * by.x, a.y * by.y, a.z * by.z, a.w * by.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < rows) p.out[(size_t)(jn.row0 + c + i) * kAtV + val] = (uint16_t)at_pack<BF16>(r[i], 0.f);
+    };
+    auto lse = [&](float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f; };
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (few) {
+      // references and sums of rows c, c + 1 and c + 2, c + 3 of a part
+      const float* src = p.part + at_part(c, tid);
+      float4 m = make_float4(kAtUnset, kAtUnset, kAtUnset, kAtUnset), l = acc;
+#pragma unroll 2
+      for (int i = 0; i < n; ++i) {
+        const float4* ml = reinterpret_cast<const float4*>(p.part_ml + slot(i) * kAtRows + c);
+        const float4 a = ml[0], b = ml[1];
+        const float4 o = *reinterpret_cast<const float4*>(src + slot(i) * kAtPart);
+        // the sums so far move to the larger reference
+        const float4 top = make_float4(fmaxf(m.x, a.x), fmaxf(m.y, a.z), fmaxf(m.z, b.x), fmaxf(m.w, b.z));
+        const float4 old = make_float4(at_exp2(m.x - top.x), at_exp2(m.y - top.y), at_exp2(m.z - top.z), at_exp2(m.w - top.w));
+        const float4 w = make_float4(at_exp2(a.x - top.x), at_exp2(a.z - top.y), at_exp2(b.x - top.z), at_exp2(b.z - top.w));
+        acc = make_float4(acc.x * old.x, acc.y * old.y, acc.z * old.z, acc.w * old.w);
+        l = make_float4(l.x * old.x, l.y * old.y, l.z * old.z, l.w * old.w);
+        add(acc, w, o);
+        add(l, w, make_float4(a.y, a.w, b.y, b.w));
+        m = top;
+      }
+      write(acc, make_float4(l.x == 0.f ? 0.f : 1.0f / l.x, l.y == 0.f ? 0.f : 1.0f / l.y, l.z == 0.f ? 0.f : 1.0f / l.z,
+                             l.w == 0.f ? 0.f : 1.0f / l.w), tid);
+      if (p.lse && tid < 4 && tid < rows)
+        p.lse[jn.row0 + c + tid] = tid == 0 ? lse(m.x, l.x) : tid == 1 ? lse(m.y, l.y) : tid == 2 ? lse(m.z, l.z) : lse(m.w, l.w);
+      continue;
+    }
     __syncthreads();                                    // the previous task's weights are read
-    for (int i = tid; i < n * nr; i += kAtJoinThreads) {
-      const int part = i / nr, r = i % nr;
-      const float2 ml = p.part_ml[slot(part) * kAtRows + c + r];
-      wgt[part][r] = ml.x;
-      sum[part][r] = ml.y;
+    for (int i = tid; i < n * 4; i += kAtJoinThreads) {
+      const float2 ml = p.part_ml[slot(i >> 2) * kAtRows + c + (i & 3)];
+      wgt[i >> 2][i & 3] = ml.x;
+      sum[i >> 2][i & 3] = ml.y;
     }
     __syncthreads();
-    if (warp < nr) {                                    // warp w: the parts' weights for row c + w
+    if (warp < 4) {                                     // warp w: the parts' weights for row c + w
       float m = kAtUnset;
       for (int i = lane; i < n; i += 32) m = fmaxf(m, wgt[i][warp]);
 #pragma unroll
@@ -991,56 +1059,21 @@ __global__ void __launch_bounds__(kAtJoinThreads) kv_attention_join_kernel(const
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       if (lane == 0) {
         inv[warp] = l == 0.f ? 0.f : 1.0f / l;
-        if (p.lse && warp < rows && (few || (sub & 7) == 0))
-          p.lse[jn.row0 + c + warp] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+        if (p.lse && warp < rows && (sub & 7) == 0) p.lse[jn.row0 + c + warp] = lse(m, l);
       }
     }
     __syncthreads();
-    auto add = [](float4& a, const float4 w, const float4 o) {
-      a.x = fmaf(w.x, o.x, a.x);
-      a.y = fmaf(w.y, o.y, a.y);
-      a.z = fmaf(w.z, o.z, a.z);
-      a.w = fmaf(w.w, o.w, a.w);
-    };
-    auto write = [&](const float4 a, int r0, int val) { // rows c + r0 .. + 3
-      const float r[4] = {a.x * inv[r0], a.y * inv[r0 + 1], a.z * inv[r0 + 2], a.w * inv[r0 + 3]};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (r0 + i < rows) p.out[(size_t)(jn.row0 + c + r0 + i) * kAtV + val] = (uint16_t)at_pack<BF16>(r[i], 0.f);
-    };
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (few) {
-      float4 acc2 = acc;
-      const float* src = p.part + at_part(c, tid);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const float* s = src + slot(i) * kAtPart;
-        const float4 o = *reinterpret_cast<const float4*>(s);
-        const float4 o2 = *reinterpret_cast<const float4*>(s + at_part(4, 0));
-        add(acc, *reinterpret_cast<const float4*>(&wgt[i][0]), o);
-        add(acc2, *reinterpret_cast<const float4*>(&wgt[i][4]), o2);
-      }
-      write(acc, 0, tid);
-      write(acc2, 4, tid);
-    } else {
-      const int grp = tid >> 6, v = tid & 63, val = (sub & 7) * 64 + v;
-      const float* src = p.part + at_part(c, val);
+    const int grp = tid >> 6, v = tid & 63, val = (sub & 7) * 64 + v;
+    const float* src = p.part + at_part(c, val);
 #pragma unroll 8
-      for (int i = grp; i < n; i += 8)
-        add(acc, *reinterpret_cast<const float4*>(&wgt[i][0]), *reinterpret_cast<const float4*>(src + slot(i) * kAtPart));
-      if (grp) meet[grp - 1][v] = acc;
-      __syncthreads();
-      if (grp) continue;
+    for (int i = grp; i < n; i += 8)
+      add(acc, *reinterpret_cast<const float4*>(&wgt[i][0]), *reinterpret_cast<const float4*>(src + slot(i) * kAtPart));
+    if (grp) meet[grp - 1][v] = acc;
+    __syncthreads();
+    if (grp) continue;
 #pragma unroll
-      for (int g = 0; g < 7; ++g) {
-        const float4 o = meet[g][v];
-        acc.x += o.x;
-        acc.y += o.y;
-        acc.z += o.z;
-        acc.w += o.w;
-      }
-      write(acc, 0, val);
-    }
+    for (int g = 0; g < 7; ++g) add(acc, make_float4(1.f, 1.f, 1.f, 1.f), meet[g][v]);
+    write(acc, make_float4(inv[0], inv[1], inv[2], inv[3]), val);
   }
 }
 
@@ -1175,6 +1208,10 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   a.scale_log2 = scale * 1.4426950408889634f;
   a.rows_per_page = (int)per_page;
   a.box = box;
+  a.box_log2 = 0;
+  while ((1 << a.box_log2) < box) ++a.box_log2;
+  a.by_page.set(desc->page_size);
+  a.by_heads.set(H);
   a.q_tok = ts * 2;
   a.q_head = hs * 2;
   a.q = static_cast<const uint8_t*>(q);
