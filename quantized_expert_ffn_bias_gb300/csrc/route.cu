@@ -21,33 +21,82 @@ struct RouteCall {
 
 template <int LT>
 __device__ __forceinline__ float route_load(const void* p, size_t i) {
-  if constexpr (LT == COLI_X_F32) return __ldg(static_cast<const float*>(p) + i);
+  float v;
+  if constexpr (LT == COLI_X_F32) v = __ldg(static_cast<const float*>(p) + i);
   else if constexpr (LT == COLI_X_BF16)
-    return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << 16);
-  else return __half2float(__ushort_as_half(__ldg(static_cast<const uint16_t*>(p) + i)));
+    v = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(p) + i) << 16);
+  else v = __half2float(__ushort_as_half(__ldg(static_cast<const uint16_t*>(p) + i)));
+  return v == v ? v : -INFINITY;
 }
 
-template <int LT, int NV>
+// VEC: rows and biases start on 16-byte borders and E is a multiple of NV, so a lane's experts are whole vectors.
+template <int LT, int NV, bool VEC>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteCall c) {
   const int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (t >= c.T) return;
-  float z[NV];
+  float z[NV], b[NV];
+  const size_t row = (size_t)t * c.stride;
+  const int e0 = lane * NV;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
-    z[i] = e < c.r.E ? route_load<LT>(c.logits, (size_t)t * c.stride + e) : -INFINITY;
-    if (!(z[i] == z[i])) z[i] = -INFINITY;
+    z[i] = -INFINITY;
+    b[i] = 0.f;
   }
-  route_token<NV>(c.r, z, c.bias, c.idx + (size_t)t * c.r.k, c.w + (size_t)t * c.r.k, nullptr, nullptr);
+  if constexpr (VEC) {
+    if (e0 < c.r.E) {
+      if constexpr (LT == COLI_X_F32) {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(c.logits) + row + e0 + i));
+          z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(c.logits) + row + e0 + i));
+          const uint32_t h[4] = {v.x & 0xFFFFu, v.x >> 16, v.y & 0xFFFFu, v.y >> 16};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            z[i + j] = LT == COLI_X_BF16 ? __uint_as_float(h[j] << 16) : __half2float(__ushort_as_half((uint16_t)h[j]));
+        }
+      }
+      if (c.bias)
+#pragma unroll
+        for (int i = 0; i < NV; i += 4) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(c.bias + e0 + i));
+          b[i] = v.x; b[i + 1] = v.y; b[i + 2] = v.z; b[i + 3] = v.w;
+        }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (!(z[i] == z[i])) z[i] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (e0 + i < c.r.E) {
+        z[i] = route_load<LT>(c.logits, row + e0 + i);
+        if (c.bias) b[i] = __ldg(c.bias + e0 + i);
+      }
+  }
+  route_token<NV>(c.r, z, b, [&](int e) { return route_load<LT>(c.logits, row + e); },
+                  c.idx + (size_t)t * c.r.k, c.w + (size_t)t * c.r.k, nullptr, nullptr);
+}
+
+template <int LT, int NV>
+static void launch_route_nv(const RouteCall& c, cudaStream_t st) {
+  const int blocks = (c.T + kRouteWarps - 1) / kRouteWarps;
+  const int size = LT == COLI_X_F32 ? 4 : 2;
+  const bool vec = c.r.E % NV == 0 && aligned(c.logits, 16) && c.stride * size % 16 == 0 && aligned(c.bias, 16);
+  if (vec) route_kernel<LT, NV, true><<<blocks, kRouteWarps * 32, 0, st>>>(c);
+  else route_kernel<LT, NV, false><<<blocks, kRouteWarps * 32, 0, st>>>(c);
 }
 
 template <int LT>
 static void launch_route_lt(const RouteCall& c, cudaStream_t st) {
-  const int blocks = (c.T + kRouteWarps - 1) / kRouteWarps;
-  if (c.r.E <= 128) route_kernel<LT, 4><<<blocks, kRouteWarps * 32, 0, st>>>(c);
-  else if (c.r.E <= 256) route_kernel<LT, 8><<<blocks, kRouteWarps * 32, 0, st>>>(c);
-  else if (c.r.E <= 512) route_kernel<LT, 16><<<blocks, kRouteWarps * 32, 0, st>>>(c);
-  else route_kernel<LT, 32><<<blocks, kRouteWarps * 32, 0, st>>>(c);
+  if (c.r.E <= 128) launch_route_nv<LT, 4>(c, st);
+  else if (c.r.E <= 256) launch_route_nv<LT, 8>(c, st);
+  else if (c.r.E <= 512) launch_route_nv<LT, 16>(c, st);
+  else launch_route_nv<LT, 32>(c, st);
 }
 
 coli_status check_route_desc(const coli_route_desc& r, const char* who) {

@@ -4,12 +4,17 @@
 // weights from s.  Shared by the stand-alone kernel (route.cu) and the layer
 // forward (router.cu).
 //
-// The choice is made in fp32 on order-preserving integer images (one
-// redux.sync a round), and is exact all the same: where the last kept and the
-// first dropped group or expert are closer than the error of the fp32 scores,
-// the warp makes the choice again with scores in 64 bits.  Experts whose logit
-// and bias are equal bit for bit tie exactly in either form and are no reason
-// for it (16-bit logits tie often).
+// Lane l holds the experts l NV .. l NV + NV - 1, so that a tie goes to the
+// lower lane, and so that groups of whole lanes are reduced with a few
+// shuffles for all groups at once.  The choice is made in fp32 with approximate
+// exponentials on order-preserving integer images (one redux.sync a round),
+// and is exact all the same: where the last kept and the first dropped group
+// or expert are closer than the error of these scores, those around the border
+// are compared by scores in 64 bits (computing all of a token's in 64 bits
+// took one warp 35 us and with it the call).  Experts whose logit and bias are equal
+// bit for bit tie exactly in either form and are no reason for it (16-bit
+// logits tie often).  The k weights come from exactly rounded arithmetic on
+// the chosen logits.
 #pragma once
 
 #include "moe_internal.cuh"
@@ -24,114 +29,168 @@ __device__ __forceinline__ float route_unimage(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
-// Bounds on the distance of two fp32 scores whose exact order may be the other one, relative to the
-// token's largest s: expf is within 2 ulp, 1 + e, the quotient and s + bias round once each (sigmoid:
-// 4 * 2^-23 a score, times two scores, doubled); a softmax also carries z - max (x e^-x 2^-24 at most)
-// and the sum of up to 32 terms a lane and 5 levels (38 * 2^-24).
-constexpr float kRouteTolSigmoid = 2e-6f, kRouteTolSoftmax = 1.2e-5f;
+// Bound on the distance of two approximate scores whose exact order may be the other one, given the token's
+// largest score.  A score's error is below s (2^-22 + 2^-22 + 2^-24) for exp2, the quotient and 1 + e, and
+// s (1 - s) |z| 2^-23 for the rounded argument of exp2; the latter is largest at the largest score or, where that
+// is above 1/2, below 2^-25 ((1 - s) |z| s <= 0.23).  A softmax also carries the sum of up to 32 terms a lane and
+// 5 levels (37 * 2^-24), and its arguments z - max enter as x e^-x <= 0.37.  Twice the bound covers two scores; it
+// is doubled once more.
+__device__ __forceinline__ float route_tol(bool softmax, float smax) {
+  if (softmax) return 4.f * smax * 4e-6f;
+  return 4.f * smax * (6e-7f + 1.3e-7f * (1.f + fabsf(__logf(fmaxf(smax, 1e-37f)))));
+}
 
-// The choice again in 64 bits.  z: this lane's logits (experts lane + 32 i).  Returns lane j < k's pick
-// in descending order of u.
+// What the 64-bit scores of a token need: its softmax's largest logit and sum.
+struct RouteExact {
+  bool softmax;
+  double m, sum;
+};
+
 template <int NV>
-__device__ __noinline__ int route_pick_exact(const coli_route_desc& r, const float* zin, const float* bias) {
-  const int lane = threadIdx.x & 31;
-  const int nv = (r.E + 31) / 32, gsz = r.E / r.n_group;
+__device__ __noinline__ RouteExact route_exact_begin(const coli_route_desc& r, const float* z) {
   const double inf = __longlong_as_double(0x7ff0000000000000ll);
-  auto warp_max = [](double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-  };
-  double u[NV], m = -inf, sum = 0.0;
-  for (int i = 0; i < nv; ++i) {
-    u[i] = lane + 32 * i < r.E ? (double)zin[i] : -inf;
-    m = fmax(m, u[i]);
+  RouteExact x{r.score == COLI_SCORE_SOFTMAX, -inf, 0.0};
+  if (!x.softmax) return x;
+  const int n_here = r.E - (int)(threadIdx.x & 31) * NV;
+  for (int i = 0; i < NV && i < n_here; ++i) x.m = fmax(x.m, (double)z[i]);
+  for (int o = 16; o > 0; o >>= 1) x.m = fmax(x.m, __shfl_xor_sync(0xffffffffu, x.m, o));
+  for (int i = 0; i < NV && i < n_here; ++i)
+    x.sum += x.m == inf ? (z[i] == INFINITY ? 1.0 : 0.0) : (z[i] == -INFINITY ? 0.0 : exp((double)z[i] - x.m));
+  for (int o = 16; o > 0; o >>= 1) x.sum += __shfl_xor_sync(0xffffffffu, x.sum, o);
+  return x;
+}
+
+// u of one expert in 64 bits (NaN: -infinity).
+static __device__ __noinline__ double route_exact_score(const RouteExact& x, float z, float b) {
+  const double inf = __longlong_as_double(0x7ff0000000000000ll);
+  double s;
+  if (x.softmax) {
+    s = x.m == inf ? (z == INFINITY ? 1.0 : 0.0) : (z == -INFINITY ? 0.0 : exp((double)z - x.m));
+    s = x.sum > 0.0 ? s / x.sum : 0.0;
+  } else {
+    s = 1.0 / (1.0 + exp(-(double)z));
   }
-  if (r.score == COLI_SCORE_SOFTMAX) {
-    m = warp_max(m);
-    for (int i = 0; i < nv; ++i) {
-      u[i] = m == inf ? (u[i] == inf ? 1.0 : 0.0) : (u[i] == -inf ? 0.0 : exp(u[i] - m));
-      sum += u[i];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
-  for (int i = 0; i < nv; ++i) {
-    const int e = lane + 32 * i;
-    u[i] = r.score == COLI_SCORE_SOFTMAX ? (sum > 0.0 ? u[i] / sum : 0.0) : 1.0 / (1.0 + exp(-u[i]));
-    if (bias && e < r.E) u[i] += (double)bias[e];
-    if (!(u[i] == u[i]) || e >= r.E) u[i] = -inf;
-  }
-  unsigned open = 0xffffffffu;
-  if (r.topk_group < r.n_group) {
-    double mine = -inf;
-    for (int g = 0; g < r.n_group; ++g) {
-      double t1 = -inf, t2 = -inf;
-      for (int i = 0; i < nv; ++i) {
-        const int e = lane + 32 * i;
-        if (e >= r.E || e / gsz != g) continue;
-        if (u[i] > t1) { t2 = t1; t1 = u[i]; }
-        else t2 = fmax(t2, u[i]);
+  s += (double)b;
+  return s == s ? s : -inf;
+}
+
+// Groups kept (a mask), by exact scores where the fp32 ones are within tol of the border score `a`: lane g
+// holds group g's fp32 score.  key: images of this lane's u; tol_u: of a single u.
+template <int NV>
+__device__ __noinline__ unsigned route_groups_exact(const coli_route_desc& r, const RouteExact& x, const float* z,
+                                                    const float* b, const uint32_t* key, float score, float a,
+                                                    float tol, float tol_u) {
+  const int lane = threadIdx.x & 31, G = r.n_group, gsz = r.E / G;
+  const double inf = __longlong_as_double(0x7ff0000000000000ll);
+  const bool in = lane < G && score > a + tol, close = lane < G && !in && score >= a - tol;
+  const unsigned closes = __ballot_sync(0xffffffffu, close);
+  double mine = -inf;
+  for (unsigned left = closes; left; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    // the group's second largest u in fp32; experts not below it by more than the tolerance may be among the two
+    uint32_t k1 = 0u, k2 = 0u;
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane * NV + i;
+      if (e >= g * gsz && e < (g + 1) * gsz) {
+        k2 = max(k2, min(k1, key[i]));
+        k1 = max(k1, key[i]);
       }
-      double sc = warp_max(t1);
-      if (r.group_score == COLI_GROUP_TOP2) {
-        const int owner = __ffs(__ballot_sync(0xffffffffu, t1 == sc)) - 1;
-        sc += warp_max(lane == owner ? t2 : t1);
-        if (!(sc == sc)) sc = -inf;
-      }
-      if (lane == g) mine = sc;
     }
-    int rank = 0;
-    for (int g = 0; g < r.n_group; ++g) {
-      const double o = __shfl_sync(0xffffffffu, mine, g);
-      rank += o > mine || (o == mine && g < lane);
+    const uint32_t m1 = __reduce_max_sync(0xffffffffu, k1);
+    const int first = __ffs(__ballot_sync(0xffffffffu, k1 == m1)) - 1;
+    const uint32_t m2 = __reduce_max_sync(0xffffffffu, lane == first ? k2 : k1);
+    const float from = route_unimage(r.group_score == COLI_GROUP_TOP2 ? m2 : m1) - tol_u;
+    double t1 = -inf, t2 = -inf;
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane * NV + i;
+      if (e < g * gsz || e >= (g + 1) * gsz || !(route_unimage(key[i]) >= from)) continue;
+      const double u = route_exact_score(x, z[i], b[i]);
+      if (u > t1) { t2 = t1; t1 = u; }
+      else t2 = fmax(t2, u);
     }
-    open = __ballot_sync(0xffffffffu, lane < r.n_group && rank < r.topk_group);
+    auto warp_max = [](double v) {
+      for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
+      return v;
+    };
+    double sc = warp_max(t1);
+    if (r.group_score == COLI_GROUP_TOP2) {
+      const int owner = __ffs(__ballot_sync(0xffffffffu, t1 == sc)) - 1;
+      sc += warp_max(lane == owner ? t2 : t1);
+      if (!(sc == sc)) sc = -inf;
+    }
+    if (lane == g) mine = sc;
   }
-  unsigned left = 0;                     // this lane's experts that can still be picked
-  for (int i = 0; i < nv; ++i) {
-    const int e = lane + 32 * i;
-    if (e < r.E && ((open >> (e / gsz)) & 1u)) left |= 1u << i;
+  int rank = __popc(__ballot_sync(0xffffffffu, in));
+  for (unsigned left = closes; left; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    const double o = __shfl_sync(0xffffffffu, mine, g);
+    rank += o > mine || (o == mine && g < lane);
   }
-  int pick = -1;
-  for (int j = 0; j < r.k; ++j) {
-    double bu = -inf;
+  return __ballot_sync(0xffffffffu, in || (close && rank < r.topk_group));
+}
+
+// The picks (lane j < k: the j-th), by exact scores where the fp32 ones are within tol of the last pick's, `a`.
+template <int NV>
+__device__ __noinline__ int route_picks_exact(const coli_route_desc& r, const RouteExact& x, const float* z,
+                                              const float* b, const uint32_t* key, float a, float tol, int pick) {
+  const int lane = threadIdx.x & 31;
+  double u[NV];
+  unsigned left = 0;                     // this lane's candidates around the border
+  int sure = 0;                          // candidates certainly above it: the first picks
+  for (int i = 0; i < NV; ++i) {
+    if (!key[i]) continue;
+    const float v = route_unimage(key[i]);
+    if (v > a + tol) {
+      ++sure;
+    } else if (v >= a - tol) {
+      left |= 1u << i;
+      u[i] = route_exact_score(x, z[i], b[i]);
+    }
+  }
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  for (int j = sure; j < r.k; ++j) {
+    double bu = 0.0;
     int be = 0x7fffffff;
-    for (int i = 0; i < nv; ++i)
-      if ((left >> i) & 1u)
-        if (be == 0x7fffffff || u[i] > bu) { bu = u[i]; be = lane + 32 * i; }
-#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (((left >> i) & 1u) && (be == 0x7fffffff || u[i] > bu)) { bu = u[i]; be = lane * NV + i; }
     for (int o = 16; o > 0; o >>= 1) {
       const double u2 = __shfl_xor_sync(0xffffffffu, bu, o);
       const int e2 = __shfl_xor_sync(0xffffffffu, be, o);
       if (e2 != 0x7fffffff && (be == 0x7fffffff || u2 > bu || (u2 == bu && e2 < be))) { bu = u2; be = e2; }
     }
     if (lane == j) pick = be;
-    if ((be & 31) == lane) left &= ~(1u << (be >> 5));
+    if (be / NV == lane) left &= ~(1u << (be % NV));
   }
   return pick;
 }
 
-// z: this lane's logits (experts lane + 32 i, NaN already -infinity).  topk_idx, topk_w: this token's [k];
-// sel_out (may be NULL): the same ids; near_tie (may be NULL) as colibri_moe_debug_routing documents it.
-template <int NV>
-__device__ __forceinline__ void route_token(const coli_route_desc& r, const float (&z)[NV], const float* bias,
-                                            int32_t* topk_idx, float* topk_w, int* sel_out, int32_t* near_tie) {
+// z: this lane's logits (experts lane NV + i; NaN already -infinity, past E anything); b: their biases (0 without
+// one); `logit(e)`: the logit of expert e again, by any lane.  topk_idx, topk_w: this token's [k]; sel_out (may be
+// NULL): the same ids; near_tie (may be NULL) as colibri_moe_debug_routing documents it.
+template <int NV, typename Logit>
+__device__ __forceinline__ void route_token(const coli_route_desc& r, const float (&z)[NV], const float (&b)[NV],
+                                            Logit logit, int32_t* topk_idx, float* topk_w, int* sel_out,
+                                            int32_t* near_tie) {
   const int lane = threadIdx.x & 31;
-  const int E = r.E, k = r.k, gsz = E / r.n_group;
+  const int E = r.E, k = r.k, n_here = E - lane * NV;    // experts of this lane: i < n_here
   const bool softmax = r.score == COLI_SCORE_SOFTMAX;
+  constexpr float kLog2e = 1.4426950408889634f;
+  auto exp2a = [](float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+  };
   // scores
-  float s[NV];
+  float s[NV], m = -INFINITY, sum = 0.f;
   if (softmax) {
-    float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) m = fmaxf(m, lane + 32 * i < E ? z[i] : -INFINITY);
+    for (int i = 0; i < NV; ++i) m = fmaxf(m, i < n_here ? z[i] : -INFINITY);
     m = route_unimage(__reduce_max_sync(0xffffffffu, route_image(m)));
-    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      s[i] = lane + 32 * i < E ? (m == INFINITY ? (z[i] == INFINITY ? 1.f : 0.f) : (z[i] == -INFINITY ? 0.f : expf(z[i] - m)))
-                               : 0.f;
+      // all of +infinity share equally; -infinity (also where every logit is) has none
+      const float d = m == INFINITY ? (z[i] == INFINITY ? 0.f : -INFINITY) : (m == -INFINITY ? -INFINITY : z[i] - m);
+      s[i] = i < n_here ? exp2a(d * kLog2e) : 0.f;
       sum += s[i];
     }
 #pragma unroll
@@ -141,153 +200,207 @@ __device__ __forceinline__ void route_token(const coli_route_desc& r, const floa
     for (int i = 0; i < NV; ++i) s[i] *= inv;
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = lane + 32 * i < E ? 1.0f / (1.0f + expf(-z[i])) : 0.f;
+    for (int i = 0; i < NV; ++i) s[i] = __fdividef(1.f, 1.f + exp2a(-z[i] * kLog2e));
   }
   uint32_t key[NV];                      // image of u; 0: not a candidate (below every image, also -infinity's)
   float smax = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
-    float u = s[i] + (bias && e < E ? __ldg(bias + e) : 0.f);
+    float u = s[i] + b[i];
     if (!(u == u)) u = -INFINITY;
     u += 0.f;                            // -0 and +0 are equal scores
-    key[i] = e < E ? route_image(u) : 0u;
-    smax = fmaxf(smax, s[i]);
+    key[i] = i < n_here ? route_image(u) : 0u;
+    smax = fmaxf(smax, i < n_here ? s[i] : 0.f);
   }
   smax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(smax)));
-  const float tol_s = (softmax ? kRouteTolSoftmax : kRouteTolSigmoid) * smax;
-  bool again = false, tie = false;       // a decision closer than the scores' error; closer than kNearTie
+  const float tol_s = route_tol(softmax, smax);
+  bool tie = false;                      // a decision closer than kNearTie
 
   // groups
-  unsigned open = 0xffffffffu;
   if (r.topk_group < r.n_group) {
-    float mine = -INFINITY, mag = 0.f;   // lane g: group g's score, the larger magnitude of its terms
-    for (int g = 0; g < r.n_group; ++g) {
-      uint32_t t1 = 0u, t2 = 0u;
+    const int G = r.n_group, gsz = E / G;
+    const bool top2 = r.group_score == COLI_GROUP_TOP2;
+    uint32_t t1 = 0u, t2 = 0u;           // a group's two largest images
+    int mine = lane;                     // this lane's group, or the group whose scores it holds
+    const int lanes = gsz / NV;          // lanes a group
+    const bool whole = lanes * NV == gsz && (lanes & (lanes - 1)) == 0;
+    if (whole) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        if (e >= g * gsz && e < (g + 1) * gsz) {
-          t2 = max(t2, min(t1, key[i]));
-          t1 = max(t1, key[i]);
+        t2 = max(t2, min(t1, key[i]));
+        t1 = max(t1, key[i]);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        if (o < lanes) {
+          const uint32_t a1 = __shfl_xor_sync(0xffffffffu, t1, o), a2 = __shfl_xor_sync(0xffffffffu, t2, o);
+          t2 = max(min(t1, a1), max(t2, a2));
+          t1 = max(t1, a1);
         }
       }
-      const uint32_t m1 = __reduce_max_sync(0xffffffffu, t1);
-      float sc = route_unimage(m1), mg = fabsf(sc);
-      if (r.group_score == COLI_GROUP_TOP2) {
-        const int owner = __ffs(__ballot_sync(0xffffffffu, t1 == m1)) - 1;
-        const float second = route_unimage(__reduce_max_sync(0xffffffffu, lane == owner ? t2 : t1));
-        mg = fmaxf(mg, fabsf(second));
+      mine = lane >> (31 - __clz(lanes));
+    } else {
+      for (int g = 0; g < G; ++g) {
+        uint32_t a1 = 0u, a2 = 0u;
+        const int lo = g * gsz - lane * NV;      // the group's experts among this lane's: lo <= i < lo + gsz
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (i >= lo && i < lo + gsz) {
+            a2 = max(a2, min(a1, key[i]));
+            a1 = max(a1, key[i]);
+          }
+        }
+        const uint32_t m1 = __reduce_max_sync(0xffffffffu, a1);
+        const int owner = __ffs(__ballot_sync(0xffffffffu, a1 == m1)) - 1;
+        const uint32_t m2 = __reduce_max_sync(0xffffffffu, lane == owner ? a2 : a1);
+        if (lane == g) {
+          t1 = m1;
+          t2 = m2;
+        }
+      }
+    }
+    float sc = -INFINITY, mag = 0.f;
+    if (mine < G) {
+      sc = route_unimage(t1);
+      mag = fabsf(sc);
+      if (top2) {
+        const float second = route_unimage(t2);
+        mag = fmaxf(mag, fabsf(second));
         sc += second;
         if (!(sc == sc)) sc = -INFINITY;
       }
-      if (lane == g) {
-        mine = sc + 0.f;
-        mag = mg < INFINITY ? mg : 0.f;
-      }
+      sc += 0.f;
+      if (!(mag < INFINITY)) mag = 0.f;
     }
     int rank = 0;
-    for (int g = 0; g < r.n_group; ++g) {
-      const float o = __shfl_sync(0xffffffffu, mine, g);
-      rank += o > mine || (o == mine && g < lane);
+    for (int g = 0; g < G; ++g) {
+      const float o = __shfl_sync(0xffffffffu, sc, whole ? g * lanes : g);
+      rank += o > sc || (o == sc && g < mine);
     }
-    if (lane >= r.n_group) rank = 64;
-    open = __ballot_sync(0xffffffffu, rank < r.topk_group);
-    const unsigned last = __ballot_sync(0xffffffffu, rank == r.topk_group - 1);
-    const unsigned next = __ballot_sync(0xffffffffu, rank == r.topk_group);
-    const float a = __shfl_sync(0xffffffffu, mine, __ffs(last) - 1), b = __shfl_sync(0xffffffffu, mine, __ffs(next) - 1);
-    const float gap = a == b ? 0.f : a - b;
+    if (mine >= G) rank = 64;
+    // the last kept and the first dropped score
+    const float a = __shfl_sync(0xffffffffu, sc, __ffs(__ballot_sync(0xffffffffu, rank == r.topk_group - 1)) - 1);
+    const float c = __shfl_sync(0xffffffffu, sc, __ffs(__ballot_sync(0xffffffffu, rank == r.topk_group)) - 1);
+    const float gap = a == c ? 0.f : a - c;
     mag = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mag)));
-    again = gap <= 2.f * tol_s + 1e-6f * mag && a > -INFINITY;   // each term and each sum rounds by 2^-24 of mag or 2 mag
+    const float tol = 2.f * tol_s + 1e-6f * mag;       // each term and each sum rounds by 2^-24 of mag or 2 mag
     tie = gap < kNearTie;
+    bool kept = rank < r.topk_group;
+    unsigned open = 0;
+    const bool again = gap <= tol && a > -INFINITY;
+    if (again || !whole) {
+      // lane g holds group g's score and whether it is kept
+      const int from = whole ? (lane * lanes) & 31 : lane;
+      const float score = __shfl_sync(0xffffffffu, sc, from);
+      open = __ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, kept ? 1 : 0, from) && lane < G);
+      if (again) {
+        float zc[NV], bc[NV];
+        uint32_t kc[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E && !((open >> (e / gsz)) & 1u)) key[i] = 0u;
+        for (int i = 0; i < NV; ++i) {
+          zc[i] = z[i];
+          bc[i] = b[i];
+          kc[i] = key[i];
+        }
+        const RouteExact x = route_exact_begin<NV>(r, zc);
+        open = route_groups_exact<NV>(r, x, zc, bc, kc, score, a, tol, tol_s + 5e-7f * mag);
+        kept = mine < G && ((open >> (mine & 31)) & 1u);
+      }
+    }
+    if (whole) {
+      if (!kept)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = 0u;
+    } else {
+      const float per = 1.0f / (float)gsz;       // (e + 1/2) / gsz is exact enough for e < 1024
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int g = (int)(((float)(lane * NV + i) + 0.5f) * per);
+        if (!((open >> (g & 31)) & 1u)) key[i] = 0u;
+      }
     }
   }
 
-  // the k largest: every round the warp takes the best lane candidate and the winning lane rescans
-  uint32_t full[NV];
+  // the k largest: every round the warp takes the best lane candidate (ties: the lower lane, the lower expert)
+  // and the winning lane looks for its next
+  uint32_t top[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) full[i] = key[i];
+  for (int i = 0; i < NV; ++i) top[i] = key[i];
   auto lane_best = [&](uint32_t& bk, int& bi) {
     bk = 0u;
     bi = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (key[i] > bk) { bk = key[i]; bi = i; }
+      if (top[i] > bk) { bk = top[i]; bi = i; }
   };
   uint32_t bk, kth = 0u;
   int bi, pick = -1;
   lane_best(bk, bi);
   for (int j = 0; j < k; ++j) {
-    const uint32_t m = __reduce_max_sync(0xffffffffu, bk);
-    const int e = (int)__reduce_min_sync(0xffffffffu, bk == m ? (unsigned)(lane + 32 * bi) : 0x7fffffffu);
+    kth = __reduce_max_sync(0xffffffffu, bk);
+    const int owner = __ffs(__ballot_sync(0xffffffffu, bk == kth)) - 1;
+    const int e = __shfl_sync(0xffffffffu, lane * NV + bi, owner);
     if (lane == j) pick = e;
-    kth = m;
-    if ((e & 31) == lane) {
+    if (lane == owner) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (i == (e >> 5)) key[i] = 0u;
+        if (i == bi) top[i] = 0u;
       lane_best(bk, bi);
     }
   }
   const uint32_t nxt = __reduce_max_sync(0xffffffffu, bk);     // best of those left (0: none)
   if (nxt) {
-    const float a = route_unimage(kth), b = route_unimage(nxt);
-    const float gap = a == b ? 0.f : a - b;
+    const float a = route_unimage(kth), c = route_unimage(nxt);
+    const float gap = a == c ? 0.f : a - c;
     const float tol = tol_s + 5e-7f * fabsf(a);
     tie |= gap < kNearTie;
-    if (!again && gap <= tol && a > -INFINITY) {
+    if (gap <= tol && a > -INFINITY) {
       // close: unless every candidate around the border has the last pick's logit and bias
       const int e_k = __shfl_sync(0xffffffffu, pick, k - 1);
-      float zk = 0.f;
+      float zk = 0.f, bk_ = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (i == (e_k >> 5)) zk = z[i];
-      zk = __shfl_sync(0xffffffffu, zk, e_k & 31);
-      const float bk_ = bias ? __ldg(bias + e_k) : 0.f;
+        if (i == e_k % NV) { zk = z[i]; bk_ = b[i]; }
+      zk = __shfl_sync(0xffffffffu, zk, e_k / NV);
+      bk_ = __shfl_sync(0xffffffffu, bk_, e_k / NV);
       bool other = false;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        if (full[i] && fabsf(route_unimage(full[i]) - a) <= 2.f * tol)
-          other |= z[i] != zk || (bias && __ldg(bias + e) != bk_);
-      }
-      again = __any_sync(0xffffffffu, other);
-    }
-  }
-  if (again) {
-    float zc[NV];
+      for (int i = 0; i < NV; ++i)
+        if (key[i] && fabsf(route_unimage(key[i]) - a) <= tol) other |= z[i] != zk || b[i] != bk_;
+      if (__any_sync(0xffffffffu, other)) {
+        float zc[NV], bc[NV];
+        uint32_t kc[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) zc[i] = z[i];
-    pick = route_pick_exact<NV>(r, zc, bias);
+        for (int i = 0; i < NV; ++i) {
+          zc[i] = z[i];
+          bc[i] = b[i];
+          kc[i] = key[i];
+        }
+        const RouteExact x = route_exact_begin<NV>(r, zc);
+        pick = route_picks_exact<NV>(r, x, zc, bc, kc, a, tol, pick);
+      }
+    }
   }
   if (near_tie && lane == 0) *near_tie = tie ? 1 : 0;
 
-  // ascending ids: rank of each pick among the picks, then weights from s
+  // ascending ids: rank of each pick among the picks; weights from the chosen logits, rounded
   int rank = 0;
   for (int i = 0; i < k; ++i) rank += __shfl_sync(0xffffffffu, pick, i) < pick;
-  float my = 0.f;
-  for (int j = 0; j < k; ++j) {
-    const int e = __shfl_sync(0xffffffffu, pick, j);
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (i == (e >> 5)) v = s[i];
-    v = __shfl_sync(0xffffffffu, v, e & 31);
-    if (lane == j) my = v;
+  float w = 0.f;
+  if (lane < k) {
+    const float v = logit(pick);
+    if (softmax) w = sum > 0.f ? expf(m == INFINITY ? (v == INFINITY ? 0.f : -INFINITY) : v - m) / sum : 0.f;
+    else w = 1.0f / (1.0f + expf(-v));
   }
-  float sum = 1.f;
+  float total = 1.f;
   if (r.renorm) {
-    sum = lane < k ? my : 0.f;
+    total = w;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   }
   if (lane < k) {
     topk_idx[rank] = pick;
-    topk_w[rank] = sum > 0.f ? r.scale * my / sum : 0.f;
+    topk_w[rank] = total > 0.f ? r.scale * w / total : 0.f;
     if (sel_out) sel_out[rank] = pick;
   }
   __syncwarp();

@@ -317,19 +317,20 @@ __device__ void topk_token(const FwdArgs& a, int t, float* u, float* s) {
 template <int NV>
 __device__ __forceinline__ void routed_token_nv(const FwdArgs& a, int t, int* sel_out) {
   const int lane = threadIdx.x & 31;
-  float z[NV];
+  auto logit = [&](int e) {
+    float v = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < kRouterKSplit; ++ks) v += __ldcg(a.logits + ((size_t)ks * a.T + t) * a.E + e);
+    return v == v ? v : -INFINITY;
+  };
+  float z[NV], b[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
-    z[i] = -INFINITY;
-    if (e < a.E) {
-      float v = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < kRouterKSplit; ++ks) v += __ldcg(a.logits + ((size_t)ks * a.T + t) * a.E + e);
-      if (v == v) z[i] = v;
-    }
+    const int e = lane * NV + i;
+    z[i] = e < a.E ? logit(e) : -INFINITY;
+    b[i] = e < a.E ? __ldg(a.bias + e) : 0.f;
   }
-  route_token<NV>(a.route, z, a.bias, a.topk_idx + (size_t)t * a.k, a.topk_w + (size_t)t * a.k, sel_out,
+  route_token<NV>(a.route, z, b, logit, a.topk_idx + (size_t)t * a.k, a.topk_w + (size_t)t * a.k, sel_out,
                   a.near_tie + t);
 }
 
