@@ -8,7 +8,7 @@
 // lower lane, and so that groups of whole lanes are reduced with a few
 // shuffles for all groups at once.  The choice is made in fp32 with approximate
 // exponentials on order-preserving integer images (one redux.sync a round),
-// and is exact all the same: where the last kept and the first dropped group
+// (sorted lists a lane) and is exact all the same: where the last kept and the first dropped group
 // or expert are closer than the error of these scores, those around the border
 // are compared by scores in 64 bits (computing all of a token's in 64 bits
 // took one warp 35 us and with it the call).  Experts whose logit and bias are equal
@@ -40,33 +40,39 @@ __device__ __forceinline__ float route_tol(bool softmax, float smax) {
   return 4.f * smax * (6e-7f + 1.3e-7f * (1.f + fabsf(__logf(fmaxf(smax, 1e-37f)))));
 }
 
-// What the 64-bit scores of a token need: its softmax's largest logit and sum.
-struct RouteExact {
-  bool softmax;
-  double m, sum;
-};
-
-template <int NV>
-__device__ __noinline__ RouteExact route_exact_begin(const coli_route_desc& r, const float* z) {
-  const double inf = __longlong_as_double(0x7ff0000000000000ll);
-  RouteExact x{r.score == COLI_SCORE_SOFTMAX, -inf, 0.0};
-  if (!x.softmax) return x;
-  const int n_here = r.E - (int)(threadIdx.x & 31) * NV;
-  for (int i = 0; i < NV && i < n_here; ++i) x.m = fmax(x.m, (double)z[i]);
-  for (int o = 16; o > 0; o >>= 1) x.m = fmax(x.m, __shfl_xor_sync(0xffffffffu, x.m, o));
-  for (int i = 0; i < NV && i < n_here; ++i)
-    x.sum += x.m == inf ? (z[i] == INFINITY ? 1.0 : 0.0) : (z[i] == -INFINITY ? 0.0 : exp((double)z[i] - x.m));
-  for (int o = 16; o > 0; o >>= 1) x.sum += __shfl_xor_sync(0xffffffffu, x.sum, o);
-  return x;
+__device__ __forceinline__ float route_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// A softmax's numerator: all of +infinity share equally, -infinity (also where every logit is) has none.
+__device__ __forceinline__ float route_numerator(float z, float m) {
+  const float d = m == INFINITY ? (z == INFINITY ? 0.f : -INFINITY) : (m == -INFINITY ? -INFINITY : z - m);
+  return route_exp2(d * 1.4426950408889634f);
+}
+__device__ __forceinline__ float route_sigmoid(float z) {
+  return __fdividef(1.f, 1.f + route_exp2(-z * 1.4426950408889634f));
+}
+// Image of u = s + b (NaN: -infinity's; -0 and +0 are equal).
+__device__ __forceinline__ uint32_t route_key(float s, float b) {
+  float u = s + b;
+  if (!(u == u)) u = -INFINITY;
+  return route_image(u + 0.f);
 }
 
-// u of one expert in 64 bits (NaN: -infinity).
-static __device__ __noinline__ double route_exact_score(const RouteExact& x, float z, float b) {
+// The rare comparisons in 64 bits.  They read the logits and biases again (arguments in arrays would have every
+// token store them: 16 us of 33 for 16384 tokens).
+struct RouteStats {
+  float m, inv;          // softmax: largest logit, 1 / sum
+};
+
+// u of one expert in 64 bits; m, sum: the softmax's in 64 bits.
+static __device__ __noinline__ double route_exact_score(bool softmax, double m, double sum, float z, float b) {
   const double inf = __longlong_as_double(0x7ff0000000000000ll);
   double s;
-  if (x.softmax) {
-    s = x.m == inf ? (z == INFINITY ? 1.0 : 0.0) : (z == -INFINITY ? 0.0 : exp((double)z - x.m));
-    s = x.sum > 0.0 ? s / x.sum : 0.0;
+  if (softmax) {
+    s = m == inf ? (z == INFINITY ? 1.0 : 0.0) : (z == -INFINITY ? 0.0 : exp((double)z - m));
+    s = sum > 0.0 ? s / sum : 0.0;
   } else {
     s = 1.0 / (1.0 + exp(-(double)z));
   }
@@ -74,14 +80,43 @@ static __device__ __noinline__ double route_exact_score(const RouteExact& x, flo
   return s == s ? s : -inf;
 }
 
-// Groups kept (a mask), by exact scores where the fp32 ones are within tol of the border score `a`: lane g
-// holds group g's fp32 score.  key: images of this lane's u; tol_u: of a single u.
 template <int NV>
-__device__ __noinline__ unsigned route_groups_exact(const coli_route_desc& r, const RouteExact& x, const float* z,
-                                                    const float* b, const uint32_t* key, float score, float a,
-                                                    float tol, float tol_u) {
+struct RouteAgain {
+  float z[NV], b[NV];
+  uint32_t key[NV];      // images of the fp32 u; 0 past E
+  double m, sum;
+  bool softmax;
+  template <typename Logit>
+  __device__ __forceinline__ RouteAgain(const coli_route_desc& r, Logit logit, const float* bias, RouteStats st) {
+    const double inf = __longlong_as_double(0x7ff0000000000000ll);
+    const int e0 = (int)(threadIdx.x & 31) * NV;
+    softmax = r.score == COLI_SCORE_SOFTMAX;
+    m = -inf;
+    sum = 0.0;
+    for (int i = 0; i < NV; ++i) {
+      const int e = e0 + i;
+      z[i] = e < r.E ? logit(e) : -INFINITY;
+      b[i] = bias && e < r.E ? __ldg(bias + e) : 0.f;
+      key[i] = e < r.E ? route_key(softmax ? route_numerator(z[i], st.m) * st.inv : route_sigmoid(z[i]), b[i]) : 0u;
+      m = fmax(m, (double)z[i]);
+    }
+    if (!softmax) return;
+    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int i = 0; i < NV; ++i)
+      if (e0 + i < r.E) sum += m == inf ? (z[i] == INFINITY ? 1.0 : 0.0) : (z[i] == -INFINITY ? 0.0 : exp((double)z[i] - m));
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  __device__ __forceinline__ double exact(int i) const { return route_exact_score(softmax, m, sum, z[i], b[i]); }
+};
+
+// Groups kept (a mask), by exact scores where the fp32 ones are within tol of the border score `a`: lane g
+// holds group g's fp32 score.  tol_u: of a single u.
+template <int NV, typename Logit>
+__device__ __noinline__ unsigned route_groups_exact(const coli_route_desc& r, Logit logit, const float* bias,
+                                                    RouteStats st, float score, float a, float tol, float tol_u) {
   const int lane = threadIdx.x & 31, G = r.n_group, gsz = r.E / G;
   const double inf = __longlong_as_double(0x7ff0000000000000ll);
+  const RouteAgain<NV> x(r, logit, bias, st);
   const bool in = lane < G && score > a + tol, close = lane < G && !in && score >= a - tol;
   const unsigned closes = __ballot_sync(0xffffffffu, close);
   double mine = -inf;
@@ -92,8 +127,8 @@ __device__ __noinline__ unsigned route_groups_exact(const coli_route_desc& r, co
     for (int i = 0; i < NV; ++i) {
       const int e = lane * NV + i;
       if (e >= g * gsz && e < (g + 1) * gsz) {
-        k2 = max(k2, min(k1, key[i]));
-        k1 = max(k1, key[i]);
+        k2 = max(k2, min(k1, x.key[i]));
+        k1 = max(k1, x.key[i]);
       }
     }
     const uint32_t m1 = __reduce_max_sync(0xffffffffu, k1);
@@ -103,8 +138,8 @@ __device__ __noinline__ unsigned route_groups_exact(const coli_route_desc& r, co
     double t1 = -inf, t2 = -inf;
     for (int i = 0; i < NV; ++i) {
       const int e = lane * NV + i;
-      if (e < g * gsz || e >= (g + 1) * gsz || !(route_unimage(key[i]) >= from)) continue;
-      const double u = route_exact_score(x, z[i], b[i]);
+      if (e < g * gsz || e >= (g + 1) * gsz || !(route_unimage(x.key[i]) >= from)) continue;
+      const double u = x.exact(i);
       if (u > t1) { t2 = t1; t1 = u; }
       else t2 = fmax(t2, u);
     }
@@ -129,24 +164,36 @@ __device__ __noinline__ unsigned route_groups_exact(const coli_route_desc& r, co
   return __ballot_sync(0xffffffffu, in || (close && rank < r.topk_group));
 }
 
-// The picks (lane j < k: the j-th), by exact scores where the fp32 ones are within tol of the last pick's, `a`.
-template <int NV>
-__device__ __noinline__ int route_picks_exact(const coli_route_desc& r, const RouteExact& x, const float* z,
-                                              const float* b, const uint32_t* key, float a, float tol, int pick) {
-  const int lane = threadIdx.x & 31;
-  double u[NV];
+// The picks (lane j < k: the j-th), by exact scores where the fp32 ones are within tol of the last pick's, `a`,
+// which is expert e_k's.  Where every expert around the border has that one's logit and bias, the picks stand.
+template <int NV, typename Logit>
+__device__ __noinline__ int route_picks_exact(const coli_route_desc& r, Logit logit, const float* bias, RouteStats st,
+                                              unsigned open, float a, float tol, int pick, int e_k) {
+  const int lane = threadIdx.x & 31, gsz = r.E / r.n_group;
+  const float zk = logit(e_k), bk = bias ? __ldg(bias + e_k) : 0.f;
+  float z[NV], b[NV];
   unsigned left = 0;                     // this lane's candidates around the border
   int sure = 0;                          // candidates certainly above it: the first picks
+  bool other = false;
   for (int i = 0; i < NV; ++i) {
-    if (!key[i]) continue;
-    const float v = route_unimage(key[i]);
+    const int e = lane * NV + i;
+    if (e >= r.E || !((open >> (e / gsz)) & 1u)) continue;
+    z[i] = logit(e);
+    b[i] = bias ? __ldg(bias + e) : 0.f;
+    const float v = route_unimage(
+        route_key(r.score == COLI_SCORE_SOFTMAX ? route_numerator(z[i], st.m) * st.inv : route_sigmoid(z[i]), b[i]));
     if (v > a + tol) {
       ++sure;
     } else if (v >= a - tol) {
       left |= 1u << i;
-      u[i] = route_exact_score(x, z[i], b[i]);
+      other |= z[i] != zk || b[i] != bk;
     }
   }
+  if (!__any_sync(0xffffffffu, other)) return pick;
+  const RouteAgain<NV> x(r, logit, bias, st);
+  double u[NV];
+  for (int i = 0; i < NV; ++i)
+    if ((left >> i) & 1u) u[i] = x.exact(i);
   sure = __reduce_add_sync(0xffffffffu, sure);
   for (int j = sure; j < r.k; ++j) {
     double bu = 0.0;
@@ -164,59 +211,74 @@ __device__ __noinline__ int route_picks_exact(const coli_route_desc& r, const Ro
   return pick;
 }
 
+// Sort a lane's keys, largest first (Batcher's odd-even merge network; N a power of two).
+template <int N>
+__device__ __forceinline__ void route_sort(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+      for (int j = q % p; j + q < N; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (j + i + q < N && (j + i) / (2 * p) == (j + i + q) / (2 * p)) {
+            const uint32_t hi = max(v[j + i], v[j + i + q]), lo = min(v[j + i], v[j + i + q]);
+            v[j + i] = hi;
+            v[j + i + q] = lo;
+          }
+}
+
 // z: this lane's logits (experts lane NV + i; NaN already -infinity, past E anything); b: their biases (0 without
-// one); `logit(e)`: the logit of expert e again, by any lane.  topk_idx, topk_w: this token's [k]; sel_out (may be
+// one); bias: where they come from (or NULL); `logit(e)`: the logit of expert e again, by any lane.  topk_idx, topk_w: this token's [k]; sel_out (may be
 // NULL): the same ids; near_tie (may be NULL) as colibri_moe_debug_routing documents it.
 template <int NV, typename Logit>
 __device__ __forceinline__ void route_token(const coli_route_desc& r, const float (&z)[NV], const float (&b)[NV],
-                                            Logit logit, int32_t* topk_idx, float* topk_w, int* sel_out,
+                                            const float* bias, Logit logit, int32_t* topk_idx, float* topk_w, int* sel_out,
                                             int32_t* near_tie) {
   const int lane = threadIdx.x & 31;
   const int E = r.E, k = r.k, n_here = E - lane * NV;    // experts of this lane: i < n_here
   const bool softmax = r.score == COLI_SCORE_SOFTMAX;
-  constexpr float kLog2e = 1.4426950408889634f;
-  auto exp2a = [](float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-  };
   // scores
-  float s[NV], m = -INFINITY, sum = 0.f;
+  float s[NV], sum = 0.f;
+  RouteStats st{-INFINITY, 0.f};
   if (softmax) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) m = fmaxf(m, i < n_here ? z[i] : -INFINITY);
-    m = route_unimage(__reduce_max_sync(0xffffffffu, route_image(m)));
+    for (int i = 0; i < NV; ++i) st.m = fmaxf(st.m, i < n_here ? z[i] : -INFINITY);
+    st.m = route_unimage(__reduce_max_sync(0xffffffffu, route_image(st.m)));
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      // all of +infinity share equally; -infinity (also where every logit is) has none
-      const float d = m == INFINITY ? (z[i] == INFINITY ? 0.f : -INFINITY) : (m == -INFINITY ? -INFINITY : z[i] - m);
-      s[i] = i < n_here ? exp2a(d * kLog2e) : 0.f;
+      s[i] = i < n_here ? route_numerator(z[i], st.m) : 0.f;
       sum += s[i];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+    st.inv = sum > 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] *= inv;
+    for (int i = 0; i < NV; ++i) s[i] *= st.inv;
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s[i] = __fdividef(1.f, 1.f + exp2a(-z[i] * kLog2e));
+    for (int i = 0; i < NV; ++i) s[i] = route_sigmoid(z[i]);
   }
-  uint32_t key[NV];                      // image of u; 0: not a candidate (below every image, also -infinity's)
+  // The lane's images of u in order, the low bits giving way to the expert (the lower one the larger): a round of
+  // the selection then only compares the lanes' heads.  0: not a candidate (below every image, also -infinity's).
+  // kCut: what that may take from a value, relative to it; it enters the tolerances.
+  constexpr uint32_t kIdx = NV - 1;
+  constexpr float kCut = (float)NV / 8388608.f;
+  uint32_t v[NV];
   float smax = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float u = s[i] + b[i];
-    if (!(u == u)) u = -INFINITY;
-    u += 0.f;                            // -0 and +0 are equal scores
-    key[i] = i < n_here ? route_image(u) : 0u;
+    v[i] = i < n_here ? (route_key(s[i], b[i]) & ~kIdx) | (kIdx - (uint32_t)i) : 0u;
     smax = fmaxf(smax, i < n_here ? s[i] : 0.f);
   }
   smax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(smax)));
+  route_sort<NV>(v);
   const float tol_s = route_tol(softmax, smax);
   bool tie = false;                      // a decision closer than kNearTie
 
   // groups
+  unsigned open = 0xffffffffu;           // kept groups
   if (r.topk_group < r.n_group) {
     const int G = r.n_group, gsz = E / G;
     const bool top2 = r.group_score == COLI_GROUP_TOP2;
@@ -225,11 +287,8 @@ __device__ __forceinline__ void route_token(const coli_route_desc& r, const floa
     const int lanes = gsz / NV;          // lanes a group
     const bool whole = lanes * NV == gsz && (lanes & (lanes - 1)) == 0;
     if (whole) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        t2 = max(t2, min(t1, key[i]));
-        t1 = max(t1, key[i]);
-      }
+      t1 = v[0];
+      t2 = NV > 1 ? v[1] : 0u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         if (o < lanes) {
@@ -245,9 +304,10 @@ __device__ __forceinline__ void route_token(const coli_route_desc& r, const floa
         const int lo = g * gsz - lane * NV;      // the group's experts among this lane's: lo <= i < lo + gsz
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          if (i >= lo && i < lo + gsz) {
-            a2 = max(a2, min(a1, key[i]));
-            a1 = max(a1, key[i]);
+          const int at = (int)(kIdx - (v[i] & kIdx));
+          if (v[i] && at >= lo && at < lo + gsz) {
+            a2 = max(a2, min(a1, v[i]));
+            a1 = max(a1, v[i]);
           }
         }
         const uint32_t m1 = __reduce_max_sync(0xffffffffu, a1);
@@ -283,103 +343,53 @@ __device__ __forceinline__ void route_token(const coli_route_desc& r, const floa
     const float c = __shfl_sync(0xffffffffu, sc, __ffs(__ballot_sync(0xffffffffu, rank == r.topk_group)) - 1);
     const float gap = a == c ? 0.f : a - c;
     mag = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mag)));
-    const float tol = 2.f * tol_s + 1e-6f * mag;       // each term and each sum rounds by 2^-24 of mag or 2 mag
-    tie = gap < kNearTie;
-    bool kept = rank < r.topk_group;
-    unsigned open = 0;
-    const bool again = gap <= tol && a > -INFINITY;
-    if (again || !whole) {
-      // lane g holds group g's score and whether it is kept
-      const int from = whole ? (lane * lanes) & 31 : lane;
-      const float score = __shfl_sync(0xffffffffu, sc, from);
-      open = __ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, kept ? 1 : 0, from) && lane < G);
-      if (again) {
-        float zc[NV], bc[NV];
-        uint32_t kc[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          zc[i] = z[i];
-          bc[i] = b[i];
-          kc[i] = key[i];
-        }
-        const RouteExact x = route_exact_begin<NV>(r, zc);
-        open = route_groups_exact<NV>(r, x, zc, bc, kc, score, a, tol, tol_s + 5e-7f * mag);
-        kept = mine < G && ((open >> (mine & 31)) & 1u);
-      }
-    }
+    const float tol = 2.f * tol_s + (1e-6f + 4.f * kCut) * mag;   // each term and sum rounds by 2^-24 of mag or 2 mag
+    tie = gap < kNearTie + 4.f * kCut * mag;
+    // lane g holds group g's score and whether it is kept
+    const int from = whole ? (lane * lanes) & 31 : lane;
+    const float score = __shfl_sync(0xffffffffu, sc, from);
+    open = __ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, rank, from) < r.topk_group && lane < G);
+    if (gap <= tol && a > -INFINITY)
+      open = route_groups_exact<NV>(r, logit, bias, st, score, a, tol, tol_s + (5e-7f + 2.f * kCut) * mag);
     if (whole) {
-      if (!kept)
+      if (!(mine < G && ((open >> (mine & 31)) & 1u)))
 #pragma unroll
-        for (int i = 0; i < NV; ++i) key[i] = 0u;
+        for (int i = 0; i < NV; ++i) v[i] = 0u;
     } else {
       const float per = 1.0f / (float)gsz;       // (e + 1/2) / gsz is exact enough for e < 1024
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int g = (int)(((float)(lane * NV + i) + 0.5f) * per);
-        if (!((open >> (g & 31)) & 1u)) key[i] = 0u;
+        const int g = (int)(((float)(lane * NV + (int)(kIdx - (v[i] & kIdx))) + 0.5f) * per);
+        if (!((open >> (g & 31)) & 1u)) v[i] = 0u;
       }
+      route_sort<NV>(v);
     }
   }
 
-  // the k largest: every round the warp takes the best lane candidate (ties: the lower lane, the lower expert)
-  // and the winning lane looks for its next
-  uint32_t top[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) top[i] = key[i];
-  auto lane_best = [&](uint32_t& bk, int& bi) {
-    bk = 0u;
-    bi = 0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (top[i] > bk) { bk = top[i]; bi = i; }
-  };
-  uint32_t bk, kth = 0u;
-  int bi, pick = -1;
-  lane_best(bk, bi);
+  // the k largest: every round the warp takes the best head (ties: the lower lane, the lower expert) and the
+  // winning lane moves its list up
+  uint32_t kth = 0u;
+  int pick = -1;
   for (int j = 0; j < k; ++j) {
-    kth = __reduce_max_sync(0xffffffffu, bk);
-    const int owner = __ffs(__ballot_sync(0xffffffffu, bk == kth)) - 1;
-    const int e = __shfl_sync(0xffffffffu, lane * NV + bi, owner);
+    kth = __reduce_max_sync(0xffffffffu, v[0]);
+    // heads that differ only in the expert's bits are equal scores: the lower lane goes first
+    const int owner = __ffs(__ballot_sync(0xffffffffu, (v[0] | kIdx) == (kth | kIdx))) - 1;
+    const int e = __shfl_sync(0xffffffffu, lane * NV + (int)(kIdx - (v[0] & kIdx)), owner);
     if (lane == j) pick = e;
     if (lane == owner) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i == bi) top[i] = 0u;
-      lane_best(bk, bi);
+      for (int i = 0; i + 1 < NV; ++i) v[i] = v[i + 1];
+      v[NV - 1] = 0u;
     }
   }
-  const uint32_t nxt = __reduce_max_sync(0xffffffffu, bk);     // best of those left (0: none)
+  const uint32_t nxt = __reduce_max_sync(0xffffffffu, v[0]);   // best of those left (0: none)
   if (nxt) {
-    const float a = route_unimage(kth), c = route_unimage(nxt);
+    const float a = route_unimage(kth & ~kIdx), c = route_unimage(nxt & ~kIdx);
     const float gap = a == c ? 0.f : a - c;
-    const float tol = tol_s + 5e-7f * fabsf(a);
-    tie |= gap < kNearTie;
-    if (gap <= tol && a > -INFINITY) {
-      // close: unless every candidate around the border has the last pick's logit and bias
-      const int e_k = __shfl_sync(0xffffffffu, pick, k - 1);
-      float zk = 0.f, bk_ = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (i == e_k % NV) { zk = z[i]; bk_ = b[i]; }
-      zk = __shfl_sync(0xffffffffu, zk, e_k / NV);
-      bk_ = __shfl_sync(0xffffffffu, bk_, e_k / NV);
-      bool other = false;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (key[i] && fabsf(route_unimage(key[i]) - a) <= tol) other |= z[i] != zk || b[i] != bk_;
-      if (__any_sync(0xffffffffu, other)) {
-        float zc[NV], bc[NV];
-        uint32_t kc[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          zc[i] = z[i];
-          bc[i] = b[i];
-          kc[i] = key[i];
-        }
-        const RouteExact x = route_exact_begin<NV>(r, zc);
-        pick = route_picks_exact<NV>(r, x, zc, bc, kc, a, tol, pick);
-      }
-    }
+    const float tol = tol_s + (5e-7f + 4.f * kCut) * fabsf(a);
+    tie |= gap < kNearTie + 2.f * kCut * fabsf(a);
+    if (gap <= tol && a > -INFINITY)
+      pick = route_picks_exact<NV>(r, logit, bias, st, open, a, tol, pick, __shfl_sync(0xffffffffu, pick, k - 1));
   }
   if (near_tie && lane == 0) *near_tie = tie ? 1 : 0;
 
@@ -388,9 +398,9 @@ __device__ __forceinline__ void route_token(const coli_route_desc& r, const floa
   for (int i = 0; i < k; ++i) rank += __shfl_sync(0xffffffffu, pick, i) < pick;
   float w = 0.f;
   if (lane < k) {
-    const float v = logit(pick);
-    if (softmax) w = sum > 0.f ? expf(m == INFINITY ? (v == INFINITY ? 0.f : -INFINITY) : v - m) / sum : 0.f;
-    else w = 1.0f / (1.0f + expf(-v));
+    const float l = logit(pick);
+    if (softmax) w = sum > 0.f ? expf(st.m == INFINITY ? (l == INFINITY ? 0.f : -INFINITY) : l - st.m) / sum : 0.f;
+    else w = 1.0f / (1.0f + expf(-l));
   }
   float total = 1.f;
   if (r.renorm) {

@@ -317,10 +317,12 @@ __device__ void topk_token(const FwdArgs& a, int t, float* u, float* s) {
 template <int NV>
 __device__ __forceinline__ void routed_token_nv(const FwdArgs& a, int t, int* sel_out) {
   const int lane = threadIdx.x & 31;
-  auto logit = [&](int e) {
+  const float* logits = a.logits + (size_t)t * a.E;
+  const size_t split = (size_t)a.T * a.E;
+  auto logit = [=](int e) {
     float v = 0.f;
 #pragma unroll
-    for (int ks = 0; ks < kRouterKSplit; ++ks) v += __ldcg(a.logits + ((size_t)ks * a.T + t) * a.E + e);
+    for (int ks = 0; ks < kRouterKSplit; ++ks) v += __ldcg(logits + ks * split + e);
     return v == v ? v : -INFINITY;
   };
   float z[NV], b[NV];
@@ -330,7 +332,7 @@ __device__ __forceinline__ void routed_token_nv(const FwdArgs& a, int t, int* se
     z[i] = e < a.E ? logit(e) : -INFINITY;
     b[i] = e < a.E ? __ldg(a.bias + e) : 0.f;
   }
-  route_token<NV>(a.route, z, b, logit, a.topk_idx + (size_t)t * a.k, a.topk_w + (size_t)t * a.k, sel_out,
+  route_token<NV>(a.route, z, b, a.bias, logit, a.topk_idx + (size_t)t * a.k, a.topk_w + (size_t)t * a.k, sel_out,
                   a.near_tie + t);
 }
 
