@@ -31,7 +31,7 @@ __device__ __forceinline__ float route_load(const void* p, size_t i) {
 
 // VEC: rows and biases start on 16-byte borders and E is a multiple of NV, so a lane's experts are whole vectors.
 template <int LT, int NV, bool VEC>
-__global__ void __launch_bounds__(kRouteWarps * 32, NV <= 8 ? 8 : 4) route_kernel(const RouteCall c) {
+__global__ void __launch_bounds__(kRouteWarps * 32, NV <= 8 ? 8 : 4) route_kernel(const __grid_constant__ RouteCall c) {
   const int t = blockIdx.x * kRouteWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (t >= c.T) return;
   float z[NV], b[NV];
@@ -79,8 +79,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NV <= 8 ? 8 : 4) route_kerne
       }
   }
   const void* logits = c.logits;
-  route_token<NV>(c.r, z, b, c.bias, [=](int e) { return route_load<LT>(logits, row + e); },
-                  c.idx + (size_t)t * c.r.k, c.w + (size_t)t * c.r.k, nullptr, nullptr);
+  auto logit = [=](int e) { return route_load<LT>(logits, row + e); };
+  int32_t* idx = c.idx + (size_t)t * c.r.k;
+  float* w = c.w + (size_t)t * c.r.k;
+  if (route_token<NV, false>(c.r, z, b, c.bias, logit, idx, w, nullptr, nullptr))
+    route_token_exact<NV>(c.r, c.bias, logit, idx, w, nullptr, nullptr);
 }
 
 template <int LT, int NV>

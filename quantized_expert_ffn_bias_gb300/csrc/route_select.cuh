@@ -33,11 +33,11 @@ __device__ __forceinline__ float route_unimage(uint32_t k) {
 // largest score.  A score's error is below s (2^-22 + 2^-22 + 2^-24) for exp2, the quotient and 1 + e, and
 // s (1 - s) |z| 2^-23 for the rounded argument of exp2; the latter is largest at the largest score or, where that
 // is above 1/2, below 2^-25 ((1 - s) |z| s <= 0.23).  A softmax also carries the sum of up to 32 terms a lane and
-// 5 levels (37 * 2^-24), and its arguments z - max enter as x e^-x <= 0.37.  Twice the bound covers two scores; it
-// is doubled once more.
+// 5 levels (37 * 2^-24), and its arguments z - max enter as x e^-x <= 0.37.  Twice that covers two scores, and a
+// quarter is added.
 __device__ __forceinline__ float route_tol(bool softmax, float smax) {
-  if (softmax) return 4.f * smax * 4e-6f;
-  return 4.f * smax * (6e-7f + 1.3e-7f * (1.f + fabsf(__logf(fmaxf(smax, 1e-37f)))));
+  if (softmax) return 2.5f * smax * 3.2e-6f;
+  return 2.5f * smax * (6e-7f + 1.3e-7f * (1.f + fabsf(__logf(fmaxf(smax, 1e-37f)))));
 }
 
 __device__ __forceinline__ float route_exp2(float x) {
@@ -106,23 +106,31 @@ struct RouteAgain {
       if (e0 + i < r.E) sum += m == inf ? (z[i] == INFINITY ? 1.0 : 0.0) : (z[i] == -INFINITY ? 0.0 : exp((double)z[i] - m));
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
-  __device__ __forceinline__ double exact(int i) const { return route_exact_score(softmax, m, sum, z[i], b[i]); }
+  // Exact scores of the experts in this lane's mask, into u: every lane its next at the same time.
+  __device__ __forceinline__ void exact(unsigned which, double (&u)[NV]) const {
+    while (__any_sync(0xffffffffu, which)) {
+      const int i = which ? __ffs(which) - 1 : 0;
+      const double v = route_exact_score(softmax, m, sum, z[i], b[i]);
+      if (which) u[i] = v;
+      which &= which - 1;
+    }
+  }
 };
 
 // Groups kept (a mask), by exact scores where the fp32 ones are within tol of the border score `a`: lane g
 // holds group g's fp32 score.  tol_u: of a single u.
 template <int NV, typename Logit>
-__device__ __noinline__ unsigned route_groups_exact(const coli_route_desc& r, Logit logit, const float* bias,
+__device__ __noinline__ unsigned route_groups_exact(const coli_route_desc r, Logit logit, const float* bias,
                                                     RouteStats st, float score, float a, float tol, float tol_u) {
   const int lane = threadIdx.x & 31, G = r.n_group, gsz = r.E / G;
   const double inf = __longlong_as_double(0x7ff0000000000000ll);
   const RouteAgain<NV> x(r, logit, bias, st);
   const bool in = lane < G && score > a + tol, close = lane < G && !in && score >= a - tol;
   const unsigned closes = __ballot_sync(0xffffffffu, close);
-  double mine = -inf;
+  // a close group's second largest u in fp32: experts not below it by more than the tolerance may be among the two
+  unsigned which = 0;
   for (unsigned left = closes; left; left &= left - 1) {
     const int g = __ffs(left) - 1;
-    // the group's second largest u in fp32; experts not below it by more than the tolerance may be among the two
     uint32_t k1 = 0u, k2 = 0u;
     for (int i = 0; i < NV; ++i) {
       const int e = lane * NV + i;
@@ -135,13 +143,22 @@ __device__ __noinline__ unsigned route_groups_exact(const coli_route_desc& r, Lo
     const int first = __ffs(__ballot_sync(0xffffffffu, k1 == m1)) - 1;
     const uint32_t m2 = __reduce_max_sync(0xffffffffu, lane == first ? k2 : k1);
     const float from = route_unimage(r.group_score == COLI_GROUP_TOP2 ? m2 : m1) - tol_u;
-    double t1 = -inf, t2 = -inf;
     for (int i = 0; i < NV; ++i) {
       const int e = lane * NV + i;
-      if (e < g * gsz || e >= (g + 1) * gsz || !(route_unimage(x.key[i]) >= from)) continue;
-      const double u = x.exact(i);
-      if (u > t1) { t2 = t1; t1 = u; }
-      else t2 = fmax(t2, u);
+      if (e >= g * gsz && e < (g + 1) * gsz && route_unimage(x.key[i]) >= from) which |= 1u << i;
+    }
+  }
+  double u[NV];
+  x.exact(which, u);
+  double mine = -inf;
+  for (unsigned left = closes; left; left &= left - 1) {
+    const int g = __ffs(left) - 1;
+    double t1 = -inf, t2 = -inf;
+    for (unsigned w = which; w; w &= w - 1) {
+      const int i = __ffs(w) - 1, e = lane * NV + i;
+      if (e < g * gsz || e >= (g + 1) * gsz) continue;
+      if (u[i] > t1) { t2 = t1; t1 = u[i]; }
+      else t2 = fmax(t2, u[i]);
     }
     auto warp_max = [](double v) {
       for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -167,7 +184,7 @@ __device__ __noinline__ unsigned route_groups_exact(const coli_route_desc& r, Lo
 // The picks (lane j < k: the j-th), by exact scores where the fp32 ones are within tol of the last pick's, `a`,
 // which is expert e_k's.  Where every expert around the border has that one's logit and bias, the picks stand.
 template <int NV, typename Logit>
-__device__ __noinline__ int route_picks_exact(const coli_route_desc& r, Logit logit, const float* bias, RouteStats st,
+__device__ __noinline__ int route_picks_exact(const coli_route_desc r, Logit logit, const float* bias, RouteStats st,
                                               unsigned open, float a, float tol, int pick, int e_k) {
   const int lane = threadIdx.x & 31, gsz = r.E / r.n_group;
   const float zk = logit(e_k), bk = bias ? __ldg(bias + e_k) : 0.f;
@@ -192,8 +209,7 @@ __device__ __noinline__ int route_picks_exact(const coli_route_desc& r, Logit lo
   if (!__any_sync(0xffffffffu, other)) return pick;
   const RouteAgain<NV> x(r, logit, bias, st);
   double u[NV];
-  for (int i = 0; i < NV; ++i)
-    if ((left >> i) & 1u) u[i] = x.exact(i);
+  x.exact(left, u);
   sure = __reduce_add_sync(0xffffffffu, sure);
   for (int j = sure; j < r.k; ++j) {
     double bu = 0.0;
@@ -232,8 +248,10 @@ __device__ __forceinline__ void route_sort(uint32_t (&v)[N]) {
 // z: this lane's logits (experts lane NV + i; NaN already -infinity, past E anything); b: their biases (0 without
 // one); bias: where they come from (or NULL); `logit(e)`: the logit of expert e again, by any lane.  topk_idx, topk_w: this token's [k]; sel_out (may be
 // NULL): the same ids; near_tie (may be NULL) as colibri_moe_debug_routing documents it.
-template <int NV, typename Logit>
-__device__ __forceinline__ void route_token(const coli_route_desc& r, const float (&z)[NV], const float (&b)[NV],
+// EXACT = false: returns whether a decision was closer than the scores' error (warp-uniform); its results are then
+// to be replaced by route_token_exact's.
+template <int NV, bool EXACT, typename Logit>
+__device__ __forceinline__ bool route_token(const coli_route_desc& r, const float (&z)[NV], const float (&b)[NV],
                                             const float* bias, Logit logit, int32_t* topk_idx, float* topk_w, int* sel_out,
                                             int32_t* near_tie) {
   const int lane = threadIdx.x & 31;
@@ -275,7 +293,7 @@ __device__ __forceinline__ void route_token(const coli_route_desc& r, const floa
   smax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(smax)));
   route_sort<NV>(v);
   const float tol_s = route_tol(softmax, smax);
-  bool tie = false;                      // a decision closer than kNearTie
+  bool tie = false, again = false;       // a decision closer than kNearTie, than the scores' error
 
   // groups
   unsigned open = 0xffffffffu;           // kept groups
@@ -343,14 +361,15 @@ __device__ __forceinline__ void route_token(const coli_route_desc& r, const floa
     const float c = __shfl_sync(0xffffffffu, sc, __ffs(__ballot_sync(0xffffffffu, rank == r.topk_group)) - 1);
     const float gap = a == c ? 0.f : a - c;
     mag = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mag)));
-    const float tol = 2.f * tol_s + (1e-6f + 4.f * kCut) * mag;   // each term and sum rounds by 2^-24 of mag or 2 mag
+    const float tol = 2.f * tol_s + (1e-6f + 3.f * kCut) * mag;   // each term and sum rounds by 2^-24 of mag or 2 mag
     tie = gap < kNearTie + 4.f * kCut * mag;
     // lane g holds group g's score and whether it is kept
     const int from = whole ? (lane * lanes) & 31 : lane;
     const float score = __shfl_sync(0xffffffffu, sc, from);
     open = __ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, rank, from) < r.topk_group && lane < G);
-    if (gap <= tol && a > -INFINITY)
-      open = route_groups_exact<NV>(r, logit, bias, st, score, a, tol, tol_s + (5e-7f + 2.f * kCut) * mag);
+    again = gap <= tol && a > -INFINITY;
+    if (EXACT && again)
+      open = route_groups_exact<NV>(r, logit, bias, st, score, a, tol, tol_s + (5e-7f + 1.5f * kCut) * mag);
     if (whole) {
       if (!(mine < G && ((open >> (mine & 31)) & 1u)))
 #pragma unroll
@@ -386,9 +405,11 @@ __device__ __forceinline__ void route_token(const coli_route_desc& r, const floa
   if (nxt) {
     const float a = route_unimage(kth & ~kIdx), c = route_unimage(nxt & ~kIdx);
     const float gap = a == c ? 0.f : a - c;
-    const float tol = tol_s + (5e-7f + 4.f * kCut) * fabsf(a);
+    const float tol = tol_s + (2e-7f + 1.5f * kCut) * fabsf(a);
     tie |= gap < kNearTie + 2.f * kCut * fabsf(a);
-    if (gap <= tol && a > -INFINITY)
+    const bool close = gap <= tol && a > -INFINITY;
+    again |= close;
+    if (EXACT && close)
       pick = route_picks_exact<NV>(r, logit, bias, st, open, a, tol, pick, __shfl_sync(0xffffffffu, pick, k - 1));
   }
   if (near_tie && lane == 0) *near_tie = tie ? 1 : 0;
@@ -414,6 +435,23 @@ __device__ __forceinline__ void route_token(const coli_route_desc& r, const floa
     if (sel_out) sel_out[rank] = pick;
   }
   __syncwarp();
+  return again;
+}
+
+// The same with exact decisions, for the few tokens that need it: from the start, out of line and last, so that it
+// costs the other tokens neither registers nor stores (calls amid the selection cost every token 130 instructions).
+template <int NV, typename Logit>
+__device__ __noinline__ void route_token_exact(const coli_route_desc r, const float* bias, Logit logit,
+                                               int32_t* topk_idx, float* topk_w, int* sel_out, int32_t* near_tie) {
+  const int lane = threadIdx.x & 31;
+  float z[NV], b[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane * NV + i;
+    z[i] = e < r.E ? logit(e) : -INFINITY;
+    b[i] = bias && e < r.E ? __ldg(bias + e) : 0.f;
+  }
+  route_token<NV, true>(r, z, b, bias, logit, topk_idx, topk_w, sel_out, near_tie);
 }
 
 }  // namespace coli

@@ -332,8 +332,10 @@ __device__ __forceinline__ void routed_token_nv(const FwdArgs& a, int t, int* se
     z[i] = e < a.E ? logit(e) : -INFINITY;
     b[i] = e < a.E ? __ldg(a.bias + e) : 0.f;
   }
-  route_token<NV>(a.route, z, b, a.bias, logit, a.topk_idx + (size_t)t * a.k, a.topk_w + (size_t)t * a.k, sel_out,
-                  a.near_tie + t);
+  int32_t* idx = a.topk_idx + (size_t)t * a.k;
+  float* w = a.topk_w + (size_t)t * a.k;
+  if (route_token<NV, false>(a.route, z, b, a.bias, logit, idx, w, sel_out, a.near_tie + t))
+    route_token_exact<NV>(a.route, a.bias, logit, idx, w, sel_out, a.near_tie + t);
 }
 
 __device__ __forceinline__ void routed_token(const FwdArgs& a, int t, int* sel_out) {
