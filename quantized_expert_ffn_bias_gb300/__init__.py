@@ -182,6 +182,14 @@ def _stream(s) -> int | None:
     return s.cuda_stream
 
 
+def _ptrs(*v) -> tuple:
+    """Pointers of several arguments; the usual ones are tensors."""
+    try:
+        return tuple([x.data_ptr() for x in v])
+    except AttributeError:
+        return tuple([_ptr(x) for x in v])
+
+
 def _check(rc: int):
     if rc:
         raise ColiError(rc, lib().colibri_moe_last_error().decode(errors="replace"))
@@ -238,10 +246,9 @@ def colibri_moe_route(desc: coli_route_desc, T: int, logits, ltype: int, logit_s
 def colibri_kv_step(desc: coli_kv_desc, B: int, n_tokens: int, new_len, seq_len, held, block_table, free_pages,
                     free_count, seq_len_out, held_out, free_count_out, q_start, position, slot, status, stream=None):
     """One step of the paged cache's bookkeeping (see the header): pages, q_start, positions and slots."""
-    _check(lib().colibri_kv_step(ctypes.byref(desc), B, n_tokens, _ptr(new_len), _ptr(seq_len), _ptr(held),
-                                 _ptr(block_table), _ptr(free_pages), _ptr(free_count), _ptr(seq_len_out),
-                                 _ptr(held_out), _ptr(free_count_out), _ptr(q_start), _ptr(position), _ptr(slot),
-                                 _ptr(status), _stream(stream)))
+    _check(lib().colibri_kv_step(ctypes.byref(desc), B, n_tokens,
+                                 *_ptrs(new_len, seq_len, held, block_table, free_pages, free_count, seq_len_out,
+                                        held_out, free_count_out, q_start, position, slot, status), _stream(stream)))
 
 
 def colibri_kv_append(desc: coli_kv_desc, n_tokens: int, n_valid, latent, latent_stride: int, rope, rope_stride: int,

@@ -26,6 +26,8 @@
 // selected) with their key tiles, dealt in equal runs of key tiles to one CTA
 // per SM (or gang of CTAs).  A unit cut by a border leaves partial results in
 // the workspace, which the join kernel adds up in order.
+#include <atomic>
+
 #include "plan.h"
 
 namespace coli {
@@ -45,6 +47,7 @@ constexpr int at_threads(bool tma) { return (1 + kAtSmWarps + (tma ? 1 : kAtLoad
 constexpr int kAtMinBox = 8;                       // fewest key rows a TMA box has
 constexpr int kAtMaxCtas = 160;                    // CTAs the workspace has room for
 constexpr int kAtMaxB = 8192, kAtMaxH = 1024;
+constexpr int kAtMaxDevices = 64;                  // devices whose properties are kept between calls
 constexpr size_t kAtSmem = (size_t)kAtBoxes * (kAtBoxBytes + kAtQBoxBytes) + 1024;
 constexpr int kAtPart = kAtRows * kAtV;            // floats of a partial O
 constexpr float kAtUnset = -1e30f;                 // reference of a part whose row has seen no key
@@ -1119,11 +1122,16 @@ static CUresult at_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m,
 
 template <bool BF16, bool TMA>
 static cudaError_t at_launch(const AtArgs& a, const CUtensorMap& kmap, const CUtensorMap& qmap, int ctas,
-                             cudaStream_t st) {
+                             int dev, cudaStream_t st) {
   static_assert((size_t)(3 * kAtMaxB + 2) * sizeof(int) + 1024 <= kAtSmem, "the plan's arrays");
-  cudaError_t e =
-      cudaFuncSetAttribute(kv_attention_kernel<BF16, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem);
-  if (e != cudaSuccess) return e;
+  // once a device: setting it again costs as much as a tenth of a launch
+  static std::atomic<bool> set[kAtMaxDevices];
+  cudaError_t e = cudaSuccess;
+  if (dev >= kAtMaxDevices || !set[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kv_attention_kernel<BF16, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAtSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < kAtMaxDevices) set[dev].store(true, std::memory_order_relaxed);
+  }
   e = launch_pdl(kv_attention_kernel<BF16, TMA>, dim3(ctas), dim3(at_threads(TMA)), kAtSmem, st, a, kmap, qmap);
   if (e != cudaSuccess) return e;
   return launch_pdl(kv_attention_join_kernel<BF16>, dim3(kAtJoinCtas), dim3(kAtJoinThreads), 0, st, a, ctas);
@@ -1182,7 +1190,12 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
                 w.max_units, tiles);
   int dev = 0, sms = 0;
   cudaError_t ce = cudaGetDevice(&dev);
-  if (ce == cudaSuccess) ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  static std::atomic<int> known_sms[kAtMaxDevices];
+  if (ce == cudaSuccess && dev < kAtMaxDevices) sms = known_sms[dev].load(std::memory_order_relaxed);
+  if (ce == cudaSuccess && !sms) {
+    ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (ce == cudaSuccess && dev < kAtMaxDevices) known_sms[dev].store(sms, std::memory_order_relaxed);
+  }
   if (ce != cudaSuccess) return cuda_fail(ce, "kv_attention: device query");
   const bool bf16 = desc->dtype == COLI_X_BF16;
   // TMA boxes where pages are whole boxes and query rows evenly spaced; else the copying kernel
@@ -1231,8 +1244,8 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   a.wait_ns = kWaitLimitNs;
   const int ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (tma) ce = bf16 ? at_launch<true, true>(a, kmap, qmap, ctas, st) : at_launch<false, true>(a, kmap, qmap, ctas, st);
-  else ce = bf16 ? at_launch<true, false>(a, kmap, qmap, ctas, st) : at_launch<false, false>(a, kmap, qmap, ctas, st);
+  if (tma) ce = bf16 ? at_launch<true, true>(a, kmap, qmap, ctas, dev, st) : at_launch<false, true>(a, kmap, qmap, ctas, dev, st);
+  else ce = bf16 ? at_launch<true, false>(a, kmap, qmap, ctas, dev, st) : at_launch<false, false>(a, kmap, qmap, ctas, dev, st);
   return ce == cudaSuccess ? COLI_OK : cuda_fail(ce, "kv_attention: launch");
 }
 

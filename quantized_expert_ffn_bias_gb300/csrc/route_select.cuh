@@ -181,33 +181,21 @@ __device__ __noinline__ unsigned route_groups_exact(const coli_route_desc r, Log
   return __ballot_sync(0xffffffffu, in || (close && rank < r.topk_group));
 }
 
-// The picks (lane j < k: the j-th), by exact scores where the fp32 ones are within tol of the last pick's, `a`,
-// which is expert e_k's.  Where every expert around the border has that one's logit and bias, the picks stand.
+// The picks (lane j < k: the j-th), by exact scores where the fp32 ones are within tol of the last pick's, `a`.
 template <int NV, typename Logit>
 __device__ __noinline__ int route_picks_exact(const coli_route_desc r, Logit logit, const float* bias, RouteStats st,
-                                              unsigned open, float a, float tol, int pick, int e_k) {
+                                              unsigned open, float a, float tol, int pick) {
   const int lane = threadIdx.x & 31, gsz = r.E / r.n_group;
-  const float zk = logit(e_k), bk = bias ? __ldg(bias + e_k) : 0.f;
-  float z[NV], b[NV];
+  const RouteAgain<NV> x(r, logit, bias, st);
   unsigned left = 0;                     // this lane's candidates around the border
   int sure = 0;                          // candidates certainly above it: the first picks
-  bool other = false;
   for (int i = 0; i < NV; ++i) {
     const int e = lane * NV + i;
     if (e >= r.E || !((open >> (e / gsz)) & 1u)) continue;
-    z[i] = logit(e);
-    b[i] = bias ? __ldg(bias + e) : 0.f;
-    const float v = route_unimage(
-        route_key(r.score == COLI_SCORE_SOFTMAX ? route_numerator(z[i], st.m) * st.inv : route_sigmoid(z[i]), b[i]));
-    if (v > a + tol) {
-      ++sure;
-    } else if (v >= a - tol) {
-      left |= 1u << i;
-      other |= z[i] != zk || b[i] != bk;
-    }
+    const float v = route_unimage(x.key[i]);
+    if (v > a + tol) ++sure;
+    else if (v >= a - tol) left |= 1u << i;
   }
-  if (!__any_sync(0xffffffffu, other)) return pick;
-  const RouteAgain<NV> x(r, logit, bias, st);
   double u[NV];
   x.exact(left, u);
   sure = __reduce_add_sync(0xffffffffu, sure);
@@ -407,10 +395,24 @@ __device__ __forceinline__ bool route_token(const coli_route_desc& r, const floa
     const float gap = a == c ? 0.f : a - c;
     const float tol = tol_s + (2e-7f + 1.5f * kCut) * fabsf(a);
     tie |= gap < kNearTie + 2.f * kCut * fabsf(a);
-    const bool close = gap <= tol && a > -INFINITY;
+    bool close = gap <= tol && a > -INFINITY;
+    if (close) {
+      // unless every candidate around the border has the last pick's logit and bias: those tie exactly
+      const int e_k = __shfl_sync(0xffffffffu, pick, k - 1), gsz = E / r.n_group;
+      const float zk = logit(e_k), bk = bias ? __ldg(bias + e_k) : 0.f;
+      bool other = false;
+#pragma unroll 1
+      for (int i = 0; i < NV && i < n_here; ++i) {
+        const int e = lane * NV + i;
+        const float ze = logit(e), be = bias ? __ldg(bias + e) : 0.f;
+        const float ue = (softmax ? route_numerator(ze, st.m) * st.inv : route_sigmoid(ze)) + be;
+        other |= fabsf(ue - a) <= 2.f * tol && (ze != zk || be != bk) && ((open >> (e / gsz)) & 1u);
+      }
+      close = __any_sync(0xffffffffu, other);
+    }
     again |= close;
     if (EXACT && close)
-      pick = route_picks_exact<NV>(r, logit, bias, st, open, a, tol, pick, __shfl_sync(0xffffffffu, pick, k - 1));
+      pick = route_picks_exact<NV>(r, logit, bias, st, open, a, tol, pick);
   }
   if (near_tie && lane == 0) *near_tie = tie ? 1 : 0;
 
