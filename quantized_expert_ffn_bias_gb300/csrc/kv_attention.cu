@@ -74,25 +74,6 @@ struct __align__(16) AtJoin {
   int pad[2];
 };
 
-// Division of 0 <= x < 2^31 by a divisor known at the launch, as a multiplication and two shifts (Granlund and
-// Montgomery 1994): the loader divides on its way to every tile.
-struct FastDiv {
-  unsigned mul, s1, s2;
-  int d;
-  void set(int div) {
-    d = div;
-    int l = 0;
-    while ((1ll << l) < div) ++l;
-    mul = (unsigned)((((1ull << l) - (unsigned)div) << 32) / (unsigned)div + 1);
-    s1 = l < 1 ? l : 1;
-    s2 = l < 1 ? 0 : l - 1;
-  }
-  __device__ __forceinline__ int operator()(int x) const {
-    const unsigned t = __umulhi(mul, (unsigned)x);
-    return (int)((t + (((unsigned)x - t) >> s1)) >> s2);
-  }
-};
-
 struct AtArgs {
   coli_kv_desc d;
   FastDiv by_page, by_heads;         // page_size, H

@@ -9,7 +9,9 @@
 // visible and ends every CTA's reading of the inputs (so the outputs may be
 // the inputs' arrays), then the new pages, the token rows and the requests'
 // results are dealt over the cluster's threads.  What bounds it is latency:
-// the launch, two dependent loads a token and the scans' barriers.
+// the launch, the loads of the lengths and of a token's page, the scan's
+// barriers (one scan where everything can be served, sums in 32 bits where
+// the sizes allow it: 14.3 -> 12.3 us a call for 500 requests of 13,000 tokens).
 #include "plan.h"
 
 namespace coli {
@@ -23,37 +25,42 @@ struct StepArgs {
   int32_t *table, *free_pages;
   const int32_t* free_count;
   int32_t *seq_out, *held_out, *count_out, *q_start, *position, *slot, *status;
+  FastDiv by_page;
 };
 
+template <typename I>
 struct Sum3 {
-  long long a, b, c;
+  I a, b, c;
 };
 
 // Block-wide exclusive sums of three values a thread (1024 threads); *total: the block's sums.
-__device__ __forceinline__ Sum3 scan3(Sum3 v, Sum3* warp_tot, Sum3* total) {
+template <typename I>
+__device__ __forceinline__ Sum3<I> scan3(Sum3<I> v, Sum3<I>* warp_tot, Sum3<I>* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto warp_inc = [lane](long long x) {
+  auto warp_inc = [lane](Sum3<I> x) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long n = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += n;
+      const Sum3<I> n{__shfl_up_sync(0xffffffffu, x.a, o), __shfl_up_sync(0xffffffffu, x.b, o),
+                      __shfl_up_sync(0xffffffffu, x.c, o)};
+      if (lane >= o) {
+        x.a += n.a;
+        x.b += n.b;
+        x.c += n.c;
+      }
     }
     return x;
   };
-  Sum3 inc{warp_inc(v.a), warp_inc(v.b), warp_inc(v.c)};
+  const Sum3<I> inc = warp_inc(v);
   if (lane == 31) warp_tot[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    const Sum3 w = warp_tot[lane];
-    const Sum3 wi{warp_inc(w.a), warp_inc(w.b), warp_inc(w.c)};
-    warp_tot[lane] = Sum3{wi.a - w.a, wi.b - w.b, wi.c - w.c};
+    const Sum3<I> w = warp_tot[lane], wi = warp_inc(w);
+    warp_tot[lane] = Sum3<I>{wi.a - w.a, wi.b - w.b, wi.c - w.c};
     if (lane == 31) *total = wi;
   }
   __syncthreads();
-  const Sum3 base = warp_tot[warp];
-  const Sum3 r{base.a + inc.a - v.a, base.b + inc.b - v.b, base.c + inc.c - v.c};
-  __syncthreads();
-  return r;
+  const Sum3<I> base = warp_tot[warp];
+  return Sum3<I>{base.a + inc.a - v.a, base.b + inc.b - v.b, base.c + inc.c - v.c};
 }
 
 // Last i in [0, n) with first[i] <= x (first ascending, first[0] <= x).
@@ -67,124 +74,134 @@ __device__ __forceinline__ int last_at_most(const int* first, int n, int x) {
   return lo;
 }
 
+// I: type of the sums (64 bits where 8192 requests of wrong lengths could leave 32).
+template <typename I>
 __global__ void __launch_bounds__(kStepThreads, 1) kv_step_kernel(const StepArgs p) {
   extern __shared__ int step_sm[];
+  const int B = p.B;
   int* qs = step_sm;                 // [B + 1] first token row
-  int* pp = qs + p.B + 1;            // [B + 1] first new page (before that: first freed page)
-  int* seq = pp + p.B + 1;           // [B] tokens before the step
-  int* hold = seq + p.B;             // [B] pages before the step
-  __shared__ Sum3 warp_tot[32], total;
-  __shared__ int s_count;
+  int* pp = qs + B + 1;              // [B + 1] first new page
+  int* seq = pp + B + 1;             // [B] tokens before the step
+  int* hold = seq + B;               // [B] pages before the step
+  int* add = hold + B;               // [B] new tokens; -1: finished; -2: lengths that are not valid
+  int* back = add + B;               // [B] first place of a finished request's pages among those that return
+  __shared__ Sum3<I> warp_tot[32], total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = blockIdx.x, ps = p.d.page_size, B = p.B;
-  if (tid == 0) s_count = *p.free_count;
-
-  // a request's lengths: what it frees, asks for, and whether it can be served at all
-  struct Req {
-    int add, seq, held;
-    long long need;
-    bool dead, ok, wrong;
-  };
-  auto request = [&](int b) {
-    Req r;
-    const int n = p.new_len[b];
-    r.seq = p.seq_len[b];
-    r.held = p.held[b];
-    r.dead = n < 0;
-    const bool fine = r.held >= 0 && r.held <= p.d.max_pages;
-    if (!fine) r.held = 0;
-    const long long after = (long long)r.seq + (n > 0 ? n : 0), pages = (after + ps - 1) / ps;
-    r.ok = fine && !r.dead && r.seq >= 0 && r.seq <= (long long)r.held * ps && pages <= p.d.max_pages;
-    r.wrong = !r.ok && !(fine && r.dead);
-    r.add = r.ok ? n : 0;
-    r.need = r.ok && pages > r.held ? pages - r.held : 0;
-    return r;
-  };
+  const int rank = blockIdx.x, ps = p.d.page_size;
+  const int count_in = *p.free_count;
   int bits = 0;
+  // pages for n more tokens (seq + n <= max_pages * page_size < 2^31)
+  auto need_of = [&](int s, int n, int h) { return max(0, p.by_page((int)((unsigned)s + n + ps - 1)) - h); };
 
-  // scan 1: pages freed, pages wanted, tokens wanted
-  Sum3 carry{0, 0, 0};
+  // sums over the requests: pages that return, pages wanted, tokens wanted
+  Sum3<I> carry{0, 0, 0};
   for (int base = 0; base < B; base += kStepThreads) {
     const int b = base + tid;
-    Req r{};
-    if (b < B) r = request(b);
-    const Sum3 v{b < B && r.dead ? r.held : 0, r.need, r.add};
-    const Sum3 e = scan3(v, warp_tot, &total);
+    Sum3<I> v{0, 0, 0};
     if (b < B) {
-      seq[b] = r.seq;
-      hold[b] = r.held;
-      pp[b] = (int)min(carry.a + e.a, (long long)p.d.n_pages);
+      const int n = p.new_len[b], s = p.seq_len[b];
+      int h = p.held[b];
+      const bool fine = h >= 0 && h <= p.d.max_pages;
+      if (!fine) h = 0;
+      int a;
+      if (n < 0) {
+        a = -1;
+        v.a = h;
+        if (!fine) bits |= COLI_DEV_KV_TABLE_FULL;
+      } else if (fine && s >= 0 && s <= (long long)h * ps && (long long)s + n <= (long long)p.d.max_pages * ps) {
+        a = n;
+        v.b = need_of(s, n, h);
+        v.c = min(n, p.n_tokens + 1);      // (more than there is room for is as good as all of it)
+      } else {
+        a = -2;
+        bits |= COLI_DEV_KV_TABLE_FULL;
+      }
+      seq[b] = s;
+      hold[b] = h;
+      add[b] = a;
+    }
+    const Sum3<I> e = scan3(v, warp_tot, &total);
+    if (b < B) {
+      back[b] = (int)min((long long)(carry.a + e.a), (long long)p.d.n_pages);
+      pp[b] = (int)min((long long)(carry.b + e.b), 0x7fffffffLL);
+      qs[b] = (int)min((long long)(carry.c + e.c), 0x7fffffffLL);
     }
     carry.a += total.a;
     carry.b += total.b;
     carry.c += total.c;
     __syncthreads();
   }
-  const int count0 = max(0, min(s_count, p.d.n_pages));
+  const int count0 = max(0, min(count_in, p.d.n_pages));
   // more pages than the cache has can only come from wrong inputs: they are dropped
-  const int avail = (int)min((long long)p.d.n_pages, count0 + carry.a);
-  if (count0 + carry.a > p.d.n_pages || s_count != count0) bits |= COLI_DEV_KV_BAD_PAGE;
+  const int avail = (int)min((long long)p.d.n_pages, (long long)count0 + carry.a);
+  if ((long long)count0 + carry.a > p.d.n_pages || count_in != count0) bits |= COLI_DEV_KV_BAD_PAGE;
   // push the finished requests' pages (a warp per request, dealt over the cluster)
-  for (int b = rank * 32 + warp; b < B; b += kStepCtas * 32) {
-    if (p.new_len[b] >= 0) continue;
-    for (int i = lane; i < hold[b]; i += 32) {
-      const long long at = (long long)count0 + pp[b] + i;
-      if (at < p.d.n_pages) p.free_pages[at] = p.table[(size_t)b * p.d.max_pages + i];
+  if (carry.a > 0)
+    for (int b = rank * 32 + warp; b < B; b += kStepCtas * 32) {
+      if (add[b] != -1) continue;
+      for (int i = lane; i < hold[b]; i += 32) {
+        const long long at = (long long)count0 + back[b] + i;
+        if (at < p.d.n_pages) p.free_pages[at] = p.table[(size_t)b * p.d.max_pages + i];
+      }
     }
-  }
-  const bool all_fit = carry.b <= avail && carry.c <= p.n_tokens;
-  __syncthreads();                   // pp's freed pages are read
-
-  // scan 2: what is served.  A request is served when what it and those before it ask for is there.
-  Sum3 ask{0, 0, 0}, given{0, 0, 0};
-  for (int base = 0; base < B; base += kStepThreads) {
-    const int b = base + tid;
-    Req r{};
-    if (b < B) r = request(b);
-    bool serve = b < B && r.ok;
-    if (!all_fit) {
-      const Sum3 e = scan3(Sum3{0, r.need, r.add}, warp_tot, &total);
-      if (serve && r.need > 0 && ask.b + e.b + r.need > avail) { serve = false; bits |= COLI_DEV_KV_NO_PAGES; }
-      if (b < B && r.ok && r.add > 0 && ask.c + e.c + r.add > p.n_tokens) { serve = false; bits |= COLI_DEV_KV_TOKENS; }
-      ask.b += total.b;
-      ask.c += total.c;
+  int n_new = (int)min((long long)carry.b, 0x7fffffffLL), n_rows = (int)min((long long)carry.c, 0x7fffffffLL);
+  if (carry.b > avail || carry.c > p.n_tokens) {
+    // Not everything can be served: a request is when what it and those before it ask for is there (the sums so
+    // far); the served ones' sums follow.
+    __syncthreads();
+    Sum3<I> given{0, 0, 0};
+    for (int base = 0; base < B; base += kStepThreads) {
+      const int b = base + tid;
+      int need = 0, want = 0;
+      if (b < B && add[b] >= 0) {
+        need = need_of(seq[b], add[b], hold[b]);
+        want = add[b];
+        const bool pages = need > 0 && (long long)pp[b] + need > avail;
+        const bool rows = want > 0 && (long long)qs[b] + min(want, p.n_tokens + 1) > p.n_tokens;
+        if (pages) bits |= COLI_DEV_KV_NO_PAGES;
+        if (rows) bits |= COLI_DEV_KV_TOKENS;
+        if (pages || rows) {
+          need = want = 0;
+          add[b] = -2;
+        }
+      }
+      const Sum3<I> e = scan3(Sum3<I>{0, (I)need, (I)want}, warp_tot, &total);
+      if (b < B) {
+        pp[b] = (int)(given.b + e.b);
+        qs[b] = (int)(given.c + e.c);
+      }
+      given.b += total.b;
+      given.c += total.c;
       __syncthreads();
     }
-    if (b < B && r.wrong) bits |= COLI_DEV_KV_TABLE_FULL;
-    const Sum3 e = scan3(Sum3{0, serve ? r.need : 0, serve ? r.add : 0}, warp_tot, &total);
-    if (b < B) {
-      pp[b] = (int)(given.b + e.b);
-      qs[b] = (int)(given.c + e.c);
-    }
-    given.b += total.b;
-    given.c += total.c;
-    __syncthreads();
+    n_new = (int)given.b;
+    n_rows = (int)given.c;
   }
   if (tid == 0) {
-    pp[B] = (int)given.b;
-    qs[B] = (int)given.c;
+    pp[B] = n_new;
+    qs[B] = n_rows;
   }
   // every CTA has read the inputs, every push is visible
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  __syncthreads();
 
   const int gtid = rank * kStepThreads + tid, gthreads = kStepCtas * kStepThreads;
   auto popped = [&](int i) { return __ldcg(p.free_pages + (avail - 1 - i)); };   // the i-th new page
-  const int n_new = pp[B], n_rows = qs[B];
-  for (int j = gtid; j < n_new; j += gthreads) {
-    const int b = last_at_most(pp, B, j);
-    p.table[(size_t)b * p.d.max_pages + hold[b] + (j - pp[b])] = popped(j);
-  }
   for (int i = gtid; i < n_rows; i += gthreads) {
     const int b = last_at_most(qs, B, i);
-    const int pos = seq[b] + (i - qs[b]), col = pos / ps;
+    const int pos = seq[b] + (i - qs[b]), col = p.by_page(pos);
     const int page = col < hold[b] ? p.table[(size_t)b * p.d.max_pages + col] : popped(pp[b] + col - hold[b]);
     const bool in = page >= 0 && page < p.d.n_pages;
     if (!in) bits |= COLI_DEV_KV_BAD_PAGE;
     p.position[i] = pos;
-    p.slot[i] = in ? page * ps + pos % ps : -1;
+    p.slot[i] = in ? page * ps + (pos - col * ps) : -1;
+  }
+  for (int j = gtid; j < n_new; j += gthreads) {
+    const int b = last_at_most(pp, B, j);
+    p.table[(size_t)b * p.d.max_pages + hold[b] + (j - pp[b])] = popped(j);
   }
   for (int b = gtid; b < B; b += gthreads) {
-    const bool dead = p.new_len[b] < 0;
+    const bool dead = add[b] == -1;
     p.q_start[b] = qs[b];
     p.seq_out[b] = dead ? 0 : seq[b] + (qs[b + 1] - qs[b]);
     p.held_out[b] = dead ? 0 : hold[b] + (pp[b + 1] - pp[b]);
@@ -197,12 +214,16 @@ __global__ void __launch_bounds__(kStepThreads, 1) kv_step_kernel(const StepArgs
 }
 
 // ------------------------------------------------------------------ append
-// A copy: 72 16-byte pieces a row, one a thread and pass, kAppendUnroll passes' loads in flight.  Bound by
-// HBM for large batches, by the launch for small ones.
-constexpr int kAppendThreads = 256, kAppendUnroll = 4, kRowPieces = COLI_KV_WIDTH * 2 / 16;
+// A copy, bound by HBM for large batches (75.5 MB for 32768 rows), by the launch for small ones.  A row has 72
+// pieces of 16 bytes, so four rows are nine full rounds of a warp, all of whose loads are in flight before the
+// first store; the rows' slots are read once, by four lanes.
+constexpr int kAppendWarps = 8, kAppendRows = 4, kRowPieces = COLI_KV_WIDTH * 2 / 16;
+constexpr int kAppendRounds = kAppendRows * kRowPieces / 32;
+static_assert(kAppendRounds * 32 == kAppendRows * kRowPieces, "whole rounds");
 
 struct AppendArgs {
   int n, page_size, n_pages;
+  FastDiv by_page;
   long long page_stride;             // bytes
   const int32_t* n_valid;
   const uint8_t *latent, *rope;
@@ -211,29 +232,32 @@ struct AppendArgs {
   uint8_t* cache;
 };
 
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs p) {
-  const int n = p.n_valid ? max(0, min(p.n, *p.n_valid)) : p.n;
-  const long long pieces = (long long)n * kRowPieces, step = (long long)gridDim.x * kAppendThreads;
-  for (long long i0 = (long long)blockIdx.x * kAppendThreads + threadIdx.x; i0 < pieces; i0 += kAppendUnroll * step) {
-    uint4 v[kAppendUnroll];
-    uint8_t* to[kAppendUnroll];
+__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const AppendArgs p) {
+  const int lane = threadIdx.x & 31;
+  const int row0 = (blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) * kAppendRows;
+  const int n = p.n_valid ? min(p.n, *p.n_valid) : p.n;
+  if (row0 >= n) return;
+  // lanes 0..3: where the rows go (-1: nowhere)
+  long long to = -1;
+  if (lane < kAppendRows && row0 + lane < n) {
+    const int s = p.slot[row0 + lane], page = p.by_page(max(s, 0));
+    if (s >= 0 && page < p.n_pages) to = page * p.page_stride + (long long)(s - page * p.page_size) * (COLI_KV_WIDTH * 2);
+  }
+  uint4 v[kAppendRounds];
 #pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u) {
-      const long long i = i0 + u * step;
-      to[u] = nullptr;
-      if (i >= pieces) continue;
-      const int row = (int)(i / kRowPieces), c = (int)(i - (long long)row * kRowPieces);
-      const int s = __ldg(p.slot + row);
-      v[u] = c < COLI_KV_VALUE * 2 / 16
+  for (int i = 0; i < kAppendRounds; ++i) {
+    const int piece = i * 32 + lane, r = piece / kRowPieces, c = piece - r * kRowPieces, row = row0 + r;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (row < n)
+      v[i] = c < COLI_KV_VALUE * 2 / 16
                  ? *reinterpret_cast<const uint4*>(p.latent + row * p.latent_stride + c * 16)
                  : *reinterpret_cast<const uint4*>(p.rope + row * p.rope_stride + (c - COLI_KV_VALUE * 2 / 16) * 16);
-      const int page = s / p.page_size;
-      if (s >= 0 && page < p.n_pages)
-        to[u] = p.cache + page * p.page_stride + (long long)(s - page * p.page_size) * (COLI_KV_WIDTH * 2) + c * 16;
-    }
+  }
 #pragma unroll
-    for (int u = 0; u < kAppendUnroll; ++u)
-      if (to[u]) *reinterpret_cast<uint4*>(to[u]) = v[u];
+  for (int i = 0; i < kAppendRounds; ++i) {
+    const int piece = i * 32 + lane, r = piece / kRowPieces, c = piece - r * kRowPieces;
+    const long long at = __shfl_sync(0xffffffffu, to, r);
+    if (at >= 0) *reinterpret_cast<uint4*>(p.cache + at + c * 16) = v[i];
   }
 }
 
@@ -273,12 +297,15 @@ coli_status colibri_kv_step(const coli_kv_desc* desc, int B, int n_tokens, const
   }
   if (n_tokens > 0 && (!position || !slot)) return fail(COLI_EINVAL, "kv_step: null pointer");
   if (!aligned(position, 4) || !aligned(slot, 4)) return fail(COLI_EALIGN, "kv_step: a pointer is not 4-byte aligned");
-  const StepArgs a{*desc, B, n_tokens, new_len, seq_len, held, block_table, free_pages, free_count, seq_len_out,
-                   held_out, free_count_out, q_start, position, slot, status};
-  const size_t smem = (size_t)(4 * B + 2) * 4;
+  StepArgs a{*desc, B, n_tokens, new_len, seq_len, held, block_table, free_pages, free_count, seq_len_out,
+             held_out, free_count_out, q_start, position, slot, status, {}};
+  a.by_page.set(desc->page_size);
+  const bool wide = (long long)B * desc->max_pages > 0x3fffffffLL || (long long)B * ((long long)n_tokens + 1) > 0x3fffffffLL;
+  auto kern = wide ? kv_step_kernel<long long> : kv_step_kernel<int>;
+  const size_t smem = (size_t)(6 * B + 2) * 4;
   cudaError_t ce = cudaSuccess;
   if (smem > 40 * 1024)
-    ce = cudaFuncSetAttribute(kv_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (4 * kStepMaxB + 2) * 4);
+    ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (6 * kStepMaxB + 2) * 4);
   if (ce != cudaSuccess) return cuda_fail(ce, "kv_step");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kStepCtas);
@@ -292,7 +319,7 @@ coli_status colibri_kv_step(const coli_kv_desc* desc, int B, int n_tokens, const
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  ce = cudaLaunchKernelEx(&cfg, kv_step_kernel, a);
+  ce = cudaLaunchKernelEx(&cfg, kern, a);
   return ce == cudaSuccess ? COLI_OK : cuda_fail(ce, "kv_step");
 }
 
@@ -320,10 +347,9 @@ coli_status colibri_kv_append(const coli_kv_desc* desc, int n_tokens, const int3
   a.rope_stride = rope_stride * 2;
   a.slot = slot;
   a.cache = static_cast<uint8_t*>(cache);
-  const long long pieces = (long long)n_tokens * kRowPieces;
-  const long long want = (pieces + kAppendThreads - 1) / kAppendThreads;
-  const int grid = (int)(want < 152 * 8 ? want : 152 * 8);
-  kv_append_kernel<<<grid, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  a.by_page.set(desc->page_size);
+  constexpr int kRows = kAppendWarps * kAppendRows;
+  kv_append_kernel<<<n_tokens / kRows + (n_tokens % kRows ? 1 : 0), kAppendWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
   const cudaError_t ce = cudaGetLastError();
   return ce == cudaSuccess ? COLI_OK : cuda_fail(ce, "kv_append");
 }

@@ -216,6 +216,27 @@ __host__ __device__ constexpr int prefill_raw_row_bytes(int qtype, bool gate_up)
   return qtype == COLI_Q_INT4_G128 ? prefill_stage_k(gate_up) / 2 : prefill_stage_k(gate_up);
 }
 
+// Division of 0 <= x < 2^31 by a divisor known at the launch, as a multiplication and two shifts (Granlund and
+// Montgomery 1994): page tables are looked up with it on the way to every key.
+struct FastDiv {
+  unsigned mul, s1, s2;
+  int d;
+  void set(int div) {
+    d = div;
+    int l = 0;
+    while ((1ll << l) < div) ++l;
+    mul = (unsigned)((((1ull << l) - (unsigned)div) << 32) / (unsigned)div + 1);
+    s1 = l < 1 ? l : 1;
+    s2 = l < 1 ? 0 : l - 1;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int x) const {
+    const unsigned t = __umulhi(mul, (unsigned)x);
+    return (int)((t + (((unsigned)x - t) >> s1)) >> s2);
+  }
+#endif
+};
+
 // ---------------------------------------------------------------- device helpers
 
 #ifdef __CUDACC__
