@@ -182,12 +182,12 @@ def _stream(s) -> int | None:
     return s.cuda_stream
 
 
-def _ptrs(*v) -> tuple:
+def _ptrs(*v) -> list:
     """Pointers of several arguments; the usual ones are tensors."""
     try:
-        return tuple([x.data_ptr() for x in v])
+        return [x.data_ptr() for x in v]
     except AttributeError:
-        return tuple([_ptr(x) for x in v])
+        return [_ptr(x) for x in v]
 
 
 def _check(rc: int):
@@ -239,8 +239,9 @@ def colibri_indexer_check_status(workspace, stream=None) -> int:
 def colibri_moe_route(desc: coli_route_desc, T: int, logits, ltype: int, logit_stride: int, bias, topk_idx, topk_w,
                       stream=None):
     """Routing to experts from given logits (see the header): ids in topk_idx, weights in topk_w."""
-    _check(lib().colibri_moe_route(ctypes.byref(desc), T, _ptr(logits), ltype, logit_stride, _ptr(bias),
-                                   _ptr(topk_idx), _ptr(topk_w), _stream(stream)))
+    z, idx, w = _ptrs(logits, topk_idx, topk_w)
+    _check(lib().colibri_moe_route(ctypes.byref(desc), T, z, ltype, logit_stride, _ptr(bias), idx, w,
+                                   _stream(stream)))
 
 
 def colibri_kv_step(desc: coli_kv_desc, B: int, n_tokens: int, new_len, seq_len, held, block_table, free_pages,
@@ -254,8 +255,9 @@ def colibri_kv_step(desc: coli_kv_desc, B: int, n_tokens: int, new_len, seq_len,
 def colibri_kv_append(desc: coli_kv_desc, n_tokens: int, n_valid, latent, latent_stride: int, rope, rope_stride: int,
                       slot, cache, stream=None):
     """Write n_tokens new rows (latent and rotary part) into the paged cache at their slots."""
-    _check(lib().colibri_kv_append(ctypes.byref(desc), n_tokens, _ptr(n_valid), _ptr(latent), latent_stride,
-                                   _ptr(rope), rope_stride, _ptr(slot), _ptr(cache), _stream(stream)))
+    lat, rot, to, kv = _ptrs(latent, rope, slot, cache)
+    _check(lib().colibri_kv_append(ctypes.byref(desc), n_tokens, _ptr(n_valid), lat, latent_stride, rot, rope_stride,
+                                   to, kv, _stream(stream)))
 
 
 def colibri_kv_attention_workspace_size(B: int, n_tokens: int, H: int) -> int:
@@ -269,9 +271,9 @@ def colibri_kv_attention(desc: coli_kv_desc, B: int, n_tokens: int, H: int, scal
                          workspace, workspace_bytes: int, stream=None):
     """Attention of the new tokens over the paged cache, over every key up to a token's position or over the keys
     topk_idx names (see the header)."""
-    _check(lib().colibri_kv_attention(ctypes.byref(desc), B, n_tokens, H, scale, _ptr(q), q_token_stride,
-                                      q_head_stride, _ptr(cache), _ptr(block_table), _ptr(q_start), _ptr(seq_len),
-                                      _ptr(topk_idx), topk, _ptr(out), _ptr(lse), _ptr(workspace), workspace_bytes,
+    qp, kv, table, start, seq, o, ws = _ptrs(q, cache, block_table, q_start, seq_len, out, workspace)
+    _check(lib().colibri_kv_attention(ctypes.byref(desc), B, n_tokens, H, scale, qp, q_token_stride, q_head_stride, kv,
+                                      table, start, seq, _ptr(topk_idx), topk, o, _ptr(lse), ws, workspace_bytes,
                                       _stream(stream)))
 
 

@@ -44,7 +44,7 @@ constexpr int kAtSmWarps = 8;                      // softmax warps: two per TME
 constexpr int kAtSmThreads = kAtSmWarps * 32, kAtHalf = kAtRows / 2;
 constexpr int kAtFirstLoad = 2 + kAtSmWarps;       // warp 0 loads; copying loaders go on from here
 constexpr int at_threads(bool tma) { return (1 + kAtSmWarps + (tma ? 1 : kAtLoadWarps)) * 32; }
-constexpr int kAtMinBox = 8;                       // fewest key rows a TMA box has
+constexpr int kAtMinBox = 64;                      // fewest key rows of a TMA box (see the kernel)
 constexpr int kAtMaxCtas = 160;                    // CTAs the workspace has room for
 constexpr int kAtMaxB = 8192, kAtMaxH = 1024;
 constexpr int kAtMaxDevices = 64;                  // devices whose properties are kept between calls
@@ -259,6 +259,11 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
         if (i0 == 0) {
           if (W == 0) W = total;
           G = min(max_ctas / gang, W);
+          // units of equal length: whole runs a unit where that makes no run longer, for fewer parts
+          if (n_units <= nthr && n_units <= G && __syncthreads_and(v == 0 || v * n_units == W)) {
+            const int whole = n_units * (G / n_units);
+            if ((W + whole - 1) / whole == (W + G - 1) / G) G = whole;
+          }
           if (r.run < G) {
             const AtCuts cut(W, G);
             before = r.run > 0 ? cut(r.run - 1) : 0;
@@ -429,10 +434,12 @@ __device__ __forceinline__ void umma_commit_elect(uint64_t* bar) {
       : "memory");
 }
 
-// TMA: key tiles arrive as TMA boxes of p.box rows (pages of a multiple of eight rows, every key up to the
+// TMA: key tiles arrive as TMA boxes of p.box = 64 or 128 rows (pages of whole boxes, every key up to the
 // position) and the queries as one box a 64 columns (token and head rows evenly spaced); otherwise two warps
-// copy row by row (cp.async), from pages of any size, for selected keys and for queries of any strides.  A
-// gathering TMA load of four rows a coordinate measured 83 cycles for 512 bytes, 12.5 us a tile of 128 keys.
+// copy row by row (cp.async), from pages of any size, for selected keys and for queries of any strides.  A TMA
+// load costs its issuing warp about 60 cycles whatever its rows: a chunk of 500 tokens over 6,000 keys takes 407,
+// 412, 468 and 601 us with boxes of 128, 64, 32 and 16 rows, 426 us with copies; a gathering TMA load of four rows a
+// coordinate measured 83 cycles for 512 bytes, 12.5 us a tile of 128 keys.
 template <bool BF16, bool TMA>
 __global__ void __launch_bounds__(at_threads(TMA), 1)
     kv_attention_kernel(const AtArgs p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
@@ -443,7 +450,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   __shared__ AtUnit unit_sm;                           // the run's first unit
   __shared__ uint32_t key_ok[2][4];                    // bit i of word w: key 32 w + i of the tile is there
   __shared__ uint32_t key_fin[2][4];                   // bit i of word w of a half: key 32 w + i has a finite score there
-  __shared__ __align__(16) float ref[kAtRows], fac[kAtRows], red[4][kAtRows];
+  __shared__ __align__(16) float ref[kAtRows], fac[kAtRows], red[4][kAtRows];   // ref: the negated references
   __shared__ __align__(16) int lim[kAtRows];           // last key position each row sees (dense)
   __shared__ int has_ref[kAtRows];                     // the row has seen a key
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -578,11 +585,8 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
         if constexpr (TMA) {
           // box j holds keys j box .. (j + 1) box - 1, there up to `seen`
           const unsigned boxes = __ballot_sync(0xffffffffu, there[0]);
-          const int per = p.box < 32 ? p.box : 32;     // keys of a word that one box decides
           if (lane < 4) {
-#pragma unroll 1
-            for (int i = 0; i < 32; i += per)
-              if ((boxes >> ((lane * 32 + i) >> p.box_log2)) & 1u) mine[0] |= (per == 32 ? 0xffffffffu : ((1u << per) - 1u) << i);
+            mine[0] = (boxes >> ((lane * 32) >> p.box_log2)) & 1u ? 0xffffffffu : 0u;
             const int left = seen - (t * kAtKeys + lane * 32);
             if (left < 32) mine[0] &= left <= 0 ? 0u : (1u << left) - 1u;
           }
@@ -609,7 +613,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
             if (d == 0 && lane < 4) key_ok[it & 1][lane] = mine[0];
             if (lane == 0) mbar_arrive_expect_tx(&full[d], (uint32_t)(2 * kAtBoxBytes));
             __syncwarp();
-            // lanes 0 .. n_box - 1: the first 64 columns, the next n_box lanes: the other 64 (n_box <= 16)
+            // lanes 0 .. n_box - 1: the first 64 columns, the next n_box lanes: the other 64
             if (lane < 2 * n_box) {
               const int x = 2 * d + (lane >= n_box), j = lane & (n_box - 1);
               tma_load_2d_nohint(smem + x * kAtBoxBytes + j * p.box * 128, &kmap, x * 64, (int)row[0], &full[d]);
@@ -681,7 +685,8 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       __syncwarp();
     }
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer (the warp stays converged)
+    // ---------------------------------------------------------------- MMA issuer (the warp stays converged; its waits
+    // are the suspending ones: polling takes issue slots from the softmax warps beside it, chunk 1.72 -> 1.69 ms)
     const uint32_t fmt = BF16 ? (1u << 7) | (1u << 10) : 0u;
     const uint32_t idesc = (1u << 4) | fmt | ((uint32_t)(kAtRows >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
     const uint32_t idesc_t = idesc | (1u << 15) | (1u << 16);            // both operands MN-major
@@ -695,15 +700,14 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       const int t0 = at - ut.first, t1 = min(end - ut.first, ut.tiles);
       at = ut.first + t1;
       if (ut.row0 + my_rows >= ut.row_end) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait_spin(&q_full, un & 1, p.wait_ns));
+      ok = __all_sync(0xffffffffu, mbar_wait(&q_full, un & 1, p.wait_ns));
       if (!TMA) fence_proxy_async_smem();              // the copies are ordinary writes; the MMA reads by the async proxy
       for (int t = t0; ok && t < t1; ++t, ++it) {
-        ok = !__shfl_sync(0xffffffffu, *abort_v, 0);
         // S^T: nine boxes of 64 columns, four steps of 16 each
 #pragma unroll
         for (int x = 0; x < kAtBoxes; ++x) {
           if ((x & 1) == 0) {
-            ok = ok && mbar_wait_spin(&full[x >> 1], it & 1, p.wait_ns);
+            ok = ok && mbar_wait(&full[x >> 1], it & 1, p.wait_ns);
             ok = __all_sync(0xffffffffu, ok);
             if (!TMA) fence_proxy_async_smem();
             tc_fence_after();
@@ -714,7 +718,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
         }
         umma_commit_elect(&s_full);
         if (t + 1 == t1) umma_commit_elect(&q_empty);
-        ok = ok && mbar_wait_spin(&p_ready, it & 1, p.wait_ns);
+        ok = ok && mbar_wait(&p_ready, it & 1, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -758,7 +762,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
         has_ref[id] = 0;
       }
       const int seen_all = ut.shift + p.by_heads(row0);      // every row sees the keys up to this one
-      float l[kAtHalf];
+      float l[kAtHalf];                                // sums of this key's weights
 #pragma unroll
       for (int c = 0; c < kAtHalf; ++c) l[c] = 0.f;
       sm_sync();
@@ -801,10 +805,10 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
 #pragma unroll
         for (int c = 0; c < kAtHalf; c += 4) {
           const float4 m = *reinterpret_cast<const float4*>(&ref[c0 + c]);
-          x[c] = fmaf(x[c], p.scale_log2, -m.x);
-          x[c + 1] = fmaf(x[c + 1], p.scale_log2, -m.y);
-          x[c + 2] = fmaf(x[c + 2], p.scale_log2, -m.z);
-          x[c + 3] = fmaf(x[c + 3], p.scale_log2, -m.w);
+          x[c] = fmaf(x[c], p.scale_log2, m.x);
+          x[c + 1] = fmaf(x[c + 1], p.scale_log2, m.y);
+          x[c + 2] = fmaf(x[c + 2], p.scale_log2, m.z);
+          x[c + 3] = fmaf(x[c + 3], p.scale_log2, m.w);
           top = fmaxf(fmaxf(fmaxf(top, x[c]), fmaxf(x[c + 1], x[c + 2])), x[c + 3]);
         }
         if (sm_any(top > kAtGrow || unset || !ok)) {
@@ -817,7 +821,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
             const bool raise = g > kAtGrow || (!has_ref[id] && g > -INFINITY);
             fac[id] = raise ? g : 0.f;                 // by how much
             if (raise) {
-              ref[id] += g;
+              ref[id] -= g;
               has_ref[id] = 1;
             }
             none = !has_ref[id];
@@ -888,9 +892,9 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
           fac[id] = sum == 0.f ? 0.f : 1.0f / sum;
           const int row = row0 + id;
           if (p.lse && row < ut.row_end)
-            p.lse[row] = sum == 0.f ? -INFINITY : (ref[id] + log2f(sum)) * 0.693147180559945309f;
+            p.lse[row] = sum == 0.f ? -INFINITY : (log2f(sum) - ref[id]) * 0.693147180559945309f;
         } else {
-          p.part_ml[(size_t)slot * kAtRows + id] = make_float2(has_ref[id] ? ref[id] : kAtUnset, sum);
+          p.part_ml[(size_t)slot * kAtRows + id] = make_float2(has_ref[id] ? -ref[id] : kAtUnset, sum);
         }
       }
       sm_sync();
