@@ -791,6 +791,17 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
           for (int c = 0; c < kAtHalf; ++c) fin |= fabsf(x[c]) < INFINITY;
           const unsigned fw = __ballot_sync(0xffffffffu, fin);
           if (lane == 0) key_fin[half][sp] = fw;
+        }
+        // distance to the references
+#pragma unroll
+        for (int c = 0; c < kAtHalf; c += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&ref[c0 + c]);
+          x[c] = fmaf(x[c], p.scale_log2, m.x);
+          x[c + 1] = fmaf(x[c + 1], p.scale_log2, m.y);
+          x[c + 2] = fmaf(x[c + 2], p.scale_log2, m.z);
+          x[c + 3] = fmaf(x[c + 3], p.scale_log2, m.w);
+        }
+        if (masked) {                                  // (after the scale, which may be 0 or negative)
 #pragma unroll
           for (int c = 0; c < kAtHalf; c += 4) {
             const int4 lm = *reinterpret_cast<const int4*>(&lim[c0 + c]);
@@ -800,17 +811,11 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
             if (!there || (!p.sel && key > lm.w)) x[c + 3] = -INFINITY;
           }
         }
-        // distance to the references; does any score exceed its row's by more than kAtGrow?
+        // does any score exceed its row's reference by more than kAtGrow?
         float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < kAtHalf; c += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&ref[c0 + c]);
-          x[c] = fmaf(x[c], p.scale_log2, m.x);
-          x[c + 1] = fmaf(x[c + 1], p.scale_log2, m.y);
-          x[c + 2] = fmaf(x[c + 2], p.scale_log2, m.z);
-          x[c + 3] = fmaf(x[c + 3], p.scale_log2, m.w);
+        for (int c = 0; c < kAtHalf; c += 4)
           top = fmaxf(fmaxf(fmaxf(top, x[c]), fmaxf(x[c + 1], x[c + 2])), x[c + 3]);
-        }
         if (sm_any(top > kAtGrow || unset || !ok)) {
           if (sm_any(!ok)) { ok = false; break; }
           red[sp][c0 + lane] = warp_columns(x, [](float a, float b) { return fmaxf(a, b); });
@@ -1149,8 +1154,9 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
     return fail(COLI_EUNSUPPORTED, "kv_attention: the cache holds bf16 or fp16 (dtype %d)", desc->dtype);
   if (!(scale == scale) || scale - scale != 0.f) return fail(COLI_EINVAL, "kv_attention: scale is not finite");
   if (topk_idx && topk < 1) return fail(COLI_EINVAL, "kv_attention: topk must be positive with topk_idx");
-  if ((long long)n_tokens * H > 0x7fffffffLL - 64)
-    return fail(COLI_EUNSUPPORTED, "kv_attention: n_tokens * H exceeds 2^31 rows");
+  if ((long long)n_tokens * H > 0x7fffffffLL - 1024)       // (row numbers of a last, partial gang of row tiles)
+    return fail(COLI_EUNSUPPORTED, "kv_attention: n_tokens * H exceeds 2^31 - 1024 rows");
+  if (topk_idx && topk > 1 << 30) return fail(COLI_EUNSUPPORTED, "kv_attention: topk exceeds 2^30");
   const long long per_page = desc->page_stride / COLI_KV_WIDTH;
   const long long cached = (desc->n_pages - 1LL) * per_page + desc->page_size;
   if (cached > 0x7fffffffLL) return fail(COLI_EUNSUPPORTED, "kv_attention: the cache exceeds 2^31 - 1 rows");

@@ -412,6 +412,14 @@ def test_attention_long_context_and_splits(torch_cuda):
         b.check()
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.04, 1e-6])
+def test_attention_any_finite_scale(torch_cuda, scale):
+    b = Batch(torch_cuda, [300, 77], [3, 2], 64, 64, seed=51)
+    b.scale = scale
+    b.check()
+    b.check(sel=selected(np.random.default_rng(3), [300, 77], [3, 2], 90, 0.8))
+
+
 def test_attention_many_requests(torch_cuda):
     """The most requests a call takes, a few keys each."""
     rng = np.random.default_rng(50)

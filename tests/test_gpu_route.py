@@ -195,3 +195,42 @@ def combine(layer, xf, idx, w):
         if layer.shared is not None:
             out[t] += O.expert_ffn(layer.shared, 0, xf[t])
     return out
+
+
+def test_set_routing_in_every_forward_call(torch_cuda):
+    """The cached forward, the static-scratch forward and the pilot use the routing set on the plan; integer-dot inputs
+    go with it."""
+    torch = torch_cuda
+    import quantized_expert_ffn_bias_gb300 as coli
+    from harness.device import DeviceLayer, to_dev
+    from tests.test_gpu_cache import pinned_bank
+    layer = H.gen_layer(73, 0, d=512, F=256, E=32, k=4, rho=2.5, qtype=H.Q_INT4_G128, bias="uniform:0.1", F_shared=256)
+    dl = DeviceLayer(layer, 12)
+    st = torch.cuda.current_stream()
+    keep, host = pinned_bank(torch, layer.experts)
+    sb = coli.colibri_moe_cache_slot_bytes(dl.plan)
+    slots = torch.empty(32 * sb, dtype=torch.uint8, device="cuda")
+    cache = coli.Cache(dl.plan, 32, 1.0, host, slots, 32 * sb, shared=dl.shared.expert(0))
+    ws = torch.empty(dl.plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    for idot in (False, True):
+        dl.plan.set_idot(idot)
+        for T in (1, 3, 12):
+            x = to_dev(H.gen_x(73, T, T, 512, H.X_BF16), dl.device)
+            dl.plan.set_route(None)
+            plain = dl.forward(x).clone()
+            dl.plan.set_route(_desc(coli, 32, 4, score="softmax", groups=8, keep=2, gscore="max", scale=1.5))
+            ref = dl.forward(x).clone()
+            ids = dl.routing(T)[0]
+            assert not torch.equal(ref, plain)
+            out = torch.full_like(ref, float("nan"))
+            cache.forward(T, x, dl.router_w, dl.bias, out, ws, stream=st)
+            torch.cuda.synchronize()
+            assert torch.equal(out, ref), "cached forward"
+            out.fill_(float("nan"))
+            dl.plan.forward_noalloc(T, x, dl.router_w, dl.bias, out, stream=st)
+            torch.cuda.synchronize()
+            assert torch.equal(out, ref), "forward with the static scratch"
+            assert cache.pilot(T, x, dl.router_w, dl.bias, ws, stream=st) == sorted(set(ids.ravel().tolist()))
+    torch.cuda.synchronize()
+    cache.close()
+    dl.close()

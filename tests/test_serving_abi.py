@@ -128,7 +128,7 @@ def test_append_arguments():
     (dict(B=0), coli.COLI_EINVAL), (dict(n=-1), coli.COLI_EINVAL), (dict(H=0), coli.COLI_EINVAL),
     (dict(B=8193), coli.COLI_EUNSUPPORTED), (dict(H=1025), coli.COLI_EUNSUPPORTED),
     (dict(scale=float("nan")), coli.COLI_EINVAL), (dict(scale=float("inf")), coli.COLI_EINVAL),
-    (dict(sel=P, topk=0), coli.COLI_EINVAL), (dict(n=1 << 26), coli.COLI_EUNSUPPORTED),
+    (dict(sel=P, topk=0), coli.COLI_EINVAL), (dict(sel=P, topk=(1 << 30) + 1), coli.COLI_EUNSUPPORTED), (dict(n=1 << 26), coli.COLI_EUNSUPPORTED),
     (dict(q=None), coli.COLI_EINVAL), (dict(cache=None), coli.COLI_EINVAL), (dict(table=None), coli.COLI_EINVAL),
     (dict(q_start=None), coli.COLI_EINVAL), (dict(seq=None), coli.COLI_EINVAL), (dict(out=None), coli.COLI_EINVAL),
     (dict(ws=None), coli.COLI_EINVAL), (dict(q=P + 8), coli.COLI_EALIGN), (dict(cache=P + 2), coli.COLI_EALIGN),
