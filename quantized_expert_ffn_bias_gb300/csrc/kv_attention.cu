@@ -259,10 +259,16 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
         if (i0 == 0) {
           if (W == 0) W = total;
           G = min(max_ctas / gang, W);
-          // units of equal length: whole runs a unit where that makes no run longer, for fewer parts
-          if (n_units <= nthr && n_units <= G && __syncthreads_and(v == 0 || v * n_units == W)) {
-            const int whole = n_units * (G / n_units);
-            if ((W + whole - 1) / whole == (W + G - 1) / G) G = whole;
+          // The longest run decides the time, so no more runs than it needs (512 tiles over 152 CTAs and over 128
+          // both take four rounds): fewer parts to write and join.  Units of equal length: whole runs a unit.
+          if (G > 0) {
+            const int longest = (W + G - 1) / G;
+            int runs = (W + longest - 1) / longest;
+            if (n_units <= nthr && n_units <= G && __syncthreads_and(v == 0 || v * n_units == W)) {
+              const int whole = n_units * (G / n_units);
+              if ((W + whole - 1) / whole == longest) runs = whole;
+            }
+            G = runs;
           }
           if (r.run < G) {
             const AtCuts cut(W, G);

@@ -99,6 +99,7 @@ template <int LT>
 static void launch_route_lt(const RouteCall& c, cudaStream_t st) {
   if (c.r.E <= 128) launch_route_nv<LT, 4>(c, st);
   else if (c.r.E <= 256) launch_route_nv<LT, 8>(c, st);
+  else if (c.r.E <= 384) launch_route_nv<LT, 12>(c, st);
   else if (c.r.E <= 512) launch_route_nv<LT, 16>(c, st);
   else launch_route_nv<LT, 32>(c, st);
 }

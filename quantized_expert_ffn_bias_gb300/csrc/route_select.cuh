@@ -215,7 +215,7 @@ __device__ __noinline__ int route_picks_exact(const coli_route_desc r, Logit log
   return pick;
 }
 
-// Sort a lane's keys, largest first (Batcher's odd-even merge network; N a power of two).
+// Sort a lane's keys, largest first (Batcher's odd-even merge network; past N, keys that are smaller than all).
 template <int N>
 __device__ __forceinline__ void route_sort(uint32_t (&v)[N]) {
 #pragma unroll
@@ -269,8 +269,8 @@ __device__ __forceinline__ bool route_token(const coli_route_desc& r, const floa
   // The lane's images of u in order, the low bits giving way to the expert (the lower one the larger): a round of
   // the selection then only compares the lanes' heads.  0: not a candidate (below every image, also -infinity's).
   // kCut: what that may take from a value, relative to it; it enters the tolerances.
-  constexpr uint32_t kIdx = NV - 1;
-  constexpr float kCut = (float)NV / 8388608.f;
+  constexpr uint32_t kIdx = NV <= 4 ? 3 : NV <= 8 ? 7 : NV <= 16 ? 15 : 31;
+  constexpr float kCut = (float)(kIdx + 1) / 8388608.f;
   uint32_t v[NV];
   float smax = 0.f;
 #pragma unroll
@@ -279,19 +279,22 @@ __device__ __forceinline__ bool route_token(const coli_route_desc& r, const floa
     smax = fmaxf(smax, i < n_here ? s[i] : 0.f);
   }
   smax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(smax)));
-  route_sort<NV>(v);
+  // groups of whole lanes (a power of two of them) are reduced by shuffles from the sorted lists; other groups one
+  // by one, and the lists are sorted when the closed groups are out of them
+  const bool grouped = r.topk_group < r.n_group;
+  const int gsz = E / r.n_group, lanes = gsz / NV;
+  const bool whole = lanes * NV == gsz && (lanes & (lanes - 1)) == 0;
+  if (!grouped || whole) route_sort<NV>(v);
   const float tol_s = route_tol(softmax, smax);
   bool tie = false, again = false;       // a decision closer than kNearTie, than the scores' error
 
   // groups
   unsigned open = 0xffffffffu;           // kept groups
-  if (r.topk_group < r.n_group) {
-    const int G = r.n_group, gsz = E / G;
+  if (grouped) {
+    const int G = r.n_group;
     const bool top2 = r.group_score == COLI_GROUP_TOP2;
     uint32_t t1 = 0u, t2 = 0u;           // a group's two largest images
     int mine = lane;                     // this lane's group, or the group whose scores it holds
-    const int lanes = gsz / NV;          // lanes a group
-    const bool whole = lanes * NV == gsz && (lanes & (lanes - 1)) == 0;
     if (whole) {
       t1 = v[0];
       t2 = NV > 1 ? v[1] : 0u;
@@ -398,7 +401,7 @@ __device__ __forceinline__ bool route_token(const coli_route_desc& r, const floa
     bool close = gap <= tol && a > -INFINITY;
     if (close) {
       // unless every candidate around the border has the last pick's logit and bias: those tie exactly
-      const int e_k = __shfl_sync(0xffffffffu, pick, k - 1), gsz = E / r.n_group;
+      const int e_k = __shfl_sync(0xffffffffu, pick, k - 1);
       const float zk = logit(e_k), bk = bias ? __ldg(bias + e_k) : 0.f;
       bool other = false;
 #pragma unroll 1

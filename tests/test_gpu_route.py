@@ -67,6 +67,10 @@ CASES = [
     dict(T=33, E=1024, k=32, groups=32, keep=5, dtype="bf16", pad=1),
     dict(T=257, E=8, k=2, score="softmax", bias=None, dtype="bf16"),
     dict(T=7, E=1, k=1),
+    dict(T=70, E=384, k=8, groups=8, keep=4),
+    dict(T=70, E=320, k=8, groups=16, keep=4, dtype="bf16", bias=None),
+    dict(T=40, E=512, k=16, groups=8, keep=3, dtype="f16"),
+    dict(T=40, E=1000, k=8, groups=8, keep=3),
     dict(T=5, E=33, k=32, groups=3, keep=3),
     dict(T=5, E=62, k=4, groups=31, keep=2, renorm=False),
 ]
