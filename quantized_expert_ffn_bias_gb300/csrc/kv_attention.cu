@@ -490,7 +490,6 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  griddep_launch_dependents();
   griddep_wait();                                      // the launch may overlap the kernel before; its results not
   const AtRun plan = at_plan(p, reinterpret_cast<int*>(smem), &unit_sm);
   const int cta = blockIdx.x, beg = plan.beg, end = plan.end, unit0 = plan.unit0;
@@ -943,6 +942,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       ++un;
     }
   }
+  griddep_launch_dependents();                         // (earlier, the join's CTAs would take slots from the next call's)
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0) p.cta_status[cta] = cta_status;
@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
 // ------------------------------------------------------------------ join
 // Adds up the parts of every cut unit, in order.  A task is four rows of a unit: 64 values where the parts are
 // many (eight thread groups take every eighth part each, then meet in shared memory), all 512 where they are
-// few (every thread then finds the parts' weights by itself, while its values are on the way).
+// few (the values of the first parts are then loaded before their weights are known).
 constexpr int kAtJoinThreads = 512, kAtJoinCtas = 304, kAtJoinFew = 8;
 __host__ __device__ constexpr int at_join_tasks(int parts) { return parts <= 0 ? 0 : parts <= kAtJoinFew ? 16 : 128; }
 
@@ -1012,28 +1012,39 @@ __global__ void __launch_bounds__(kAtJoinThreads, 2) kv_attention_join_kernel(co
     auto lse = [&](float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f; };
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (few) {
-      // references and sums of rows c, c + 1 and c + 2, c + 3 of a part
+      // the values of the first parts, and all references and sums, on their way at the same time
+      constexpr int kAhead = 4;
+      float4 o[kAhead];
       const float* src = p.part + at_part(c, tid);
-      float4 m = make_float4(kAtUnset, kAtUnset, kAtUnset, kAtUnset), l = acc;
-#pragma unroll 2
-      for (int i = 0; i < n; ++i) {
-        const float4* ml = reinterpret_cast<const float4*>(p.part_ml + slot(i) * kAtRows + c);
-        const float4 a = ml[0], b = ml[1];
-        const float4 o = *reinterpret_cast<const float4*>(src + slot(i) * kAtPart);
-        // the sums so far move to the larger reference
-        const float4 top = make_float4(fmaxf(m.x, a.x), fmaxf(m.y, a.z), fmaxf(m.z, b.x), fmaxf(m.w, b.z));
-        const float4 old = make_float4(at_exp2(m.x - top.x), at_exp2(m.y - top.y), at_exp2(m.z - top.z), at_exp2(m.w - top.w));
-        const float4 w = make_float4(at_exp2(a.x - top.x), at_exp2(a.z - top.y), at_exp2(b.x - top.z), at_exp2(b.z - top.w));
-        acc = make_float4(acc.x * old.x, acc.y * old.y, acc.z * old.z, acc.w * old.w);
-        l = make_float4(l.x * old.x, l.y * old.y, l.z * old.z, l.w * old.w);
-        add(acc, w, o);
-        add(l, w, make_float4(a.y, a.w, b.y, b.w));
-        m = top;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i < n) o[i] = *reinterpret_cast<const float4*>(src + slot(i) * kAtPart);
+      float2 ml = make_float2(0.f, 0.f);
+      if (tid < 4 * n) ml = p.part_ml[slot(tid >> 2) * kAtRows + c + (tid & 3)];
+      __syncthreads();                                  // the previous task's weights are read
+      if (tid < 4 * n) {
+        wgt[tid >> 2][tid & 3] = ml.x;
+        sum[tid >> 2][tid & 3] = ml.y;
       }
-      write(acc, make_float4(l.x == 0.f ? 0.f : 1.0f / l.x, l.y == 0.f ? 0.f : 1.0f / l.y, l.z == 0.f ? 0.f : 1.0f / l.z,
-                             l.w == 0.f ? 0.f : 1.0f / l.w), tid);
-      if (p.lse && tid < 4 && tid < rows)
-        p.lse[jn.row0 + c + tid] = tid == 0 ? lse(m.x, l.x) : tid == 1 ? lse(m.y, l.y) : tid == 2 ? lse(m.z, l.z) : lse(m.w, l.w);
+      __syncthreads();
+      if (tid < 4) {                                    // thread r: the parts' weights for row c + r
+        float m = kAtUnset, l = 0.f;
+        for (int i = 0; i < n; ++i) m = fmaxf(m, wgt[i][tid]);
+        for (int i = 0; i < n; ++i) {
+          const float w = at_exp2(wgt[i][tid] - m);
+          wgt[i][tid] = w;
+          l += w * sum[i][tid];
+        }
+        inv[tid] = l == 0.f ? 0.f : 1.0f / l;
+        if (p.lse && tid < rows) p.lse[jn.row0 + c + tid] = lse(m, l);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i < n) add(acc, *reinterpret_cast<const float4*>(&wgt[i][0]), o[i]);
+      for (int i = kAhead; i < n; ++i)
+        add(acc, *reinterpret_cast<const float4*>(&wgt[i][0]), *reinterpret_cast<const float4*>(src + slot(i) * kAtPart));
+      write(acc, make_float4(inv[0], inv[1], inv[2], inv[3]), tid);
       continue;
     }
     __syncthreads();                                    // the previous task's weights are read
@@ -1064,7 +1075,7 @@ __global__ void __launch_bounds__(kAtJoinThreads, 2) kv_attention_join_kernel(co
     __syncthreads();
     const int grp = tid >> 6, v = tid & 63, val = (sub & 7) * 64 + v;
     const float* src = p.part + at_part(c, val);
-#pragma unroll 8
+#pragma unroll 4
     for (int i = grp; i < n; i += 8)
       add(acc, *reinterpret_cast<const float4*>(&wgt[i][0]), *reinterpret_cast<const float4*>(src + slot(i) * kAtPart));
     if (grp) meet[grp - 1][v] = acc;
