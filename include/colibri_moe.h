@@ -590,8 +590,8 @@ COLI_API coli_status colibri_kv_append(const coli_kv_desc* desc, int n_tokens, c
  * A row that sees no key gets 0 and lse -infinity.  Rows outside
  * [q_start[0], q_start[B]) are left as they were.  Keys that a row does not see
  * do not reach its output, whatever values (infinities, NaN) they hold.  A
- * key whose page id is outside [0, n_pages) is left out and reported
- * (COLI_DEV_KV_BAD_PAGE).  Softmax and sums in fp32; the weights are rounded
+ * key whose page id is outside [0, n_pages), or beyond the block table, is left
+ * out and reported (COLI_DEV_KV_BAD_PAGE).  Softmax and sums in fp32; the weights are rounded
  * to dtype for the product with the values.  The result does not depend on
  * timing.
  * Asynchronous on stream, two launches.  n_tokens = 0 does nothing.  Errors: COLI_EINVAL, COLI_EALIGN,

@@ -10,6 +10,8 @@
 // accumulators in tensor memory):
 //   S^T[128 keys][64 rows]  = K Q^T    (K as it lies: keys are the MMA's M)
 //   O^T[512][64 rows]      += V^T P^T  (V^T is the same tile read transposed)
+// What bounds a tile is shared memory: its MMAs read 408 KB of operands (A and B of 68 MMAs, 4 and 2 KB each), loads and
+// P^T write 160 KB, 4,550 cycles at 128 bytes a cycle of the 5,080 that it takes where the rows come from L2.
 // The transposed form is what makes it fit: O^T takes 256 of the 512 TMEM
 // columns, where 128 rows of O would take all of them, and each thread of the
 // softmax holds one key's 64 scores, so that its weights are one 128-byte row
@@ -127,6 +129,7 @@ struct AtRun {
   int beg, end, unit0;   // its key tiles, the unit of the first
   int prefetch;          // 1: the keys exceed what stays in L2
   int wrong;             // 1: q_start does not ascend
+  int status;            // what is wrong with the lengths (COLI_DEV_KV_*)
 };
 
 // `sm`: shared memory for 3 B + 2 ints, free again when the call returns.  Every thread of the CTA calls it.
@@ -136,11 +139,11 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
   int* qs = sm;                      // [B + 1] q_start, kept inside the batch
   int* base = qs + p.B + 1;          // [B + 1] first unit of each request
   int* seq = base + p.B + 1;         // [B]
-  __shared__ int warp_tot[32], total, s_unit0, s_flags[2];
+  __shared__ int warp_tot[32], total, s_unit0, s_flags[3];
   __shared__ unsigned sums[kAtGangs + 1];
   const int tid = threadIdx.x, nthr = blockDim.x, B = p.B, max_ctas = gridDim.x;
   if (tid <= kAtGangs) sums[tid] = 0;
-  if (tid < 2) s_flags[tid] = 0;
+  if (tid < 3) s_flags[tid] = 0;
   {
     const int lo = max(0, min(p.q_start[0], p.n_tokens)), hi = max(lo, min(p.q_start[B], p.n_tokens));
 #pragma unroll 1
@@ -173,12 +176,13 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
     const int g = tid & 7, size = g < kAtGangs ? at_gang(g) : 1 << 30;
     const unsigned third = size == 3 ? 0x55555556u : 0x2AAAAAABu;      // of x < 2^31: x / 3, x / 6
     unsigned s = 0;
-    bool down = false, many = false;
+    bool down = false, many = false, beyond = false;
 #pragma unroll 1
     for (int b = tid >> 3; b < B; b += nthr >> 3) {
       const Req q = request(b);
       down |= qs[b + 1] < qs[b];                       // not ascending: nothing is computed
       many |= q.n && q.rows > 1;                       // a gang is of use where row tiles share keys
+      beyond |= q.n && seq[b] > most;                  // keys without a place in the block table: left out
       const unsigned x = (unsigned)(q.rows + size - 1);
       s += q.tiles * (g >= kAtGangs ? 1u : (size == 3 || size == 6) ? __umulhi(x, third) : x >> (31 - __clz(size)));
     }
@@ -187,10 +191,12 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
     if ((tid & 31) <= kAtGangs && s) atomicAdd(&sums[tid & 7], s);
     if (down) s_flags[0] = 1;
     if (many) s_flags[1] = 1;
+    if (beyond) s_flags[2] = 1;
   }
   __syncthreads();
   AtRun r;
   r.wrong = s_flags[0];
+  r.status = (s_flags[0] ? COLI_DEV_KV_TOKENS : 0) | (s_flags[2] ? COLI_DEV_KV_BAD_PAGE : 0);
   r.gang = 1;
   r.prefetch = sums[kAtGangs] > (unsigned)kAtL2Tiles;
   if (s_flags[1]) {
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   const int cta = blockIdx.x, beg = plan.beg, end = plan.end, unit0 = plan.unit0;
   const int my_rows = (cta - plan.run * plan.gang) * kAtRows;    // this member's rows of a unit begin there
   const AtUnit* units = p.units + plan.run;
-  if (threadIdx.x == 0) cta_status = plan.wrong ? COLI_DEV_KV_TOKENS : 0;
+  if (threadIdx.x == 0) cta_status = plan.status;
   // (the plan's use of shared memory ends before the TMA and MMA use of it)
   fence_proxy_async_smem();
   __syncthreads();

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, NV <= 8 ? 8 : 4) route_kerne
 
 template <int LT, int NV>
 static void launch_route_nv(const RouteCall& c, cudaStream_t st) {
-  const int blocks = (c.T + kRouteWarps - 1) / kRouteWarps;
+  const int blocks = c.T / kRouteWarps + (c.T % kRouteWarps ? 1 : 0);
   const int size = LT == COLI_X_F32 ? 4 : 2;
   const bool vec = c.r.E % NV == 0 && aligned(c.logits, 16) && c.stride * size % 16 == 0 && aligned(c.bias, 16);
   if (vec) route_kernel<LT, NV, true><<<blocks, kRouteWarps * 32, 0, st>>>(c);

@@ -389,6 +389,9 @@ def test_attention_reports_bad_pages(torch_cuda):
     b = Batch(torch_cuda, [300, 100], [1, 2], 64, 32, seed=14)
     b.table[0, 3], b.table[0, 5] = -1, b.n_pages
     b.check(status=R.BAD_PAGE)
+    b = Batch(torch_cuda, [256, 100], [1, 2], 64, 32, seed=16)      # a request longer than its row of the table
+    b.table, b.max_pages = np.ascontiguousarray(b.table[:, :4]), 4
+    b.check(status=R.BAD_PAGE)
 
 
 def test_attention_refuses_a_wrong_q_start(torch_cuda):
@@ -425,6 +428,24 @@ def test_attention_many_requests(torch_cuda):
     rng = np.random.default_rng(50)
     lens = rng.integers(0, 9, 8192)
     Batch(torch_cuda, lens, np.minimum(lens, rng.integers(0, 3, 8192)), 2, 16, seed=50).check()
+
+
+def test_attention_gangs(torch_cuda):
+    """Keys beyond what stays in L2, several row tiles over the same keys: gangs of CTAs walk them together, some with idle
+    members (requests of one, two and four tokens among those of three)."""
+    rng = np.random.default_rng(60)
+    new = [3, 1, 3, 2, 3, 3, 4, 3, 3, 3]
+    b = Batch(torch_cuda, rng.integers(5500, 9000, 10), new, 64, 64, seed=60)
+    b.check()
+    b = Batch(torch_cuda, rng.integers(5500, 9000, 8), [1] * 8, 160, 128, seed=61, dtype="f16")
+    b.check()
+
+
+def test_attention_gangs_over_selected_keys(torch_cuda):
+    rng = np.random.default_rng(62)
+    lens, new = list(rng.integers(3000, 5000, 10)), [3] * 10
+    b = Batch(torch_cuda, lens, new, 128, 64, seed=62)
+    b.check(sel=selected(rng, lens, new, 2048))
 
 
 def test_attention_does_not_depend_on_timing_or_workspace(torch_cuda):
