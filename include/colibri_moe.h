@@ -455,7 +455,8 @@ COLI_API coli_status colibri_indexer_select(int T, int L, int pos0, int topk, in
  * The choice is that of the exact scores: scores that fp32 cannot tell apart
  * are computed again in 64 bits before they are compared.  A NaN logit counts
  * as -infinity; a NaN u ranks as -infinity; +infinity logits share a softmax
- * equally; where every chosen s is 0 the weights are 0.
+ * equally; infinite biases force experts in or shut them out; where every
+ * chosen s is 0 the weights are 0.
  * 1 <= k <= min(32, topk_group * E / n_group), E <= 1024, n_group <= 32 a
  * divisor of E, 2 <= E / n_group for COLI_GROUP_TOP2 with topk_group < n_group.
  */
@@ -591,11 +592,11 @@ COLI_API coli_status colibri_kv_append(const coli_kv_desc* desc, int n_tokens, c
  * [q_start[0], q_start[B]) are left as they were.  Keys that a row does not see
  * do not reach its output, whatever values (infinities, NaN) they hold.  A
  * key whose page id is outside [0, n_pages), or beyond the block table, is left
- * out and reported (COLI_DEV_KV_BAD_PAGE).  Softmax and sums in fp32; the weights are rounded
- * to dtype for the product with the values.  The result does not depend on
- * timing.
- * Asynchronous on stream, two launches.  n_tokens = 0 does nothing.  Errors: COLI_EINVAL, COLI_EALIGN,
- * COLI_EWORKSPACE, COLI_EUNSUPPORTED, COLI_ECUDA.
+ * out and reported (COLI_DEV_KV_BAD_PAGE).  Softmax and sums in fp32; the
+ * weights are rounded to dtype for the product with the values.  The result
+ * does not depend on timing.
+ * Asynchronous on stream, two launches.  n_tokens = 0 does nothing.  Errors:
+ * COLI_EINVAL, COLI_EALIGN, COLI_EWORKSPACE, COLI_EUNSUPPORTED, COLI_ECUDA.
  */
 COLI_API coli_status colibri_kv_attention_workspace_size(int B, int n_tokens, int H, size_t* bytes);
 COLI_API coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, int H, float scale,

@@ -28,6 +28,11 @@ __device__ __forceinline__ uint32_t route_image(float v) {
 __device__ __forceinline__ float route_unimage(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
+// The value of an image whose low bits were replaced: an infinity's read as a NaN otherwise.
+__device__ __forceinline__ float route_unimage_cut(uint32_t k) {
+  const float v = route_unimage(k);
+  return v == v ? v : (k & 0x80000000u) ? INFINITY : -INFINITY;
+}
 
 // Bound on the distance of two approximate scores whose exact order may be the other one, given the token's
 // largest score.  A score's error is below s (2^-22 + 2^-22 + 2^-24) for exp2, the quotient and 1 + e, and
@@ -209,7 +214,7 @@ __device__ __noinline__ int route_picks_exact(const coli_route_desc r, Logit log
       const int e2 = __shfl_xor_sync(0xffffffffu, be, o);
       if (e2 != 0x7fffffff && (be == 0x7fffffff || u2 > bu || (u2 == bu && e2 < be))) { bu = u2; be = e2; }
     }
-    if (lane == j) pick = be;
+    if (lane == j && be < r.E) pick = be;
     if (be / NV == lane) left &= ~(1u << (be % NV));
   }
   return pick;
@@ -234,8 +239,9 @@ __device__ __forceinline__ void route_sort(uint32_t (&v)[N]) {
 }
 
 // z: this lane's logits (experts lane NV + i; NaN already -infinity, past E anything); b: their biases (0 without
-// one); bias: where they come from (or NULL); `logit(e)`: the logit of expert e again, by any lane.  topk_idx, topk_w: this token's [k]; sel_out (may be
-// NULL): the same ids; near_tie (may be NULL) as colibri_moe_debug_routing documents it.
+// one); bias: where they come from (or NULL); `logit(e)`: the logit of expert e again, by any lane.  topk_idx, topk_w:
+// this token's [k]; sel_out (may be NULL): the same ids; near_tie (may be NULL) as colibri_moe_debug_routing
+// documents it.
 // EXACT = false: returns whether a decision was closer than the scores' error (warp-uniform); its results are then
 // to be replaced by route_token_exact's.
 template <int NV, bool EXACT, typename Logit>
@@ -330,10 +336,10 @@ __device__ __forceinline__ bool route_token(const coli_route_desc& r, const floa
     }
     float sc = -INFINITY, mag = 0.f;
     if (mine < G) {
-      sc = route_unimage(t1);
+      sc = route_unimage_cut(t1);
       mag = fabsf(sc);
       if (top2) {
-        const float second = route_unimage(t2);
+        const float second = route_unimage_cut(t2);
         mag = fmaxf(mag, fabsf(second));
         sc += second;
         if (!(sc == sc)) sc = -INFINITY;
@@ -398,7 +404,7 @@ __device__ __forceinline__ bool route_token(const coli_route_desc& r, const floa
     const float gap = a == c ? 0.f : a - c;
     const float tol = tol_s + (2e-7f + 1.5f * kCut) * fabsf(a);
     tie |= gap < kNearTie + 2.f * kCut * fabsf(a);
-    bool close = gap <= tol && a > -INFINITY;
+    bool close = gap <= tol && fabsf(a) < INFINITY;     // infinite u are exact, and tol is infinite there
     if (close) {
       // unless every candidate around the border has the last pick's logit and bias: those tie exactly
       const int e_k = __shfl_sync(0xffffffffu, pick, k - 1);

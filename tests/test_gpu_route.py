@@ -132,6 +132,34 @@ def test_route_special_values(torch_cuda):
             check(torch_cuda, z, b, k=6, **kw)
 
 
+@pytest.mark.parametrize("E,groups", [(64, 8), (62, 31), (96, 4), (160, 5), (384, 8), (1000, 8)])
+def test_route_infinite_biases(torch_cuda, E, groups):
+    """Biases that force experts in (+infinity) or shut them out (-infinity): fewer and more of them than there are
+    picks, whole groups, groups that are not whole lanes; sums that pass fp32's largest value."""
+    rng = np.random.default_rng(E)
+    z = rng.standard_normal((16, E)).astype(np.float32)
+    size, k = E // groups, 4
+    base = (rng.standard_normal(E) * 0.05).astype(np.float32)
+    biases = []
+    for n in (1, 3, k, k + 3):
+        b = base.copy()
+        b[rng.choice(E, n, replace=False)] = np.inf
+        biases.append(b.copy())
+        b[rng.choice(E, E // 2, replace=False)] = -np.inf
+        biases.append(b)
+    shut = base.copy()
+    shut[size - 1:-size] = -np.inf
+    force = base.copy()
+    force[size + 1:2 * size] = np.inf
+    big = base.copy()
+    big[size:] = np.finfo(np.float32).max
+    biases += [shut, force, big, np.full(E, np.inf, np.float32), np.full(E, -np.inf, np.float32)]
+    for b in biases:
+        for kw in (dict(score="sigmoid"), dict(score="softmax"), dict(score="sigmoid", groups=groups, keep=2),
+                   dict(score="softmax", groups=groups, keep=2, gscore="max")):
+            check(torch_cuda, z, b, k=k, **kw)
+
+
 def test_route_zero_tokens_and_graph_replay(torch_cuda):
     torch = torch_cuda
     import quantized_expert_ffn_bias_gb300 as coli
