@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   __shared__ AtUnit unit_sm;                           // the run's first unit
   __shared__ uint32_t key_ok[2][4];                    // bit i of word w: key 32 w + i of the tile is there
   __shared__ uint32_t key_fin[2][4];                   // bit i of word w of a half: key 32 w + i has a finite score there
-  __shared__ __align__(16) float ref[kAtRows], fac[kAtRows], red[4][kAtRows];   // ref: the negated references
+  __shared__ __align__(16) float ref[kAtRows], fac[kAtRows], keep[kAtRows], red[4][kAtRows];   // ref: the negated references
   __shared__ __align__(16) int lim[kAtRows];           // last key position each row sees (dense)
   __shared__ int has_ref[kAtRows];                     // the row has seen a key
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -836,6 +836,8 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
             const float g = ceilf(fmaxf(fmaxf(red[0][id], red[1][id]), fmaxf(red[2][id], red[3][id])));
             const bool raise = g > kAtGrow || (!has_ref[id] && g > -INFINITY);
             fac[id] = raise ? g : 0.f;                 // by how much
+            // what that leaves of the sums so far: a first reference may lie far below 0, but they are 0 (or NaN) then
+            keep[id] = raise && has_ref[id] ? at_exp2(-g) : 1.f;
             if (raise) {
               ref[id] -= g;
               has_ref[id] = 1;
@@ -845,9 +847,8 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
           unset = sm_any(none);
 #pragma unroll
           for (int c = 0; c < kAtHalf; ++c) {
-            const float g = fac[c0 + c];
-            x[c] -= g;
-            l[c] *= at_exp2(-g);
+            x[c] -= fac[c0 + c];
+            l[c] *= keep[c0 + c];
           }
           if (t > t0) {                                // (the first tile's products overwrite O^T)
 #pragma unroll 1
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
               tmem_ld_wait();
 #pragma unroll
               for (int j = 0; j < 16; ++j)
-                r[j] = __float_as_uint(__uint_as_float(r[j]) * at_exp2(-fac[c0 + (i & 1) * 16 + j]));
+                r[j] = __float_as_uint(__uint_as_float(r[j]) * keep[c0 + (i & 1) * 16 + j]);
               tmem_st16(trow + col, r);
             }
             tmem_st_wait();

@@ -1,0 +1,85 @@
+"""Attention over the paged cache where its arithmetic or its arguments are at an edge (needs a GB300): very low and very
+uneven scores, row offsets that do not ascend or pass the batch, lengths of the step's token rows at the type's limit, and
+a pipeline wait that runs out."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from tests import serving_ref as R
+from tests.test_gpu_kv import Batch, V, W, ints, selected, torch_cuda  # noqa: F401  (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def rows_of(b, request):
+    """The cached rows of a request's keys, in key order: a view to read, and a function that writes them."""
+    n = b.lens[request]
+    pages = np.asarray(b.table[request])[np.arange(n) // b.page]
+    at = pages.astype(np.int64) * (b.stride // W) + np.arange(n) % b.page
+    flat = b.cache.view(-1, W)
+    idx = b.torch.from_numpy(at).cuda()
+    return flat, idx
+
+
+def shift_scores(b, request, nats):
+    """Lower (or raise) the scores of a request's keys by about nats[j], the same for every head: the last rotary value of
+    the queries is 48, so that the keys' last value v adds 48 v / 24 to a score."""
+    flat, idx = rows_of(b, request)
+    b.q[..., W - 1] = 48.0
+    add = b.torch.as_tensor(np.broadcast_to(np.asarray(nats, np.float32) / 2.0, (b.lens[request],)).copy()).cuda()
+    flat[idx, W - 1] = add.to(b.dt)
+
+
+FORMS = [(64, "bf16"), (64, "f16"), (16, "bf16"), (16, "f16")]      # TMA boxes, copied rows
+
+
+@pytest.mark.parametrize("page,dtype", FORMS)
+@pytest.mark.parametrize("nats", [-95.0, -150.0, -1000.0])
+def test_attention_every_score_very_low(torch_cuda, page, dtype, nats):
+    """One key, 300 keys and a chunk whose scores all lie far below the smallest power of two of fp32."""
+    for lens, new in (([1], [1]), ([300], [2]), ([150, 1], [150, 1])):
+        b = Batch(torch_cuda, lens, new, 16, page, dtype=dtype, seed=80)
+        for i in range(len(lens)):
+            shift_scores(b, i, nats)
+        out, z = b.check()
+        assert torch_cuda.isfinite(out).all() and torch_cuda.isfinite(z).all()
+
+
+@pytest.mark.parametrize("page,dtype", FORMS)
+@pytest.mark.parametrize("nats", [-100.0, -1000.0])
+def test_attention_first_tile_very_low(torch_cuda, page, dtype, nats):
+    """Very low scores in the first tile, or in all tiles but the last, and higher ones behind; the reverse order."""
+    for low in (slice(0, 128), slice(0, 500), slice(100, 700)):
+        shift = np.zeros(700)
+        shift[low] = nats
+        b = Batch(torch_cuda, [700, 700], [2, 1], 16, page, dtype=dtype, seed=81)
+        shift_scores(b, 0, shift)
+        shift_scores(b, 1, shift)
+        out, z = b.check()
+        assert torch_cuda.isfinite(out).all() and torch_cuda.isfinite(z).all()
+
+
+@pytest.mark.parametrize("page,dtype", FORMS)
+def test_attention_cut_runs_of_very_low_scores(torch_cuda, page, dtype):
+    """A request cut over the card: runs that see very low scores alone, next to runs that do not; and all of them low."""
+    for shift in (np.where(np.arange(12000) < 8000, -200.0, 0.0), np.where(np.arange(12000) < 5000, 0.0, -2000.0),
+                  np.full(12000, -300.0)):
+        b = Batch(torch_cuda, [12000], [1], 16, page, dtype=dtype, seed=82)
+        shift_scores(b, 0, shift)
+        out, z = b.check()
+        assert torch_cuda.isfinite(out).all() and torch_cuda.isfinite(z).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("empty", [0, 128, 300])
+def test_attention_selected_keys_of_very_low_scores(torch_cuda, dtype, empty):
+    """Selections whose first tiles hold no entry and whose keys all score very low."""
+    lens, new = [900, 700], [2, 1]
+    b = Batch(torch_cuda, lens, new, 64, 64, dtype=dtype, seed=83)
+    shift_scores(b, 0, -120.0)
+    shift_scores(b, 1, -900.0)
+    sel = selected(np.random.default_rng(83), lens, new, 600)
+    sel[:, :empty] = -1
+    out, z = b.check(sel=sel)
+    assert torch_cuda.isfinite(out).all() and torch_cuda.isfinite(z).all()
