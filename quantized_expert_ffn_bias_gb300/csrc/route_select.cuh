@@ -187,23 +187,29 @@ __device__ __noinline__ unsigned route_groups_exact(const coli_route_desc r, Log
 }
 
 // The picks (lane j < k: the j-th), by exact scores where the fp32 ones are within tol of the last pick's, `a`.
+// Those certainly above it are listed here, not taken from the rounds: these went by scores cut to buckets, inside
+// which the lower id goes first, so that where a + tol falls into a bucket an expert that is not certain may stand
+// among their first picks in the place of one that is.
 template <int NV, typename Logit>
 __device__ __noinline__ int route_picks_exact(const coli_route_desc r, Logit logit, const float* bias, RouteStats st,
                                               unsigned open, float a, float tol, int pick) {
   const int lane = threadIdx.x & 31, gsz = r.E / r.n_group;
   const RouteAgain<NV> x(r, logit, bias, st);
   unsigned left = 0;                     // this lane's candidates around the border
-  int sure = 0;                          // candidates certainly above it: the first picks
+  int sure = 0;                          // candidates certainly above it (fewer than k): the first picks
   for (int i = 0; i < NV; ++i) {
     const int e = lane * NV + i;
-    if (e >= r.E || !((open >> (e / gsz)) & 1u)) continue;
-    const float v = route_unimage(x.key[i]);
-    if (v > a + tol) ++sure;
-    else if (v >= a - tol) left |= 1u << i;
+    bool above = false;
+    if (e < r.E && ((open >> (e / gsz)) & 1u)) {
+      const float v = route_unimage(x.key[i]);
+      above = v > a + tol;
+      if (!above && v >= a - tol) left |= 1u << i;
+    }
+    for (unsigned b = __ballot_sync(0xffffffffu, above); b; b &= b - 1)
+      if (lane == sure++) pick = (__ffs(b) - 1) * NV + i;
   }
   double u[NV];
   x.exact(left, u);
-  sure = __reduce_add_sync(0xffffffffu, sure);
   for (int j = sure; j < r.k; ++j) {
     double bu = 0.0;
     int be = 0x7fffffff;
