@@ -455,8 +455,9 @@ COLI_API coli_status colibri_indexer_select(int T, int L, int pos0, int topk, in
  * The choice is that of the exact scores: scores that fp32 cannot tell apart
  * are computed again in 64 bits before they are compared.  A NaN logit counts
  * as -infinity; a NaN u ranks as -infinity; +infinity logits share a softmax
- * equally; infinite biases force experts in or shut them out; where every
- * chosen s is 0 the weights are 0.
+ * equally; infinite biases force experts in or shut them out.  Renormalised
+ * weights are the ratios of the chosen s also where these lie below fp32's
+ * range; where every chosen s is 0 in 64 bits the weights are 0.
  * 1 <= k <= min(32, topk_group * E / n_group), E <= 1024, n_group <= 32 a
  * divisor of E, 2 <= E / n_group for COLI_GROUP_TOP2 with topk_group < n_group.
  */

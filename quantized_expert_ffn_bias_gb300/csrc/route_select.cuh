@@ -65,6 +65,10 @@ __device__ __forceinline__ uint32_t route_key(float s, float b) {
   return route_image(u + 0.f);
 }
 
+// Renormalised weights whose sum is below this are computed again in 64 bits.  Above it a score that fp32 cannot hold
+// is less than 2^-66 of the sum, and a softmax's arguments stay above -46.
+constexpr float kTinyScores = 8.6736174e-19f;   // 2^-60
+
 // The rare comparisons in 64 bits.  They read the logits and biases again (arguments in arrays would have every
 // token store them: 16 us of 33 for 16384 tokens).
 struct RouteStats {
@@ -83,6 +87,14 @@ static __device__ __noinline__ double route_exact_score(bool softmax, double m, 
   }
   s += (double)b;
   return s == s ? s : -inf;
+}
+
+// Share of this lane's chosen expert in the sum of the warp's chosen scores, in 64 bits; .y: 1, or 0 where all are 0.
+// The softmax's own sum cancels.
+static __device__ __noinline__ float2 route_ratio(bool softmax, float m, float z, bool chosen) {
+  double s = chosen ? route_exact_score(softmax, (double)m, 1.0, z, 0.f) : 0.0, sum = s;
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum > 0.0 ? make_float2((float)(s / sum), 1.f) : make_float2(0.f, 0.f);
 }
 
 template <int NV>
@@ -445,6 +457,15 @@ __device__ __forceinline__ bool route_token(const coli_route_desc& r, const floa
     total = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  // chosen scores near or below fp32's range: their ratios are taken in 64 bits (unless every chosen logit is -infinity)
+  if (r.renorm && total < kTinyScores && __any_sync(0xffffffffu, lane < k && logit(pick) > -INFINITY)) {
+    again = true;
+    if constexpr (EXACT) {
+      const float2 ratio = route_ratio(softmax, st.m, lane < k ? logit(pick) : -INFINITY, lane < k);
+      w = ratio.x;
+      total = ratio.y;
+    }
   }
   if (lane < k) {
     topk_idx[rank] = pick;

@@ -41,3 +41,39 @@ def test_route_border_inside_a_bucket(torch_cuda, E):
                 for e, off in ((50, 0), (60, -1), (10, d), (100, d + gap)):
                     u[e] = np.int32(a + off).view(np.float32)
                 check(torch_cuda, np.zeros((1, E), np.float32), u - np.float32(0.5), k=3)
+
+
+@pytest.mark.parametrize("level", [-70.0, -100.0, -300.0, -700.0])
+def test_route_renormalised_weights_of_tiny_scores(torch_cuda, level):
+    """Every chosen score is below fp32's range (or close to it); their ratios are not."""
+    rng = np.random.default_rng(int(-level))
+    z = (level + rng.uniform(-3, 3, (40, 64))).astype(np.float32)
+    check(torch_cuda, z, None, k=6)
+    check(torch_cuda, z, None, k=6, groups=8, keep=3)
+    bias = (rng.standard_normal(64) * 0.1).astype(np.float32)
+    check(torch_cuda, z, bias, k=6)
+    # softmax: logits far above all others, shut out by their biases or by their group
+    z2 = (rng.uniform(-3, 3, (40, 64))).astype(np.float32)
+    z2[:, 7] = -level
+    shut = np.zeros(64, np.float32)
+    shut[7] = -np.inf
+    check(torch_cuda, z2, shut, k=6, score="softmax")
+    forced = np.zeros(64, np.float32)
+    forced[16:32] = 2.0
+    check(torch_cuda, z2, forced, k=6, score="softmax", groups=4, keep=1, gscore="max")
+    check(torch_cuda, z2, forced, k=6, score="softmax", renorm=False, groups=4, keep=1, gscore="max")
+
+
+def test_route_weights_without_any_score(torch_cuda):
+    """Scores of 0 in 64 bits: the weights are 0."""
+    z = np.full((3, 64), -np.inf, np.float32)
+    z[1] = np.finfo(np.float32).min
+    z[2] = -2000.0
+    check(torch_cuda, z, None, k=6)
+    z[:, 0] = 1.0
+    shut = np.zeros(64, np.float32)
+    shut[0] = -np.inf
+    check(torch_cuda, z, shut, k=6)
+    check(torch_cuda, z, shut, k=6, score="softmax")
+    z[:, 0] = np.inf
+    check(torch_cuda, z, shut, k=6, score="softmax")
