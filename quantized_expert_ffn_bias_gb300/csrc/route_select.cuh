@@ -39,10 +39,11 @@ __device__ __forceinline__ float route_unimage_cut(uint32_t k) {
 // s (1 - s) |z| 2^-23 for the rounded argument of exp2; the latter is largest at the largest score or, where that
 // is above 1/2, below 2^-25 ((1 - s) |z| s <= 0.23).  A softmax also carries the sum of up to 32 terms a lane and
 // 5 levels (37 * 2^-24), and its arguments z - max enter as x e^-x <= 0.37.  Twice that covers two scores, and a
-// quarter is added.
+// quarter is added.  A score below 2^-126 may be flushed to 0 (kFlush: two of them).
 __device__ __forceinline__ float route_tol(bool softmax, float smax) {
-  if (softmax) return 2.5f * smax * 3.2e-6f;
-  return 2.5f * smax * (6e-7f + 1.3e-7f * (1.f + fabsf(__logf(fmaxf(smax, 1e-37f)))));
+  constexpr float kFlush = 2.5e-38f;
+  if (softmax) return 2.5f * smax * 3.2e-6f + kFlush;
+  return 2.5f * smax * (6e-7f + 1.3e-7f * (1.f + fabsf(__logf(fmaxf(smax, 1e-37f))))) + kFlush;
 }
 
 __device__ __forceinline__ float route_exp2(float x) {

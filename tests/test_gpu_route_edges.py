@@ -77,3 +77,24 @@ def test_route_weights_without_any_score(torch_cuda):
     check(torch_cuda, z, shut, k=6, score="softmax")
     z[:, 0] = np.inf
     check(torch_cuda, z, shut, k=6, score="softmax")
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+def test_route_scores_around_the_smallest_normal_number(torch_cuda, score):
+    """Scores of 2^-120 to 2^-132, of which fp32 arithmetic may flush any below 2^-126 to 0: in sums of two they decide
+    between groups, with biases as small between experts."""
+    rng = np.random.default_rng(126)
+    for E, groups in ((64, 8), (256, 8), (384, 6), (62, 31)):
+        z = rng.uniform(-91.5, -86.0, (300, E)).astype(np.float32)
+        if score == "softmax":
+            z[:, 3] = 0.0                              # the sum is 1, the others' scores are exp(z)
+        shut = np.zeros(E, np.float32)
+        shut[3] = -np.inf
+        small = (rng.standard_normal(E) * 2.0 ** -126).astype(np.float32)
+        small[3] = -np.inf
+        keep = max(2, groups // 3)
+        for bias in (shut, small):
+            check(torch_cuda, z, bias, k=4, score=score, renorm=False)
+            check(torch_cuda, z, bias, k=4, score=score)
+            for gscore in ("top2", "max"):
+                check(torch_cuda, z, bias, k=4, score=score, groups=groups, keep=keep, gscore=gscore)
