@@ -582,6 +582,8 @@ COLI_API coli_status colibri_kv_append(const coli_kv_desc* desc, int n_tokens, c
  *                (a stride along an axis of one is not read).  1 <= H <= 1024.
  *   q_start      int32 [B + 1] ascending (else nothing is computed and the
  *                status word gets COLI_DEV_KV_TOKENS), seq_len int32 [B].
+ *                Rows of q_start outside [0, n_tokens) do not exist; those of
+ *                the same request that do are computed.
  *   topk_idx     device int32 [n_tokens][topk], or NULL (topk is then not read).
  *   out          device [n_tokens][H][512] of desc->dtype, 16-byte aligned.
  *   lse          device float [n_tokens][H] or NULL: log of the softmax's sum.

@@ -136,7 +136,7 @@ struct AtRun {
 // unit_sm receives the run's first unit.  The code runs once a launch, and what it costs is mostly fetching it:
 // loops are kept rolled and each step is written once.
 __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_sm) {
-  int* qs = sm;                      // [B + 1] q_start, kept inside the batch
+  int* qs = sm;                      // [B + 1] q_start
   int* base = qs + p.B + 1;          // [B + 1] first unit of each request
   int* seq = base + p.B + 1;         // [B]
   __shared__ int warp_tot[32], total, s_unit0, s_flags[3];
@@ -144,18 +144,16 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
   const int tid = threadIdx.x, nthr = blockDim.x, B = p.B, max_ctas = gridDim.x;
   if (tid <= kAtGangs) sums[tid] = 0;
   if (tid < 3) s_flags[tid] = 0;
-  {
-    const int lo = max(0, min(p.q_start[0], p.n_tokens)), hi = max(lo, min(p.q_start[B], p.n_tokens));
 #pragma unroll 1
-    for (int b = tid; b <= B; b += nthr) {
-      qs[b] = max(lo, min(p.q_start[b], hi));
-      if (b < B) seq[b] = p.seq_len[b];
-    }
+  for (int b = tid; b <= B; b += nthr) {
+    qs[b] = p.q_start[b];
+    if (b < B) seq[b] = max(0, p.seq_len[b]);
   }
   __syncthreads();
   const int heads = (p.H + kAtRows - 1) / kAtRows;
   const int most = p.d.max_pages * p.d.page_size;      // (at most 2^31 - 1: checked by the host)
   const int sel_tiles = (p.topk + kAtKeys - 1) / kAtKeys;
+  auto row_of_batch = [&](int i) { return max(0, min(qs[i], p.n_tokens)); };      // rows outside the batch do not exist
   // Requests: row tiles over the same keys (a row tile group), how many such groups, key tiles of each.  Sums of
   // key tiles stay below 2^31 (checked by the host).
   struct Req {
@@ -164,10 +162,10 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
   };
   auto request = [&](int b) {
     Req r;
-    const int T = max(0, qs[b + 1] - qs[b]);
+    const int T = max(0, row_of_batch(b + 1) - row_of_batch(b));
     r.n = p.sel ? T : min(T, 1);
     r.rows = p.sel ? heads : (T * p.H + kAtRows - 1) / kAtRows;        // (n_tokens * H < 2^31 - 64)
-    const int keys = max(0, min(seq[b], most));
+    const int keys = min(seq[b], most);
     r.tiles = (unsigned)r.n * (unsigned)(p.sel ? sel_tiles : max(1, (int)(((unsigned)keys + kAtKeys - 1) / kAtKeys)));
     return r;
   };
@@ -240,10 +238,10 @@ __device__ __forceinline__ AtRun at_plan(const AtArgs& p, int* sm, AtUnit* unit_
           if (base[mid] <= i) l = mid;
           else h = mid;
         }
-        const int q0 = qs[l], q1 = qs[l + 1];
+        const int q0 = row_of_batch(l), q1 = row_of_batch(l + 1);
         un.b = l;
         un.seq = seq[l];
-        un.shift = un.seq - q1;                        // seq - (q1 - q0) - q0
+        un.shift = un.seq - qs[l + 1];                 // seq - (qs[l + 1] - qs[l]) - qs[l]
         un.pad = 0;
         if (p.sel) {
           const int per = (heads + gang - 1) / gang, j = i - base[l], tok = q0 + (per == 1 ? j : j / per);

@@ -83,3 +83,26 @@ def test_attention_selected_keys_of_very_low_scores(torch_cuda, dtype, empty):
     sel[:, :empty] = -1
     out, z = b.check(sel=sel)
     assert torch_cuda.isfinite(out).all() and torch_cuda.isfinite(z).all()
+
+
+@pytest.mark.parametrize("starts", [[0, 5, 4], [3, 0, 4], [0, 9, 2], [9, 8, 4], [0, 2, -1], [0, -5, 4]])
+@pytest.mark.parametrize("page", [64, 16])
+def test_attention_refuses_any_q_start_that_descends(torch_cuda, starts, page):
+    """Also where the entries lie outside the batch: nothing is written, the status says so."""
+    b = Batch(torch_cuda, [300, 100], [2, 2], 64, page, seed=85)
+    b.q_start = np.array(starts, np.int32)
+    out, z = b.run(status=R.TOKENS)
+    assert (out == 3.0).all() and (z == 3.0).all()
+
+
+@pytest.mark.parametrize("page", [64, 16])
+def test_attention_rows_of_a_request_that_passes_the_batch(torch_cuda, page):
+    """A request of five new tokens of which the batch holds two: those are its first two, at their own positions."""
+    b = Batch(torch_cuda, [300, 100], [2, 5], 64, page, seed=86)
+    cache = R.Cache(b.cache.double().cpu().numpy().ravel(), b.page, b.stride)
+    ref, lse, tol, tol_lse, _ = R.attention(b.q.double().cpu().numpy(), cache, b.table, b.q_start, b.lens, b.scale,
+                                            torch_cuda.finfo(b.dt).eps)
+    b.q, b.N = b.q[:4].contiguous(), 4
+    out, z = b.run()
+    assert (np.abs(out.double().cpu().numpy() - ref[:4]) <= tol[:4]).all()
+    assert (np.abs(z.double().cpu().numpy() - lse[:4]) <= tol_lse[:4]).all()
