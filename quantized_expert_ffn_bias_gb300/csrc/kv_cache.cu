@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) kv_step_kernel(const StepArgs
       } else if (fine && s >= 0 && s <= (long long)h * ps && (long long)s + n <= (long long)p.d.max_pages * ps) {
         a = n;
         v.b = need_of(s, n, h);
-        v.c = min(n, p.n_tokens + 1);      // (more than there is room for is as good as all of it)
+        v.c = (I)min(n, p.n_tokens) + (n > p.n_tokens);      // (more than there is room for is as good as all of it)
       } else {
         a = -2;
         bits |= COLI_DEV_KV_TABLE_FULL;
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kStepThreads, 1) kv_step_kernel(const StepArgs
         need = need_of(seq[b], add[b], hold[b]);
         want = add[b];
         const bool pages = need > 0 && (long long)pp[b] + need > avail;
-        const bool rows = want > 0 && (long long)qs[b] + min(want, p.n_tokens + 1) > p.n_tokens;
+        const bool rows = want > 0 && (long long)qs[b] + want > p.n_tokens;
         if (pages) bits |= COLI_DEV_KV_NO_PAGES;
         if (rows) bits |= COLI_DEV_KV_TOKENS;
         if (pages || rows) {

@@ -106,3 +106,31 @@ def test_attention_rows_of_a_request_that_passes_the_batch(torch_cuda, page):
     out, z = b.run()
     assert (np.abs(out.double().cpu().numpy() - ref[:4]) <= tol[:4]).all()
     assert (np.abs(z.double().cpu().numpy() - lse[:4]) <= tol_lse[:4]).all()
+
+
+@pytest.mark.parametrize("n_tokens", [(1 << 31) - 1, (1 << 31) - 2])
+def test_step_of_as_many_rows_as_the_type_counts(torch_cuda, n_tokens):
+    """Room for 2^31 - 1 token rows: the sums of new tokens do not wrap.  Only the rows before q_start[B] are written, so
+    the arrays here hold no more than those."""
+    torch = torch_cuda
+    import quantized_expert_ffn_bias_gb300 as coli
+    page, mp, n_pages = 16, 4, 12
+    new, seq, held = [3, 0, 20, -1, 1], [5, 0, 0, 7, 16], [1, 0, 0, 1, 1]
+    table = np.full((5, mp), -1, np.int32)
+    table[0, 0], table[3, 0], table[4, 0] = 4, 5, 6
+    free = np.array([0, 1, 2, 3, 7, 8, 9, 10, 11, -1, -1, -1], np.int32)
+    want = R.step(page, mp, n_pages, n_tokens, new, seq, held, table, free, 9)
+    t = {k: ints(torch, v) for k, v in dict(new=new, seq=seq, held=held, table=table, free=free, count=[9], seq_out=[0] * 5,
+                                            held_out=[0] * 5, count_out=[0], q_start=[0] * 6, position=[-9] * 64,
+                                            slot=[-9] * 64, status=[0]).items()}
+    d = coli.coli_kv_desc(page, mp, n_pages, 0, page * W)
+    coli.colibri_kv_step(d, 5, n_tokens, *t.values(), torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    got = {k: v.cpu().numpy() for k, v in t.items()}
+    for k in ("seq_out", "held_out", "q_start", "table", "free"):
+        np.testing.assert_array_equal(got[k], want[k], err_msg=k)
+    n = len(want["position"])
+    np.testing.assert_array_equal(got["position"][:n], want["position"])
+    np.testing.assert_array_equal(got["slot"][:n], want["slot"])
+    assert (got["position"][n:] == -9).all() and got["status"][0] == want["status"] == 0
+    assert got["count_out"][0] == want["count_out"]
