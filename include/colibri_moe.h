@@ -541,7 +541,9 @@ typedef struct {
  * A request is not served (no tokens, nothing changed, a status bit) when its
  * lengths are not valid or exceed max_pages, or when the pages or the token
  * rows that it and the requests before it ask for exceed those there are
- * (requests that ask for none of what ran out are still served).
+ * (requests that ask for none of what ran out are still served).  A held count
+ * outside [0, max_pages] names no pages: it counts as 0 and is 0 in held_out,
+ * also for a finished request (the caller keeps a copy where it may be wrong).
  * A held page id outside [0, n_pages) gives slot -1 (COLI_DEV_KV_BAD_PAGE).
  * Asynchronous on stream; one launch.  Errors: COLI_EINVAL, COLI_EALIGN,
  * COLI_EUNSUPPORTED, COLI_ECUDA.
