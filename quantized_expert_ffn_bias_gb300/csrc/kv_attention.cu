@@ -52,7 +52,6 @@ constexpr int kAtMaxB = 8192, kAtMaxH = 1024;
 constexpr int kAtMaxDevices = 64;                  // devices whose properties are kept between calls
 constexpr size_t kAtSmem = (size_t)kAtBoxes * (kAtBoxBytes + kAtQBoxBytes) + 1024;
 constexpr int kAtPart = kAtRows * kAtV;            // floats of a partial O
-constexpr float kAtUnset = -1e30f;                 // reference of a part whose row has seen no key
 constexpr float kAtGrow = 8.f;                     // growth (log2) that raises a reference
 constexpr uint32_t kAtSCol = 256;                  // TMEM column of S^T (O^T: 0..255)
 
@@ -909,7 +908,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
           if (p.lse && row < ut.row_end)
             p.lse[row] = sum == 0.f ? -INFINITY : (log2f(sum) - ref[id]) * 0.693147180559945309f;
         } else {
-          p.part_ml[(size_t)slot * kAtRows + id] = make_float2(has_ref[id] ? -ref[id] : kAtUnset, sum);
+          p.part_ml[(size_t)slot * kAtRows + id] = make_float2(has_ref[id] ? -ref[id] : -INFINITY, sum);
         }
       }
       sm_sync();
@@ -961,6 +960,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
 // Adds up the parts of every cut unit, in order.  A task is four rows of a unit: 64 values where the parts are
 // many (eight thread groups take every eighth part each, then meet in shared memory), all 512 where they are
 // few (the values of the first parts are then loaded before their weights are known).
+constexpr float kAtLowest = -3.402823466e38f;      // below every reference; a part whose row saw no key has -infinity
 constexpr int kAtJoinThreads = 512, kAtJoinCtas = 304, kAtJoinFew = 8;
 __host__ __device__ constexpr int at_join_tasks(int parts) { return parts <= 0 ? 0 : parts <= kAtJoinFew ? 16 : 128; }
 
@@ -1033,7 +1033,7 @@ __global__ void __launch_bounds__(kAtJoinThreads, 2) kv_attention_join_kernel(co
       }
       __syncthreads();
       if (tid < 4) {                                    // thread r: the parts' weights for row c + r
-        float m = kAtUnset, l = 0.f;
+        float m = kAtLowest, l = 0.f;
         for (int i = 0; i < n; ++i) m = fmaxf(m, wgt[i][tid]);
         for (int i = 0; i < n; ++i) {
           const float w = at_exp2(wgt[i][tid] - m);
@@ -1060,7 +1060,7 @@ __global__ void __launch_bounds__(kAtJoinThreads, 2) kv_attention_join_kernel(co
     }
     __syncthreads();
     if (warp < 4) {                                     // warp w: the parts' weights for row c + w
-      float m = kAtUnset;
+      float m = kAtLowest;
       for (int i = lane; i < n; i += 32) m = fmaxf(m, wgt[i][warp]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));

@@ -134,3 +134,22 @@ def test_step_of_as_many_rows_as_the_type_counts(torch_cuda, n_tokens):
     np.testing.assert_array_equal(got["slot"][:n], want["slot"])
     assert (got["position"][n:] == -9).all() and got["status"][0] == want["status"] == 0
     assert got["count_out"][0] == want["count_out"]
+
+
+def test_attention_scores_below_any_reference(torch_cuda):
+    """Finite scores of -5e34, equal for all keys (so the result is the mean of their values), in a unit cut over CTAs of
+    which half see no key.  Weights are 1, their sum and the products' sums in fp32: 2^-23 a term, then one rounding."""
+    torch = torch_cuda
+    b = Batch(torch, [5000], [1], 64, 64, seed=87)
+    flat, idx = rows_of(b, 0)
+    b.q[..., W - 1] = 2.0 ** 60
+    flat[idx, W - 1] = -2.0 ** 60
+    sel = selected(np.random.default_rng(87), [5000], [1], 2048)
+    sel[0, :1024] = -1
+    out, z = b.run(sel=sel)
+    v = flat[idx[torch.from_numpy(sel[0, 1024:]).cuda().long()], :V].double()
+    want, mag = v.mean(0), v.abs().mean(0)
+    tol = 2.0 ** -23 * 1100 * mag + torch.finfo(b.dt).eps / 2 * want.abs() * 1.01
+    assert ((out[0].double() - want).abs() <= tol).all()
+    s = -(2.0 ** 120) * b.scale
+    assert ((z.double() - s).abs() <= 2.0 ** -21 * abs(s)).all()
