@@ -19,10 +19,10 @@
 // P^T takes the place of the rotary part, which only S^T reads.
 //
 // Softmax: per row a reference m (log2 units) that is raised, with the sums and
-// O^T rescaled, only when a score exceeds it by 8: weights stay below 2^8, and
-// a tile needs no reduction over its keys (they lie across lanes).  References
-// are whole numbers, so that raising one rounds nothing.  Each thread sums its
-// own key's weights; the sums are reduced once at the end.
+// O^T rescaled, only when a score exceeds it by 8 (fp16: 15, see at_top): a tile
+// needs no reduction over its keys (they lie across lanes).  References are
+// whole numbers, so that raising one rounds nothing.  Each thread sums its own
+// key's weights; the sums are reduced once at the end.
 //
 // Work: units (row tiles of one request, or of one token where keys are
 // selected) with their key tiles, dealt in equal runs of key tiles to one CTA
@@ -52,7 +52,10 @@ constexpr int kAtMaxB = 8192, kAtMaxH = 1024;
 constexpr int kAtMaxDevices = 64;                  // devices whose properties are kept between calls
 constexpr size_t kAtSmem = (size_t)kAtBoxes * (kAtBoxBytes + kAtQBoxBytes) + 1024;
 constexpr int kAtPart = kAtRows * kAtV;            // floats of a partial O
-constexpr float kAtGrow = 8.f;                     // growth (log2) that raises a reference
+// A reference makes the largest weight 2^(top - 1) .. 2^top; growth to 2^(top + kAtGrow) raises it.  bf16 has fp32's
+// range; fp16 ends at 2^16 and loses bits below 2^-14 (all below 2^-25), so its weights take the upper part.
+constexpr float kAtGrow = 8.f;
+__host__ __device__ constexpr float at_top(bool bf16) { return bf16 ? 0.f : 7.f; }
 constexpr uint32_t kAtSCol = 256;                  // TMEM column of S^T (O^T: 0..255)
 
 // A unit: the work of one gang of CTAs, 64 rows each, over the same keys.
@@ -824,13 +827,13 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
 #pragma unroll
         for (int c = 0; c < kAtHalf; c += 4)
           top = fmaxf(fmaxf(fmaxf(top, x[c]), fmaxf(x[c + 1], x[c + 2])), x[c + 3]);
-        if (sm_any(top > kAtGrow || unset || !ok)) {
+        if (sm_any(top > kAtGrow + at_top(BF16) || unset || !ok)) {
           if (sm_any(!ok)) { ok = false; break; }
           red[sp][c0 + lane] = warp_columns(x, [](float a, float b) { return fmaxf(a, b); });
           sm_sync();
           bool none = false;
           if (id < kAtRows) {
-            const float g = ceilf(fmaxf(fmaxf(red[0][id], red[1][id]), fmaxf(red[2][id], red[3][id])));
+            const float g = ceilf(fmaxf(fmaxf(red[0][id], red[1][id]), fmaxf(red[2][id], red[3][id]))) - at_top(BF16);
             const bool raise = g > kAtGrow || (!has_ref[id] && g > -INFINITY);
             fac[id] = raise ? g : 0.f;                 // by how much
             // what that leaves of the sums so far: a first reference may lie far below 0, but they are 0 (or NaN) then

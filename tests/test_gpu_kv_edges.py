@@ -153,3 +153,44 @@ def test_attention_scores_below_any_reference(torch_cuda):
     assert ((out[0].double() - want).abs() <= tol).all()
     s = -(2.0 ** 120) * b.scale
     assert ((z.double() - s).abs() <= 2.0 ** -21 * abs(s)).all()
+
+
+@pytest.mark.parametrize("page", [64, 16])
+def test_attention_many_small_weights_in_fp16(torch_cuda, page):
+    """One strong key, then 20,000 whose weights are 2^-25 of it: together 2^-10.7 of the weights, times values of 1,000,
+    which the weights' rounding to fp16 must not lose.  The largest weight is kept above 2^6, so what a weight loses below
+    fp16's normal range is half of 2^-24 of 2^6 at most: the bound's `tiny` is 2^-7 of the one for a largest weight of 1/2.
+    As many requests as there are SMs share the keys, so that no request is cut (a part without the strong key would have
+    a reference of its own)."""
+    torch = torch_cuda
+    n, B = 20001, torch.cuda.get_device_properties(0).multi_processor_count
+    b = Batch(torch, [n], [1], 2, page, dtype="f16", seed=88)
+    b.scale = float(np.log(2.0))                       # scores in log2 units are the products themselves
+    b.q.zero_()
+    b.q[..., W - 1] = 1.0
+    flat, idx = rows_of(b, 0)
+    rows = torch.zeros((n, W), dtype=b.dt, device="cuda")
+    rows[:, :V] = 1000.0
+    rows[:, W - 1] = -25.015625
+    rows[0, :V] = 0.0
+    rows[0, W - 1] = 0.0
+    flat[idx] = rows
+    cache = R.Cache(b.cache.double().cpu().numpy().ravel(), b.page, b.stride)
+    info = torch.finfo(b.dt)
+    ref, lse, tol, tol_lse, _ = R.attention(b.q.double().cpu().numpy(), cache, b.table, b.q_start, b.lens, b.scale,
+                                            info.eps, tiny=float(info.smallest_normal) * info.eps / 128)
+    b.lens, b.table, b.q_start, b.N = [n] * B, np.repeat(b.table, B, 0), np.arange(B + 1, dtype=np.int32), B
+    b.q = b.q.expand(B, -1, -1).contiguous()
+    out, z = b.run()
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all(), (out[0, 0, :3], ref[0, 0, :3], tol[0, 0, :3])
+    assert (np.abs(z.double().cpu().numpy() - lse) <= tol_lse).all()
+
+
+def test_attention_fp16_references_rise_far(torch_cuda):
+    """Scores that climb by 2 to 14 (log2) a tile, with fp16 weights up to 2^15: no weight or sum leaves its type."""
+    torch = torch_cuda
+    for step in (1.5, 5.0, 9.5):
+        b = Batch(torch, [1300], [2], 16, 64, dtype="f16", seed=89)
+        shift_scores(b, 0, np.arange(1300) // 128 * step)
+        out, z = b.check()
+        assert torch.isfinite(out).all() and torch.isfinite(z).all()
