@@ -613,6 +613,17 @@ COLI_API coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n
  * COLI_DEV_KV_BAD_PAGE, COLI_DEV_KV_TOKENS, COLI_DEV_WAIT_TIMEOUT (then
  * COLI_EDEVICE). */
 COLI_API coli_status colibri_kv_check_status(const void* workspace, int32_t* device_status, void* stream);
+/*
+ * Failure-path testing of colibri_kv_attention, for the following calls of this
+ * thread.  flags: 0 (off) or COLI_INJECT_WITHHOLD_STAGE, with which the first
+ * CTA's first key rows never count as there, so that the roles waiting for them
+ * reach the wait limit, record COLI_DEV_WAIT_TIMEOUT, let their copies and products
+ * end, free tensor memory and return.  wait_limit_ms as for
+ * colibri_moe_debug_inject, at most the default.  The outputs of an injected
+ * call are not meaningful; the next call without injection, also on the same
+ * workspace, is a normal one.  Errors: COLI_EINVAL.
+ */
+COLI_API coli_status colibri_kv_debug_inject(int flags, double wait_limit_ms);
 
 /* Number of kernel launches the last forward call of this plan issued. */
 COLI_API int colibri_moe_last_launch_count(const coli_moe_plan_t* plan);

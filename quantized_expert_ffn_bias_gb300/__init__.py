@@ -156,6 +156,8 @@ def lib():
             L.colibri_kv_attention.restype = st
             L.colibri_kv_check_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), vp]
             L.colibri_kv_check_status.restype = st
+            L.colibri_kv_debug_inject.argtypes = [i32, ctypes.c_double]
+            L.colibri_kv_debug_inject.restype = st
             L.colibri_moe_last_launch_count.argtypes = [vp]
             L.colibri_moe_last_launch_count.restype = i32
             L.colibri_moe_last_error.argtypes = []
@@ -283,6 +285,11 @@ def colibri_kv_check_status(workspace, stream=None) -> int:
     if rc not in (COLI_OK, COLI_EDEVICE):
         _check(rc)
     return v.value
+
+
+def colibri_kv_debug_inject(flags: int, wait_limit_ms: float = 0.0):
+    """Failure-path testing of colibri_kv_attention: COLI_INJECT_WITHHOLD_STAGE for this thread's next calls (0 = off)."""
+    _check(lib().colibri_kv_debug_inject(flags, wait_limit_ms))
 
 
 class coli_cache_stats(ctypes.Structure):

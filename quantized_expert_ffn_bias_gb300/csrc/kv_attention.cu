@@ -97,6 +97,7 @@ struct AtArgs {
   float* part;                       // [2 kAtMaxCtas] partial O, in the order the main kernel's threads hold it (at_part)
   float2* part_ml;                   // [2 kAtMaxCtas][64] reference, sum
   unsigned long long wait_ns;
+  int withhold;                      // failure-path test: 1: CTA 0's first copies never count as complete
 };
 
 // Place of row c (a multiple of four: four rows follow one another) and value v in a partial O.  A thread of
@@ -477,7 +478,9 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
   }
   if (threadIdx.x == 0) {
     // copying warps: one arrival a thread, and one a warp for key_ok (with the rotary box)
-    for (int i = 0; i < 5; ++i) mbar_init(&full[i], TMA ? 1 : kAtLoadWarps * 32 + (i == 4 ? kAtLoadWarps : 0));
+    // (an arrival too many for a withheld stage; a test of it where the copies are issued costs 3 % of short runs)
+    for (int i = 0; i < 5; ++i)
+      mbar_init(&full[i], (TMA ? 1 : kAtLoadWarps * 32 + (i == 4 ? kAtLoadWarps : 0)) + (i == 0 && blockIdx.x == 0 ? p.withhold : 0));
     for (int i = 0; i < 4; ++i) mbar_init(&empty[i], 1);
     mbar_init(&q_full, TMA ? 1 : kAtLoadWarps * 32);
     mbar_init(&q_empty, 1);
@@ -515,6 +518,9 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
     const int lw = warp == 0 ? 0 : warp - kAtFirstLoad + 1;           // copying: this warp's keys of a tile start at 32 kAtLaneKeys lw
     bool ok = true;
     int it = 0, un = 0;
+    // it, un: tiles begun, units whose queries are on their way, when the loop ends; the last tile's barriers d < given
+    // have copies on their way
+    int given = 5;
     const int n_box = TMA ? kAtKeys >> p.box_log2 : 0;       // boxes of 64 columns a tile
     for (int at = beg, u = unit0; ok && at < end; ++u) {
       const AtUnit ut = u == unit0 ? unit_sm : units[u];
@@ -619,7 +625,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
         // pairs of value boxes as the previous tile's products free them, then the rotary box
 #pragma unroll 1
         for (int d = 0; d < 4 && ok; ++d) {
-          if (it > 0 && !mbar_wait(&empty[d], (it - 1) & 1, p.wait_ns)) { ok = false; break; }
+          if (it > 0 && !mbar_wait(&empty[d], (it - 1) & 1, p.wait_ns)) { ok = false; given = d; break; }
           if constexpr (TMA) {
             if (d == 0 && lane < 4) key_ok[it & 1][lane] = mine[0];
             if (lane == 0) mbar_arrive_expect_tx(&full[d], (uint32_t)(2 * kAtBoxBytes));
@@ -643,7 +649,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
             copies_arrive(&full[d]);
           }
         }
-        if (!ok) break;
+        if (!ok) { ++it; break; }
         if constexpr (TMA) {
           if (lane == 0) mbar_arrive_expect_tx(&full[4], (uint32_t)kAtBoxBytes);
           __syncwarp();
@@ -678,23 +684,22 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
           }
         }
       }
-      if (!ok) break;
       at = ut.first + t1;
       ++un;
     }
-    if (!ok) {
-      fail_wait();
-      // copies in flight land before the CTA leaves
-      if constexpr (!TMA) asm volatile("cp.async.wait_all;" ::: "memory");
-      if (TMA && lane == 0) {
-        mbar_wait(&q_full, un & 1, 1000000ull);
-        for (int d = 0; d < 5; ++d) {
-          if (it > 0) mbar_wait(&full[d], (it - 1) & 1, 1000000ull);
-          mbar_wait(&full[d], it & 1, 1000000ull);
-        }
+    if (!ok) fail_wait();
+    // Copies in flight land before the CTA leaves, whichever role gave up: this warp may have issued its last ones long
+    // before.  A barrier's phase before the awaited one is complete: its copies were waited for by way of `empty`.
+    if constexpr (!TMA) asm volatile("cp.async.wait_all;" ::: "memory");
+    if (TMA && lane == 0) {
+      if (un > 0) mbar_wait(&q_full, (un - 1) & 1, kWaitLimitNs);
+#pragma unroll 1
+      for (int d = 0; d < 5; ++d) {
+        const int t = it - (d < given ? 1 : 2);
+        if (t >= 0) mbar_wait(&full[d], t & 1, d == 0 && p.withhold ? 1000000ull : kWaitLimitNs);
       }
-      __syncwarp();
     }
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (the warp stays converged; its waits
     // are the suspending ones: polling takes issue slots from the softmax warps beside it, chunk 1.72 -> 1.69 ms)
@@ -727,6 +732,7 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
             umma_steps<4, 2, 2>(tmem + kAtSCol, kd + (uint64_t)(x * (kAtBoxBytes >> 4)),
                                 qd + (uint64_t)(x * (kAtQBoxBytes >> 4)), idesc, x ? 1u : 0u);
         }
+        if (!ok) break;
         umma_commit_elect(&s_full);
         if (t + 1 == t1) umma_commit_elect(&q_empty);
         ok = ok && mbar_wait(&p_ready, it & 1, p.wait_ns);
@@ -745,11 +751,13 @@ __global__ void __launch_bounds__(at_threads(TMA), 1)
       umma_commit_elect(&o_full);
       ++un;
     }
+    // What was issued ends before tensor memory is freed, whichever role gave up: the last unit's products and then
+    // those of a unit left in its middle (committed after that wait: a barrier's phases are awaited one by one).
+    if (un > 0) mbar_wait(&o_full, (un - 1) & 1, kWaitLimitNs);
     if (!ok) {
       if (lane == 0) fail_wait();
-      // what was issued ends before tensor memory is freed
       umma_commit_elect(&o_full);
-      mbar_wait(&o_full, un & 1, p.wait_ns);
+      mbar_wait(&o_full, un & 1, kWaitLimitNs);
     }
   } else {
     // ---------------------------------------------------------------- softmax and output (warps 2 ..)
@@ -1152,6 +1160,12 @@ static cudaError_t at_launch(const AtArgs& a, const CUtensorMap& kmap, const CUt
   return launch_pdl(kv_attention_join_kernel<BF16>, dim3(kAtJoinCtas), dim3(kAtJoinThreads), 0, st, a, ctas);
 }
 
+// Failure-path testing (colibri_kv_debug_inject): of the calls of this thread.
+static thread_local struct {
+  int flags = 0;
+  unsigned long long wait_ns = kWaitLimitNs;
+} at_inject;
+
 }  // namespace coli
 
 using namespace coli;
@@ -1257,12 +1271,24 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   a.joins = reinterpret_cast<AtJoin*>(ws + w.joins);
   a.part = reinterpret_cast<float*>(ws + w.part);
   a.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
-  a.wait_ns = kWaitLimitNs;
+  a.wait_ns = at_inject.wait_ns;
+  a.withhold = at_inject.flags & COLI_INJECT_WITHHOLD_STAGE ? 1 : 0;
   const int ctas = sms < kAtMaxCtas ? sms : kAtMaxCtas;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (tma) ce = bf16 ? at_launch<true, true>(a, kmap, qmap, ctas, dev, st) : at_launch<false, true>(a, kmap, qmap, ctas, dev, st);
   else ce = bf16 ? at_launch<true, false>(a, kmap, qmap, ctas, dev, st) : at_launch<false, false>(a, kmap, qmap, ctas, dev, st);
   return ce == cudaSuccess ? COLI_OK : cuda_fail(ce, "kv_attention: launch");
+}
+
+coli_status colibri_kv_debug_inject(int flags, double wait_limit_ms) {
+  if (flags & ~COLI_INJECT_WITHHOLD_STAGE) return fail(COLI_EINVAL, "kv_debug_inject: unknown flag bits 0x%x", flags);
+  if (!(wait_limit_ms == wait_limit_ms)) return fail(COLI_EINVAL, "kv_debug_inject: wait limit is NaN");
+  at_inject.flags = flags;
+  // between a microsecond and the ordinary limit
+  at_inject.wait_ns = wait_limit_ms > 0 && wait_limit_ms * 1e6 < (double)kWaitLimitNs
+                          ? (unsigned long long)(wait_limit_ms * 1e6) : kWaitLimitNs;
+  if (at_inject.wait_ns < 1000) at_inject.wait_ns = 1000;
+  return COLI_OK;
 }
 
 coli_status colibri_kv_check_status(const void* workspace, int32_t* device_status, void* stream) {

@@ -194,3 +194,29 @@ def test_attention_fp16_references_rise_far(torch_cuda):
         shift_scores(b, 0, np.arange(1300) // 128 * step)
         out, z = b.check()
         assert torch.isfinite(out).all() and torch.isfinite(z).all()
+
+
+@pytest.mark.parametrize("lens,new,H,page,topk", [
+    ([100], [1], 16, 64, 0), ([9000, 300], [3, 1], 64, 64, 0),        # TMA: one tile; tiles of a unit cut over the card
+    ([100], [1], 16, 16, 0), ([9000, 300], [3, 1], 64, 16, 0),        # copied rows
+    ([5000], [2], 64, 64, 512), ([60], [40], 64, 128, 0)])            # selected keys; several units
+def test_attention_wait_that_runs_out(torch_cuda, lens, new, H, page, topk):
+    """Copies that never come: the waits end after 2 ms, the status says so, the call and the next one on the same
+    workspace return, and the next one is right."""
+    import time
+    torch = torch_cuda
+    import quantized_expert_ffn_bias_gb300 as coli
+    b = Batch(torch, lens, new, H, page, seed=90)
+    sel = selected(np.random.default_rng(90), lens, new, topk) if topk else None
+    want, lse = b.check(sel=sel)
+    ws = torch.empty(coli.colibri_kv_attention_workspace_size(len(lens), b.N, H), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        coli.colibri_kv_debug_inject(coli.COLI_INJECT_WITHHOLD_STAGE, 2.0)
+        try:
+            t0 = time.perf_counter()
+            b.run(sel=sel, ws=ws, status=coli.COLI_DEV_WAIT_TIMEOUT)
+            assert time.perf_counter() - t0 < 0.5
+        finally:
+            coli.colibri_kv_debug_inject(0)
+        out, z = b.run(sel=sel, ws=ws)
+        assert torch.equal(out, want) and torch.equal(z, lse)

@@ -1,0 +1,11 @@
+"""More refusals of the serving entry points, before any CUDA call (no GPU)."""
+import quantized_expert_ffn_bias_gb300 as coli
+from tests.test_serving_abi import attn, built, kv, refused  # noqa: F401  (a fixture)
+
+
+def test_kv_debug_inject_arguments():
+    refused(coli.COLI_EINVAL, coli.colibri_kv_debug_inject, coli.COLI_INJECT_BAD_EXPERT_ID, 1.0)
+    refused(coli.COLI_EINVAL, coli.colibri_kv_debug_inject, -1, 1.0)
+    refused(coli.COLI_EINVAL, coli.colibri_kv_debug_inject, 0, float("nan"))
+    for ms in (2.0, -1.0, 1e-9, float("inf"), 0.0):
+        coli.colibri_kv_debug_inject(0, ms)
