@@ -574,11 +574,12 @@ COLI_API coli_status colibri_kv_append(const coli_kv_desc* desc, int n_tokens, c
  * new tokens (seq_len_out of colibri_kv_step).  With k[j] the cached row of
  * key j and v[j] its first 512 values, head h of row n gets
  *   out[n][h] = sum_j softmax_j(scale * q[n][h] . k[j]) v[j]
- * over the keys j up to the row's position, or, with topk_idx, over
- * the keys topk_idx[n][0 .. topk) (colibri_indexer_topk's output: entries that
- * are negative or beyond the row's position are left out, an entry that occurs
- * twice counts twice).  Queries are in the latent space (the up-projection of
- * the keys absorbed): 512 latent values, then 64 rotary.
+ * (scale of any sign, |scale| log2(e) finite) over the keys j up to the row's
+ * position, or, with topk_idx, over the keys topk_idx[n][0 .. topk)
+ * (colibri_indexer_topk's output: entries that are negative or beyond the row's
+ * position are left out, an entry that occurs twice counts twice).  Queries are
+ * in the latent space (the up-projection of the keys absorbed): 512 latent
+ * values, then 64 rotary.
  *   q            device [n_tokens][H][576] of desc->dtype with the strides (in
  *                elements) given; 16-byte aligned; the strides multiples of 8
  *                (a stride along an axis of one is not read).  1 <= H <= 1024.

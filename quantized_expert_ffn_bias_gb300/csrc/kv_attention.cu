@@ -1191,7 +1191,8 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   if (B > kAtMaxB || H > kAtMaxH) return fail(COLI_EUNSUPPORTED, "kv_attention: at most 8192 requests of 1024 heads");
   if (desc->dtype != COLI_X_BF16 && desc->dtype != COLI_X_F16)
     return fail(COLI_EUNSUPPORTED, "kv_attention: the cache holds bf16 or fp16 (dtype %d)", desc->dtype);
-  if (!(scale == scale) || scale - scale != 0.f) return fail(COLI_EINVAL, "kv_attention: scale is not finite");
+  const float scale_log2 = scale * 1.4426950408889634f;    // (beyond 2.36e38 not finite either)
+  if (!(scale_log2 - scale_log2 == 0.f)) return fail(COLI_EINVAL, "kv_attention: scale is not finite, or its product with log2(e) is not");
   if (topk_idx && topk < 1) return fail(COLI_EINVAL, "kv_attention: topk must be positive with topk_idx");
   if ((long long)n_tokens * H > 0x7fffffffLL - 1024)       // (row numbers of a last, partial gang of row tiles)
     return fail(COLI_EUNSUPPORTED, "kv_attention: n_tokens * H exceeds 2^31 - 1024 rows");
@@ -1248,7 +1249,7 @@ coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n_tokens, 
   a.n_tokens = n_tokens;
   a.H = H;
   a.topk = topk_idx ? topk : 0;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.rows_per_page = (int)per_page;
   a.box = box;
   a.box_log2 = 0;
