@@ -7,14 +7,16 @@
 // Lane l holds the experts l NV .. l NV + NV - 1, so that a tie goes to the
 // lower lane, and so that groups of whole lanes are reduced with a few
 // shuffles for all groups at once.  The choice is made in fp32 with approximate
-// exponentials on order-preserving integer images (one redux.sync a round),
-// (sorted lists a lane) and is exact all the same: where the last kept and the first dropped group
-// or expert are closer than the error of these scores, those around the border
-// are compared by scores in 64 bits (computing all of a token's in 64 bits
-// took one warp 35 us and with it the call).  Experts whose logit and bias are equal
-// bit for bit tie exactly in either form and are no reason for it (16-bit
-// logits tie often).  The k weights come from exactly rounded arithmetic on
-// the chosen logits.
+// exponentials on order-preserving integer images, sorted a lane (one
+// redux.sync a round).  It is the exact scores' choice all the same: where the
+// last kept and the first dropped group or expert are closer than the error of
+// the fp32 scores, those around the border are compared by scores in 64 bits
+// (computing all of a token's in 64 bits took one warp 35 us and with it the
+// call).  Experts whose logit and bias are equal bit for bit tie exactly in
+// either form and are no reason for it (16-bit logits tie often); groups whose
+// scores are equal are.  The k weights come from fp32 arithmetic on the chosen
+// logits (expf, a softmax's sum of approximate terms), within the error that
+// the tests derive, or from 64 bits where the chosen scores leave fp32's range.
 #pragma once
 
 #include "moe_internal.cuh"
