@@ -11,7 +11,8 @@
 // results are dealt over the cluster's threads.  What bounds it is latency:
 // the launch, the loads of the lengths and of a token's page, the scan's
 // barriers (one scan where everything can be served, sums in 32 bits where
-// the sizes allow it: 14.3 -> 10.6 us a call for 500 requests of 13,000 tokens).
+// the sizes allow it: 14.3 -> 10.5 us a call for 500 requests of 13,000 tokens,
+// a median; a process's calls from Python move it by 2 us).
 #include "plan.h"
 
 namespace coli {
