@@ -508,6 +508,7 @@ COLI_API coli_status colibri_moe_set_route(coli_moe_plan_t* plan, const coli_rou
  */
 #define COLI_KV_WIDTH 576
 #define COLI_KV_VALUE 512
+#define COLI_KV_ROTARY 64
 typedef struct {
   int page_size;         /* >= 1 */
   int max_pages;         /* columns of the block table */
@@ -610,13 +611,13 @@ COLI_API coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n
                                           const void* cache, const int32_t* block_table, const int32_t* q_start,
                                           const int32_t* seq_len, const int32_t* topk_idx, int topk, void* out,
                                           float* lse, void* workspace, size_t workspace_bytes, void* stream);
-/* The status word of an attention workspace (synchronises `stream`): 0, or
- * COLI_DEV_KV_BAD_PAGE, COLI_DEV_KV_TOKENS, COLI_DEV_WAIT_TIMEOUT (then
- * COLI_EDEVICE). */
+/* The status word of a workspace of colibri_kv_attention or
+ * colibri_prompt_attention (synchronises `stream`): 0, or COLI_DEV_KV_BAD_PAGE,
+ * COLI_DEV_KV_TOKENS, COLI_DEV_WAIT_TIMEOUT (then COLI_EDEVICE). */
 COLI_API coli_status colibri_kv_check_status(const void* workspace, int32_t* device_status, void* stream);
 /*
- * Failure-path testing of colibri_kv_attention, for the following calls of this
- * thread.  flags: 0 (off) or COLI_INJECT_WITHHOLD_STAGE, with which the first
+ * Failure-path testing of colibri_kv_attention and colibri_prompt_attention, for
+ * the following calls of this thread.  flags: 0 (off) or COLI_INJECT_WITHHOLD_STAGE, with which the first
  * CTA's first key rows never count as there, so that the roles waiting for them
  * reach the wait limit, record COLI_DEV_WAIT_TIMEOUT, let their copies and products
  * end, free tensor memory and return.  wait_limit_ms as for
@@ -625,6 +626,158 @@ COLI_API coli_status colibri_kv_check_status(const void* workspace, int32_t* dev
  * workspace, is a normal one.  Errors: COLI_EINVAL.
  */
 COLI_API coli_status colibri_kv_debug_inject(int flags, double wait_limit_ms);
+
+/*
+ * Rotary positions.  "25GB RAM runs 744B GLM-5.2" page, section 3.2: 64 of the
+ * 576 cached values carry the positions.  A pair (a, b) of values at position
+ * t becomes amplitude * (a cos w - b sin w, a sin w + b cos w), w = t * f_j for
+ * pair j of dim / 2:
+ *   layout       pairs (2j, 2j + 1), or (j, j + dim / 2).
+ *   f_j          base^(-2j / dim) radians a position, changed by `scaling` for
+ *                contexts longer than the original one:
+ *                LINEAR  all divided by factor;
+ *                NTK     base * factor^(dim / (dim - 2)) in the place of base
+ *                        (dim = 2 has the one frequency 1);
+ *                YARN    divided by factor where a pair turns fewer than
+ *                        beta_slow times over original_len positions, unchanged
+ *                        where it turns more than beta_fast times, a ramp
+ *                        between them: with j(n) = dim ln(original_len /
+ *                        (2 pi n)) / (2 ln base), low = max(0,
+ *                        floor(j(beta_fast))), high = min(dim - 1,
+ *                        ceil(j(beta_slow))) (low + 0.001 where high <= low),
+ *                        g = clamp((j - low) / (high - low), 0, 1):
+ *                        f_j (1 - g) + f_j / factor g.
+ *   amplitude    factor of the rotated values (1: a rotation alone).
+ * dim is even, 2 <= dim <= 256.
+ */
+typedef enum { COLI_ROPE_INTERLEAVED = 0, COLI_ROPE_HALF = 1 } coli_rope_layout;
+typedef enum { COLI_ROPE_NONE = 0, COLI_ROPE_LINEAR = 1, COLI_ROPE_NTK = 2, COLI_ROPE_YARN = 3 } coli_rope_scaling;
+typedef struct {
+  int dim;
+  int layout;          /* coli_rope_layout */
+  int scaling;         /* coli_rope_scaling; this and the following are read by colibri_rope_frequencies alone, but amplitude */
+  float amplitude;     /* finite */
+  double base;         /* > 1 */
+  double factor;       /* >= 1; not read by NONE */
+  double original_len; /* > 0; YARN */
+  double beta_fast;    /* beta_fast > beta_slow > 0; YARN */
+  double beta_slow;
+} coli_rope_desc;
+/*
+ * The frequencies of a description as the calls below read them: freq (HOST
+ * uint64 [dim / 2]) receives f_j / (2 pi) in units of 2^-64 turns a position, so
+ * that a position times a frequency, kept modulo 2^64, is the exact fraction of
+ * a turn at any position.  The program copies them to the device once (another
+ * scaling can be written there in the same units).  Host only.  Errors:
+ * COLI_EINVAL.
+ */
+COLI_API coli_status colibri_rope_frequencies(const coli_rope_desc* desc, uint64_t* freq);
+/*
+ * Rotate dim values of each of H heads of n_tokens rows: x + row * x_token_stride
+ * + head * x_head_stride to out + row * out_token_stride + head *
+ * out_head_stride (in elements of dtype: bf16, fp16 or fp32; a stride along an
+ * axis of one is not read), the part of the heads that carries the positions:
+ * what lies beside it is neither read nor written.
+ *   position     device int32 [n_tokens], any values (negative ones too).
+ *   freq         device uint64 [dim / 2], 8-byte aligned.
+ *   n_valid      device int32 or NULL: rows from *n_valid on are not written
+ *                (q_start + B of colibri_kv_step).
+ *   out          x itself with the same strides, or memory that does not
+ *                overlap x; no two outputs overlap.
+ * Angles are exact to 2^-24 relative; sums in fp32, each result is rounded once.
+ * x and out need the alignment of their elements (16 bytes, with strides of
+ * whole 16 bytes and dim a multiple of 16, are faster).  1 <= H <= 1024.
+ * n_tokens = 0 does nothing.  Asynchronous on stream.  Errors: COLI_EINVAL,
+ * COLI_EALIGN, COLI_EUNSUPPORTED, COLI_ECUDA.
+ */
+COLI_API coli_status colibri_rope(const coli_rope_desc* desc, int dtype, int n_tokens, const int32_t* n_valid, int H,
+                                  const int32_t* position, const uint64_t* freq, const void* x, long long x_token_stride,
+                                  long long x_head_stride, void* out, long long out_token_stride,
+                                  long long out_head_stride, void* stream);
+/*
+ * colibri_kv_append with the latent's norm and the rotation on the way: row i of
+ * the down-projection's output goes to slot[i] as
+ *   latent[i] / sqrt(mean(latent[i]^2) + eps) * gain   (gain NULL: as it is),
+ *   rope[i] rotated by position[i] (rope->dim must be 64).
+ * desc->dtype is that of latent, rope and cache (bf16 or fp16); gain is device
+ * float [512]; eps >= 0.  Sums in fp32, one rounding of each result.  gain
+ * 16-byte, position 4-byte, freq 8-byte aligned; everything else as
+ * colibri_kv_append.
+ */
+COLI_API coli_status colibri_kv_append_rope(const coli_kv_desc* desc, const coli_rope_desc* rope_desc, int n_tokens,
+                                            const int32_t* n_valid, const void* latent, long long latent_stride,
+                                            const float* gain, float eps, const void* rope, long long rope_stride,
+                                            const int32_t* position, const uint64_t* freq, const int32_t* slot,
+                                            void* cache, void* stream);
+/*
+ * Rows of whole requests out of the paged cache, side by side, as the
+ * up-projection to keys and values of every head reads them: key j of request b
+ * (j < seq_len[b]) becomes row k_start[b] + j of latent (512 values at
+ * latent + row * latent_stride) and of rope (64 at rope + row * rope_stride).
+ *   seq_len      device int32 [B] (seq_len_out of colibri_kv_step).
+ *   k_start      device int32 [B + 1], written: exclusive sums of the lengths.
+ *   n_rows       rows that latent and rope have room for; what exceeds it is
+ *                left out (k_start ends at n_rows, COLI_DEV_KV_TOKENS).  Rows
+ *                from k_start[B] on are left as they were.
+ *   status       device int32: COLI_DEV_KV_* bits are OR-ed into it (the caller
+ *                clears it).  A key whose page id is outside [0, n_pages), or
+ *                beyond the block table, becomes a row of zeros
+ *                (COLI_DEV_KV_BAD_PAGE); a negative length counts as 0
+ *                (COLI_DEV_KV_TABLE_FULL).
+ * Elements are copied as they are (desc->dtype is not read).  latent, rope and
+ * cache 16-byte aligned, the strides multiples of 8 and at least the rows'
+ * width.  1 <= B <= 8192.  Asynchronous on stream.  Errors: COLI_EINVAL,
+ * COLI_EALIGN, COLI_EUNSUPPORTED, COLI_ECUDA.
+ */
+COLI_API coli_status colibri_kv_gather(const coli_kv_desc* desc, int B, int n_rows, const int32_t* seq_len,
+                                       const int32_t* block_table, const void* cache, int32_t* k_start, void* latent,
+                                       long long latent_stride, void* rope, long long rope_stride, int32_t* status,
+                                       void* stream);
+/*
+ * Attention of prompts and chunks in the expanded form: the latent rows have
+ * been projected up to keys (128 values) and values (128) of every head; the 64
+ * rotary values of a key are shared by the heads.  Row i of request b
+ * (q_start[b] + i of the T = q_start[b+1] - q_start[b] new ones) sees the first
+ * L - T + i + 1 of the request's L = k_start[b+1] - k_start[b] keys, its own
+ * last:
+ *   out[n][h] = sum_j softmax_j(scale * (q[n][h][0..128) . k[j][h] +
+ *               q[n][h][128..192) . k_rope[j])) v[j][h]
+ * (scale of any sign, |scale| log2(e) finite).  A (row, key, head) costs 320
+ * multiply-adds, in colibri_kv_attention 1088; that one reads 1152 bytes a key
+ * for all heads, this one 512 a head.
+ *   q            device [n_tokens][H][192], k and v device [n_keys][H][128],
+ *                k_rope device [n_keys][64], of dtype (bf16 or fp16), 16-byte
+ *                aligned, with the strides (in elements) given: positive
+ *                multiples of 8 below 2^38 (a stride along an axis of one is
+ *                not read).  1 <= H <= 1024, 1 <= B <= 8192.
+ *   q_start, k_start  device int32 [B + 1], ascending, from 0 at least to
+ *                n_tokens and n_keys at most (else nothing is computed and the
+ *                status word gets COLI_DEV_KV_TOKENS).
+ *   out          device [n_tokens][H][128] of dtype, 16-byte aligned.
+ *   lse          device float [n_tokens][H] or NULL: log of the softmax's sum.
+ *   workspace    device, >= colibri_prompt_attention_workspace_size bytes,
+ *                256-byte aligned; its first int32 is the status word
+ *                (colibri_kv_check_status).  Two calls that overlap on the GPU
+ *                need two workspaces.
+ * A row that sees no key gets 0 and lse -infinity.  Rows outside
+ * [q_start[0], q_start[B]) are left as they were.  Keys and values that a row
+ * does not see do not reach its output, whatever values (infinities, NaN) they
+ * hold.  Softmax and sums in fp32; the weights are rounded to dtype for the
+ * product with the values.  The result does not depend on timing.
+ * Asynchronous on stream, two launches.  n_tokens = 0 does nothing.  Errors:
+ * COLI_EINVAL, COLI_EALIGN, COLI_EWORKSPACE, COLI_EUNSUPPORTED, COLI_ECUDA.
+ */
+#define COLI_PROMPT_KEY 128
+#define COLI_PROMPT_ROTARY 64
+#define COLI_PROMPT_VALUE 128
+COLI_API coli_status colibri_prompt_attention_workspace_size(int B, int n_tokens, int n_keys, int H, size_t* bytes);
+COLI_API coli_status colibri_prompt_attention(int dtype, int B, int n_tokens, int n_keys, int H, float scale,
+                                              const void* q, long long q_token_stride, long long q_head_stride,
+                                              const void* k, long long k_token_stride, long long k_head_stride,
+                                              const void* k_rope, long long rope_stride, const void* v,
+                                              long long v_token_stride, long long v_head_stride,
+                                              const int32_t* q_start, const int32_t* k_start, void* out, float* lse,
+                                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* Number of kernel launches the last forward call of this plan issued. */
 COLI_API int colibri_moe_last_launch_count(const coli_moe_plan_t* plan);

@@ -21,7 +21,10 @@ COLI_Q_INT4_G128, COLI_Q_INT8_PC = 0, 1
 COLI_X_BF16, COLI_X_F32, COLI_X_F16 = 0, 1, 2
 COLI_SCORE_SIGMOID, COLI_SCORE_SOFTMAX = 0, 1
 COLI_GROUP_TOP2, COLI_GROUP_MAX = 0, 1
-COLI_KV_WIDTH, COLI_KV_VALUE = 576, 512
+COLI_KV_WIDTH, COLI_KV_VALUE, COLI_KV_ROTARY = 576, 512, 64
+COLI_PROMPT_KEY, COLI_PROMPT_ROTARY, COLI_PROMPT_VALUE = 128, 64, 128
+COLI_ROPE_INTERLEAVED, COLI_ROPE_HALF = 0, 1
+COLI_ROPE_NONE, COLI_ROPE_LINEAR, COLI_ROPE_NTK, COLI_ROPE_YARN = range(4)
 COLI_DEV_BAD_EXPERT_ID, COLI_DEV_WAIT_TIMEOUT, COLI_DEV_SELECT_ROUNDS = 1, 2, 4
 COLI_DEV_KV_NO_PAGES, COLI_DEV_KV_TABLE_FULL, COLI_DEV_KV_TOKENS, COLI_DEV_KV_BAD_PAGE = 8, 16, 32, 64
 COLI_INJECT_WITHHOLD_STAGE, COLI_INJECT_BAD_EXPERT_ID = 1, 2
@@ -65,6 +68,12 @@ class coli_route_desc(ctypes.Structure):
 class coli_kv_desc(ctypes.Structure):
     _fields_ = [("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("n_pages", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("page_stride", ctypes.c_longlong)]
+
+
+class coli_rope_desc(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int), ("layout", ctypes.c_int), ("scaling", ctypes.c_int), ("amplitude", ctypes.c_float),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double)]
 
 
 def build(force: bool = False) -> str:
@@ -154,6 +163,21 @@ def lib():
             L.colibri_kv_attention.argtypes = [kdesc, i32, i32, i32, ctypes.c_float, vp, i64, i64, vp, vp, vp, vp, vp,
                                                i32, vp, vp, vp, sz, vp]
             L.colibri_kv_attention.restype = st
+            pdesc = ctypes.POINTER(coli_rope_desc)
+            L.colibri_rope_frequencies.argtypes = [pdesc, vp]
+            L.colibri_rope_frequencies.restype = st
+            L.colibri_rope.argtypes = [pdesc, i32, i32, vp, i32, vp, vp, vp, i64, i64, vp, i64, i64, vp]
+            L.colibri_rope.restype = st
+            L.colibri_kv_append_rope.argtypes = [kdesc, pdesc, i32, vp, vp, i64, vp, ctypes.c_float, vp, i64, vp, vp, vp,
+                                                 vp, vp]
+            L.colibri_kv_append_rope.restype = st
+            L.colibri_kv_gather.argtypes = [kdesc, i32, i32, vp, vp, vp, vp, vp, i64, vp, i64, vp, vp]
+            L.colibri_kv_gather.restype = st
+            L.colibri_prompt_attention_workspace_size.argtypes = [i32, i32, i32, i32, ctypes.POINTER(sz)]
+            L.colibri_prompt_attention_workspace_size.restype = st
+            L.colibri_prompt_attention.argtypes = [i32, i32, i32, i32, i32, ctypes.c_float, vp, i64, i64, vp, i64, i64, vp,
+                                                   i64, vp, i64, i64, vp, vp, vp, vp, vp, sz, vp]
+            L.colibri_prompt_attention.restype = st
             L.colibri_kv_check_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int32), vp]
             L.colibri_kv_check_status.restype = st
             L.colibri_kv_debug_inject.argtypes = [i32, ctypes.c_double]
@@ -279,6 +303,57 @@ def colibri_kv_attention(desc: coli_kv_desc, B: int, n_tokens: int, H: int, scal
                                       _stream(stream)))
 
 
+def colibri_rope_frequencies(desc: coli_rope_desc) -> list[int]:
+    """Frequencies of a description in units of 2^-64 turns a position (see the header), to be kept on the device as
+    64-bit integers (all are below 2^63)."""
+    out = (ctypes.c_uint64 * max(1, desc.dim // 2))()
+    _check(lib().colibri_rope_frequencies(ctypes.byref(desc), out))
+    return list(out)
+
+
+def colibri_rope(desc: coli_rope_desc, dtype: int, n_tokens: int, n_valid, H: int, position, freq, x, x_token_stride: int,
+                 x_head_stride: int, out, out_token_stride: int, out_head_stride: int, stream=None):
+    """Rotate desc.dim values of every head of n_tokens rows by their positions (see the header); out may be x."""
+    pos, f, xp, o = _ptrs(position, freq, x, out)
+    _check(lib().colibri_rope(ctypes.byref(desc), dtype, n_tokens, _ptr(n_valid), H, pos, f, xp, x_token_stride,
+                              x_head_stride, o, out_token_stride, out_head_stride, _stream(stream)))
+
+
+def colibri_kv_append_rope(desc: coli_kv_desc, rope_desc: coli_rope_desc, n_tokens: int, n_valid, latent,
+                           latent_stride: int, gain, eps: float, rope, rope_stride: int, position, freq, slot, cache,
+                           stream=None):
+    """colibri_kv_append with the latent's norm (gain None: none) and the rotation of the rotary part on the way."""
+    lat, rot, pos, f, to, kv = _ptrs(latent, rope, position, freq, slot, cache)
+    _check(lib().colibri_kv_append_rope(ctypes.byref(desc), ctypes.byref(rope_desc), n_tokens, _ptr(n_valid), lat,
+                                        latent_stride, _ptr(gain), eps, rot, rope_stride, pos, f, to, kv,
+                                        _stream(stream)))
+
+
+def colibri_kv_gather(desc: coli_kv_desc, B: int, n_rows: int, seq_len, block_table, cache, k_start, latent,
+                      latent_stride: int, rope, rope_stride: int, status, stream=None):
+    """Rows of whole requests out of the paged cache, side by side (see the header); k_start is written."""
+    seq, table, kv, start, lat, rot, st = _ptrs(seq_len, block_table, cache, k_start, latent, rope, status)
+    _check(lib().colibri_kv_gather(ctypes.byref(desc), B, n_rows, seq, table, kv, start, lat, latent_stride, rot,
+                                   rope_stride, st, _stream(stream)))
+
+
+def colibri_prompt_attention_workspace_size(B: int, n_tokens: int, n_keys: int, H: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().colibri_prompt_attention_workspace_size(B, n_tokens, n_keys, H, ctypes.byref(n)))
+    return n.value
+
+
+def colibri_prompt_attention(dtype: int, B: int, n_tokens: int, n_keys: int, H: int, scale: float, q, q_token_stride: int,
+                             q_head_stride: int, k, k_token_stride: int, k_head_stride: int, k_rope, rope_stride: int, v,
+                             v_token_stride: int, v_head_stride: int, q_start, k_start, out, lse, workspace,
+                             workspace_bytes: int, stream=None):
+    """Attention of prompts and chunks in the expanded form of latent attention (see the header)."""
+    qp, kp, rp, vp, qs, ks, o, ws = _ptrs(q, k, k_rope, v, q_start, k_start, out, workspace)
+    _check(lib().colibri_prompt_attention(dtype, B, n_tokens, n_keys, H, scale, qp, q_token_stride, q_head_stride, kp,
+                                          k_token_stride, k_head_stride, rp, rope_stride, vp, v_token_stride,
+                                          v_head_stride, qs, ks, o, _ptr(lse), ws, workspace_bytes, _stream(stream)))
+
+
 def colibri_kv_check_status(workspace, stream=None) -> int:
     v = ctypes.c_int32()
     rc = lib().colibri_kv_check_status(_ptr(workspace), ctypes.byref(v), _stream(stream))
@@ -288,7 +363,7 @@ def colibri_kv_check_status(workspace, stream=None) -> int:
 
 
 def colibri_kv_debug_inject(flags: int, wait_limit_ms: float = 0.0):
-    """Failure-path testing of colibri_kv_attention: COLI_INJECT_WITHHOLD_STAGE for this thread's next calls (0 = off)."""
+    """Failure-path testing of the attention calls: COLI_INJECT_WITHHOLD_STAGE for this thread's next calls (0 = off)."""
     _check(lib().colibri_kv_debug_inject(flags, wait_limit_ms))
 
 

@@ -1161,10 +1161,8 @@ static cudaError_t at_launch(const AtArgs& a, const CUtensorMap& kmap, const CUt
 }
 
 // Failure-path testing (colibri_kv_debug_inject): of the calls of this thread.
-static thread_local struct {
-  int flags = 0;
-  unsigned long long wait_ns = kWaitLimitNs;
-} at_inject;
+static thread_local KvInject at_inject = {0, kWaitLimitNs};
+KvInject kv_inject() { return at_inject; }
 
 }  // namespace coli
 

@@ -66,6 +66,12 @@ struct coli_moe_plan {
 namespace coli {
 // Ranges of a routing description (route.cu); `who` begins the message.
 coli_status check_route_desc(const coli_route_desc& r, const char* who);
+// Failure-path testing of the attention kernels, of the calls of this thread (colibri_kv_debug_inject).
+struct KvInject {
+  int flags;
+  unsigned long long wait_ns;
+};
+KvInject kv_inject();
 // Ranges of a paged cache description (kv_cache.cu).
 coli_status check_kv_desc(const coli_kv_desc* d, const char* who);
 coli_status forward_impl(coli_moe_plan* plan, const ExpertTables& tb, BetweenFn between, void* ctx, int T,
