@@ -17,8 +17,10 @@
 // PV_1(t), S_1(t + 1), ...  A thread of the softmax holds a whole row of S, so that maxima and sums need no other
 // thread.
 //
-// Softmax: per row a reference m (log2 units, a whole number) that is raised, with the sum and O rescaled, only when a
-// score exceeds it by 8.
+// Softmax: per row a reference m (log2 units, a whole number) that is raised, with the sum and O rescaled, only when it
+// has to be: a tile whose every key is seen takes its weights against the reference as it is, without looking for the
+// largest score; only where a row's weights sum to more than 2^15 (or the tile is a unit's first, or masked) are the scores
+// read again, their maximum taken and the reference raised (where a score exceeds it by 8, or the sum was too large).
 //
 // Work: units (256 rows of one head, or of a gang of CTAs that walk the same keys) with their key tiles, in the order
 // request, head, rows, dealt in equal runs of key tiles.  A unit cut by a border leaves partial results in the
@@ -45,6 +47,7 @@ constexpr int kPaMaxB = 8192, kPaMaxH = 1024;
 constexpr int kPaMaxDevices = 64;
 constexpr int kPaPart = kPaRows * kPaV;            // floats of a partial O
 constexpr float kPaGrow = 8.f;
+constexpr float kPaSumLimit = 32768.f;             // a row's weights of one tile sum to at most this, or its reference is looked at
 // A reference makes the largest weight 2^(top - 1) .. 2^top; growth to 2^(top + kPaGrow) raises it.  bf16 has fp32's
 // range; fp16 ends at 2^16 and loses bits below 2^-14, so its weights take the upper part.
 __host__ __device__ constexpr float pa_top(bool bf16) { return bf16 ? 0.f : 7.f; }
@@ -403,6 +406,17 @@ __device__ __forceinline__ uint32_t pa_pack(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // 32 consecutive TMEM columns of this warp's 32 lanes -> registers (issue only)
 __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -413,6 +427,17 @@ __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+// registers -> 32 consecutive TMEM columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
 }
 // Uses of the registers stay behind the wait.
 template <int N>
@@ -788,39 +813,57 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], it & 1, p.wait_ns));
         if (!ok) break;
         tc_fence_after();
-        uint32_t y[kPaTile];
-#pragma unroll
-        for (int c = 0; c < kPaTile; c += 32) tmem_ld32_issue(ts + c, y + c);
-        tmem_ld_done<kPaTile>(y);
-        auto f = [&](int c) { return __uint_as_float(y[c]); };
-        // distance to the reference
-#pragma unroll
-        for (int c = 0; c < kPaTile; c += 2) {
-          const float2 d = ffma2(make_float2(f(c), f(c + 1)), make_float2(p.scale_log2, p.scale_log2), make_float2(-m, -m));
-          y[c] = __float_as_uint(d.x);
-          y[c + 1] = __float_as_uint(d.y);
-        }
         const int key0 = (t0 + i) * kPaTile;
-        if (key0 + kPaTile - 1 > lim0) {               // (after the scale, which may be 0 or negative)
+        bool slow = key0 + kPaTile - 1 > lim0 || __any_sync(0xffffffffu, !has);
+        float grow = kPaGrow;                          // by how much a score exceeds a reference that is raised
+        if (!slow) {
+          // every key is seen: weights against the reference as it is; the sum tells whether it still serves
+          uint32_t w[kPaTile / 2];
+          const float2 by = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-m, -m);
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < kPaTile; ++c)
-            if (key0 + c > lim) y[c] = __float_as_uint(-INFINITY);
+          for (int c = 0; c < kPaTile; c += 32) {
+            uint32_t r[32];
+            tmem_ld32_issue(ts + c, r);
+            tmem_ld_done<32>(r);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 d = ffma2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), by, off);
+              const float2 e = make_float2(pa_exp2(d.x), pa_exp2(d.y));
+              sum = fadd2(sum, e);
+              w[(c + j) / 2] = pa_pack<BF16>(e.x, e.y);
+            }
+          }
+          const float add = sum.x + sum.y;
+          slow = __any_sync(0xffffffffu, !(add <= kPaSumLimit));
+          grow = 0.f;
+          if (!slow) {
+            l += add;
+#pragma unroll
+            for (int c = 0; c < kPaTile / 2; c += 32) tmem_st32(ts + c, w + c);
+          }
         }
-        float top = -INFINITY;
+        if (slow) {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kPaTile; c += 32) {
+            uint32_t r[32];
+            tmem_ld32_issue(ts + c, r);
+            tmem_ld_done<32>(r);
 #pragma unroll
-        for (int c = 0; c < kPaTile; c += 2) top = fmaxf(fmaxf(top, f(c)), f(c + 1));
-        if (__any_sync(0xffffffffu, top > kPaGrow + pa_top(BF16) || !has)) {
+            for (int j = 0; j < 32; ++j) {             // (masks after the scale, which may be 0 or negative)
+              const float d = fmaf(__uint_as_float(r[j]), p.scale_log2, -m);
+              top = fmaxf(top, key0 + c + j > lim ? -INFINITY : d);
+            }
+          }
           const float g = ceilf(top) - pa_top(BF16);
-          const bool raise = g > kPaGrow || (!has && g > -INFINITY);
-          const float by = raise ? g : 0.f;
+          const bool raise = g > grow || (!has && g > -INFINITY);
           // what that leaves of the sums so far: a first reference may lie far below 0, but they are 0 (or NaN) then
           const float keep = raise && has ? pa_exp2(-g) : 1.f;
-          m += by;
+          // (the distance to the old reference is taken first: a product with the scale may lie far beyond their difference)
+          const float by = raise ? g : 0.f;
           l *= keep;
-          has |= raise;
-#pragma unroll
-          for (int c = 0; c < kPaTile; ++c) y[c] = __float_as_uint(f(c) - by);
-          if (i > 0 && __any_sync(0xffffffffu, keep != 1.f)) {   // (the first tile's products overwrite O)
+          if (i > 0 && __any_sync(0xffffffffu, keep != 1.f)) {     // (the first tile's products overwrite O)
 #pragma unroll 1
             for (int c = 0; c < kPaV; c += 16) {
               uint32_t o[16];
@@ -831,22 +874,28 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
               tmem_st16(to + c, o);
             }
           }
-        }
-        // weights, their sum, and the row of P in the place of S
-        float s0 = 0.f, s1 = 0.f;
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < kPaTile; c += 32) {      // (a chunk's weights take columns that are read already)
+            uint32_t r[32], w[16];
+            tmem_ld32_issue(ts + c, r);
+            tmem_ld_done<32>(r);
 #pragma unroll
-        for (int c = 0; c < kPaTile; c += 32) {
-          uint32_t w[16];
+            for (int j = 0; j < 32; j += 2) {
+              float d[2];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float a = pa_exp2(f(c + 2 * j)), b = pa_exp2(f(c + 2 * j + 1));
-            s0 += a;
-            s1 += b;
-            w[j] = pa_pack<BF16>(a, b);
+              for (int k = 0; k < 2; ++k)
+                d[k] = key0 + c + j + k > lim ? 0.f : pa_exp2(fmaf(__uint_as_float(r[j + k]), p.scale_log2, -m) - by);
+              s0 += d[0];
+              s1 += d[1];
+              w[j / 2] = pa_pack<BF16>(d[0], d[1]);
+            }
+            tmem_st16(ts + c / 2, w);
           }
-          tmem_st16(ts + c / 2, w);
+          m += by;
+          has |= raise;
+          l += s0 + s1;
         }
-        l += s0 + s1;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
