@@ -9,23 +9,26 @@
 // turn reads 1152 bytes a key where this one reads 512 a head: prompts and
 // chunks belong here, single tokens there.
 //
-// A CTA takes 256 rows of one head as two tiles of 128 and walks the keys in
-// tiles of 128 (tcgen05, fp32 accumulators in tensor memory):
-//   S_x[128 rows][128 keys] = Q_x [K | R]^T   (12 products of depth 16)
-//   O_x[128 rows][128]     += P_x V           (8 products; P_x takes S_x's place in tensor memory as 16-bit weights)
+// A pair of CTAs (a cluster, one on each SM of a TPC) takes 512 rows of one head as two row tiles of 256, 128 rows of
+// either in each CTA, and walks the keys in tiles of 128 (tcgen05 with cta_group::2, fp32 accumulators in tensor memory):
+//   S_x[256 rows][128 keys] = Q_x [K | R]^T   (12 products of depth 16)
+//   O_x[256 rows][128]     += P_x V           (8 products; P_x takes S_x's place in tensor memory as 16-bit weights)
+// Each CTA holds half of a key tile (64 keys of K and R, 64 of V's 128 columns: 40 KB), so three tiles fit beside the
+// queries' 96 KB, and each product reads half the operand bytes of a CTA's own; with whole tiles in each CTA (1.6 of them
+// fitted) the products waited 1,000 of 4,260 cycles a tile for keys and values.
 // While the softmax warps of one row tile work, the tensor cores take the other's products: PV_0(t), S_0(t + 1),
-// PV_1(t), S_1(t + 1), ...  A thread of the softmax holds a whole row of S, so that maxima and sums need no other
-// thread.
+// PV_1(t), S_1(t + 1), ...  A thread of the softmax holds a whole row of S, so that sums need no other thread.
 //
-// Softmax: per row a reference m (log2 units, a whole number) that is raised, with the sum and O rescaled, only when it
-// has to be: a tile whose every key is seen takes its weights against the reference as it is, without looking for the
-// largest score; only where a row's weights sum to more than 2^15 (or the tile is a unit's first, or masked) are the scores
-// read again, their maximum taken and the reference raised (where a score exceeds it by 8, or the sum was too large).
+// Softmax: per row a reference m (log2 units, a whole number; at first that of scores near 0).  A tile takes its weights
+// against the reference as it is, without looking for the largest score; only where a row's weights sum to more than 2^15,
+// or those of its first keys to less than 2^-6 of the aim, are the scores read again, their maximum taken and the
+// reference (with the sum and O) moved.
 //
-// Work: units (256 rows of one head, or of a gang of CTAs that walk the same keys) with their key tiles, in the order
-// request, head, rows, dealt in equal runs of key tiles.  A unit cut by a border leaves partial results in the
-// workspace, which the join kernel adds up in order.
+// Work: units (512 rows of one head) with their key tiles, in the order request, head, rows, dealt in equal runs of key
+// tiles to the pairs.  A unit cut by a border leaves partial results in the workspace, which the join kernel adds up in
+// order.
 #include <atomic>
+#include <type_traits>
 
 #include "plan.h"
 
@@ -33,33 +36,40 @@ namespace coli {
 
 constexpr int kPaQk = COLI_PROMPT_KEY + COLI_PROMPT_ROTARY, kPaV = COLI_PROMPT_VALUE;
 static_assert(kPaQk == 192 && kPaV == 128, "three boxes of 64 columns of queries and keys, two of values");
-constexpr int kPaTile = 128;                       // rows of a row tile, keys of a key tile
-constexpr int kPaRows = 2 * kPaTile;               // rows a CTA takes of a unit
-constexpr int kPaSlotBytes = kPaTile * 128;        // 64 columns of 128 keys (K, R), or 128 columns of 64 keys (V)
-constexpr int kPaSlots = 8;                        // ring of slots: K, K, R, V, V of tile after tile
-constexpr int kPaQBytes = 3 * kPaTile * 128;       // a row tile's queries
-constexpr size_t kPaSmem = 2 * (size_t)kPaQBytes + (size_t)kPaSlots * kPaSlotBytes + 1024;
+constexpr int kPaTile = 128;                       // rows of a CTA in a row tile, keys of a key tile
+constexpr int kPaRows = 4 * kPaTile;               // rows of a unit
+constexpr int kPaCtaRows = kPaRows / 2;
+constexpr int kPaKeyBox = 64 * 128;                // 64 columns of 64 keys
+constexpr int kPaValues = kPaTile * 128;           // 64 columns of 128 values' rows
+constexpr int kPaKeys3 = 3 * kPaKeyBox;            // a CTA's K and R of a tile
+constexpr int kPaStage = kPaKeys3 + kPaValues;     // its part of a key tile
+constexpr int kPaStages = 3;
+constexpr int kPaQBytes = 3 * kPaTile * 128;       // its part of a row tile's queries
+constexpr int kPaOutStage = 8 * 128;               // a softmax warp's place for results on their way out
 constexpr int kPaSmWarps = 8;                      // softmax: warps 0..3 row tile 0, 4..7 row tile 1
+constexpr size_t kPaSmem = 2 * (size_t)kPaQBytes + (size_t)kPaStages * kPaStage + kPaSmWarps * kPaOutStage + 1024;
 constexpr int kPaLoader = 8, kPaMma = 9, kPaCheck = 10, kPaCheckWarps = 2;
 constexpr int kPaThreads = (kPaCheck + kPaCheckWarps) * 32;
+constexpr int kPaMasked = kPaRows / kPaTile + 1;   // tiles of a unit of which some row does not see some key, at most
 constexpr int kPaMaxCtas = 160;                    // CTAs the workspace has room for
 constexpr int kPaMaxB = 8192, kPaMaxH = 1024;
 constexpr int kPaMaxDevices = 64;
-constexpr int kPaPart = kPaRows * kPaV;            // floats of a partial O
+constexpr int kPaPart = kPaCtaRows * kPaV;         // floats of a CTA's partial O
+// A reference is set so that the largest weight is 2^(top - 1) .. 2^top, and raised where one exceeds 2^(top + kPaGrow).
+// bf16 has fp32's range; fp16 ends at 2^16 and loses bits below 2^-14, so its weights take the upper part.
 constexpr float kPaGrow = 8.f;
-constexpr float kPaSumLimit = 32768.f;             // a row's weights of one tile sum to at most this, or its reference is looked at
-// A reference makes the largest weight 2^(top - 1) .. 2^top; growth to 2^(top + kPaGrow) raises it.  bf16 has fp32's
-// range; fp16 ends at 2^16 and loses bits below 2^-14, so its weights take the upper part.
 __host__ __device__ constexpr float pa_top(bool bf16) { return bf16 ? 0.f : 7.f; }
+constexpr float kPaSumLimit = 32768.f;             // a row's weights of a tile sum to at most this,
+__host__ __device__ constexpr float pa_first(bool bf16) { return bf16 ? 1.f / 64 : 2.f; }   // those of its first keys to at least this
 constexpr uint32_t kPaOCol = 256;                  // TMEM columns: S_0 0.., S_1 128.., O_0 256.., O_1 384..
 
-// 256 rows of a unit cut by borders: its parts are those of CTAs cta, cta + gang, ...
+// A unit cut by borders: its parts are those of pairs pair, pair + 1, ...
 struct __align__(16) PaJoin {
   int row0, rows;   // first row of the batch, rows
   int h;
-  int cta, parts, gang;
-  int slot;         // of the first part (the others': 2 * their CTA)
-  int pad;
+  int pair, parts;
+  int which;        // of the first pair's two partial results (the others': the first)
+  int pad[2];
 };
 
 struct PaArgs {
@@ -72,76 +82,70 @@ struct PaArgs {
   float* lse;
   int32_t* status;
   int32_t* cta_status;               // [kPaMaxCtas]
-  PaJoin* joins;                     // [kPaMaxCtas] written by every CTA (parts = 0: none)
-  float* part;                       // [2 kPaMaxCtas] partial O (pa_part)
+  PaJoin* joins;                     // [kPaMaxCtas / 2] written by every pair (parts = 0: none)
+  float* part;                       // [2 kPaMaxCtas] partial O (pa_slot, pa_part)
   float2* part_ml;                   // [2 kPaMaxCtas][256] reference, sum
   unsigned long long wait_ns;
-  int withhold;                      // failure-path test: 1: CTA 0's first copy never counts as complete
+  int withhold;                      // failure-path test: 1: the first pair's first keys never count as there
 };
 
 struct PaMaps {
   CUtensorMap q, k, r, v;
 };
 
-// Place of row r and value c (a multiple of four) in a partial O: neighbouring rows' four values lie together, as a
-// warp's threads hold them.
-__host__ __device__ constexpr int pa_part(int r, int c) { return ((c >> 2) * kPaRows + r) * 4; }
+// Partial results: two a pair (of its run's first unit, of its last), a half in each CTA.  A CTA's row i is row
+// (i / 128) 256 + rank 128 + i % 128 of the unit.
+__host__ __device__ constexpr size_t pa_slot(int pair, int which, int rank) { return ((size_t)pair * 2 + which) * 2 + rank; }
+// Place of row r and value c (a multiple of four) in one: neighbouring rows' four values lie together, as a warp's
+// threads hold them.
+__host__ __device__ constexpr int pa_part(int r, int c) { return ((c >> 2) * kPaCtaRows + r) * 4; }
 
 // ------------------------------------------------------------------ plan
-// Every CTA finds its own run of the work from the lengths.  A request's new rows come in blocks of 256 * gang;
-// block j of a request (1, 2, ...) sees keys up to its last row: max(1, a + 2 gang j) tiles with
-// a = ceil((keys - rows) / 128), the last block all of them.  Units are (request, head, block), block fastest.
-// Members of a gang take 256 rows each of the same keys at about the same time, so that a key tile comes from memory
-// once for all of them: a CTA alone takes 80 KB a tile in about the time that memory needs for 152 of those.
-struct PaRequest {
-  int T, L, nb, a, g2;     // new rows, keys, blocks, see above, 2 * gang
-  __device__ __forceinline__ PaRequest(int T_, int L_, int gang) : T(T_), L(L_), g2(2 * gang) {
-    const int rows = kPaRows * gang;
-    nb = (int)(((long long)T + rows - 1) / rows);
-    a = (L - T + kPaTile - 1) >> 7;
-  }
-  // tiles of the first n blocks
-  __device__ __forceinline__ long long before(int n) const {
-    const int m = min(n, nb - 1);
-    long long s = 0;
-    if (m > 0) {
-      const int flat = a < 0 ? min(m, -a / g2) : 0;        // blocks whose rows see nothing: one tile each
-      s = flat + (long long)(m - flat) * a + (long long)g2 * (((long long)m * (m + 1) - (long long)flat * (flat + 1)) / 2);
-    }
-    if (n == nb && nb > 0) s += max(1, (L + kPaTile - 1) >> 7);
-    return s;
-  }
+// Every CTA finds its pair's run of the work from the lengths.  A request's T new rows over L keys come in blocks of 512;
+// block j (1, 2, ...) sees keys up to its last row: max(1, a + 4 j) tiles with a = ceil((L - T) / 128), the last block all
+// of them.  Units are (request, head, block), block fastest: neighbouring pairs work on the same head's keys.
+// The code runs once a launch and what it costs is mostly fetching it: 32 bits, few divisions, each step written once.
+constexpr int kPaTilesPerBlock = kPaRows / kPaTile;
+__device__ __forceinline__ int pa_blocks(int T) { return (int)(((unsigned)T + kPaRows - 1) / kPaRows); }
+__device__ __forceinline__ int pa_key_tiles(int keys) { return max(1, (keys + kPaTile - 1) >> 7); }
+// Tiles of the first n of nb blocks, saturating (a sum that does not fit 31 bits is refused).
+__device__ __forceinline__ unsigned pa_before(int T, int L, int nb, int n) {
+  const int a = (L - T + kPaTile - 1) >> 7;
+  const int m = min(n, nb - 1);
+  const int flat = a < 0 ? min(m, -a / kPaTilesPerBlock) : 0;        // blocks whose rows see nothing: one tile each
+  const long long s = flat + (long long)(m - flat) * a +
+                      (long long)(kPaTilesPerBlock / 2) * ((long long)m * (m + 1) - (long long)flat * (flat + 1)) +
+                      (n == nb ? pa_key_tiles(L) : 0);
+  return (unsigned)min(s, 0x7fffffffll);
+}
+
+// Borders of G <= kPaMaxCtas equal runs of the W key tiles: floor(W j / G), without leaving 32 bits.  The
+// remainder's part is below kPaMaxCtas^2, where the fp32 quotient of x + 1/2 is exact.
+struct PaCuts {
+  int q, r;
+  float inv;
+  __device__ __forceinline__ PaCuts(int W, int G) : q(W / G), r(W - q * G), inv(1.0f / (float)G) {}
+  __device__ __forceinline__ int operator()(int j) const { return q * j + (int)(((float)(r * j) + 0.5f) * inv); }
 };
 
-// A unit as its CTA (member `mem` of the gang) sees it.
-struct PaUnit {
+struct __align__(16) PaUnit {
   int b, h, blk, nb;
   int q0, T, k0, L;
-  long long first;   // key tiles of the units before it
+  int first;         // key tiles of the units before it
   int tiles;
 };
 
 struct PaRun {
-  int gang, member;
-  long long beg, end;
+  int beg, end;
   PaUnit unit0;      // that of `beg`
   int status;
 };
 
-__device__ __forceinline__ void pa_open(const PaArgs& p, PaUnit& u, int b, int gang) {
-  u.b = b;
-  u.q0 = p.q_start[b];
-  u.T = p.q_start[b + 1] - u.q0;
-  u.k0 = p.k_start[b];
-  u.L = p.k_start[b + 1] - u.k0;
-  u.nb = (int)(((long long)u.T + kPaRows * gang - 1) / (kPaRows * gang));
-}
-__device__ __forceinline__ void pa_tiles(PaUnit& u, int gang) {
-  const int last = (int)min((long long)u.T, ((long long)u.blk + 1) * (kPaRows * gang));
-  u.tiles = max(1, (u.L - u.T + last + kPaTile - 1) >> 7);
+__device__ __forceinline__ void pa_tiles(PaUnit& u) {
+  u.tiles = pa_key_tiles(u.blk + 1 == u.nb ? u.L : u.L - u.T + (u.blk + 1) * kPaRows);
 }
 // The unit after u (of the same or a later request; the caller has not reached the end of the work).
-__device__ __forceinline__ void pa_next(const PaArgs& p, PaUnit& u, int gang) {
+__device__ __forceinline__ void pa_next(const PaArgs& p, PaUnit& u) {
   u.first += u.tiles;
   if (++u.blk == u.nb) {
     u.blk = 0;
@@ -149,28 +153,32 @@ __device__ __forceinline__ void pa_next(const PaArgs& p, PaUnit& u, int gang) {
       u.h = 0;
       do {
         if (u.b + 1 >= p.B) return;
-        pa_open(p, u, u.b + 1, gang);
+        ++u.b;
+        u.q0 = p.q_start[u.b];
+        u.T = p.q_start[u.b + 1] - u.q0;
+        u.k0 = p.k_start[u.b];
+        u.L = p.k_start[u.b + 1] - u.k0;
       } while (u.T == 0);
+      u.nb = pa_blocks(u.T);
     }
   }
-  pa_tiles(u, gang);
+  pa_tiles(u);
 }
 
-// What a part [t0, t1) of a unit is for this member.
+// What a part [t0, t1) of a unit is.
 struct PaPart {
-  int row0, rows;    // its first row of the request, its rows (<= 0: none)
+  int row0, rows;    // its first row of the request, its rows
   int shift;         // the last key that row i of the request sees: shift + i
   int n[2];          // key tiles of row tile x in the part
   int all;           // the larger
-  __device__ __forceinline__ PaPart(const PaUnit& u, int gang, int member, int t0, int t1) {
-    const long long at = ((long long)u.blk * gang + member) * kPaRows;
-    rows = (int)max(-1ll, min((long long)kPaRows, u.T - at));
-    row0 = rows > 0 ? (int)at : 0;
+  __device__ __forceinline__ PaPart(const PaUnit& u, int t0, int t1) {
+    row0 = u.blk * kPaRows;
+    rows = min(kPaRows, u.T - row0);
     shift = u.L - u.T;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int r = min(kPaTile, rows - x * kPaTile);
-      const int seen = r > 0 ? (shift + row0 + x * kPaTile + r + kPaTile - 1) >> 7 : 0;
+      const int r = min(2 * kPaTile, rows - x * 2 * kPaTile);
+      const int seen = r > 0 ? (shift + row0 + x * 2 * kPaTile + r + kPaTile - 1) >> 7 : 0;
       n[x] = max(0, min(t1, seen) - t0);
     }
     all = max(n[0], n[1]);
@@ -179,213 +187,202 @@ struct PaPart {
   __device__ __forceinline__ int masked() const { return max(0, (shift + row0 + 1) >> 7); }
 };
 
-constexpr float kPaTileNs = 1650.f;        // a key tile for 256 rows on one SM (measured)
-constexpr float kPaTileMemNs = 12.1f;      // 82 KB at the memory's measured copy rate
-constexpr long long kPaL2Keys = 100000;    // (key, head) pairs that stay in L2 between row blocks: 51 MB of keys and values
 constexpr int kPaWhole = 4;                // units of at most so many tiles are not cut: a join costs more
 
-// `sm`: shared memory for 16 (B + 1) bytes, free again when the call returns.  Every thread of the CTA calls it.
-__device__ __forceinline__ PaRun pa_plan(const PaArgs& p, uint8_t* sm) {
-  long long* first = reinterpret_cast<long long*>(sm);               // [B + 1] key tiles of the requests before
-  int* qs = reinterpret_cast<int*>(first + p.B + 1);                 // [B + 1]
-  int* ks = qs + p.B + 1;                                            // [B + 1]
-  __shared__ long long sums[4], warp_tot[kPaThreads / 32 + 1];
-  __shared__ int s_wrong, s_longest;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.B;
-  if (tid < 4) sums[tid] = 0;
-  if (tid == 0) s_wrong = s_longest = 0;
-#pragma unroll 1
-  for (int b = tid; b <= B; b += kPaThreads) {
-    qs[b] = p.q_start[b];
-    ks[b] = p.k_start[b];
-  }
-  __syncthreads();
-  {
-    bool wrong = false;
-    long long s1 = 0, s2 = 0, s4 = 0, keys = 0;
-    int longest = 0;
-#pragma unroll 1
-    for (int b = tid; b < B; b += kPaThreads) {
-      const int q0 = qs[b], q1 = qs[b + 1], k0 = ks[b], k1 = ks[b + 1];
-      if (q0 < 0 || q1 < q0 || q1 > p.n_tokens || k0 < 0 || k1 < k0 || k1 > p.n_keys) {
-        wrong = true;
-      } else if (q1 > q0) {
-        const PaRequest r1(q1 - q0, k1 - k0, 1), r2(q1 - q0, k1 - k0, 2), r4(q1 - q0, k1 - k0, 4);
-        s1 += r1.before(r1.nb);
-        s2 += r2.before(r2.nb);
-        s4 += r4.before(r4.nb);
-        keys += k1 - k0;
-        longest = max(longest, max(1, (k1 - k0 + kPaTile - 1) >> 7));
-      }
+// Every thread of the CTA calls it.  Each thread sums a stretch of the requests.
+__device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
+  __shared__ unsigned warp_tot[kPaThreads / 32];
+  __shared__ PaUnit found;
+  __shared__ int s_longest;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + kPaThreads - 1) / kPaThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  if (tid == 0) s_longest = 0;
+  bool wrong = false;
+  unsigned sum = 0;
+  int longest = 0;
+  auto tiles_of = [&](int b, int& q0, int& T, int& k0, int& L) {
+    const int q1 = p.q_start[b + 1], k1 = p.k_start[b + 1];
+    q0 = p.q_start[b];
+    k0 = p.k_start[b];
+    if (q0 < 0 || q1 < q0 || q1 > p.n_tokens || k0 < 0 || k1 < k0 || k1 > p.n_keys) {
+      wrong = true;
+      return 0u;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
-      s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-      s4 += __shfl_xor_sync(0xffffffffu, s4, o);
-      keys += __shfl_xor_sync(0xffffffffu, keys, o);
-    }
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    if (lane == 0 && longest) {
-      atomicAdd(reinterpret_cast<unsigned long long*>(&sums[0]), (unsigned long long)s1);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&sums[1]), (unsigned long long)s2);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&sums[2]), (unsigned long long)s4);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&sums[3]), (unsigned long long)keys);
-      atomicMax(&s_longest, longest);
-    }
-    if (wrong) s_wrong = 1;
-  }
-  __syncthreads();
-  PaRun r;
-  r.status = s_wrong ? COLI_DEV_KV_TOKENS : 0;
-  r.gang = 1;
-  if (sums[3] * p.H > kPaL2Keys) {
-    float best = INFINITY;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int g = 1 << i;
-      if (g > (int)gridDim.x) break;
-      const float w = (float)sums[i] * (float)p.H;
-      const float cost = fmaxf(w / (float)((int)gridDim.x / g) * kPaTileNs, w * kPaTileMemNs);
-      if (cost < best) {
-        best = cost;
-        r.gang = g;
-      }
-    }
-  }
-  const int gang = r.gang, run = blockIdx.x / gang;
-  r.member = blockIdx.x - run * gang;
-  r.beg = r.end = 0;
-  // key tiles of the requests before each
-  long long carry = 0;
-#pragma unroll 1
-  for (int b0 = 0; b0 < B; b0 += kPaThreads) {
-    const int b = b0 + tid;
-    long long v = 0;
-    if (b < B && !s_wrong) {
-      const PaRequest q(qs[b + 1] - qs[b], ks[b + 1] - ks[b], gang);
-      v = q.before(q.nb) * p.H;
-    }
-    long long inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long n = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += n;
-    }
-    if (lane == 31) warp_tot[warp] = inc;
-    __syncthreads();
-    if (tid == 0) {
-      long long s = 0;
-#pragma unroll 1
-      for (int w = 0; w < kPaThreads / 32; ++w) {
-        const long long t = warp_tot[w];
-        warp_tot[w] = s;
-        s += t;
-      }
-      warp_tot[kPaThreads / 32] = s;
-    }
-    __syncthreads();
-    if (b < B) first[b] = carry + warp_tot[warp] + inc - v;
-    carry += warp_tot[kPaThreads / 32];
-    __syncthreads();
-  }
-  if (tid == 0) first[B] = carry;
-  __syncthreads();
-  const long long W = carry;
-  if (tid == 0) p.joins[blockIdx.x].parts = 0;
-  if (W == 0) return r;
-  // The longest run decides the time, so no more runs than it needs: fewer parts to write and join.
-  long long G = min((long long)((int)gridDim.x / gang), W);
-  const long long longest = (W + G - 1) / G;
-  G = (W + longest - 1) / longest;
-  if (run >= G) return r;
-  auto cut = [&](long long j) { return W * j / G; };       // (W < 2^44, G < 2^8)
-  auto locate = [&](long long x) {
-    int l = 0, h = B;                                      // last b with first[b] <= x: it has rows
-#pragma unroll 1
-    while (h - l > 1) {
-      const int mid = (l + h) >> 1;
-      if (first[mid] <= x) l = mid;
-      else h = mid;
-    }
-    PaUnit u;
-    u.b = l;
-    u.q0 = qs[l];
-    u.T = qs[l + 1] - qs[l];
-    u.k0 = ks[l];
-    u.L = ks[l + 1] - ks[l];
-    const PaRequest q(u.T, u.L, gang);
-    u.nb = q.nb;
-    const long long per = q.before(q.nb);
-    long long rest = x - first[l];
-    u.h = (int)(rest / per);
-    rest -= u.h * per;
-    int i = 0, n = q.nb;                                   // last block with before(block) <= rest
-#pragma unroll 1
-    while (n - i > 1) {
-      const int mid = (i + n) >> 1;
-      if (q.before(mid) <= rest) i = mid;
-      else n = mid;
-    }
-    u.blk = i;
-    u.first = x - rest + q.before(i);
-    pa_tiles(u, gang);
-    return u;
+    T = q1 - q0;
+    L = k1 - k0;
+    const int nb = pa_blocks(T);
+    return (unsigned)min((unsigned long long)(T ? pa_before(T, L, nb, nb) : 0u) * p.H, 0x7fffffffull);
   };
-  r.beg = cut(run);
-  r.end = cut(run + 1);
-  r.unit0 = locate(r.beg);
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    int q0, T, k0, L;
+    const unsigned t = tiles_of(b, q0, T, k0, L);
+    sum = min(sum + t, 0x7fffffffu);
+    if (t) longest = max(longest, pa_key_tiles(L));
+  }
+  unsigned inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned n = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc = min(inc + n, 0x7fffffffu);
+  }
+  if (lane == 31) warp_tot[warp] = inc;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  wrong = __syncthreads_or(wrong);
+  if (lane == 0 && longest) atomicMax(&s_longest, longest);
+  unsigned total = 0, base = 0;
+#pragma unroll 1
+  for (int w = 0; w < kPaThreads / 32; ++w) {
+    if (w == warp) base = total;
+    total = min(total + warp_tot[w], 0x7fffffffu);
+  }
+  base += inc - sum;
+  wrong |= total == 0x7fffffffu;
+  PaRun r;
+  r.status = wrong ? COLI_DEV_KV_TOKENS : 0;
+  r.beg = r.end = 0;
+  const int W = wrong ? 0 : (int)total, pair = blockIdx.x >> 1;
+  if ((blockIdx.x & 1) == 0 && tid == 0) p.joins[pair].parts = 0;
+  // The longest run decides the time, so no more runs than it needs: fewer parts to write and join.
+  int G = min((int)gridDim.x >> 1, W);
+  if (pair >= G) return r;
+  const int most = (W + G - 1) / G;
+  G = (W + most - 1) / most;
+  if (pair >= G) return r;
+  const PaCuts cut(W, G);
+  r.beg = cut(pair);
+  r.end = cut(pair + 1);
+  // the unit of tile x, found by the thread whose requests hold it
+  auto locate = [&](int x) {
+    __syncthreads();
+    if (x >= (int)base && x < (int)(base + sum)) {
+      PaUnit u;
+      int rest = x - (int)base, b = b0;
+#pragma unroll 1
+      for (;; ++b) {
+        const int t = (int)tiles_of(b, u.q0, u.T, u.k0, u.L);
+        if (rest < t) break;
+        rest -= t;
+      }
+      u.b = b;
+      u.nb = pa_blocks(u.T);
+      const int unit = (int)pa_before(u.T, u.L, u.nb, u.nb);
+      u.h = rest / unit;
+      rest -= u.h * unit;
+      int i = 0, n = u.nb;                             // last block with before(block) <= rest
+#pragma unroll 1
+      while (n - i > 1) {
+        const int mid = (i + n) >> 1;
+        if ((int)pa_before(u.T, u.L, u.nb, mid) <= rest) i = mid;
+        else n = mid;
+      }
+      u.blk = i;
+      u.first = x - rest + (int)pa_before(u.T, u.L, u.nb, i);
+      pa_tiles(u);
+      found = u;
+    }
+    __syncthreads();
+    return found;
+  };
+  r.unit0 = locate(r.beg);                             // (its barriers make s_longest known, too)
   if (s_longest <= kPaWhole) {
     // short units are not cut: a run takes those that begin in it
-    auto up = [&](long long x) {
-      if (x == W) return W;
-      const PaUnit u = locate(x);
-      return u.first == x ? x : u.first + u.tiles;
-    };
-    r.beg = up(r.beg);
-    r.end = up(r.end);
-    if (r.beg < r.end) r.unit0 = locate(r.beg);
+    if (r.unit0.first < r.beg) {
+      r.beg = r.unit0.first + r.unit0.tiles;
+      pa_next(p, r.unit0);
+    }
+    if (r.end < W) {
+      const PaUnit u = locate(r.end);
+      if (u.first < r.end) r.end = u.first + u.tiles;
+    }
     return r;
   }
-  // a run that begins with the first border inside its unit lists the join of its member's rows
-  if (tid == 0 && run > 0 && r.unit0.first < r.beg) {
-    const PaUnit& u = r.unit0;
-    const long long before = cut(run - 1);
-    const PaPart part(u, gang, r.member, 0, u.tiles);
-    if (before <= u.first && part.rows > 0) {
-      int m = run;
-      while (m < G && cut(m) < u.first + u.tiles) ++m;     // runs run - 1 .. m - 1 begin before the unit's end
-      PaJoin jn;
-      jn.row0 = u.q0 + part.row0;
-      jn.rows = part.rows;
-      jn.h = u.h;
-      jn.cta = (run - 1) * gang + r.member;
-      jn.parts = m - (run - 1);
-      jn.gang = gang;
-      jn.slot = 2 * jn.cta + (before < u.first ? 1 : 0);
-      jn.pad = 0;
-      p.joins[blockIdx.x] = jn;
-    }
+  // a run that begins with the first border inside its unit lists the join
+  const PaUnit& u = r.unit0;
+  if ((blockIdx.x & 1) == 0 && tid == 0 && pair > 0 && u.first < r.beg && cut(pair - 1) <= u.first) {
+    int m = pair;
+    while (m < G && cut(m) < u.first + u.tiles) ++m;   // runs pair - 1 .. m - 1 begin before the unit's end
+    PaJoin jn;
+    jn.row0 = u.q0 + u.blk * kPaRows;
+    jn.rows = min(kPaRows, u.T - u.blk * kPaRows);
+    jn.h = u.h;
+    jn.pair = pair - 1;
+    jn.parts = m - (pair - 1);
+    jn.which = cut(pair - 1) < u.first ? 1 : 0;
+    jn.pad[0] = jn.pad[1] = 0;
+    p.joins[pair] = jn;
   }
   return r;
 }
 
 // ------------------------------------------------------------------ main kernel
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+// Address of the same place of shared memory in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* at, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void cluster_store(uint32_t at, uint32_t v) {
+  asm volatile("st.volatile.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same where what comes before is ordered by tcgen05 fences alone (a release for the cluster waits for every store:
+// 1,000 cycles a tile).
+__device__ __forceinline__ void cluster_arrive_tmem(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// mbar_wait for arrivals of either CTA.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+  unsigned long long t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (it == 0) t0 = globaltimer();
+    else if ((it & 63u) == 0 && globaltimer() - t0 > limit_ns) return false;
+  }
+}
+
+// TMA loads of a pair: into this CTA's shared memory, counted on a barrier of either CTA.
+__device__ __forceinline__ void tma_pair_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_pair_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 
-// Operand read transposed (MN-major), 128-byte swizzle: 64 elements of N an atom of 8 K rows, the next 64 `mn_bytes`
-// further, the next 8 of K 1024 bytes further.
-__device__ __forceinline__ uint64_t pa_desc_mn(uint32_t saddr, uint32_t mn_bytes) {
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+// Operand read transposed (MN-major), 128-byte swizzle: 64 elements of N an atom of 8 K rows, the next 8 of K 1024 bytes
+// further (an operand here has one atom of N a CTA).
+__device__ __forceinline__ uint64_t pa_desc_mn(uint32_t saddr) {
   uint64_t d = 0;
   d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(mn_bytes >> 4) << 16;
+  d |= (uint64_t)(kPaValues >> 4) << 16;
   d |= (uint64_t)(1024 >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
@@ -447,18 +444,18 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t* r) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// Four products of depth 16, both operands in shared memory, issued by one elected lane of a converged warp; acc = 0:
-// the first overwrites.
+// Four products of depth 16 of a pair of CTAs, both operands in shared memory, issued by one elected lane of a converged
+// warp; acc = 0: the first overwrites.
 __device__ __forceinline__ void pa_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
       "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
       "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
       "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
@@ -469,18 +466,27 @@ __device__ __forceinline__ void pa_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
       "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
       "add.u64 b1, %2, 128;\n\tadd.u64 b2, %2, 256;\n\tadd.u64 b3, %2, 384;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a2], b2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [a3], b3, %3, q;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// Arrive on `bar` when the products issued so far are complete (one elected lane of a converged warp).
+// Arrive on `bar` in both CTAs when the products issued so far are complete (one elected lane of a converged warp).
 __device__ __forceinline__ void pa_commit(uint64_t* bar) {
   asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .b16 m;\n\telect.sync _|e, 0xffffffff;\n\tmov.b16 m, 3;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+
+// The same in this CTA alone.
+__device__ __forceinline__ void pa_commit_here(uint64_t* bar) {
+  asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
 
@@ -496,37 +502,42 @@ __device__ __forceinline__ uint32_t pa_finite_part(uint32_t w) {
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const PaArgs p, const __grid_constant__ PaMaps maps) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
+    prompt_attention_kernel(const PaArgs p, const __grid_constant__ PaMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ uint64_t full[kPaSlots], empty[kPaSlots], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], v_full[2][2], v_ok[2], drained;
+  // Barriers of the first CTA, for its product issuer: what is there in both CTAs.
+  __shared__ uint64_t q_full[2], k_full[kPaStages], v_full[kPaStages], v_ok[kPaStages], p_ready[2];
+  // Barriers of either CTA: what the products are done with; values that the check awaits.
+  __shared__ uint64_t q_empty[2], k_empty[kPaStages], v_empty[kPaStages], s_full[2], o_full[2], v_here[kPaStages], drained;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, cta_status;
-  // keys of the masked tiles (at most three a unit) whose values are not all finite, of four units; done: units whose
-  // output each softmax warp has written
-  __shared__ uint32_t bad[4][3][4], done[kPaSmWarps];
+  // Keys of the masked tiles whose values are not all finite in the columns of either CTA, of four units; done: units whose
+  // output each softmax warp of either CTA has written.
+  __shared__ uint32_t bad[2][4][kPaMasked][4], done[2][kPaSmWarps];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qsm = smem + kPaSlots * kPaSlotBytes;
+  uint8_t* qsm = smem + kPaStages * kPaStage;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;                     // of this CTA in its pair (clusters are two neighbouring blocks)
   volatile int* abort_v = &abort_flag;
 
   if (threadIdx.x == 0) {
-    // (an arrival too many for a withheld stage)
-    for (int i = 0; i < kPaSlots; ++i) {
-      mbar_init(&full[i], 1 + (i == 0 && blockIdx.x == 0 ? p.withhold : 0));
-      mbar_init(&empty[i], 1);
-    }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
       mbar_init(&q_empty[x], 1);
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_ready[x], 4);
+      mbar_init(&p_ready[x], 8);
       mbar_init(&o_full[x], 1);
-      mbar_init(&v_full[x][0], 1);
-      mbar_init(&v_full[x][1], 1);
-      mbar_init(&v_ok[x], kPaCheckWarps);
+    }
+    for (int i = 0; i < kPaStages; ++i) {
+      mbar_init(&k_full[i], 1 + (i == 0 && blockIdx.x == 0 ? p.withhold : 0));     // (an arrival too many for a withheld stage)
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_here[i], 1);
+      mbar_init(&v_ok[i], 2 * kPaCheckWarps);
     }
     mbar_init(&drained, 1);
-    for (int i = 0; i < kPaSmWarps; ++i) done[i] = 0;
+    for (int i = 0; i < 2 * kPaSmWarps; ++i) done[i / kPaSmWarps][i % kPaSmWarps] = 0;
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -537,20 +548,18 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     prefetch_tensormap(&maps.v);
   }
   if (warp == kPaMma) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
                  "r"(512));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();                                      // both CTAs' barriers are there
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   griddep_wait();                                      // the launch may overlap the kernel before; its results not
-  const PaRun run = pa_plan(p, smem);
-  const int gang = run.gang, member = run.member;
+  const PaRun run = pa_plan(p);
   if (threadIdx.x == 0) cta_status = run.status;
-  // (the plan's use of shared memory ends before the TMA use of it)
-  fence_proxy_async_smem();
   __syncthreads();
   auto fail_wait = [&]() {
     atomicOr(&cta_status, COLI_DEV_WAIT_TIMEOUT);
@@ -560,202 +569,203 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
   if (warp == kPaLoader) {
     // ---------------------------------------------------------------- loader
     bool ok = true;
-    unsigned pos = 0;                                  // slots filled so far
-    unsigned checked[2] = {0, 0};                      // slots of values that go through the check, of either half
+    unsigned tile = 0;                                 // key tiles begun
     int un[2] = {0, 0};                                // units whose queries are on their way
+    auto wait = [&](uint64_t* bar, unsigned phase) { ok = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.wait_ns)); };
     PaUnit u = run.unit0;
-    for (long long at = run.beg; ok && at < run.end; pa_next(p, u, gang)) {
-      const int t0 = (int)(at - u.first), t1 = (int)min(run.end - u.first, (long long)u.tiles);
+    for (int at = run.beg; ok && at < run.end; pa_next(p, u)) {
+      const int t0 = at - u.first, t1 = min(run.end - u.first, u.tiles);
       at = u.first + t1;
-      const PaPart part(u, gang, member, t0, t1);
+      const PaPart part(u, t0, t1);
       if (part.all == 0) continue;
       const int masked = part.masked();
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (!ok || part.n[x] == 0) continue;
-        if (un[x] > 0) ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[x], (un[x] - 1) & 1, p.wait_ns));
-        if (!ok) continue;
+      for (int t = t0; ok && t < t0 + part.all; ++t, ++tile) {
+        if (__any_sync(0xffffffffu, *abort_v)) { ok = false; break; }
+        const unsigned s = tile % kPaStages, use = tile / kPaStages;
+        uint8_t* dst = smem + s * kPaStage;
+        const int key = u.k0 + t * kPaTile;
+        if (use > 0) wait(&k_empty[s], use - 1);
+        if (!ok) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[x], (uint32_t)kPaQBytes);
-          // rows past the unit's last are other rows' or, behind the tensor, zeros: computed, not written
-          for (int i = 0; i < 3; ++i)
-            tma_load_3d(qsm + x * kPaQBytes + i * (kPaTile * 128), &maps.q, i * 64, u.h, u.q0 + part.row0 + x * kPaTile, &q_full[x]);
+          if (rank == 0) mbar_arrive_expect_tx(&k_full[s], (uint32_t)(2 * kPaKeys3));
+          const uint32_t bar = cluster_addr(&k_full[s], 0);
+          tma_pair_3d(dst, &maps.k, 0, u.h, key + rank * 64, bar);
+          tma_pair_3d(dst + kPaKeyBox, &maps.k, 64, u.h, key + rank * 64, bar);
+          tma_pair_2d(dst + 2 * kPaKeyBox, &maps.r, 0, key + rank * 64, bar);
         }
         __syncwarp();
-        ++un[x];
-      }
-      for (int t = t0; ok && t < t0 + part.all; ++t) {
-        if (__any_sync(0xffffffffu, *abort_v)) { ok = false; break; }
-        const int key = u.k0 + t * kPaTile;
-        const bool check = t >= masked;                // its values then count on v_full, which the check awaits
-#pragma unroll 1
-        for (int i = 0; i < 5; ++i, ++pos) {
-          const unsigned s = pos % kPaSlots;
-          if (pos >= kPaSlots) ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], (pos / kPaSlots - 1) & 1, p.wait_ns));
-          if (!ok) break;
-          if (lane == 0) {
-            uint8_t* dst = smem + s * kPaSlotBytes;
-            uint64_t* bar = &full[s];
-            if (check && i >= 3) {
-              mbar_arrive(bar);
-              bar = &v_full[(i == 3 ? checked[0] : checked[1]) & 1][i - 3];
+        if (t == t0) {                                 // the queries: rows past the unit's last are other rows' or, behind
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {                // the tensor, zeros: computed, not written
+            if (!ok || part.n[x] == 0) continue;
+            if (un[x] > 0) wait(&q_empty[x], un[x] - 1);
+            if (!ok) continue;
+            if (lane == 0) {
+              if (rank == 0) mbar_arrive_expect_tx(&q_full[x], (uint32_t)(2 * kPaQBytes));
+              const uint32_t bar = cluster_addr(&q_full[x], 0);
+              for (int i = 0; i < 3; ++i)
+                tma_pair_3d(qsm + x * kPaQBytes + i * (kPaTile * 128), &maps.q, i * 64, u.h,
+                            u.q0 + part.row0 + x * 2 * kPaTile + rank * kPaTile, bar);
             }
-            mbar_arrive_expect_tx(bar, (uint32_t)kPaSlotBytes);
-            if (i < 2) {
-              tma_load_3d(dst, &maps.k, i * 64, u.h, key, bar);
-            } else if (i == 2) {
-              tma_load_2d_nohint(dst, &maps.r, 0, key, bar);
-            } else {                                   // 64 keys: two boxes of 64 values
-              tma_load_3d(dst, &maps.v, 0, u.h, key + (i - 3) * 64, bar);
-              tma_load_3d(dst + kPaSlotBytes / 2, &maps.v, 64, u.h, key + (i - 3) * 64, bar);
-            }
+            __syncwarp();
+            ++un[x];
+          }
+          if (ok && at < run.end && lane < 6) {        // and the next unit's on their way to L2
+            PaUnit w = u;
+            pa_next(p, w);
+            tma_prefetch_3d(&maps.q, (lane % 3) * 64, w.h, w.q0 + w.blk * kPaRows + (lane / 3 * 2 + rank) * kPaTile);
           }
           __syncwarp();
-          checked[0] += check && i == 3;
-          checked[1] += check && i == 4;
         }
+        if (use > 0) wait(&v_empty[s], use - 1);
+        if (!ok) break;
+        if (lane == 0) {
+          uint32_t bar = cluster_addr(&v_full[s], 0);
+          if (t >= masked) {                           // these values go through the check: it says when they are ready
+            mbar_arrive_expect_tx(&v_here[s], (uint32_t)kPaValues);
+            if (rank == 0) mbar_arrive(&v_full[s]);
+            bar = smem_u32(&v_here[s]);
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(&v_full[s], (uint32_t)(2 * kPaValues));
+          }
+          tma_pair_3d(dst + kPaKeys3, &maps.v, rank * 64, u.h, key, bar);
+        }
+        __syncwarp();
       }
     }
-    if (!ok) fail_wait();
-    // Copies in flight land before the CTA leaves, whichever role gave up.  A slot's phases before its last are
-    // complete: it was filled again only after its use.
-    if (lane == 0) {
-      for (int x = 0; x < 2; ++x)
-        if (un[x] > 0) mbar_wait(&q_full[x], (un[x] - 1) & 1, kWaitLimitNs);
-      for (unsigned s = 0; s < kPaSlots; ++s)
-        if (pos > s) mbar_wait(&full[s], ((pos - s - 1) / kPaSlots) & 1, s == 0 && p.withhold ? 1000000ull : kWaitLimitNs);
-      for (int h = 0; h < 2; ++h)
-        for (unsigned j = 0; j < 2; ++j)
-          if (checked[h] > j) mbar_wait(&v_full[j][h], ((checked[h] - j - 1) / 2) & 1, kWaitLimitNs);
+    // the products' last arrivals come before the CTA leaves
+    for (unsigned s = 0; s < kPaStages; ++s) {
+      if (!ok || tile <= s) continue;
+      wait(&k_empty[s], (tile - s - 1) / kPaStages);
+      if (ok) wait(&v_empty[s], (tile - s - 1) / kPaStages);
     }
-    __syncwarp();
+    for (int x = 0; x < 2; ++x)
+      if (ok && un[x] > 0) wait(&q_empty[x], un[x] - 1);
+    if (!ok) fail_wait();
   } else if (warp == kPaMma) {
     // ---------------------------------------------------------------- product issuer (the warp stays converged)
-    const uint32_t idesc = BF16 ? umma_idesc_bf16(128, 128) : umma_idesc_f16(128, 128);
-    const uint32_t idesc_v = idesc | (1u << 16);       // B MN-major
-    const uint64_t kd = umma_desc_sw128(smem_u32(smem)), qd = umma_desc_sw128(smem_u32(qsm));
-    const uint64_t vd = pa_desc_mn(smem_u32(smem), kPaSlotBytes / 2);
-    bool ok = true;
-    unsigned pos = 0;                                  // slots consumed before this unit's tile
-    unsigned checked = 0, un[2] = {0, 0}, it[2] = {0, 0};
-    auto wait = [&](uint64_t* bar, unsigned phase) {
-      ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, phase & 1, p.wait_ns));
-      return ok;
-    };
-    PaUnit u = run.unit0;
-    for (long long at = run.beg; ok && at < run.end; pa_next(p, u, gang)) {
-      const int t0 = (int)(at - u.first), t1 = (int)min(run.end - u.first, (long long)u.tiles);
-      at = u.first + t1;
-      const PaPart part(u, gang, member, t0, t1);
-      if (part.all == 0) continue;
-      const int masked = part.masked();
-      // S of row tile x and key tile i of the part, whose slots begin at `from`
-      auto scores = [&](int x, int i, unsigned from, bool wait_keys) {
-#pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          const unsigned s = (from + c) % kPaSlots;
-          if (wait_keys) {
-            if (!wait(&full[s], (from + c) / kPaSlots)) return;
-            tc_fence_after();
-          }
-          pa_mma_ss(tmem + x * kPaTile, qd + (uint64_t)((x * kPaQBytes + c * (kPaTile * 128)) >> 4),
-                    kd + (uint64_t)(s * (kPaSlotBytes >> 4)), idesc, c ? 1u : 0u);
-        }
-        pa_commit(&s_full[x]);
-        if (i + 1 == part.n[x]) pa_commit(&q_empty[x]);
+    if (rank == 0) {
+      const uint32_t idesc = BF16 ? umma_idesc_bf16(256, 128) : umma_idesc_f16(256, 128);
+      const uint32_t idesc_v = idesc | (1u << 16);     // B MN-major
+      const uint64_t kd = umma_desc_sw128(smem_u32(smem)), qd = umma_desc_sw128(smem_u32(qsm));
+      const uint64_t vd = pa_desc_mn(smem_u32(smem + kPaKeys3));
+      bool ok = true;
+      unsigned tile = 0, un[2] = {0, 0}, it[2] = {0, 0}, checked = 0;      // checked: bit s: parity of v_ok[s]
+      auto wait = [&](uint64_t* bar, unsigned phase) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, phase & 1, p.wait_ns));
+        return ok;
       };
-      auto release = [&](unsigned from, int n) {
-        for (int c = 0; c < n; ++c) pa_commit(&empty[(from + c) % kPaSlots]);
-      };
-      bool fresh = true;
+      PaUnit u = run.unit0;
+      for (int at = run.beg; ok && at < run.end; pa_next(p, u)) {
+        const int t0 = at - u.first, t1 = min(run.end - u.first, u.tiles);
+        at = u.first + t1;
+        const PaPart part(u, t0, t1);
+        if (part.all == 0) continue;
+        const int masked = part.masked();
+        // S of row tile x and the part's key tile i in stage s
+        auto scores = [&](int x, int i, unsigned s) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (!ok || part.n[x] == 0) continue;
-        if (!wait(&q_full[x], un[x])) continue;
-        ++un[x];
-        scores(x, 0, pos, fresh);
-        fresh = false;
-      }
-      if (!ok) break;
-      release(pos, 3);
-      for (int i = 0; ok && i < part.all; ++i, pos += 5) {
-        const unsigned vpos = pos + 3, next = pos + 5;
-        // the values, or, where some row does not see some key, the values after their check.  (Every phase of a
-        // barrier is awaited or, for the value slots of a checked tile, known to be over: a parity tells neighbours apart.)
-        if (t0 + i >= masked) {
-          wait(&v_ok[checked & 1], checked >> 1);
-          ++checked;
-        } else {
-          wait(&full[vpos % kPaSlots], vpos / kPaSlots);
-          wait(&full[(vpos + 1) % kPaSlots], (vpos + 1) / kPaSlots);
-        }
-        if (!ok) break;
-        fresh = true;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok || i >= part.n[x]) continue;
-          if (!wait(&p_ready[x], it[x])) continue;
-          ++it[x];
+          for (int c = 0; c < 3; ++c)
+            pa_mma_ss(tmem + x * kPaTile, qd + (uint64_t)((x * kPaQBytes + c * (kPaTile * 128)) >> 4),
+                      kd + (uint64_t)((s * kPaStage + c * kPaKeyBox) >> 4), idesc, c ? 1u : 0u);
+          pa_commit(&s_full[x]);
+          if (i + 1 == part.n[x]) pa_commit(&q_empty[x]);
+        };
+        {
+          const unsigned s = tile % kPaStages;
+          if (!wait(&k_full[s], tile / kPaStages)) break;
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            pa_mma_ts(tmem + kPaOCol + x * kPaTile, tmem + x * kPaTile + c * 32,
-                      vd + (uint64_t)(((vpos + c) % kPaSlots) * (kPaSlotBytes >> 4)), idesc_v, i || c ? 1u : 0u);
-          if (i + 1 < part.n[x]) {
-            scores(x, i + 1, next, fresh);
-            fresh = false;
-          } else {
-            pa_commit(&o_full[x]);
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || part.n[x] == 0 || !wait(&q_full[x], un[x])) continue;
+            ++un[x];
+            tc_fence_after();
+            scores(x, 0, s);
           }
+          if (!ok) break;
+          pa_commit(&k_empty[s]);
         }
-        if (!ok) break;
-        release(vpos, 2);
-        if (i + 1 < part.all) release(next, 3);
+        for (int i = 0; ok && i < part.all; ++i, ++tile) {
+          const unsigned s = tile % kPaStages, next = (tile + 1) % kPaStages;
+          // the values, or, where some row does not see some key, the values after their check.  (Every phase of a
+          // barrier is awaited or, v_full's of a checked tile, known to be over: a parity tells neighbours apart.)
+          if (t0 + i >= masked) {
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&v_ok[s], (checked >> s) & 1, p.wait_ns));
+            checked ^= 1u << s;
+          } else {
+            wait(&v_full[s], tile / kPaStages);
+          }
+          if (!ok) break;
+          bool keys = false;                           // the next tile's keys are there
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || i >= part.n[x]) continue;
+            if (!wait(&p_ready[x], it[x])) continue;
+            ++it[x];
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              pa_mma_ts(tmem + kPaOCol + x * kPaTile, tmem + x * kPaTile + c * 32,
+                        vd + (uint64_t)((s * kPaStage + c * (kPaValues / 2)) >> 4), idesc_v, i || c ? 1u : 0u);
+            if (i + 1 < part.n[x]) {
+              if (!keys && !wait(&k_full[next], (tile + 1) / kPaStages)) continue;
+              keys = true;
+              tc_fence_after();
+              scores(x, i + 1, next);
+            } else {
+              pa_commit(&o_full[x]);
+            }
+          }
+          if (!ok) break;
+          pa_commit(&v_empty[s]);
+          if (keys) pa_commit(&k_empty[next]);
+        }
       }
+      if (!ok && lane == 0) fail_wait();
+      __syncwarp();
+      // what was issued ends before tensor memory is freed, whichever role gave up
+      pa_commit_here(&drained);
+      mbar_wait(&drained, 0, kWaitLimitNs);
     }
-    if (!ok && lane == 0) fail_wait();
-    __syncwarp();
-    // what was issued ends before tensor memory is freed, whichever role gave up
-    pa_commit(&drained);
-    mbar_wait(&drained, 0, kWaitLimitNs);
   } else if (warp >= kPaCheck) {
     // ---------------------------------------------------------------- check of the values of masked tiles
     // A row's weight for a key that it does not see is 0, and 0 times an infinity or a NaN is a NaN: such values
     // become 0 in shared memory before the product, and the rows that do see the key add them in the end.  Only the
-    // tiles that cross the diagonal are looked at.
+    // tiles that cross the diagonal are looked at, by either CTA in its columns.
     const int half = warp - kPaCheck;                  // of the tile's keys
-    volatile uint32_t* done_v = done;
+    const volatile uint32_t* done_v = &done[0][0];
     // the softmax warps have read what `bad` holds of four units before
     auto free_again = [&](unsigned uu) {
       if (uu < 4) return true;
       const unsigned long long from = globaltimer();
-      while (__any_sync(0xffffffffu, (int)(done_v[lane & (kPaSmWarps - 1)] - (uu - 3)) < 0))
+      while (__any_sync(0xffffffffu, (int)(done_v[lane & (2 * kPaSmWarps - 1)] - (uu - 3)) < 0))
         if (__any_sync(0xffffffffu, globaltimer() - from > p.wait_ns)) return false;
       return true;
     };
     bool ok = true;
-    unsigned pos = 0, checked = 0, uu = 0;
+    unsigned tile = 0, checked = 0, uu = 0;
     PaUnit u = run.unit0;
-    for (long long at = run.beg; ok && at < run.end; pa_next(p, u, gang)) {
-      const int t0 = (int)(at - u.first), t1 = (int)min(run.end - u.first, (long long)u.tiles);
+    for (int at = run.beg; ok && at < run.end; pa_next(p, u)) {
+      const int t0 = at - u.first, t1 = min(run.end - u.first, u.tiles);
       at = u.first + t1;
-      const PaPart part(u, gang, member, t0, t1);
+      const PaPart part(u, t0, t1);
       if (part.all == 0) continue;
       const int masked = part.masked();
       if (masked < t0 + part.all) ok = free_again(uu);
       for (int i = max(0, masked - t0); ok && i < part.all; ++i) {
-        const unsigned v = pos + 5 * i + 3 + half, s = v % kPaSlots;
-        ok = __all_sync(0xffffffffu, mbar_wait(&v_full[checked & 1][half], (checked >> 1) & 1, p.wait_ns));
+        const unsigned s = (tile + i) % kPaStages;
+        ok = __all_sync(0xffffffffu, mbar_wait(&v_here[s], (checked >> s) & 1, p.wait_ns));
+        checked ^= 1u << s;
         if (!ok) break;
-        uint8_t* box = smem + s * kPaSlotBytes;
+        uint8_t* box = smem + s * kPaStage + kPaKeys3 + half * (kPaValues / 2);
         uint32_t flags[2];
-#pragma unroll 1
+#pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint8_t* row = box + (k * 32 + lane) * 128;  // and the same row of the second box
+          uint8_t* row = box + (k * 32 + lane) * 128;
           uint32_t top = 0;                            // the largest magnitude of either half of the words
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {               // (the lanes' rows meet the banks evenly by the rotation)
-            const uint4 w = *reinterpret_cast<const uint4*>(row + (c >> 3) * (kPaSlotBytes / 2) + (((c + lane) & 7) << 4));
+          for (int c = 0; c < 8; ++c) {                // (the lanes' rows meet the banks evenly by the rotation)
+            const uint4 w = *reinterpret_cast<const uint4*>(row + (((c + lane) & 7) << 4));
             top = __vmaxu2(__vmaxu2(top, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu);
             top = __vmaxu2(__vmaxu2(top, w.z & 0x7fff7fffu), w.w & 0x7fff7fffu);
           }
@@ -763,23 +773,25 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
           flags[k] = __ballot_sync(0xffffffffu, wrong);
           if (wrong) {
 #pragma unroll 1
-            for (int c = 0; c < 16; ++c) {
-              uint4* w = reinterpret_cast<uint4*>(row + (c >> 3) * (kPaSlotBytes / 2) + ((c & 7) << 4));
+            for (int c = 0; c < 8; ++c) {
+              uint4* w = reinterpret_cast<uint4*>(row + (c << 4));
               *w = make_uint4(pa_finite_part<BF16>(w->x), pa_finite_part<BF16>(w->y), pa_finite_part<BF16>(w->z),
                               pa_finite_part<BF16>(w->w));
             }
           }
         }
-        if (lane == 0) {
-          bad[uu & 3][t0 + i - masked][half * 2] = flags[0];
-          bad[uu & 3][t0 + i - masked][half * 2 + 1] = flags[1];
+        if (lane < 4) {                                // two words into either CTA
+          uint32_t* at_word = &bad[rank][uu & 3][t0 + i - masked][half * 2 + (lane & 1)];
+          cluster_store(cluster_addr(at_word, lane >> 1), (lane & 1) ? flags[1] : flags[0]);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&v_ok[checked & 1]);
-        ++checked;
+        if (lane == 0) {
+          asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          cluster_arrive(cluster_addr(&v_ok[s], 0));
+        }
       }
-      pos += 5 * part.all;
+      tile += part.all;
       ++uu;
     }
     if (!ok && lane == 0) fail_wait();
@@ -787,81 +799,101 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
     // ---------------------------------------------------------------- softmax and output
     const int x = warp >> 2, sp = warp & 3;            // row tile, TMEM sub-partition
     const uint32_t ts = tmem + ((uint32_t)(sp * 32) << 16) + (uint32_t)(x * kPaTile), to = ts + kPaOCol;
-    const int in_unit = x * kPaTile + sp * 32 + lane;  // this thread's row of the CTA's 256
+    const int warp_row = x * 2 * kPaTile + rank * kPaTile + sp * 32, in_unit = warp_row + lane;    // of the unit's 512
+    const int in_cta = x * kPaTile + sp * 32 + lane;
+    const uint32_t ready = cluster_addr(&p_ready[x], 0);
+    uint8_t* stage = qsm + 2 * kPaQBytes + warp * kPaOutStage;
     unsigned it = 0, un = 0, uu = 0;
     bool ok = true;
     PaUnit u = run.unit0;
-    for (long long at = run.beg; at < run.end; pa_next(p, u, gang)) {
-      const int t0 = (int)(at - u.first), t1 = (int)min(run.end - u.first, (long long)u.tiles);
+    for (int at = run.beg; at < run.end; pa_next(p, u)) {
+      const int t0 = at - u.first, t1 = min(run.end - u.first, u.tiles);
       const bool opening = at == run.beg, whole = t0 == 0 && t1 == u.tiles;
       at = u.first + t1;
-      const PaPart part(u, gang, member, t0, t1);
+      const PaPart part(u, t0, t1);
       const int n = part.n[x];
-      if (part.rows <= x * kPaTile) {
-        uu += part.all > 0;
-        if (lane == 0) *const_cast<volatile uint32_t*>(&done[warp]) = uu;
-        continue;
-      }
-      const bool mine = in_unit < part.rows;           // rows past the last are not written
+      const bool mine = in_unit < part.rows, any = warp_row < part.rows;       // rows past the last are not written
       const int row = part.row0 + in_unit;             // of the request
       const int lim = part.shift + min(row, u.T - 1);  // the last key it sees
-      const int lim0 = part.shift + part.row0 + x * kPaTile + sp * 32;      // of the warp's first row
-      float m = 0.f, l = 0.f;                          // reference, sum of the weights
+      const int lim0 = part.shift + part.row0 + warp_row;      // of the warp's first row
+      float m = -pa_top(BF16), l = 0.f;                // reference, sum of the weights
       bool has = false;                                // the row has seen a key
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++it) {
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], it & 1, p.wait_ns));
         if (!ok) break;
         tc_fence_after();
-        const int key0 = (t0 + i) * kPaTile;
-        bool slow = key0 + kPaTile - 1 > lim0 || __any_sync(0xffffffffu, !has);
-        float grow = kPaGrow;                          // by how much a score exceeds a reference that is raised
-        if (!slow) {
-          // every key is seen: weights against the reference as it is; the sum tells whether it still serves
+        const int key0 = (t0 + i) * kPaTile, rel = lim - key0;       // the tile's columns up to rel are seen
+        // the tile's weights against the reference as it is; false where the sum tells that it does not serve
+        auto weights = [&](auto all_seen) {
           uint32_t w[kPaTile / 2];
           const float2 by = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-m, -m);
           float2 sum = make_float2(0.f, 0.f);
+          // (the next chunk of scores is on its way while one is worked on)
+          uint32_t r[2][32];
+          tmem_ld32_issue(ts, r[0]);
+          tmem_ld_done<32>(r[0]);
 #pragma unroll
           for (int c = 0; c < kPaTile; c += 32) {
-            uint32_t r[32];
-            tmem_ld32_issue(ts + c, r);
-            tmem_ld_done<32>(r);
+            uint32_t(&a)[32] = r[(c / 32) & 1];
+            uint32_t(&b)[32] = r[(c / 32 + 1) & 1];
+            if (c + 32 < kPaTile) tmem_ld32_issue(ts + c + 32, b);
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-              const float2 d = ffma2(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), by, off);
-              const float2 e = make_float2(pa_exp2(d.x), pa_exp2(d.y));
+              const float2 d = ffma2(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])), by, off);
+              float2 e = make_float2(pa_exp2(d.x), pa_exp2(d.y));
+              if constexpr (!decltype(all_seen)::value) {
+                if (c + j > rel) e.x = 0.f;
+                if (c + j + 1 > rel) e.y = 0.f;
+              }
               sum = fadd2(sum, e);
               w[(c + j) / 2] = pa_pack<BF16>(e.x, e.y);
             }
+            if (c + 32 < kPaTile) tmem_ld_done<32>(b);
           }
           const float add = sum.x + sum.y;
-          slow = __any_sync(0xffffffffu, !(add <= kPaSumLimit));
-          grow = 0.f;
-          if (!slow) {
-            l += add;
+          const bool off_range = !(add <= kPaSumLimit) || (!has && rel >= 0 && !(add >= pa_first(BF16)));
+          if (__any_sync(0xffffffffu, mine && off_range)) return false;
+          l += add;
+          has |= rel >= 0;
 #pragma unroll
-            for (int c = 0; c < kPaTile / 2; c += 32) tmem_st32(ts + c, w + c);
+          for (int c = 0; c < kPaTile / 2; c += 32) tmem_st32(ts + c, w + c);
+          return true;
+        };
+        bool fine = true;
+        if (any) {
+          if (key0 > lim0 + 31) {                      // no row of the warp sees any of these keys
+            uint32_t zero[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) zero[j] = 0u;
+            tmem_st32(ts, zero);
+            tmem_st32(ts + 32, zero);
+          } else if (key0 + kPaTile - 1 <= lim0) {
+            fine = weights(std::true_type());
+          } else {
+            fine = weights(std::false_type());
           }
         }
-        if (slow) {
+        if (!fine) {
+          // the maximum, a reference that serves, and the weights against it.  Rare: small code, the scores read twice
           float top = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < kPaTile; c += 32) {
-            uint32_t r[32];
-            tmem_ld32_issue(ts + c, r);
-            tmem_ld_done<32>(r);
+          for (int c = 0; c < kPaTile; c += 16) {
+            uint32_t r[16];
+            tmem_ld16_issue(ts + c, r);
+            tmem_ld_done<16>(r);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {             // (masks after the scale, which may be 0 or negative)
+            for (int j = 0; j < 16; ++j) {             // (masks after the scale, which may be 0 or negative)
               const float d = fmaf(__uint_as_float(r[j]), p.scale_log2, -m);
-              top = fmaxf(top, key0 + c + j > lim ? -INFINITY : d);
+              top = fmaxf(top, c + j > rel ? -INFINITY : d);
             }
           }
           const float g = ceilf(top) - pa_top(BF16);
-          const bool raise = g > grow || (!has && g > -INFINITY);
-          // what that leaves of the sums so far: a first reference may lie far below 0, but they are 0 (or NaN) then
-          const float keep = raise && has ? pa_exp2(-g) : 1.f;
+          const bool move = has ? g > 0.f : g > -INFINITY;
+          // what that leaves of the sums so far: a first reference may lie far from 0, but they are 0 (or NaN) then
+          const float keep = move && has ? pa_exp2(-g) : 1.f;
           // (the distance to the old reference is taken first: a product with the scale may lie far beyond their difference)
-          const float by = raise ? g : 0.f;
+          const float by = move ? g : 0.f;
           l *= keep;
           if (i > 0 && __any_sync(0xffffffffu, keep != 1.f)) {     // (the first tile's products overwrite O)
 #pragma unroll 1
@@ -874,7 +906,7 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
               tmem_st16(to + c, o);
             }
           }
-          float s0 = 0.f, s1 = 0.f;
+          float add = 0.f;
 #pragma unroll 1
           for (int c = 0; c < kPaTile; c += 32) {      // (a chunk's weights take columns that are read already)
             uint32_t r[32], w[16];
@@ -884,22 +916,22 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
             for (int j = 0; j < 32; j += 2) {
               float d[2];
 #pragma unroll
-              for (int k = 0; k < 2; ++k)
-                d[k] = key0 + c + j + k > lim ? 0.f : pa_exp2(fmaf(__uint_as_float(r[j + k]), p.scale_log2, -m) - by);
-              s0 += d[0];
-              s1 += d[1];
+              for (int k = 0; k < 2; ++k) {
+                d[k] = c + j + k > rel ? 0.f : pa_exp2(fmaf(__uint_as_float(r[j + k]), p.scale_log2, -m) - by);
+                add += d[k];
+              }
               w[j / 2] = pa_pack<BF16>(d[0], d[1]);
             }
             tmem_st16(ts + c / 2, w);
           }
           m += by;
-          has |= raise;
-          l += s0 + s1;
+          has |= move;
+          l += add;
         }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_ready[x]);
+        if (lane == 0) cluster_arrive_tmem(ready);
       }
       // -------------------------------------------------------------- the unit's rows
       if (ok && n > 0) {
@@ -908,77 +940,103 @@ __global__ void __launch_bounds__(kPaThreads, 1) prompt_attention_kernel(const P
       }
       if (!ok) break;
       tc_fence_after();
-      const int slot = 2 * (int)blockIdx.x + (opening ? 0 : 1);
+      const size_t slot = pa_slot(blockIdx.x >> 1, opening ? 0 : 1, rank);
       const int masked = part.masked();
-      // values that were taken out of masked tiles (keys of this row tile only: the others' products come first)
+      // values that were taken out of masked tiles
       uint32_t any_bad = 0;
       for (int t = max(masked, t0); t < t0 + n; ++t)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) any_bad |= bad[uu & 3][t - masked][w];
+        for (int w = 0; w < 4; ++w) any_bad |= bad[0][uu & 3][t - masked][w] | bad[1][uu & 3][t - masked][w];
       float by = 1.f;
+      const size_t at_row = (size_t)(u.q0 + row) * p.H + u.h;
       if (whole) {
         by = l == 0.f ? 0.f : 1.0f / l;
-        if (mine && p.lse) p.lse[(size_t)(u.q0 + row) * p.H + u.h] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.693147180559945309f;
+        if (mine && p.lse) p.lse[at_row] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.693147180559945309f;
       } else if (mine) {
-        p.part_ml[(size_t)slot * kPaRows + in_unit] = make_float2(has || l != 0.f ? m : -INFINITY, l);
+        p.part_ml[slot * kPaCtaRows + in_cta] = make_float2(has || l != 0.f ? m : -INFINITY, l);
       }
-      uint16_t* out = p.out + ((size_t)(u.q0 + row) * p.H + u.h) * kPaV;
-      float* po = p.part + (size_t)slot * kPaPart;
+      uint8_t* out = reinterpret_cast<uint8_t*>(p.out + ((size_t)(u.q0 + part.row0 + warp_row) * p.H + u.h) * kPaV);   // the warp's first row
+      float* po = p.part + slot * kPaPart;
+      if (any) {
+        const int rows = min(32, part.rows - warp_row);
 #pragma unroll 1
-      for (int c = 0; c < kPaV; c += 32) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32_issue(to + c, o);
-          tmem_ld_done<32>(o);
-        } else {
+        for (int c = 0; c < kPaV; c += 64) {
+          uint32_t o[64];
+          if (n > 0) {
+            tmem_ld32_issue(to + c, o);
+            tmem_ld32_issue(to + c + 32, o + 32);
+            tmem_ld_done<64>(o);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
-        }
-        if (any_bad) {
+            for (int j = 0; j < 64; ++j) o[j] = 0u;
+          }
+          if (any_bad) {
 #pragma unroll 1
-          for (int e = (max(masked, t0) - masked) * 128; e < (t0 + n - masked) * 128; ++e) {
-            if (!((bad[uu & 3][e >> 7][(e >> 5) & 3] >> (e & 31)) & 1u)) continue;
-            const int key = masked * kPaTile + e;
-            if (!mine || key > lim) continue;
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + (u.k0 + (long long)key) * p.v_tok + u.h * p.v_head) + c;
+            for (int e = (max(masked, t0) - masked) * 128; e < (t0 + n - masked) * 128; ++e) {
+              const uint32_t word = bad[0][uu & 3][e >> 7][(e >> 5) & 3] | bad[1][uu & 3][e >> 7][(e >> 5) & 3];
+              if (!((word >> (e & 31)) & 1u)) continue;
+              const int key = masked * kPaTile + e;
+              if (!mine || key > lim) continue;
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + (u.k0 + (long long)key) * p.v_tok + u.h * p.v_head) + c;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const uint32_t b = v[j];
-              const float val = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
-              if (pa_not_finite<BF16>(b)) o[j] = __float_as_uint(__uint_as_float(o[j]) + val);
+              for (int j = 0; j < 64; ++j) {
+                const uint32_t b = v[j];
+                const float val = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
+                if (pa_not_finite<BF16>(b)) o[j] = __float_as_uint(__uint_as_float(o[j]) + val);
+              }
             }
           }
-        }
-        if (!mine) continue;
-        if (whole) {
+          if (whole) {
+            // eight rows of 128 bytes at a time by way of shared memory, so that a store covers whole lines (a row a lane:
+            // 32 lines a store, 8,000 cycles a unit)
+            uint8_t* mine8 = stage + (lane & 7) * 128;
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            uint32_t w[4];
+            for (int j = 0; j < 32; ++j)
+              o[j] = pa_pack<BF16>(__uint_as_float(o[2 * j]) * by, __uint_as_float(o[2 * j + 1]) * by);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pa_pack<BF16>(__uint_as_float(o[j + 2 * k]) * by, __uint_as_float(o[j + 2 * k + 1]) * by);
-            *reinterpret_cast<uint4*>(out + c + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int g = 0; g < 4; ++g) {
+              if ((lane >> 3) == g) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  *reinterpret_cast<uint4*>(mine8 + ((j ^ (lane & 7)) << 4)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int r = (lane >> 3) + 4 * k, j = lane & 7;
+                const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((j ^ r) << 4));
+                if (g * 8 + r < rows)
+                  *reinterpret_cast<uint4*>(out + (size_t)(g * 8 + r) * p.H * (kPaV * 2) + c * 2 + j * 16) = w;
+              }
+              __syncwarp();
+            }
+          } else if (n > 0 && mine) {
+#pragma unroll
+            for (int j = 0; j < 64; j += 4)
+              *reinterpret_cast<uint4*>(po + pa_part(in_cta, c + j)) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
-        } else if (n > 0) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<uint4*>(po + pa_part(in_unit, c + j)) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
         }
       }
       tc_fence_before();
       __syncwarp();                                    // (every lane has read `bad`)
       uu += part.all > 0;
-      if (lane == 0) *const_cast<volatile uint32_t*>(&done[warp]) = uu;
+      if (lane < 2) cluster_store(cluster_addr(&done[rank][warp], lane), uu);
     }
     if (!ok && lane == 0) fail_wait();
   }
   griddep_launch_dependents();                         // (earlier, the join's CTAs would take slots from the next call's)
   tc_fence_before();
   __syncthreads();
+  if (abort_flag) {
+    // copies may be on their way that no wait tells of: they end long before this does
+    const unsigned long long from = globaltimer();
+    while (globaltimer() - from < 1000000ull) {}
+  }
   if (threadIdx.x == 0) p.cta_status[blockIdx.x] = cta_status;
+  cluster_sync();                                      // the pair's products, copies and arrivals are over in both CTAs
   if (warp == kPaMma) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
 }
 
@@ -989,12 +1047,12 @@ constexpr int kPaJoinThreads = 256, kPaJoinCtas = 304;
 
 template <bool BF16>
 __global__ void __launch_bounds__(kPaJoinThreads) prompt_attention_join_kernel(const PaArgs p, int ctas) {
-  __shared__ int starts[kPaJoinThreads], warp_tot[32], total;        // first task of each CTA's join
+  __shared__ int starts[kPaJoinThreads], warp_tot[32], total;        // first task of each pair's join
   static_assert(kPaMaxCtas <= kPaJoinThreads, "a thread each");
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool listed = tid < ctas && p.joins[tid].parts > 0;
+  const bool listed = tid < ctas / 2 && p.joins[tid].parts > 0;
   const int bits = blockIdx.x == 0 && tid < ctas ? p.cta_status[tid] : 0;
   starts[tid] = block_exclusive_scan(listed ? (p.joins[tid].rows + 31) / 32 : 0, warp_tot, &total);
   if (blockIdx.x == 0) {
@@ -1004,7 +1062,7 @@ __global__ void __launch_bounds__(kPaJoinThreads) prompt_attention_join_kernel(c
   __syncthreads();
   const int n_tasks = total;
   for (int task = blockIdx.x; task < n_tasks; task += gridDim.x) {
-    int j = 0, h = kPaJoinThreads;                     // last CTA whose join starts at or before the task
+    int j = 0, h = kPaJoinThreads;                     // last pair whose join starts at or before the task
     while (h - j > 1) {
       const int mid = (j + h) >> 1;
       if (starts[mid] <= task) j = mid;
@@ -1013,22 +1071,23 @@ __global__ void __launch_bounds__(kPaJoinThreads) prompt_attention_join_kernel(c
     const PaJoin jn = p.joins[j];
     const int r = (task - starts[j]) * 32 + lane, c0 = warp * 16;
     if (r >= jn.rows) continue;
-    auto slot = [&](int i) { return (size_t)(i ? 2 * (jn.cta + i * jn.gang) : jn.slot); };
+    const int rank = (r >> 7) & 1, i_cta = (r >> 8) * kPaTile + (r & 127);
+    auto slot = [&](int i) { return pa_slot(jn.pair + i, i ? 0 : jn.which, rank); };
     float m = kPaLowest, l = 0.f;
 #pragma unroll 4
-    for (int i = 0; i < jn.parts; ++i) m = fmaxf(m, p.part_ml[slot(i) * kPaRows + r].x);
+    for (int i = 0; i < jn.parts; ++i) m = fmaxf(m, p.part_ml[slot(i) * kPaCtaRows + i_cta].x);
     float4 acc[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
     for (int i = 0; i < jn.parts; ++i) {
-      const float2 ml = p.part_ml[slot(i) * kPaRows + r];
+      const float2 ml = p.part_ml[slot(i) * kPaCtaRows + i_cta];
       const float* src = p.part + slot(i) * kPaPart;
       const float w = pa_exp2(ml.x - m);
       l += w * ml.y;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const float4 o = *reinterpret_cast<const float4*>(src + pa_part(r, c0 + 4 * c));
+        const float4 o = *reinterpret_cast<const float4*>(src + pa_part(i_cta, c0 + 4 * c));
         if (w != 0.f) {                                // (a part without keys has written no values)
           acc[c].x = fmaf(w, o.x, acc[c].x);
           acc[c].y = fmaf(w, o.y, acc[c].y);
@@ -1069,7 +1128,7 @@ static PaWs pa_ws() {
   w.cta_status = take(kPaMaxCtas * sizeof(int32_t));
   w.joins = take((size_t)kPaMaxCtas * sizeof(PaJoin));
   w.part = take((size_t)2 * kPaMaxCtas * kPaPart * sizeof(float));
-  w.part_ml = take((size_t)2 * kPaMaxCtas * kPaRows * sizeof(float2));
+  w.part_ml = take((size_t)2 * kPaMaxCtas * kPaCtaRows * sizeof(float2));
   w.total = off;
   return w;
 }
@@ -1090,7 +1149,7 @@ static CUresult pa_map_rope(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMa
                             long long rows, long long row_stride) {
   const cuuint64_t gdim[2] = {(cuuint64_t)COLI_PROMPT_ROTARY, (cuuint64_t)rows};
   const cuuint64_t gstr[1] = {(cuuint64_t)(rows > 1 ? row_stride : COLI_PROMPT_ROTARY) * 2};
-  const cuuint32_t bdim[2] = {64, (cuuint32_t)kPaTile};
+  const cuuint32_t bdim[2] = {64, (cuuint32_t)kPaTile / 2};
   const cuuint32_t es[2] = {1, 1};
   return encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
                 const_cast<void*>(base), gdim, gstr, bdim, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1099,7 +1158,6 @@ static CUresult pa_map_rope(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMa
 
 template <bool BF16>
 static cudaError_t pa_launch(const PaArgs& a, const PaMaps& maps, int ctas, int dev, cudaStream_t st) {
-  static_assert((size_t)(kPaMaxB + 1) * 16 + 1024 <= kPaSmem, "the plan's arrays");
   // once a device: setting it again costs as much as a tenth of a launch
   static std::atomic<bool> set[kPaMaxDevices];
   cudaError_t e = cudaSuccess;
@@ -1179,11 +1237,11 @@ coli_status colibri_prompt_attention(int dtype, int B, int n_tokens, int n_keys,
   const bool keys = n_keys > 0;
   if (r == CUDA_SUCCESS)
     r = pa_map(encode, &maps.k, bf16, keys ? k : q, COLI_PROMPT_KEY, H, keys ? k_head_stride : q_head_stride,
-               keys ? n_keys : 1, k_token_stride, kPaTile);
+               keys ? n_keys : 1, k_token_stride, kPaTile / 2);
   if (r == CUDA_SUCCESS) r = pa_map_rope(encode, &maps.r, bf16, keys ? k_rope : q, keys ? n_keys : 1, rope_stride);
   if (r == CUDA_SUCCESS)
     r = pa_map(encode, &maps.v, bf16, keys ? v : q, kPaV, H, keys ? v_head_stride : q_head_stride, keys ? n_keys : 1,
-               v_token_stride, kPaTile / 2);
+               v_token_stride, kPaTile);
   if (r != CUDA_SUCCESS) return fail(COLI_ECUDA, "prompt_attention: tensor map (%d)", (int)r);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PaArgs a;
@@ -1207,7 +1265,7 @@ coli_status colibri_prompt_attention(int dtype, int B, int n_tokens, int n_keys,
   const KvInject inject = kv_inject();
   a.wait_ns = inject.wait_ns;
   a.withhold = inject.flags & COLI_INJECT_WITHHOLD_STAGE ? 1 : 0;
-  const int ctas = sms < kPaMaxCtas ? sms : kPaMaxCtas;
+  const int ctas = (sms < kPaMaxCtas ? sms : kPaMaxCtas) & ~1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   ce = bf16 ? pa_launch<true>(a, maps, ctas, dev, st) : pa_launch<false>(a, maps, ctas, dev, st);
   return ce == cudaSuccess ? COLI_OK : cuda_fail(ce, "prompt_attention: launch");
