@@ -24,8 +24,9 @@
 // or those of its first keys to less than 2^-6 of the aim, are the scores read again, their maximum taken and the
 // reference (with the sum and O) moved.
 //
-// Work: units (512 rows of one head) with their key tiles, in the order request, head, rows, dealt in equal runs of key
-// tiles to the pairs.  A unit cut by a border leaves partial results in the workspace, which the join kernel adds up in
+// Work: units with their key tiles, dealt in equal runs of key tiles to the pairs.  A unit is 512 rows of one head, or, for
+// the last rows of a request where they are 256 at most, those of two heads, one to either row tile: with one row tile the
+// tensor cores would wait while its softmax runs.  A unit cut by a border leaves partial results in the workspace, which the join kernel adds up in
 // order.
 #include <atomic>
 #include <type_traits>
@@ -45,12 +46,12 @@ constexpr int kPaKeys3 = 3 * kPaKeyBox;            // a CTA's K and R of a tile
 constexpr int kPaStage = kPaKeys3 + kPaValues;     // its part of a key tile
 constexpr int kPaStages = 3;
 constexpr int kPaQBytes = 3 * kPaTile * 128;       // its part of a row tile's queries
-constexpr int kPaOutStage = 8 * 128;               // a softmax warp's place for results on their way out
+constexpr int kPaOutStage = 8 * 128;               // a warp's place for results on their way out
 constexpr int kPaSmWarps = 8;                      // softmax: warps 0..3 row tile 0, 4..7 row tile 1
-constexpr size_t kPaSmem = 2 * (size_t)kPaQBytes + (size_t)kPaStages * kPaStage + kPaSmWarps * kPaOutStage + 1024;
 constexpr int kPaLoader = 8, kPaMma = 9, kPaCheck = 10, kPaCheckWarps = 2;
 constexpr int kPaThreads = (kPaCheck + kPaCheckWarps) * 32;
-constexpr int kPaMasked = kPaRows / kPaTile + 1;   // tiles of a unit of which some row does not see some key, at most
+constexpr size_t kPaSmem = 2 * (size_t)kPaQBytes + (size_t)kPaStages * kPaStage + kPaSmWarps * kPaOutStage + 1024;
+constexpr int kPaMasked = 6;                       // key tiles of a unit of which some row does not see some key: 5, or 3 of two heads
 constexpr int kPaMaxCtas = 160;                    // CTAs the workspace has room for
 constexpr int kPaMaxB = 8192, kPaMaxH = 1024;
 constexpr int kPaMaxDevices = 64;
@@ -66,10 +67,10 @@ constexpr uint32_t kPaOCol = 256;                  // TMEM columns: S_0 0.., S_1
 // A unit cut by borders: its parts are those of pairs pair, pair + 1, ...
 struct __align__(16) PaJoin {
   int row0, rows;   // first row of the batch, rows
-  int h;
+  int h, heads;     // first head; 2: two heads of the same rows
   int pair, parts;
   int which;        // of the first pair's two partial results (the others': the first)
-  int pad[2];
+  int pad;
 };
 
 struct PaArgs {
@@ -94,7 +95,7 @@ struct PaMaps {
 };
 
 // Partial results: two a pair (of its run's first unit, of its last), a half in each CTA.  A CTA's row i is row
-// (i / 128) 256 + rank 128 + i % 128 of the unit.
+// rank 128 + i % 128 of row tile i / 128.
 __host__ __device__ constexpr size_t pa_slot(int pair, int which, int rank) { return ((size_t)pair * 2 + which) * 2 + rank; }
 // Place of row r and value c (a multiple of four) in one: neighbouring rows' four values lie together, as a warp's
 // threads hold them.
@@ -103,10 +104,13 @@ __host__ __device__ constexpr int pa_part(int r, int c) { return ((c >> 2) * kPa
 // ------------------------------------------------------------------ plan
 // Every CTA finds its pair's run of the work from the lengths.  A request's T new rows over L keys come in blocks of 512;
 // block j (1, 2, ...) sees keys up to its last row: max(1, a + 4 j) tiles with a = ceil((L - T) / 128), the last block all
-// of them.  Units are (request, head, block), block fastest: neighbouring pairs work on the same head's keys.
+// of them.  Units are (request, head, block), block fastest, so that neighbouring pairs work on the same head's keys; a last
+// block of at most 256 rows comes behind them, two heads a unit.
 // The code runs once a launch and what it costs is mostly fetching it: 32 bits, few divisions, each step written once.
 constexpr int kPaTilesPerBlock = kPaRows / kPaTile;
 __device__ __forceinline__ int pa_blocks(int T) { return (int)(((unsigned)T + kPaRows - 1) / kPaRows); }
+// blocks that units take head by head; 1 more where the last one goes by two heads
+__device__ __forceinline__ bool pa_short(int T) { return (unsigned)(T - 1) % kPaRows < (unsigned)kPaRows / 2; }
 __device__ __forceinline__ int pa_key_tiles(int keys) { return max(1, (keys + kPaTile - 1) >> 7); }
 // Tiles of the first n of nb blocks, saturating (a sum that does not fit 31 bits is refused).
 __device__ __forceinline__ unsigned pa_before(int T, int L, int nb, int n) {
@@ -129,7 +133,8 @@ struct PaCuts {
 };
 
 struct __align__(16) PaUnit {
-  int b, h, blk, nb;
+  int b, h, blk;
+  int nb;            // blocks that go head by head; block nb goes by two heads
   int q0, T, k0, L;
   int first;         // key tiles of the units before it
   int tiles;
@@ -142,15 +147,23 @@ struct PaRun {
 };
 
 __device__ __forceinline__ void pa_tiles(PaUnit& u) {
-  u.tiles = pa_key_tiles(u.blk + 1 == u.nb ? u.L : u.L - u.T + (u.blk + 1) * kPaRows);
+  const int rows = u.T - u.blk * kPaRows;              // of the request from the block's first on
+  u.tiles = pa_key_tiles(rows <= kPaRows ? u.L : u.L - rows + kPaRows);
 }
 // The unit after u (of the same or a later request; the caller has not reached the end of the work).
 __device__ __forceinline__ void pa_next(const PaArgs& p, PaUnit& u) {
   u.first += u.tiles;
-  if (++u.blk == u.nb) {
+  if (u.blk == u.nb) {
+    u.h += 2;
+  } else if (++u.blk == u.nb) {
     u.blk = 0;
-    if (++u.h == p.H) {
-      u.h = 0;
+    ++u.h;
+  }
+  if (u.h >= p.H) {
+    u.h = 0;
+    if (u.blk < u.nb && pa_short(u.T)) {
+      u.blk = u.nb;
+    } else {
       do {
         if (u.b + 1 >= p.B) return;
         ++u.b;
@@ -159,7 +172,8 @@ __device__ __forceinline__ void pa_next(const PaArgs& p, PaUnit& u) {
         u.k0 = p.k_start[u.b];
         u.L = p.k_start[u.b + 1] - u.k0;
       } while (u.T == 0);
-      u.nb = pa_blocks(u.T);
+      u.nb = pa_blocks(u.T) - (pa_short(u.T) ? 1 : 0);
+      u.blk = 0;
     }
   }
   pa_tiles(u);
@@ -167,22 +181,28 @@ __device__ __forceinline__ void pa_next(const PaArgs& p, PaUnit& u) {
 
 // What a part [t0, t1) of a unit is.
 struct PaPart {
-  int row0, rows;    // its first row of the request, its rows
+  bool two;          // row tile 1 has the rows of tile 0 and the next head
+  int heads;         // key tiles a step: 2 where there are two heads
+  int row0;          // its first row of the request
+  int rows[2];       // rows of either row tile
   int shift;         // the last key that row i of the request sees: shift + i
   int n[2];          // key tiles of row tile x in the part
   int all;           // the larger
-  __device__ __forceinline__ PaPart(const PaUnit& u, int t0, int t1) {
+  __device__ __forceinline__ PaPart(const PaUnit& u, int H, int t0, int t1) {
     row0 = u.blk * kPaRows;
-    rows = min(kPaRows, u.T - row0);
+    two = u.blk == u.nb;
     shift = u.L - u.T;
+    heads = two && u.h + 1 < H ? 2 : 1;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int r = min(2 * kPaTile, rows - x * 2 * kPaTile);
-      const int seen = r > 0 ? (shift + row0 + x * 2 * kPaTile + r + kPaTile - 1) >> 7 : 0;
+      const int from = row0 + (two ? 0 : x * 2 * kPaTile);
+      rows[x] = two && x >= heads ? 0 : max(0, min(2 * kPaTile, u.T - from));
+      const int seen = rows[x] > 0 ? (shift + from + rows[x] + kPaTile - 1) >> 7 : 0;
       n[x] = max(0, min(t1, seen) - t0);
     }
     all = max(n[0], n[1]);
   }
+  __device__ __forceinline__ int first_row(int x) const { return row0 + (two ? 0 : x * 2 * kPaTile); }
   // first tile of which some row does not see some key
   __device__ __forceinline__ int masked() const { return max(0, (shift + row0 + 1) >> 7); }
 };
@@ -200,6 +220,7 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
   bool wrong = false;
   unsigned sum = 0;
   int longest = 0;
+  unsigned by_head = 0;                                // of the request looked at last: tiles that go head by head
   auto tiles_of = [&](int b, int& q0, int& T, int& k0, int& L) {
     const int q1 = p.q_start[b + 1], k1 = p.k_start[b + 1];
     q0 = p.q_start[b];
@@ -210,8 +231,11 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
     }
     T = q1 - q0;
     L = k1 - k0;
-    const int nb = pa_blocks(T);
-    return (unsigned)min((unsigned long long)(T ? pa_before(T, L, nb, nb) : 0u) * p.H, 0x7fffffffull);
+    if (T == 0) return 0u;
+    const int nb = pa_blocks(T), shrt = pa_short(T) ? 1 : 0;
+    by_head = pa_before(T, L, nb, nb - shrt);
+    return (unsigned)min((unsigned long long)by_head * p.H + (shrt ? (unsigned long long)pa_key_tiles(L) * ((p.H + 1) >> 1) : 0ull),
+                         0x7fffffffull);
   };
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
@@ -265,19 +289,28 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
         rest -= t;
       }
       u.b = b;
-      u.nb = pa_blocks(u.T);
-      const int unit = (int)pa_before(u.T, u.L, u.nb, u.nb);
-      u.h = rest / unit;
-      rest -= u.h * unit;
-      int i = 0, n = u.nb;                             // last block with before(block) <= rest
+      const int blocks = pa_blocks(u.T), unit = (int)by_head;
+      u.nb = blocks - (pa_short(u.T) ? 1 : 0);
+      if (rest < unit * p.H) {                         // (the sum fits 31 bits)
+        u.h = rest / unit;
+        rest -= u.h * unit;
+        int i = 0, n = u.nb;                           // last block with before(block) <= rest
 #pragma unroll 1
-      while (n - i > 1) {
-        const int mid = (i + n) >> 1;
-        if ((int)pa_before(u.T, u.L, u.nb, mid) <= rest) i = mid;
-        else n = mid;
+        while (n - i > 1) {
+          const int mid = (i + n) >> 1;
+          if ((int)pa_before(u.T, u.L, blocks, mid) <= rest) i = mid;
+          else n = mid;
+        }
+        u.blk = i;
+        rest -= (int)pa_before(u.T, u.L, blocks, i);
+      } else {
+        rest -= unit * p.H;
+        const int tiles = pa_key_tiles(u.L);
+        u.blk = u.nb;
+        u.h = rest / tiles * 2;
+        rest -= (u.h >> 1) * tiles;
       }
-      u.blk = i;
-      u.first = x - rest + (int)pa_before(u.T, u.L, u.nb, i);
+      u.first = x - rest;
       pa_tiles(u);
       found = u;
     }
@@ -306,10 +339,11 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
     jn.row0 = u.q0 + u.blk * kPaRows;
     jn.rows = min(kPaRows, u.T - u.blk * kPaRows);
     jn.h = u.h;
+    jn.heads = u.blk == u.nb && u.h + 1 < p.H ? 2 : 1;
     jn.pair = pair - 1;
     jn.parts = m - (pair - 1);
     jn.which = cut(pair - 1) < u.first ? 1 : 0;
-    jn.pad[0] = jn.pad[1] = 0;
+    jn.pad = 0;
     p.joins[pair] = jn;
   }
   return r;
@@ -337,21 +371,33 @@ __device__ __forceinline__ void cluster_arrive_tmem(uint32_t bar) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// mbar_wait for arrivals of either CTA.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+// Wait for a phase, at most about limit_ns, suspended by the hardware meanwhile: twelve of the sixteen warps wait for most
+// of the time, and looks at the barrier would take issue slots from the softmax.  CLUSTER: for writes of either CTA.
+constexpr uint32_t kPaSuspendNs = 20000;
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
   unsigned long long t0 = 0;
   for (uint32_t it = 0;; ++it) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
+    if constexpr (CLUSTER)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(kPaSuspendNs)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(kPaSuspendNs)
+          : "memory");
     if (ok) return true;
     if (it == 0) t0 = globaltimer();
-    else if ((it & 63u) == 0 && globaltimer() - t0 > limit_ns) return false;
+    else if (globaltimer() - t0 > limit_ns) return false;
   }
 }
 
@@ -425,6 +471,9 @@ __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+constexpr int kPaChunk = 16;
+__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16_issue(taddr, r); }
+__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32_issue(taddr, r); }
 // registers -> 32 consecutive TMEM columns of this warp's 32 lanes
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -512,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, cta_status;
   // Keys of the masked tiles whose values are not all finite in the columns of either CTA, of four units; done: units whose
-  // output each softmax warp of either CTA has written.
+  // output each warp of either CTA has written.
   __shared__ uint32_t bad[2][4][kPaMasked][4], done[2][kPaSmWarps];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qsm = smem + kPaStages * kPaStage;
@@ -558,9 +607,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   griddep_wait();                                      // the launch may overlap the kernel before; its results not
-  const PaRun run = pa_plan(p);
-  if (threadIdx.x == 0) cta_status = run.status;
+  __shared__ PaUnit units[kPaThreads / 32];            // the unit that each warp is at (out of its registers)
+  int beg, end;
+  {
+    const PaRun run = pa_plan(p);
+    beg = run.beg;
+    end = run.end;
+    if (threadIdx.x == 0) cta_status = run.status;
+    if (lane == 0) units[warp] = run.unit0;
+  }
   __syncthreads();
+  PaUnit& u = units[warp];
+  auto next_unit = [&]() {
+    __syncwarp();
+    if (lane == 0) pa_next(p, u);
+    __syncwarp();
+  };
   auto fail_wait = [&]() {
     atomicOr(&cta_status, COLI_DEV_WAIT_TIMEOUT);
     atomicExch(&abort_flag, 1);
@@ -571,16 +633,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
     bool ok = true;
     unsigned tile = 0;                                 // key tiles begun
     int un[2] = {0, 0};                                // units whose queries are on their way
-    auto wait = [&](uint64_t* bar, unsigned phase) { ok = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.wait_ns)); };
-    PaUnit u = run.unit0;
-    for (int at = run.beg; ok && at < run.end; pa_next(p, u)) {
-      const int t0 = at - u.first, t1 = min(run.end - u.first, u.tiles);
+    auto wait = [&](uint64_t* bar, unsigned phase) { ok = __all_sync(0xffffffffu, pa_wait(bar, phase & 1, p.wait_ns)); };
+    for (int at = beg; ok && at < end; next_unit()) {
+      const int t0 = at - u.first, t1 = min(end - u.first, u.tiles);
       at = u.first + t1;
-      const PaPart part(u, t0, t1);
+      const PaPart part(u, p.H, t0, t1);
       if (part.all == 0) continue;
       const int masked = part.masked();
-      for (int t = t0; ok && t < t0 + part.all; ++t, ++tile) {
+      for (int i = 0; ok && i < part.all * part.heads; ++i, ++tile) {
         if (__any_sync(0xffffffffu, *abort_v)) { ok = false; break; }
+        const int t = t0 + (part.heads == 2 ? i >> 1 : i), head = u.h + (part.heads == 2 ? i & 1 : 0);
         const unsigned s = tile % kPaStages, use = tile / kPaStages;
         uint8_t* dst = smem + s * kPaStage;
         const int key = u.k0 + t * kPaTile;
@@ -589,12 +651,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
         if (lane == 0) {
           if (rank == 0) mbar_arrive_expect_tx(&k_full[s], (uint32_t)(2 * kPaKeys3));
           const uint32_t bar = cluster_addr(&k_full[s], 0);
-          tma_pair_3d(dst, &maps.k, 0, u.h, key + rank * 64, bar);
-          tma_pair_3d(dst + kPaKeyBox, &maps.k, 64, u.h, key + rank * 64, bar);
+          tma_pair_3d(dst, &maps.k, 0, head, key + rank * 64, bar);
+          tma_pair_3d(dst + kPaKeyBox, &maps.k, 64, head, key + rank * 64, bar);
           tma_pair_2d(dst + 2 * kPaKeyBox, &maps.r, 0, key + rank * 64, bar);
         }
         __syncwarp();
-        if (t == t0) {                                 // the queries: rows past the unit's last are other rows' or, behind
+        if (i == 0) {                                  // the queries: rows past the unit's last are other rows' or, behind
 #pragma unroll
           for (int x = 0; x < 2; ++x) {                // the tensor, zeros: computed, not written
             if (!ok || part.n[x] == 0) continue;
@@ -603,21 +665,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
             if (lane == 0) {
               if (rank == 0) mbar_arrive_expect_tx(&q_full[x], (uint32_t)(2 * kPaQBytes));
               const uint32_t bar = cluster_addr(&q_full[x], 0);
-              for (int i = 0; i < 3; ++i)
-                tma_pair_3d(qsm + x * kPaQBytes + i * (kPaTile * 128), &maps.q, i * 64, u.h,
-                            u.q0 + part.row0 + x * 2 * kPaTile + rank * kPaTile, bar);
+              for (int c = 0; c < 3; ++c)
+                tma_pair_3d(qsm + x * kPaQBytes + c * (kPaTile * 128), &maps.q, c * 64, u.h + (part.two ? x : 0),
+                            u.q0 + part.first_row(x) + rank * kPaTile, bar);
             }
             __syncwarp();
             ++un[x];
           }
-          if (ok && at < run.end && lane < 6) {        // and the next unit's on their way to L2
+          if (ok && at < end && lane < 6) {        // and the next unit's on their way to L2
             PaUnit w = u;
             pa_next(p, w);
-            tma_prefetch_3d(&maps.q, (lane % 3) * 64, w.h, w.q0 + w.blk * kPaRows + (lane / 3 * 2 + rank) * kPaTile);
+            const int x = lane / 3;
+            tma_prefetch_3d(&maps.q, (lane % 3) * 64, min(w.h + (w.blk == w.nb ? x : 0), p.H - 1),
+                            w.q0 + w.blk * kPaRows + ((w.blk == w.nb ? 0 : x * 2) + rank) * kPaTile);
           }
           __syncwarp();
         }
-        if (use > 0) wait(&v_empty[s], use - 1);
+        if (ok && use > 0) wait(&v_empty[s], use - 1);
         if (!ok) break;
         if (lane == 0) {
           uint32_t bar = cluster_addr(&v_full[s], 0);
@@ -628,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
           } else if (rank == 0) {
             mbar_arrive_expect_tx(&v_full[s], (uint32_t)(2 * kPaValues));
           }
-          tma_pair_3d(dst + kPaKeys3, &maps.v, rank * 64, u.h, key, bar);
+          tma_pair_3d(dst + kPaKeys3, &maps.v, rank * 64, head, key, bar);
         }
         __syncwarp();
       }
@@ -652,54 +716,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
       bool ok = true;
       unsigned tile = 0, un[2] = {0, 0}, it[2] = {0, 0}, checked = 0;      // checked: bit s: parity of v_ok[s]
       auto wait = [&](uint64_t* bar, unsigned phase) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, phase & 1, p.wait_ns));
+        ok = __all_sync(0xffffffffu, ok && pa_wait(bar, phase & 1, p.wait_ns));
         return ok;
       };
-      PaUnit u = run.unit0;
-      for (int at = run.beg; ok && at < run.end; pa_next(p, u)) {
-        const int t0 = at - u.first, t1 = min(run.end - u.first, u.tiles);
+            for (int at = beg; ok && at < end; next_unit()) {
+        const int t0 = at - u.first, t1 = min(end - u.first, u.tiles);
         at = u.first + t1;
-        const PaPart part(u, t0, t1);
+        const PaPart part(u, p.H, t0, t1);
         if (part.all == 0) continue;
-        const int masked = part.masked();
-        // S of row tile x and the part's key tile i in stage s
-        auto scores = [&](int x, int i, unsigned s) {
+        const int masked = part.masked(), heads = part.heads;
+        // S of row tile x and the part's step i; its keys are the ring's tile j
+        auto scores = [&](int x, int i, unsigned j) {
+          const unsigned s = j % kPaStages;
+          if (x == 0 || heads == 2 || i >= part.n[0]) {        // (else the keys of row tile 0: awaited)
+            if (!wait(&k_full[s], j / kPaStages)) return;
+          }
+          tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 3; ++c)
             pa_mma_ss(tmem + x * kPaTile, qd + (uint64_t)((x * kPaQBytes + c * (kPaTile * 128)) >> 4),
                       kd + (uint64_t)((s * kPaStage + c * kPaKeyBox) >> 4), idesc, c ? 1u : 0u);
           pa_commit(&s_full[x]);
           if (i + 1 == part.n[x]) pa_commit(&q_empty[x]);
+          if (heads == 2 || x == 1 || i >= part.n[1]) pa_commit(&k_empty[s]);      // (else row tile 1 is yet to read them)
         };
-        {
-          const unsigned s = tile % kPaStages;
-          if (!wait(&k_full[s], tile / kPaStages)) break;
-          tc_fence_after();
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || part.n[x] == 0 || !wait(&q_full[x], un[x])) continue;
-            ++un[x];
-            tc_fence_after();
-            scores(x, 0, s);
-          }
-          if (!ok) break;
-          pa_commit(&k_empty[s]);
+        for (int x = 0; x < 2; ++x) {
+          if (!ok || part.n[x] == 0 || !wait(&q_full[x], un[x])) continue;
+          scores(x, 0, tile + (heads == 2 ? x : 0));
         }
-        for (int i = 0; ok && i < part.all; ++i, ++tile) {
-          const unsigned s = tile % kPaStages, next = (tile + 1) % kPaStages;
-          // the values, or, where some row does not see some key, the values after their check.  (Every phase of a
-          // barrier is awaited or, v_full's of a checked tile, known to be over: a parity tells neighbours apart.)
-          if (t0 + i >= masked) {
-            ok = __all_sync(0xffffffffu, mbar_wait_cluster(&v_ok[s], (checked >> s) & 1, p.wait_ns));
-            checked ^= 1u << s;
-          } else {
-            wait(&v_full[s], tile / kPaStages);
-          }
-          if (!ok) break;
-          bool keys = false;                           // the next tile's keys are there
+        for (int i = 0; ok && i < part.all; ++i, tile += heads) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (!ok || i >= part.n[x]) continue;
+            const unsigned j = tile + (heads == 2 ? x : 0), s = j % kPaStages;
+            // the values, or, where some row does not see some key, the values after their check.  (Every phase of a
+            // barrier is awaited or, v_full's of a checked tile, known to be over: a parity tells neighbours apart.)
+            if (x == 0 || heads == 2 || i >= part.n[0]) {
+              if (t0 + i >= masked) {
+                ok = __all_sync(0xffffffffu, pa_wait<true>(&v_ok[s], (checked >> s) & 1, p.wait_ns));
+                checked ^= 1u << s;
+              } else {
+                wait(&v_full[s], j / kPaStages);
+              }
+            }
             if (!wait(&p_ready[x], it[x])) continue;
             ++it[x];
             tc_fence_after();
@@ -707,25 +767,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
             for (int c = 0; c < 2; ++c)
               pa_mma_ts(tmem + kPaOCol + x * kPaTile, tmem + x * kPaTile + c * 32,
                         vd + (uint64_t)((s * kPaStage + c * (kPaValues / 2)) >> 4), idesc_v, i || c ? 1u : 0u);
+            if (heads == 2 || x == 1 || i >= part.n[1]) pa_commit(&v_empty[s]);
             if (i + 1 < part.n[x]) {
-              if (!keys && !wait(&k_full[next], (tile + 1) / kPaStages)) continue;
-              keys = true;
-              tc_fence_after();
-              scores(x, i + 1, next);
+              scores(x, i + 1, j + heads);
             } else {
               pa_commit(&o_full[x]);
+              ++un[x];
             }
           }
-          if (!ok) break;
-          pa_commit(&v_empty[s]);
-          if (keys) pa_commit(&k_empty[next]);
         }
       }
       if (!ok && lane == 0) fail_wait();
       __syncwarp();
       // what was issued ends before tensor memory is freed, whichever role gave up
       pa_commit_here(&drained);
-      mbar_wait(&drained, 0, kWaitLimitNs);
+      pa_wait(&drained, 0, kWaitLimitNs);
     }
   } else if (warp >= kPaCheck) {
     // ---------------------------------------------------------------- check of the values of masked tiles
@@ -734,7 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
     // tiles that cross the diagonal are looked at, by either CTA in its columns.
     const int half = warp - kPaCheck;                  // of the tile's keys
     const volatile uint32_t* done_v = &done[0][0];
-    // the softmax warps have read what `bad` holds of four units before
+    // the warps that write the rows have read what `bad` holds of four units before
     auto free_again = [&](unsigned uu) {
       if (uu < 4) return true;
       const unsigned long long from = globaltimer();
@@ -744,17 +800,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
     };
     bool ok = true;
     unsigned tile = 0, checked = 0, uu = 0;
-    PaUnit u = run.unit0;
-    for (int at = run.beg; ok && at < run.end; pa_next(p, u)) {
-      const int t0 = at - u.first, t1 = min(run.end - u.first, u.tiles);
+    for (int at = beg; ok && at < end; next_unit()) {
+      const int t0 = at - u.first, t1 = min(end - u.first, u.tiles);
       at = u.first + t1;
-      const PaPart part(u, t0, t1);
+      const PaPart part(u, p.H, t0, t1);
       if (part.all == 0) continue;
       const int masked = part.masked();
       if (masked < t0 + part.all) ok = free_again(uu);
-      for (int i = max(0, masked - t0); ok && i < part.all; ++i) {
+      for (int i = max(0, masked - t0) * part.heads; ok && i < part.all * part.heads; ++i) {
         const unsigned s = (tile + i) % kPaStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&v_here[s], (checked >> s) & 1, p.wait_ns));
+        ok = __all_sync(0xffffffffu, pa_wait(&v_here[s], (checked >> s) & 1, p.wait_ns));
         checked ^= 1u << s;
         if (!ok) break;
         uint8_t* box = smem + s * kPaStage + kPaKeys3 + half * (kPaValues / 2);
@@ -781,7 +836,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
           }
         }
         if (lane < 4) {                                // two words into either CTA
-          uint32_t* at_word = &bad[rank][uu & 3][t0 + i - masked][half * 2 + (lane & 1)];
+          uint32_t* at_word = &bad[rank][uu & 3][(t0 - masked) * part.heads + i][half * 2 + (lane & 1)];
           cluster_store(cluster_addr(at_word, lane >> 1), (lane & 1) ? flags[1] : flags[0]);
         }
         fence_proxy_async_smem();
@@ -791,7 +846,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
           cluster_arrive(cluster_addr(&v_ok[s], 0));
         }
       }
-      tile += part.all;
+      tile += part.all * part.heads;
       ++uu;
     }
     if (!ok && lane == 0) fail_wait();
@@ -799,28 +854,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
     // ---------------------------------------------------------------- softmax and output
     const int x = warp >> 2, sp = warp & 3;            // row tile, TMEM sub-partition
     const uint32_t ts = tmem + ((uint32_t)(sp * 32) << 16) + (uint32_t)(x * kPaTile), to = ts + kPaOCol;
-    const int warp_row = x * 2 * kPaTile + rank * kPaTile + sp * 32, in_unit = warp_row + lane;    // of the unit's 512
-    const int in_cta = x * kPaTile + sp * 32 + lane;
+    const int warp_row = rank * kPaTile + sp * 32, in_tile = warp_row + lane;      // of the row tile's 256
     const uint32_t ready = cluster_addr(&p_ready[x], 0);
     uint8_t* stage = qsm + 2 * kPaQBytes + warp * kPaOutStage;
     unsigned it = 0, un = 0, uu = 0;
     bool ok = true;
-    PaUnit u = run.unit0;
-    for (int at = run.beg; at < run.end; pa_next(p, u)) {
-      const int t0 = at - u.first, t1 = min(run.end - u.first, u.tiles);
-      const bool opening = at == run.beg, whole = t0 == 0 && t1 == u.tiles;
+    for (int at = beg; ok && at < end; next_unit()) {
+      const int t0 = at - u.first, t1 = min(end - u.first, u.tiles);
+      const bool opening = at == beg, whole = t0 == 0 && t1 == u.tiles;
       at = u.first + t1;
-      const PaPart part(u, t0, t1);
+      const PaPart part(u, p.H, t0, t1);
       const int n = part.n[x];
-      const bool mine = in_unit < part.rows, any = warp_row < part.rows;       // rows past the last are not written
-      const int row = part.row0 + in_unit;             // of the request
-      const int lim = part.shift + min(row, u.T - 1);  // the last key it sees
-      const int lim0 = part.shift + part.row0 + warp_row;      // of the warp's first row
+      const bool mine = in_tile < part.rows[x], any = warp_row < part.rows[x];     // rows past the last are not written
+      const int lim = part.shift + min(part.first_row(x) + in_tile, u.T - 1);      // the last key this row sees
+      const int lim0 = part.shift + part.first_row(x) + warp_row;      // of the warp's first row
       float m = -pa_top(BF16), l = 0.f;                // reference, sum of the weights
       bool has = false;                                // the row has seen a key
 #pragma unroll 1
       for (int i = 0; i < n; ++i, ++it) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], it & 1, p.wait_ns));
+        ok = __all_sync(0xffffffffu, pa_wait(&s_full[x], it & 1, p.wait_ns));
         if (!ok) break;
         tc_fence_after();
         const int key0 = (t0 + i) * kPaTile, rel = lim - key0;       // the tile's columns up to rel are seen
@@ -830,16 +882,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
           const float2 by = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-m, -m);
           float2 sum = make_float2(0.f, 0.f);
           // (the next chunk of scores is on its way while one is worked on)
-          uint32_t r[2][32];
-          tmem_ld32_issue(ts, r[0]);
-          tmem_ld_done<32>(r[0]);
+          uint32_t r[2][kPaChunk];
+          tmem_ld_chunk(ts, r[0]);
+          tmem_ld_done<kPaChunk>(r[0]);
 #pragma unroll
-          for (int c = 0; c < kPaTile; c += 32) {
-            uint32_t(&a)[32] = r[(c / 32) & 1];
-            uint32_t(&b)[32] = r[(c / 32 + 1) & 1];
-            if (c + 32 < kPaTile) tmem_ld32_issue(ts + c + 32, b);
+          for (int c = 0; c < kPaTile; c += kPaChunk) {
+            uint32_t(&a)[kPaChunk] = r[(c / kPaChunk) & 1];
+            uint32_t(&b)[kPaChunk] = r[(c / kPaChunk + 1) & 1];
+            if (c + kPaChunk < kPaTile) tmem_ld_chunk(ts + c + kPaChunk, b);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
+            for (int j = 0; j < kPaChunk; j += 2) {
               const float2 d = ffma2(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])), by, off);
               float2 e = make_float2(pa_exp2(d.x), pa_exp2(d.y));
               if constexpr (!decltype(all_seen)::value) {
@@ -849,7 +901,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
               sum = fadd2(sum, e);
               w[(c + j) / 2] = pa_pack<BF16>(e.x, e.y);
             }
-            if (c + 32 < kPaTile) tmem_ld_done<32>(b);
+            if (c + kPaChunk < kPaTile) tmem_ld_done<kPaChunk>(b);
           }
           const float add = sum.x + sum.y;
           const bool off_range = !(add <= kPaSumLimit) || (!has && rel >= 0 && !(add >= pa_first(BF16)));
@@ -935,30 +987,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
       }
       // -------------------------------------------------------------- the unit's rows
       if (ok && n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], un & 1, p.wait_ns));
+        ok = __all_sync(0xffffffffu, pa_wait(&o_full[x], un & 1, p.wait_ns));
         ++un;
       }
       if (!ok) break;
       tc_fence_after();
-      const size_t slot = pa_slot(blockIdx.x >> 1, opening ? 0 : 1, rank);
-      const int masked = part.masked();
-      // values that were taken out of masked tiles
-      uint32_t any_bad = 0;
-      for (int t = max(masked, t0); t < t0 + n; ++t)
+      const int masked = part.masked(), head = u.h + (part.two ? x : 0), row = part.first_row(x) + in_tile;
+      if (masked < t0 + n) {
+        // values that were taken out of masked tiles are added to the rows that see them (rare: small code)
+        const int e0 = max(masked, t0) - masked, e1 = t0 + n - masked, step = part.heads, mine_of = part.two ? x : 0;
+        uint32_t any_bad = 0;
+        for (int e = e0; e < e1; ++e)
+          any_bad |= bad[lane >> 2 & 1][uu & 3][e * step + mine_of][lane & 3];
+        if (__any_sync(0xffffffffu, any_bad != 0)) {
+#pragma unroll 1
+          for (int e = e0 * 128; e < e1 * 128; ++e) {
+            const int w = (e >> 7) * step + mine_of;
+            const uint32_t word = bad[0][uu & 3][w][(e >> 5) & 3] | bad[1][uu & 3][w][(e >> 5) & 3];
+            if (!((word >> (e & 31)) & 1u)) continue;
+            const int key = masked * kPaTile + e;
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + (u.k0 + (long long)key) * p.v_tok + head * p.v_head);
+#pragma unroll 1
+            for (int c = 0; c < kPaV; c += 16) {
+              uint32_t o[16];
+              tmem_ld16_issue(to + c, o);
+              tmem_ld_done<16>(o);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) any_bad |= bad[0][uu & 3][t - masked][w] | bad[1][uu & 3][t - masked][w];
-      float by = 1.f;
-      const size_t at_row = (size_t)(u.q0 + row) * p.H + u.h;
-      if (whole) {
-        by = l == 0.f ? 0.f : 1.0f / l;
-        if (mine && p.lse) p.lse[at_row] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.693147180559945309f;
-      } else if (mine) {
-        p.part_ml[slot * kPaCtaRows + in_cta] = make_float2(has || l != 0.f ? m : -INFINITY, l);
+              for (int j = 0; j < 16; ++j) {
+                const uint32_t b = v[c + j];
+                const float val = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
+                if (pa_not_finite<BF16>(b) && key <= lim) o[j] = __float_as_uint(__uint_as_float(o[j]) + val);
+              }
+              tmem_st16(to + c, o);
+              tmem_st_wait();
+            }
+          }
+        }
       }
-      uint8_t* out = reinterpret_cast<uint8_t*>(p.out + ((size_t)(u.q0 + part.row0 + warp_row) * p.H + u.h) * kPaV);   // the warp's first row
-      float* po = p.part + slot * kPaPart;
       if (any) {
-        const int rows = min(32, part.rows - warp_row);
+        const float by = l == 0.f ? 0.f : 1.0f / l;
+        const size_t slot = pa_slot(blockIdx.x >> 1, opening ? 0 : 1, rank);
+        const int in_cta = x * kPaTile + sp * 32 + lane;
+        if (whole) {
+          if (mine && p.lse)
+            p.lse[(size_t)(u.q0 + row) * p.H + head] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.693147180559945309f;
+        } else if (mine) {
+          p.part_ml[slot * kPaCtaRows + in_cta] = make_float2(has || l != 0.f ? m : -INFINITY, l);
+        }
+        const int rows = part.rows[x] - warp_row;
+        uint8_t* out = reinterpret_cast<uint8_t*>(p.out + ((size_t)(u.q0 + row - lane) * p.H + head) * kPaV);    // the warp's first row
+        float* po = p.part + slot * kPaPart;
 #pragma unroll 1
         for (int c = 0; c < kPaV; c += 64) {
           uint32_t o[64];
@@ -970,25 +1048,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
 #pragma unroll
             for (int j = 0; j < 64; ++j) o[j] = 0u;
           }
-          if (any_bad) {
-#pragma unroll 1
-            for (int e = (max(masked, t0) - masked) * 128; e < (t0 + n - masked) * 128; ++e) {
-              const uint32_t word = bad[0][uu & 3][e >> 7][(e >> 5) & 3] | bad[1][uu & 3][e >> 7][(e >> 5) & 3];
-              if (!((word >> (e & 31)) & 1u)) continue;
-              const int key = masked * kPaTile + e;
-              if (!mine || key > lim) continue;
-              const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + (u.k0 + (long long)key) * p.v_tok + u.h * p.v_head) + c;
-#pragma unroll
-              for (int j = 0; j < 64; ++j) {
-                const uint32_t b = v[j];
-                const float val = BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
-                if (pa_not_finite<BF16>(b)) o[j] = __float_as_uint(__uint_as_float(o[j]) + val);
-              }
-            }
-          }
           if (whole) {
             // eight rows of 128 bytes at a time by way of shared memory, so that a store covers whole lines (a row a lane:
-            // 32 lines a store, 8,000 cycles a unit)
+            // 32 lines a store)
             uint8_t* mine8 = stage + (lane & 7) * 128;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -1054,7 +1116,7 @@ __global__ void __launch_bounds__(kPaJoinThreads) prompt_attention_join_kernel(c
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool listed = tid < ctas / 2 && p.joins[tid].parts > 0;
   const int bits = blockIdx.x == 0 && tid < ctas ? p.cta_status[tid] : 0;
-  starts[tid] = block_exclusive_scan(listed ? (p.joins[tid].rows + 31) / 32 : 0, warp_tot, &total);
+  starts[tid] = block_exclusive_scan(listed ? (p.joins[tid].rows + 31) / 32 * p.joins[tid].heads : 0, warp_tot, &total);
   if (blockIdx.x == 0) {
     const int timed = __syncthreads_or(bits & COLI_DEV_WAIT_TIMEOUT), order = __syncthreads_or(bits & COLI_DEV_KV_TOKENS);
     if (tid == 0) *p.status = (timed ? COLI_DEV_WAIT_TIMEOUT : 0) | (order ? COLI_DEV_KV_TOKENS : 0);
@@ -1069,9 +1131,10 @@ __global__ void __launch_bounds__(kPaJoinThreads) prompt_attention_join_kernel(c
       else h = mid;
     }
     const PaJoin jn = p.joins[j];
-    const int r = (task - starts[j]) * 32 + lane, c0 = warp * 16;
+    const int per = (jn.rows + 31) / 32, sub = task - starts[j], second = jn.heads == 2 && sub >= per ? 1 : 0;
+    const int r = (sub - second * per) * 32 + lane, c0 = warp * 16;        // (a second head's rows are row tile 1's)
     if (r >= jn.rows) continue;
-    const int rank = (r >> 7) & 1, i_cta = (r >> 8) * kPaTile + (r & 127);
+    const int rank = (r >> 7) & 1, i_cta = ((r >> 8) + second) * kPaTile + (r & 127);
     auto slot = [&](int i) { return pa_slot(jn.pair + i, i ? 0 : jn.which, rank); };
     float m = kPaLowest, l = 0.f;
 #pragma unroll 4
@@ -1097,7 +1160,7 @@ __global__ void __launch_bounds__(kPaJoinThreads) prompt_attention_join_kernel(c
       }
     }
     const float by = l == 0.f ? 0.f : 1.0f / l;
-    const size_t row = (size_t)(jn.row0 + r) * p.H + jn.h;
+    const size_t row = (size_t)(jn.row0 + r) * p.H + jn.h + second;
     if (p.lse && warp == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 #pragma unroll
     for (int c = 0; c < 4; c += 2) {
