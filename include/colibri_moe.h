@@ -618,7 +618,8 @@ COLI_API coli_status colibri_kv_check_status(const void* workspace, int32_t* dev
 /*
  * Failure-path testing of colibri_kv_attention and colibri_prompt_attention, for
  * the following calls of this thread.  flags: 0 (off) or COLI_INJECT_WITHHOLD_STAGE, with which the first
- * CTA's first key rows never count as there, so that the roles waiting for them
+ * CTA's first key rows (colibri_prompt_attention: every pair of CTAs') never
+ * count as there, so that the roles waiting for them
  * reach the wait limit, record COLI_DEV_WAIT_TIMEOUT, let their copies and products
  * end, free tensor memory and return.  wait_limit_ms as for
  * colibri_moe_debug_inject, at most the default.  The outputs of an injected

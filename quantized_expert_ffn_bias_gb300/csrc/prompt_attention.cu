@@ -50,7 +50,8 @@ constexpr int kPaOutStage = 8 * 128;               // a warp's place for results
 constexpr int kPaSmWarps = 8;                      // softmax: warps 0..3 row tile 0, 4..7 row tile 1
 constexpr int kPaLoader = 8, kPaMma = 9, kPaCheck = 10, kPaCheckWarps = 2;
 constexpr int kPaThreads = (kPaCheck + kPaCheckWarps) * 32;
-constexpr size_t kPaSmem = 2 * (size_t)kPaQBytes + (size_t)kPaStages * kPaStage + kPaSmWarps * kPaOutStage + 1024;
+constexpr size_t kPaSmem = 2 * (size_t)kPaQBytes + (size_t)kPaStages * kPaStage + kPaSmWarps * kPaOutStage;
+static_assert(kPaSmem + 3072 <= 232448, "with the kernel's own arrays");
 constexpr int kPaMasked = 6;                       // key tiles of a unit of which some row does not see some key: 5, or 3 of two heads
 constexpr int kPaMaxCtas = 160;                    // CTAs the workspace has room for
 constexpr int kPaMaxB = 8192, kPaMaxH = 1024;
@@ -87,7 +88,7 @@ struct PaArgs {
   float* part;                       // [2 kPaMaxCtas] partial O (pa_slot, pa_part)
   float2* part_ml;                   // [2 kPaMaxCtas][256] reference, sum
   unsigned long long wait_ns;
-  int withhold;                      // failure-path test: 1: the first pair's first keys never count as there
+  int withhold;                      // failure-path test: 1: no pair's first keys ever count as there
 };
 
 struct PaMaps {
@@ -106,20 +107,23 @@ __host__ __device__ constexpr int pa_part(int r, int c) { return ((c >> 2) * kPa
 // block j (1, 2, ...) sees keys up to its last row: max(1, a + 4 j) tiles with a = ceil((L - T) / 128), the last block all
 // of them.  Units are (request, head, block), block fastest, so that neighbouring pairs work on the same head's keys; a last
 // block of at most 256 rows comes behind them, two heads a unit.
+// What a unit costs beside its tiles (its rows' way out, the first softmax: about 9,000 cycles, a tile 3,100) is dealt with
+// them: a unit's places are kPaUnitCost and then its tiles; a border among the first is one before its first tile.
 // The code runs once a launch and what it costs is mostly fetching it: 32 bits, few divisions, each step written once.
+constexpr int kPaUnitCost = 3;
 constexpr int kPaTilesPerBlock = kPaRows / kPaTile;
 __device__ __forceinline__ int pa_blocks(int T) { return (int)(((unsigned)T + kPaRows - 1) / kPaRows); }
 // blocks that units take head by head; 1 more where the last one goes by two heads
 __device__ __forceinline__ bool pa_short(int T) { return (unsigned)(T - 1) % kPaRows < (unsigned)kPaRows / 2; }
 __device__ __forceinline__ int pa_key_tiles(int keys) { return max(1, (keys + kPaTile - 1) >> 7); }
-// Tiles of the first n of nb blocks, saturating (a sum that does not fit 31 bits is refused).
+// Places of the first n of nb blocks, saturating (a sum that does not fit 31 bits is refused).
 __device__ __forceinline__ unsigned pa_before(int T, int L, int nb, int n) {
   const int a = (L - T + kPaTile - 1) >> 7;
   const int m = min(n, nb - 1);
   const int flat = a < 0 ? min(m, -a / kPaTilesPerBlock) : 0;        // blocks whose rows see nothing: one tile each
   const long long s = flat + (long long)(m - flat) * a +
                       (long long)(kPaTilesPerBlock / 2) * ((long long)m * (m + 1) - (long long)flat * (flat + 1)) +
-                      (n == nb ? pa_key_tiles(L) : 0);
+                      (n == nb ? pa_key_tiles(L) : 0) + (long long)kPaUnitCost * n;
   return (unsigned)min(s, 0x7fffffffll);
 }
 
@@ -136,8 +140,11 @@ struct __align__(16) PaUnit {
   int b, h, blk;
   int nb;            // blocks that go head by head; block nb goes by two heads
   int q0, T, k0, L;
-  int first;         // key tiles of the units before it
+  int first;         // places of the units before it
   int tiles;
+  // The tiles of it between two borders.
+  __device__ __forceinline__ int from(int beg) const { return max(0, beg - first - kPaUnitCost); }
+  __device__ __forceinline__ int to(int end) const { return min(end - first - kPaUnitCost, tiles); }
 };
 
 struct PaRun {
@@ -152,7 +159,7 @@ __device__ __forceinline__ void pa_tiles(PaUnit& u) {
 }
 // The unit after u (of the same or a later request; the caller has not reached the end of the work).
 __device__ __forceinline__ void pa_next(const PaArgs& p, PaUnit& u) {
-  u.first += u.tiles;
+  u.first += kPaUnitCost + u.tiles;
   if (u.blk == u.nb) {
     u.h += 2;
   } else if (++u.blk == u.nb) {
@@ -220,7 +227,7 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
   bool wrong = false;
   unsigned sum = 0;
   int longest = 0;
-  unsigned by_head = 0;                                // of the request looked at last: tiles that go head by head
+  unsigned by_head = 0;                                // of the request looked at last: a head's places
   auto tiles_of = [&](int b, int& q0, int& T, int& k0, int& L) {
     const int q1 = p.q_start[b + 1], k1 = p.k_start[b + 1];
     q0 = p.q_start[b];
@@ -234,7 +241,7 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
     if (T == 0) return 0u;
     const int nb = pa_blocks(T), shrt = pa_short(T) ? 1 : 0;
     by_head = pa_before(T, L, nb, nb - shrt);
-    return (unsigned)min((unsigned long long)by_head * p.H + (shrt ? (unsigned long long)pa_key_tiles(L) * ((p.H + 1) >> 1) : 0ull),
+    return (unsigned)min((unsigned long long)by_head * p.H + (shrt ? (unsigned long long)(kPaUnitCost + pa_key_tiles(L)) * ((p.H + 1) >> 1) : 0ull),
                          0x7fffffffull);
   };
 #pragma unroll 1
@@ -276,7 +283,7 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
   const PaCuts cut(W, G);
   r.beg = cut(pair);
   r.end = cut(pair + 1);
-  // the unit of tile x, found by the thread whose requests hold it
+  // the unit of place x, found by the thread whose requests hold it
   auto locate = [&](int x) {
     __syncthreads();
     if (x >= (int)base && x < (int)(base + sum)) {
@@ -305,7 +312,7 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
         rest -= (int)pa_before(u.T, u.L, blocks, i);
       } else {
         rest -= unit * p.H;
-        const int tiles = pa_key_tiles(u.L);
+        const int tiles = kPaUnitCost + pa_key_tiles(u.L);
         u.blk = u.nb;
         u.h = rest / tiles * 2;
         rest -= (u.h >> 1) * tiles;
@@ -320,21 +327,21 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
   r.unit0 = locate(r.beg);                             // (its barriers make s_longest known, too)
   if (s_longest <= kPaWhole) {
     // short units are not cut: a run takes those that begin in it
-    if (r.unit0.first < r.beg) {
-      r.beg = r.unit0.first + r.unit0.tiles;
+    if (r.unit0.from(r.beg) > 0) {
+      r.beg = r.unit0.first + kPaUnitCost + r.unit0.tiles;
       pa_next(p, r.unit0);
     }
     if (r.end < W) {
       const PaUnit u = locate(r.end);
-      if (u.first < r.end) r.end = u.first + u.tiles;
+      if (u.from(r.end) > 0) r.end = u.first + kPaUnitCost + u.tiles;
     }
     return r;
   }
   // a run that begins with the first border inside its unit lists the join
   const PaUnit& u = r.unit0;
-  if ((blockIdx.x & 1) == 0 && tid == 0 && pair > 0 && u.first < r.beg && cut(pair - 1) <= u.first) {
+  if ((blockIdx.x & 1) == 0 && tid == 0 && pair > 0 && u.from(r.beg) > 0 && u.from(cut(pair - 1)) == 0) {
     int m = pair;
-    while (m < G && cut(m) < u.first + u.tiles) ++m;   // runs pair - 1 .. m - 1 begin before the unit's end
+    while (m < G && cut(m) < u.first + kPaUnitCost + u.tiles) ++m;     // runs pair - 1 .. m - 1 begin before the unit's end
     PaJoin jn;
     jn.row0 = u.q0 + u.blk * kPaRows;
     jn.rows = min(kPaRows, u.T - u.blk * kPaRows);
@@ -560,10 +567,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
   __shared__ uint64_t q_empty[2], k_empty[kPaStages], v_empty[kPaStages], s_full[2], o_full[2], v_here[kPaStages], drained;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag, cta_status;
-  // Keys of the masked tiles whose values are not all finite in the columns of either CTA, of four units; done: units whose
-  // output each warp of either CTA has written.
-  __shared__ uint32_t bad[2][4][kPaMasked][4], done[2][kPaSmWarps];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // Keys (bits of two words, for either half) of the masked tiles whose values are not all finite in the columns of either
+  // CTA, of four units, written only where there are any: the third word then is the unit's number plus one.  done: units
+  // whose output each warp of either CTA has written.
+  __shared__ uint32_t bad[2][4][kPaMasked][2][3], done[2][kPaSmWarps];
+  uint8_t* smem = smem_raw;                            // (aligned as declared: the kernel's own arrays fill whole KB)
   uint8_t* qsm = smem + kPaStages * kPaStage;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x & 1;                     // of this CTA in its pair (clusters are two neighbouring blocks)
@@ -578,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
       mbar_init(&o_full[x], 1);
     }
     for (int i = 0; i < kPaStages; ++i) {
-      mbar_init(&k_full[i], 1 + (i == 0 && blockIdx.x == 0 ? p.withhold : 0));     // (an arrival too many for a withheld stage)
+      mbar_init(&k_full[i], 1 + (i == 0 ? p.withhold : 0));     // (an arrival too many for a withheld stage)
       mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
@@ -587,6 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
     }
     mbar_init(&drained, 1);
     for (int i = 0; i < 2 * kPaSmWarps; ++i) done[i / kPaSmWarps][i % kPaSmWarps] = 0;
+    for (int i = 0; i < 2 * 4 * kPaMasked * 2; ++i) (&bad[0][0][0][0][0])[i * 3 + 2] = 0;
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -635,8 +644,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
     int un[2] = {0, 0};                                // units whose queries are on their way
     auto wait = [&](uint64_t* bar, unsigned phase) { ok = __all_sync(0xffffffffu, pa_wait(bar, phase & 1, p.wait_ns)); };
     for (int at = beg; ok && at < end; next_unit()) {
-      const int t0 = at - u.first, t1 = min(end - u.first, u.tiles);
-      at = u.first + t1;
+      const int t0 = u.from(at), t1 = u.to(end);
+      at = u.first + kPaUnitCost + u.tiles;
+      if (t1 <= 0) break;                              // (the border lies before its first tile)
       const PaPart part(u, p.H, t0, t1);
       if (part.all == 0) continue;
       const int masked = part.masked();
@@ -720,8 +730,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
         return ok;
       };
             for (int at = beg; ok && at < end; next_unit()) {
-        const int t0 = at - u.first, t1 = min(end - u.first, u.tiles);
-        at = u.first + t1;
+        const int t0 = u.from(at), t1 = u.to(end);
+        at = u.first + kPaUnitCost + u.tiles;
+      if (t1 <= 0) break;                              // (the border lies before its first tile)
         const PaPart part(u, p.H, t0, t1);
         if (part.all == 0) continue;
         const int masked = part.masked(), heads = part.heads;
@@ -801,12 +812,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
     bool ok = true;
     unsigned tile = 0, checked = 0, uu = 0;
     for (int at = beg; ok && at < end; next_unit()) {
-      const int t0 = at - u.first, t1 = min(end - u.first, u.tiles);
-      at = u.first + t1;
+      const int t0 = u.from(at), t1 = u.to(end);
+      at = u.first + kPaUnitCost + u.tiles;
+      if (t1 <= 0) break;                              // (the border lies before its first tile)
       const PaPart part(u, p.H, t0, t1);
       if (part.all == 0) continue;
       const int masked = part.masked();
-      if (masked < t0 + part.all) ok = free_again(uu);
       for (int i = max(0, masked - t0) * part.heads; ok && i < part.all * part.heads; ++i) {
         const unsigned s = (tile + i) % kPaStages;
         ok = __all_sync(0xffffffffu, pa_wait(&v_here[s], (checked >> s) & 1, p.wait_ns));
@@ -835,15 +846,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
             }
           }
         }
-        if (lane < 4) {                                // two words into either CTA
-          uint32_t* at_word = &bad[rank][uu & 3][(t0 - masked) * part.heads + i][half * 2 + (lane & 1)];
-          cluster_store(cluster_addr(at_word, lane >> 1), (lane & 1) ? flags[1] : flags[0]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
+        if (flags[0] | flags[1]) {
+          ok = free_again(uu);
+          if (!ok) break;
+          if (lane < 6) {                              // three words into either CTA
+            const int w = lane % 3;
+            cluster_store(cluster_addr(&bad[rank][uu & 3][(t0 - masked) * part.heads + i][half][w], lane / 3),
+                          w == 2 ? uu + 1 : w == 1 ? flags[1] : flags[0]);
+          }
+          fence_proxy_async_smem();
           asm volatile("fence.acq_rel.cluster;" ::: "memory");
-          cluster_arrive(cluster_addr(&v_ok[s], 0));
+          __syncwarp();
+          if (lane == 0) cluster_arrive(cluster_addr(&v_ok[s], 0));
+        } else if (lane == 0) {                        // (nothing was written)
+          cluster_arrive_tmem(cluster_addr(&v_ok[s], 0));
         }
       }
       tile += part.all * part.heads;
@@ -860,9 +876,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
     unsigned it = 0, un = 0, uu = 0;
     bool ok = true;
     for (int at = beg; ok && at < end; next_unit()) {
-      const int t0 = at - u.first, t1 = min(end - u.first, u.tiles);
+      const int t0 = u.from(at), t1 = u.to(end);
       const bool opening = at == beg, whole = t0 == 0 && t1 == u.tiles;
-      at = u.first + t1;
+      at = u.first + kPaUnitCost + u.tiles;
+      if (t1 <= 0) break;                              // (the border lies before its first tile)
       const PaPart part(u, p.H, t0, t1);
       const int n = part.n[x];
       const bool mine = in_tile < part.rows[x], any = warp_row < part.rows[x];     // rows past the last are not written
@@ -998,12 +1015,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
         const int e0 = max(masked, t0) - masked, e1 = t0 + n - masked, step = part.heads, mine_of = part.two ? x : 0;
         uint32_t any_bad = 0;
         for (int e = e0; e < e1; ++e)
-          any_bad |= bad[lane >> 2 & 1][uu & 3][e * step + mine_of][lane & 3];
+          any_bad |= bad[lane & 1][uu & 3][e * step + mine_of][lane >> 1 & 1][2] == uu + 1;
         if (__any_sync(0xffffffffu, any_bad != 0)) {
 #pragma unroll 1
           for (int e = e0 * 128; e < e1 * 128; ++e) {
             const int w = (e >> 7) * step + mine_of;
-            const uint32_t word = bad[0][uu & 3][w][(e >> 5) & 3] | bad[1][uu & 3][w][(e >> 5) & 3];
+            uint32_t word = 0;
+            for (int src = 0; src < 2; ++src) {
+              const uint32_t* b = bad[src][uu & 3][w][(e >> 6) & 1];
+              if (b[2] == uu + 1) word |= b[(e >> 5) & 1];
+            }
             if (!((word >> (e & 31)) & 1u)) continue;
             const int key = masked * kPaTile + e;
             const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + (u.k0 + (long long)key) * p.v_tok + head * p.v_head);
@@ -1105,18 +1126,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
 // ------------------------------------------------------------------ join
 // Adds up the parts of every cut unit, in order.  A task is 32 rows of a unit (a row a lane, 16 values a warp).
 constexpr float kPaLowest = -3.402823466e38f;      // below every reference; a part whose row saw no key has -infinity
-constexpr int kPaJoinThreads = 256, kPaJoinCtas = 304;
+constexpr int kPaJoinThreads = 256, kPaJoinCtas = 608, kPaAhead = 3;
 
 template <bool BF16>
 __global__ void __launch_bounds__(kPaJoinThreads) prompt_attention_join_kernel(const PaArgs p, int ctas) {
   __shared__ int starts[kPaJoinThreads], warp_tot[32], total;        // first task of each pair's join
+  __shared__ PaJoin joins[kPaMaxCtas / 2];
   static_assert(kPaMaxCtas <= kPaJoinThreads, "a thread each");
   griddep_launch_dependents();
   griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool listed = tid < ctas / 2 && p.joins[tid].parts > 0;
+  int tasks = 0;
+  if (tid < ctas / 2) {
+    const PaJoin jn = p.joins[tid];
+    joins[tid] = jn;
+    if (jn.parts > 0) tasks = (jn.rows + 31) / 32 * jn.heads;
+  }
   const int bits = blockIdx.x == 0 && tid < ctas ? p.cta_status[tid] : 0;
-  starts[tid] = block_exclusive_scan(listed ? (p.joins[tid].rows + 31) / 32 * p.joins[tid].heads : 0, warp_tot, &total);
+  starts[tid] = block_exclusive_scan(tasks, warp_tot, &total);
   if (blockIdx.x == 0) {
     const int timed = __syncthreads_or(bits & COLI_DEV_WAIT_TIMEOUT), order = __syncthreads_or(bits & COLI_DEV_KV_TOKENS);
     if (tid == 0) *p.status = (timed ? COLI_DEV_WAIT_TIMEOUT : 0) | (order ? COLI_DEV_KV_TOKENS : 0);
@@ -1130,32 +1157,49 @@ __global__ void __launch_bounds__(kPaJoinThreads) prompt_attention_join_kernel(c
       if (starts[mid] <= task) j = mid;
       else h = mid;
     }
-    const PaJoin jn = p.joins[j];
-    const int per = (jn.rows + 31) / 32, sub = task - starts[j], second = jn.heads == 2 && sub >= per ? 1 : 0;
+    const PaJoin& jn = joins[j];
+    const int n = jn.parts, per = (jn.rows + 31) / 32, sub = task - starts[j], second = jn.heads == 2 && sub >= per ? 1 : 0;
     const int r = (sub - second * per) * 32 + lane, c0 = warp * 16;        // (a second head's rows are row tile 1's)
     if (r >= jn.rows) continue;
     const int rank = (r >> 7) & 1, i_cta = ((r >> 8) + second) * kPaTile + (r & 127);
-    auto slot = [&](int i) { return pa_slot(jn.pair + i, i ? 0 : jn.which, rank); };
     float m = kPaLowest, l = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < jn.parts; ++i) m = fmaxf(m, p.part_ml[slot(i) * kPaCtaRows + i_cta].x);
     float4 acc[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int i = 0; i < jn.parts; ++i) {
-      const float2 ml = p.part_ml[slot(i) * kPaCtaRows + i_cta];
-      const float* src = p.part + slot(i) * kPaPart;
-      const float w = pa_exp2(ml.x - m);
-      l += w * ml.y;
+    // three parts at a time, all of their loads in flight at once, against a maximum that grows
+    for (int i0 = 0; i0 < n; i0 += kPaAhead) {
+      float2 ml[kPaAhead];
+      float4 o[kPaAhead][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float4 o = *reinterpret_cast<const float4*>(src + pa_part(i_cta, c0 + 4 * c));
+      for (int k = 0; k < kPaAhead; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (i0 + k < n) {
+          const size_t slot = pa_slot(jn.pair + i0 + k, i0 + k ? 0 : jn.which, rank);
+          ml[k] = p.part_ml[slot * kPaCtaRows + i_cta];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[k][c] = *reinterpret_cast<const float4*>(p.part + slot * kPaPart + pa_part(i_cta, c0 + 4 * c));
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < kPaAhead; ++k) top = fmaxf(top, ml[k].x);
+      const float keep = pa_exp2(m - top);
+      m = top;
+      l *= keep;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c] = make_float4(acc[c].x * keep, acc[c].y * keep, acc[c].z * keep, acc[c].w * keep);
+#pragma unroll
+      for (int k = 0; k < kPaAhead; ++k) {
+        const float w = pa_exp2(ml[k].x - m);
+        l += w * ml[k].y;
         if (w != 0.f) {                                // (a part without keys has written no values)
-          acc[c].x = fmaf(w, o.x, acc[c].x);
-          acc[c].y = fmaf(w, o.y, acc[c].y);
-          acc[c].z = fmaf(w, o.z, acc[c].z);
-          acc[c].w = fmaf(w, o.w, acc[c].w);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            acc[c].x = fmaf(w, o[k][c].x, acc[c].x);
+            acc[c].y = fmaf(w, o[k][c].y, acc[c].y);
+            acc[c].z = fmaf(w, o[k][c].z, acc[c].z);
+            acc[c].w = fmaf(w, o[k][c].w, acc[c].w);
+          }
         }
       }
     }
@@ -1231,7 +1275,10 @@ static cudaError_t pa_launch(const PaArgs& a, const PaMaps& maps, int ctas, int 
   }
   e = launch_pdl(prompt_attention_kernel<BF16>, dim3(ctas), dim3(kPaThreads), kPaSmem, st, a, maps);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prompt_attention_join_kernel<BF16>, dim3(kPaJoinCtas), dim3(kPaJoinThreads), 0, st, a, ctas);
+  // no more CTAs than there can be tasks
+  const long long tasks = (long long)a.n_tokens * a.H / 32 + ctas;
+  return launch_pdl(prompt_attention_join_kernel<BF16>, dim3(tasks < kPaJoinCtas ? (int)tasks : kPaJoinCtas),
+                    dim3(kPaJoinThreads), 0, st, a, ctas);
 }
 
 }  // namespace coli
