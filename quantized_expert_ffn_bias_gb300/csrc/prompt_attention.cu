@@ -21,7 +21,7 @@
 //
 // Softmax: per row a reference m (log2 units, a whole number; at first that of scores near 0).  A tile takes its weights
 // against the reference as it is, without looking for the largest score; only where a row's weights sum to more than 2^15,
-// or those of its first keys to less than 2^-6 of the aim, are the scores read again, their maximum taken and the
+// or those of its first keys to less than 2^-6 (fp16: 32, so that weights down to 2^-29 of the sum count), are the scores read again, their maximum taken and the
 // reference (with the sum and O) moved.
 //
 // Work: units with their key tiles, dealt in equal runs of key tiles to the pairs.  A unit is 512 rows of one head, or, for
@@ -62,7 +62,7 @@ constexpr int kPaPart = kPaCtaRows * kPaV;         // floats of a CTA's partial 
 constexpr float kPaGrow = 8.f;
 __host__ __device__ constexpr float pa_top(bool bf16) { return bf16 ? 0.f : 7.f; }
 constexpr float kPaSumLimit = 32768.f;             // a row's weights of a tile sum to at most this,
-__host__ __device__ constexpr float pa_first(bool bf16) { return bf16 ? 1.f / 64 : 2.f; }   // those of its first keys to at least this
+__host__ __device__ constexpr float pa_first(bool bf16) { return bf16 ? 1.f / 64 : 32.f; }   // those of its first keys to at least this
 constexpr uint32_t kPaOCol = 256;                  // TMEM columns: S_0 0.., S_1 128.., O_0 256.., O_1 384..
 
 // A unit cut by borders: its parts are those of pairs pair, pair + 1, ...

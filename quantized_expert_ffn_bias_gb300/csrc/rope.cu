@@ -83,9 +83,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
   constexpr int kPairs = WIDE && !HALF ? kV / 2 : kV;      // pairs of a piece
   const int tid = threadIdx.x;
   const int tok0 = blockIdx.x * p.tokens, head0 = blockIdx.y * p.heads;
-  const int n = p.n_valid ? min(p.n, *p.n_valid) : p.n;
-  const int tokens = min(p.tokens, n - tok0), heads = min(p.heads, p.H - head0);
-  if (tokens <= 0) return;
+  const int tokens = min(p.tokens, p.n - tok0), heads = min(p.heads, p.H - head0);
+  const int valid = p.n_valid ? *p.n_valid - tok0 : tokens;          // (awaited where the results are written)
   const int items = p.tokens * p.heads * p.pieces;
   const T* x = reinterpret_cast<const T*>(p.x);
   T* out = reinterpret_cast<T*>(p.out);
@@ -129,7 +128,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
     }
 #pragma unroll
     for (int k = 0; k < kRopeItems; ++k) {
-      if (tok[k] < 0) continue;
+      if (tok[k] < 0 || tok[k] >= valid) continue;
       const float2* w = turn + tok[k] * p.pairs + pair[k];
       T* dst = out + at[k];
       if constexpr (!WIDE) {
@@ -181,9 +180,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
 }
 
 // ------------------------------------------------------------------ append with norm and rotation
-// A warp takes four rows, all of whose loads are in flight before the first sum; a lane holds 16 of a row's latent values
-// and one pair of its rotary ones.
-constexpr int kArWarps = 8, kArRows = 4;
+// A warp takes a row: a lane holds 16 of its latent values and one pair of its rotary ones.  Nothing waits for *n_valid,
+// slots or positions before the row's loads are in flight.  A copy in its traffic (75.8 MB for 32768 rows: 18.0 us; four rows
+// a warp: 19.1, two: 18.6, and 192 rows 4.2 and 3.3 in place of 2.8).
+constexpr int kArWarps = 8;
 static_assert(COLI_KV_VALUE == 32 * 16 && COLI_KV_ROTARY == 64, "16 values and a pair a lane");
 
 struct AppendRopeArgs {
@@ -202,72 +202,65 @@ struct AppendRopeArgs {
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kArWarps * 32) kv_append_rope_kernel(const AppendRopeArgs p) {
   const int lane = threadIdx.x & 31;
-  const int row0 = (blockIdx.x * kArWarps + (threadIdx.x >> 5)) * kArRows;
-  const int n = p.n_valid ? min(p.n, *p.n_valid) : p.n;
-  if (row0 >= n) return;
-  // lanes 0..3: where the rows go (-1: nowhere), their positions
-  long long to = -1;
-  int pos = 0;
-  if (lane < kArRows && row0 + lane < n) {
-    const int s = p.slot[row0 + lane], page = p.by_page(max(s, 0));
-    pos = p.position[row0 + lane];
-    if (s >= 0 && page < p.n_pages) to = page * p.page_stride + (long long)(s - page * p.page_size) * COLI_KV_WIDTH;
-  }
-  uint4 v[kArRows][2];
-  uint32_t rot[kArRows];
-#pragma unroll
-  for (int r = 0; r < kArRows; ++r) {
-    v[r][0] = v[r][1] = make_uint4(0, 0, 0, 0);
-    rot[r] = 0;
-    if (row0 + r < n) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.latent + (row0 + r) * p.latent_stride);
-      v[r][0] = src[lane];
-      v[r][1] = src[32 + lane];
-      const uint16_t* rs = p.rope + (row0 + r) * p.rope_stride;
-      rot[r] = HALF ? (uint32_t)rs[lane] | ((uint32_t)rs[lane + 32] << 16) : *reinterpret_cast<const uint32_t*>(rs + 2 * lane);
-    }
-  }
+  const int row = blockIdx.x * kArWarps + (threadIdx.x >> 5);
+  if (row >= p.n) return;
+  const uint4* src = reinterpret_cast<const uint4*>(p.latent + row * p.latent_stride);
+  uint4 v[2] = {src[lane], src[32 + lane]};
+  const uint16_t* rs = p.rope + row * p.rope_stride;
+  const uint32_t rot = HALF ? (uint32_t)rs[lane] | ((uint32_t)rs[lane + 32] << 16) : *reinterpret_cast<const uint32_t*>(rs + 2 * lane);
+  const int slot = p.slot[row], position = p.position[row];
   const unsigned long long freq = p.freq[lane];
-  float g[16];
+  const int page = p.by_page(max(slot, 0));
+  if ((p.n_valid && row >= *p.n_valid) || slot < 0 || page >= p.n_pages) return;       // (the same in every lane)
+  uint16_t* dst = p.cache + page * p.page_stride + (long long)(slot - page * p.page_size) * COLI_KV_WIDTH;
   if (p.gain) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4*>(g + 4 * i) = *reinterpret_cast<const float4*>(p.gain + (i >> 1) * 256 + lane * 8 + (i & 1) * 4);
-  }
-#pragma unroll
-  for (int r = 0; r < kArRows; ++r) {
-    const long long at = __shfl_sync(0xffffffffu, to, r);
-    const int position = __shfl_sync(0xffffffffu, pos, r);
-    if (at < 0) continue;
-    uint16_t* dst = p.cache + at;
-    if (p.gain) {
-      uint32_t* w = &v[r][0].x;
+    uint32_t* w = &v[0].x;
+    auto squares = [&](float s) {                      // sum of the row's (s x)^2
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 f = rope_unpack<T>(w[i]);
-        sum = fmaf(f.x, f.x, fmaf(f.y, f.y, sum));
+        sum = fmaf(f.x * s, f.x * s, fmaf(f.y * s, f.y * s, sum));
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float by = 1.0f / sqrtf(sum * (1.0f / COLI_KV_VALUE) + p.eps);
+      return sum * (1.0f / COLI_KV_VALUE);
+    };
+    float s = 1.f, mean = squares(1.f) + p.eps;
+    if (!(mean > 1e-30f && mean < 1e36f)) {
+      // squares that leave fp32's range: the row times a power of two near 1 / its largest value (not so large that eps,
+      // which then decides, would overflow)
+      float top = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 f = rope_unpack<T>(w[i]);
-        w[i] = rope_pack<T>(f.x * by * g[2 * i], f.y * by * g[2 * i + 1]);
+        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = (int)(__float_as_uint(top) >> 23) - 127;
+      s = __uint_as_float((uint32_t)(max(-126, min(-e, p.eps > 0.f ? 60 : 126)) + 127) << 23);
+      mean = squares(s) + p.eps * s * s;
     }
-    reinterpret_cast<uint4*>(dst)[lane] = v[r][0];
-    reinterpret_cast<uint4*>(dst)[32 + lane] = v[r][1];
-    const float2 f = rope_unpack<T>(rot[r]);
-    const float2 z = rope_rotate(f.x, f.y, rope_turn(position, freq, p.amplitude));
-    const uint32_t two = rope_pack<T>(z.x, z.y);
-    if (HALF) {
-      dst[COLI_KV_VALUE + lane] = (uint16_t)two;
-      dst[COLI_KV_VALUE + 32 + lane] = (uint16_t)(two >> 16);
-    } else {
-      *reinterpret_cast<uint32_t*>(dst + COLI_KV_VALUE + 2 * lane) = two;
+    const float by = 1.0f / sqrtf(mean);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 g = *reinterpret_cast<const float4*>(p.gain + (i >> 1) * 256 + lane * 8 + (i & 1) * 4);
+      const float2 a = rope_unpack<T>(w[2 * i]), b = rope_unpack<T>(w[2 * i + 1]);
+      w[2 * i] = rope_pack<T>(a.x * s * by * g.x, a.y * s * by * g.y);
+      w[2 * i + 1] = rope_pack<T>(b.x * s * by * g.z, b.y * s * by * g.w);
     }
+  }
+  reinterpret_cast<uint4*>(dst)[lane] = v[0];
+  reinterpret_cast<uint4*>(dst)[32 + lane] = v[1];
+  const float2 f = rope_unpack<T>(rot);
+  const float2 z = rope_rotate(f.x, f.y, rope_turn(position, freq, p.amplitude));
+  const uint32_t two = rope_pack<T>(z.x, z.y);
+  if (HALF) {
+    dst[COLI_KV_VALUE + lane] = (uint16_t)two;
+    dst[COLI_KV_VALUE + 32 + lane] = (uint16_t)(two >> 16);
+  } else {
+    *reinterpret_cast<uint32_t*>(dst + COLI_KV_VALUE + 2 * lane) = two;
   }
 }
 
@@ -423,8 +416,7 @@ coli_status colibri_kv_append_rope(const coli_kv_desc* desc, const coli_rope_des
   a.rope_stride = rope_stride;
   a.gain = gain;
   a.cache = static_cast<uint16_t*>(cache);
-  constexpr int kRows = kArWarps * kArRows;
-  const int grid = n_tokens / kRows + (n_tokens % kRows ? 1 : 0);
+  const int grid = n_tokens / kArWarps + (n_tokens % kArWarps ? 1 : 0);
   const bool half = rope_desc->layout == COLI_ROPE_HALF, bf16 = desc->dtype == COLI_X_BF16;
   auto k = bf16 ? (half ? kv_append_rope_kernel<__nv_bfloat16, true> : kv_append_rope_kernel<__nv_bfloat16, false>)
                 : (half ? kv_append_rope_kernel<__half, true> : kv_append_rope_kernel<__half, false>);

@@ -185,6 +185,28 @@ def test_append_rope_of_layers_that_interleave(torch):
     assert torch.equal(both[:, 1], alone) and not both[:, 0].any()
 
 
+@pytest.mark.parametrize("dtype,sizes,eps", [("bf16", (1e-38, 3e-30, 1e-16, 1e15, 1e19, 2e36), 0.0), ("bf16", (1e-38, 1e-20, 1e19, 1e36), 1e-6),
+                                             ("bf16", (1e-30, 1e-17, 1e-10), 1e-33), ("f16", (6e-8, 1e-4, 6e4), 0.0)])
+def test_append_rope_norm_of_any_size(torch, dtype, sizes, eps):
+    """Rows whose squares leave fp32's range have their norm all the same; a row of zeros stays one where eps is not 0."""
+    import quantized_expert_ffn_bias_gb300 as coli
+    from tests import prompt_ref as R
+    t, n = dt(torch, dtype), len(sizes)
+    c = append_case(torch, dtype, n + 1, 16, "half", True, 3)
+    unit = torch.rand((n, V), generator=gen(torch, 4), device="cuda") * 0.9 + 0.1
+    wide = torch.zeros((n + 1, V), device="cuda")
+    wide[:n] = unit * torch.tensor(sizes, device="cuda")[:, None] if max(sizes) < 1e30 else (unit.double() * torch.tensor(sizes, device="cuda", dtype=torch.float64)[:, None]).float()
+    c["latent"] = wide.to(t)
+    rd = rope_desc(64, "half")
+    cache = c["cache"].clone()
+    call_append(c, coli.coli_kv_desc(16, 1, c["n_pages"], TYPES[dtype], 16 * W), rd, rope_table(torch, rd), n + 1, None, eps, cache)
+    torch.cuda.synchronize()
+    got = cache.view(-1, W)[c["slot"].long(), :V]
+    ref = R.norm(c["latent"].double(), c["gain"].double(), eps)
+    within(torch, got[:n], ref[:n], R.norm_bound(ref[:n], t), "latent")
+    assert torch.isnan(got[n]).all() if eps == 0 else (got[n] == 0).all()
+
+
 # ---------------------------------------------------------------- gather
 
 
@@ -519,3 +541,88 @@ def test_prompt_wait_that_runs_out(torch):
     torch.cuda.synchronize()
     assert coli.colibri_kv_check_status(again[2]) == 0
     assert torch.equal(good[0], again[0])
+
+
+# ---------------------------------------------------------------- together
+
+
+def test_prompt_steps_together(torch):
+    """Prompts, chunks behind them and a finished request through bookkeeping, appending, gathering, the up-projection, the queries'
+    rotation and both forms of attention, everything on one stream with lengths that live on the GPU."""
+    import quantized_expert_ffn_bias_gb300 as coli
+    from tests import prompt_ref as R
+    t, page, H, B, eps = torch.float16, 16, 4, 3, 1e-6
+    max_pages, n_pages, g = 40, 90, gen(torch, 1)
+    kd = coli.coli_kv_desc(page, max_pages, n_pages, coli.COLI_X_F16, page * W)
+    rd = rope_desc(ROT, "interleaved", "yarn")
+    freq, f = rope_table(torch, rd), R.frequencies(ROT, "yarn")
+    cache = torch.zeros((n_pages, page, W), dtype=t, device="cuda")
+    table, free = ints(torch, np.full((B, max_pages), -1)), ints(torch, np.arange(n_pages))
+    seq, held, count, status = ints(torch, [0] * B), ints(torch, [0] * B), ints(torch, [n_pages]), ints(torch, [0])
+    gain = 1 + 0.2 * torch.randn(V, generator=g, device="cuda")
+    up_k = (torch.randn((H, 128, V), generator=g, device="cuda") / V ** 0.5).to(t)
+    up_v = (torch.randn((H, 128, V), generator=g, device="cuda") / V ** 0.5).to(t)
+    scale = 192 ** -0.5
+    lens = [0] * B
+    for new in ([40, 7, 300], [60, 1, 33], [-1, 5, 0], [9, 0, 260]):
+        add = [max(v, 0) for v in new]
+        n = sum(add)
+        lens = [0 if v < 0 else x + v for x, v in zip(lens, new)]
+        m = sum(lens)
+        q_start, pos, slot = ints(torch, [0] * (B + 1)), ints(torch, [0] * n), ints(torch, [-1] * n)
+        coli.colibri_kv_step(kd, B, n, ints(torch, new), seq, held, table, free, count, seq, held, count, q_start, pos, slot, status)
+        raw = (torch.randn((n, W), generator=g, device="cuda") * 2).to(t)
+        coli.colibri_kv_append_rope(kd, rd, n, q_start[B:], raw, W, gain, eps, raw[:, V:], W, pos, freq, slot, cache)
+        k_start = ints(torch, [0] * (B + 1))
+        latent, rope = torch.zeros((m, V), dtype=t, device="cuda"), torch.zeros((m, ROT), dtype=t, device="cuda")
+        coli.colibri_kv_gather(kd, B, m, seq, table, cache, k_start, latent, V, rope, ROT, status)
+        k = torch.einsum("mv,hdv->mhd", latent.double(), up_k.double()).to(t)
+        v = torch.einsum("mv,hdv->mhd", latent.double(), up_v.double()).to(t)
+        q_raw = torch.randn((n, H, 192), generator=g, device="cuda").to(t)
+        q = q_raw.clone()
+        coli.colibri_rope(rd, coli.COLI_X_F16, n, q_start[B:], H, pos, freq, q[..., 128:], H * 192, 192, q[..., 128:], H * 192, 192)
+        c = dict(new=add, seq=lens, H=H, dtype="f16", n=n, m=m, scale=scale, q=q, k=k, v=v, r=rope)
+        out, lse, ws, _ = call_prompt(torch, c, q_start=q_start, k_start=k_start)
+        absorbed = torch.cat([torch.einsum("nhd,hdv->nhv", q[..., :128].double(), up_k.double()).to(t), q[..., 128:]], 2).contiguous()
+        out2 = torch.zeros((n, H, V), dtype=t, device="cuda")
+        need = coli.colibri_kv_attention_workspace_size(B, n, H)
+        ws2 = torch.zeros(need, dtype=torch.uint8, device="cuda")
+        coli.colibri_kv_attention(kd, B, n, H, scale, absorbed, H * W, W, cache, table, q_start, seq, None, 0, out2, None, ws2, need)
+        torch.cuda.synchronize()
+        assert int(status) == 0 and coli.colibri_kv_check_status(ws) == 0 and coli.colibri_kv_check_status(ws2) == 0
+        np.testing.assert_array_equal(seq.cpu().numpy(), lens)
+        np.testing.assert_array_equal(q_start.cpu().numpy(), np.concatenate([[0], np.cumsum(add)]))
+        np.testing.assert_array_equal(k_start.cpu().numpy(), np.concatenate([[0], np.cumsum(lens)]))
+        want_pos = np.concatenate([np.arange(x - a, x) for x, a in zip(lens, add)])
+        np.testing.assert_array_equal(pos.cpu().numpy(), want_pos)
+        # the new rows, as they came out of the cache
+        at = torch.tensor(np.concatenate([s0 + np.arange(x - a, x) for s0, x, a in zip(np.cumsum([0] + lens), lens, add)]).astype(np.int64), device="cuda")
+        ref = R.norm(raw[:, :V].double(), gain.double(), eps)
+        within(torch, latent[at], ref, R.norm_bound(ref, t), "latent")
+        ref, size = R.rotate(raw[:, V:].double(), pos, f, "interleaved")
+        within(torch, rope[at], ref, R.rotate_bound(ref, size, t) + size * 2.0 ** -40, "rotary keys")
+        ref, size = R.rotate(q_raw[..., 128:].double(), pos, f, "interleaved")
+        within(torch, q[..., 128:], ref, R.rotate_bound(ref, size, t) + size * 2.0 ** -40, "queries")
+        assert torch.equal(q[..., :128], q_raw[..., :128])
+        ref, ref_lse, tol, tol_lse = reference(c)
+        within(torch, out, ref, tol, "attention")
+        within(torch, lse, ref_lse, tol_lse, "lse")
+        # the absorbed form: the same weights up to the rounding of k (there of the absorbed query), which moves a score by
+        # ds = 2^-11 scale (sum |q||k| + sum |q'||latent|), a weight by 2 ds; v and the latent result are rounded once each,
+        # and weights in both (2^-11): all of sum p |v|, but the latent result's rounding, which the projection carries on
+        lat, n0, m0 = latent.double(), 0, 0
+        other = torch.einsum("nhv,hdv->nhd", out2.double(), up_v.double())
+        carried = 2.0 ** -11 * torch.einsum("nhv,hdv->nhd", out2.double().abs(), up_v.double().abs())
+        for a, x in zip(add, lens):
+            for h in range(H):
+                if not a:
+                    continue
+                rows, keys = slice(n0, n0 + a), slice(m0, m0 + x)
+                kk, vv = k[keys, h].double(), v[keys, h].double()
+                seen = torch.arange(x, device="cuda")[None] <= torch.arange(x - a, x, device="cuda")[:, None]
+                s = torch.where(seen, (q[rows, h, :128].double() @ kk.T + q[rows, h, 128:].double() @ rope[keys].double().T) * scale, -math.inf)
+                ds = 2.0 ** -11 * scale * (q[rows, h, :128].double().abs() @ kk.abs().T + absorbed[rows, h, :V].double().abs() @ lat[keys].abs().T).amax(1)
+                big = torch.softmax(s, 1) @ vv.abs()
+                bound = 1.1 * ((4 * ds[:, None] + 4 * 2.0 ** -11 + 2.0 ** -14) * big + carried[rows, h]) + tol[rows, h]
+                within(torch, other[rows, h], out[rows, h].double(), bound, "both forms")
+            n0, m0 = n0 + a, m0 + x
