@@ -617,11 +617,11 @@ COLI_API coli_status colibri_kv_attention(const coli_kv_desc* desc, int B, int n
 COLI_API coli_status colibri_kv_check_status(const void* workspace, int32_t* device_status, void* stream);
 /*
  * Failure-path testing of colibri_kv_attention and colibri_prompt_attention, for
- * the following calls of this thread.  flags: 0 (off) or COLI_INJECT_WITHHOLD_STAGE, with which the first
- * CTA's first key rows (colibri_prompt_attention: every pair of CTAs') never
- * count as there, so that the roles waiting for them
- * reach the wait limit, record COLI_DEV_WAIT_TIMEOUT, let their copies and products
- * end, free tensor memory and return.  wait_limit_ms as for
+ * the following calls of this thread.  flags: 0 (off) or
+ * COLI_INJECT_WITHHOLD_STAGE, with which the first CTA's first key rows
+ * (colibri_prompt_attention: every pair of CTAs') never count as there, so that
+ * the roles waiting for them reach the wait limit, record COLI_DEV_WAIT_TIMEOUT,
+ * let their copies and products end, free tensor memory and return.  wait_limit_ms as for
  * colibri_moe_debug_inject, at most the default.  The outputs of an injected
  * call are not meaningful; the next call without injection, also on the same
  * workspace, is a normal one.  Errors: COLI_EINVAL.
@@ -763,7 +763,9 @@ COLI_API coli_status colibri_kv_gather(const coli_kv_desc* desc, int B, int n_ro
  * A row that sees no key gets 0 and lse -infinity.  Rows outside
  * [q_start[0], q_start[B]) are left as they were.  Keys and values that a row
  * does not see do not reach its output, whatever values (infinities, NaN) they
- * hold.  Softmax and sums in fp32; the weights are rounded to dtype for the
+ * hold; a value that is not finite reaches the rows that see its key.  Work of
+ * more than 2^31 - 2 places (three and the tiles of 128 keys for every 512 rows of
+ * a head: hours of it) is not computed (COLI_DEV_KV_TOKENS).  Softmax and sums in fp32; the weights are rounded to dtype for the
  * product with the values.  The result does not depend on timing.
  * Asynchronous on stream, two launches.  n_tokens = 0 does nothing.  Errors:
  * COLI_EINVAL, COLI_EALIGN, COLI_EWORKSPACE, COLI_EUNSUPPORTED, COLI_ECUDA.
