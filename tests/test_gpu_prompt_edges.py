@@ -1,0 +1,140 @@
+"""Calls of the prompt operators that their documentation allows and that lie at an edge (needs a GB300): workspaces used again,
+one graph of several operators, values that are not finite in many units, rows behind the last request."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+from tests import test_gpu_prompt as P
+from tests.test_gpu_prompt import torch  # noqa: F401  (fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def test_one_workspace_for_calls_of_other_sizes(torch):  # noqa: F811
+    """What an earlier call left in the workspace (joins, partial results, status) does not reach a later one."""
+    cases = [P.prompt_case(torch, new, seq, H, dtype, 3) for new, seq, H, dtype in (
+        ([7], [20000], 6, "bf16"), ([3, 200], [3, 200], 2, "f16"), ([600, 9], [4000, 9000], 16, "bf16"), ([1], [1], 1, "bf16"),
+        ([20, 2, 300], [5000, 2, 400], 9, "f16"))]
+    alone = [P.call_prompt(torch, c)[:2] for c in cases]
+    ws = torch.full_like(P.call_prompt(torch, cases[0])[2], 0xff)
+    for i in (0, 1, 2, 3, 4, 2, 0, 4, 1):
+        out, lse, _, _ = P.call_prompt(torch, cases[i], ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1])
+    # calls in a row without a wait between them
+    outs = [P.call_prompt(torch, cases[i], ws=ws)[:2] for i in (2, 0, 3, 4, 1)]
+    torch.cuda.synchronize()
+    for (out, lse), i in zip(outs, (2, 0, 3, 4, 1)):
+        assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1])
+
+
+@pytest.mark.parametrize("new,seq,H", [([3, 2], [30000, 7], 5), ([256], [256], 7), ([768, 257], [768, 300], 3), ([1], [4000], 1024)])
+def test_heads_in_pairs(torch, new, seq, H):  # noqa: F811
+    """Last rows by two heads: odd numbers of heads, units cut into parts, many heads."""
+    P.check_prompt(torch, P.prompt_case(torch, new, seq, H, "bf16", H))
+
+
+@pytest.mark.parametrize("new,seq,H,dtype", [([300], [300], 456, "bf16"), ([200], [330], 700, "f16"), ([40, 513], [9000, 700], 12, "bf16")])
+def test_values_that_are_not_finite_in_many_units(torch, new, seq, H, dtype):  # noqa: F811
+    """Spoiled values in every second head, seen by the last rows: exactly those are spoiled, whatever else a CTA works on."""
+    c = P.prompt_case(torch, new, seq, H, dtype, 9)
+    ref, ref_lse, tol, tol_lse = P.reference(c) if H < 100 else (None,) * 4
+    clean = P.call_prompt(torch, c)[:2]
+    torch.cuda.synchronize()
+    n0 = m0 = 0
+    want = clean[0].double()
+    for t, s in zip(new, seq):
+        key = s - (t + 1) // 2
+        c["v"][m0 + key, ::2, 5] = math.nan
+        c["v"][m0 + key, ::2, 100] = math.inf
+        first = n0 + max(0, key - (s - t))
+        want[first:n0 + t, ::2, 5] = math.nan
+        want[first:n0 + t, ::2, 100] = math.inf
+        n0, m0 = n0 + t, m0 + s
+    out, lse, ws, _ = P.call_prompt(torch, c)
+    torch.cuda.synchronize()
+    odd = ~torch.isfinite(want)
+    assert torch.equal(torch.isnan(out)[odd], torch.isnan(want)[odd]) and (out[odd & torch.isinf(want)] == math.inf).all()
+    # the other columns: the taken-out value no longer adds to them (nor did it: columns are separate), so bit for bit
+    assert torch.equal(out[~odd], clean[0][~odd]) and torch.equal(lse, clean[1])
+    if ref is not None:
+        P.within(torch, out.double()[~odd], ref[~odd], tol[~odd], "out")
+
+
+def test_rows_behind_the_last_request(torch):  # noqa: F811
+    """Queries behind the last request hold anything; keys behind it too."""
+    c = P.prompt_case(torch, [100, 30], [400, 30], 3, "bf16", 2)
+    good = P.call_prompt(torch, c)[:2]
+    d = dict(c)
+    d["q"] = torch.cat([c["q"], torch.full((200, 3, 192), math.nan, dtype=torch.bfloat16, device="cuda")])
+    for k in ("k", "v"):
+        d[k] = torch.cat([c[k], torch.full((300, 3, 128), math.nan, dtype=torch.bfloat16, device="cuda")])
+    d["r"] = torch.cat([c["r"], torch.full((300, 64), math.inf, dtype=torch.bfloat16, device="cuda")])
+    d["n"], d["m"] = 330, 730
+    out, lse, ws, _ = P.call_prompt(torch, d)
+    torch.cuda.synchronize()
+    assert torch.equal(out[:130], good[0]) and torch.equal(lse[:130], good[1])
+    assert (out[130:] == 7).all() and (lse[130:] == 7).all()
+
+
+def test_one_graph_of_the_operators(torch):  # noqa: F811
+    """Append, gather, rotation and attention captured once; replayed with new rows, positions and lengths."""
+    import quantized_expert_ffn_bias_gb300 as coli
+    t, page, H, B, room, rows = torch.bfloat16, 32, 4, 2, 400, 80
+    W, V, ROT = P.W, P.V, P.ROT
+    n_pages, max_pages = 30, 12
+    kd = coli.coli_kv_desc(page, max_pages, n_pages, coli.COLI_X_BF16, page * W)
+    rd = P.rope_desc(ROT, "half", "linear")
+    freq = P.rope_table(torch, rd)
+    g = P.gen(torch, 5)
+    cache = torch.randn((n_pages, page, W), generator=g, device="cuda").to(t)
+    table = P.ints(torch, np.random.default_rng(0).permutation(n_pages)[:B * max_pages].reshape(B, max_pages))
+    seq, q_start = P.ints(torch, [200, 100]), P.ints(torch, [0, 50, 70])
+    raw, q_raw = torch.zeros((rows, W), dtype=t, device="cuda"), torch.zeros((rows, H, 192), dtype=t, device="cuda")
+    pos, slot = P.ints(torch, [0] * rows), P.ints(torch, [-1] * rows)
+    kv = torch.randn((room, H, 256), generator=g, device="cuda").to(t)
+    k_start, status = P.ints(torch, [0] * (B + 1)), P.ints(torch, [0])
+    latent, rope = torch.zeros((room, V), dtype=t, device="cuda"), torch.zeros((room, ROT), dtype=t, device="cuda")
+    q, out = torch.zeros_like(q_raw), torch.zeros((rows, H, 128), dtype=t, device="cuda")
+    n_ws = coli.colibri_prompt_attention_workspace_size(B, rows, room, H)
+    ws = torch.zeros(n_ws, dtype=torch.uint8, device="cuda")
+
+    def step():
+        st = torch.cuda.current_stream()
+        coli.colibri_kv_append_rope(kd, rd, rows, q_start[B:], raw, W, None, 0.0, raw[:, V:], W, pos, freq, slot, cache, st)
+        coli.colibri_kv_gather(kd, B, room, seq, table, cache, k_start, latent, V, rope, ROT, status, st)
+        q.copy_(q_raw)
+        coli.colibri_rope(rd, coli.COLI_X_BF16, rows, q_start[B:], H, pos, freq, q[..., 128:], H * 192, 192, q[..., 128:], H * 192, 192, st)
+        coli.colibri_prompt_attention(coli.COLI_X_BF16, B, rows, room, H, 0.07, q, H * 192, 192, kv, H * 256, 256, rope, ROT,
+                                      kv[..., 128:], H * 256, 256, q_start, k_start, out, None, ws, n_ws, st)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    free = np.setdiff1d(np.arange(n_pages), table.cpu().numpy())
+    for i, (lens, new) in enumerate((([200, 100], [50, 20]), ([1, 384], [1, 79]), ([384, 0], [30, 0]), ([7, 9], [0, 9]))):
+        raw.copy_(torch.randn(raw.shape, generator=g, device="cuda").to(t))
+        q_raw.copy_(torch.randn(q_raw.shape, generator=g, device="cuda").to(t))
+        pos.copy_(P.ints(torch, np.random.default_rng(i).integers(0, 5000, rows)))
+        slot[page:] = -1                               # (one spare page: its rows once each)
+        slot[:page] = P.ints(torch, free[0] * page + np.random.default_rng(i).permutation(page))
+        seq.copy_(P.ints(torch, lens))
+        q_start.copy_(P.ints(torch, np.concatenate([[0], np.cumsum(new)])))
+        before = cache.clone()
+        got = []
+        for run in (graph.replay, step):
+            cache.copy_(before)
+            for x in (latent, rope, out, k_start):
+                x.fill_(3)
+            run()
+            torch.cuda.synchronize()
+            got.append([x.clone() for x in (cache, latent, rope, k_start, q, out)])
+            assert coli.colibri_kv_check_status(ws) == 0 and int(status) == 0
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+        assert (got[0][5][sum(new):] == 3).all()
