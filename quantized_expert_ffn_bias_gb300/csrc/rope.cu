@@ -12,7 +12,7 @@
 
 namespace coli {
 
-constexpr int kRopeThreads = 256, kRopeItems = 4;   // items (a piece of a row) a thread, all loads in flight at once
+constexpr int kRopeThreads = 128, kRopeItems = 4;   // items (a piece of a row) a thread, all loads in flight at once
 constexpr int kRopeMaxDim = 256;
 
 // (amplitude cos, amplitude sin) of position * freq
@@ -75,7 +75,8 @@ struct RopeArgs {
 
 // A piece is 16 bytes (WIDE; in the half layout 16 of either half), or one pair.  A CTA takes some tokens and heads;
 // its threads' pieces are loaded first, the tokens' sines and cosines computed meanwhile, once for all heads.
-// A copy in its traffic: 128 bytes a head of 64 16-bit values, read and written.
+// A copy in its traffic, 128 bytes a head of 64 16-bit values read and written: 8192 tokens of 64 heads take 22.0 us, 6.1 TB/s
+// (24.1 with 256 threads a CTA; with those 26.2 by two pieces a thread and 29.0 by eight).  One token: 2.3 us.
 template <typename T, bool HALF, bool WIDE>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
   extern __shared__ float2 turn[];               // [tokens][pairs]
@@ -181,9 +182,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
 
 // ------------------------------------------------------------------ append with norm and rotation
 // A warp takes a row: a lane holds 16 of its latent values and one pair of its rotary ones.  Nothing waits for *n_valid,
-// slots or positions before the row's loads are in flight.  A copy in its traffic (75.8 MB for 32768 rows: 18.0 us; four rows
-// a warp: 19.1, two: 18.6, and 192 rows 4.2 and 3.3 in place of 2.8).
-constexpr int kArWarps = 8;
+// slots or positions before the row's loads are in flight.  A copy in its traffic (75.8 MB for 32768 rows: 16.3 us, 4.65 TB/s;
+// with four rows a warp 19.1, two 18.6, one 17.6, and one with 40 registers, so that 48 warps an SM fit, 16.3).  192 rows: 2.2 us.
+constexpr int kArWarps = 4;
 static_assert(COLI_KV_VALUE == 32 * 16 && COLI_KV_ROTARY == 64, "16 values and a pair a lane");
 
 struct AppendRopeArgs {
@@ -200,7 +201,7 @@ struct AppendRopeArgs {
 };
 
 template <typename T, bool HALF>
-__global__ void __launch_bounds__(kArWarps * 32) kv_append_rope_kernel(const AppendRopeArgs p) {
+__global__ void __launch_bounds__(kArWarps * 32, 12) kv_append_rope_kernel(const AppendRopeArgs p) {
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * kArWarps + (threadIdx.x >> 5);
   if (row >= p.n) return;
