@@ -682,7 +682,7 @@ COLI_API coli_status colibri_rope_frequencies(const coli_rope_desc* desc, uint64
  *   position     device int32 [n_tokens], any values (negative ones too).
  *   freq         device uint64 [dim / 2], 8-byte aligned.
  *   n_valid      device int32 or NULL: rows from *n_valid on are not written
- *                (q_start + B of colibri_kv_step).
+ *                (q_start + B of colibri_kv_step; all n_tokens may be read).
  *   out          x itself with the same strides, or memory that does not
  *                overlap x; no two outputs overlap.
  * Angles are exact to 2^-24 relative; sums in fp32, each result is rounded once.
@@ -699,11 +699,11 @@ COLI_API coli_status colibri_rope(const coli_rope_desc* desc, int dtype, int n_t
  * colibri_kv_append with the latent's norm and the rotation on the way: row i of
  * the down-projection's output goes to slot[i] as
  *   latent[i] / sqrt(mean(latent[i]^2) + eps) * gain   (gain NULL: as it is),
- *   rope[i] rotated by position[i] (rope->dim must be 64).
+ *   rope[i] rotated by position[i] (rope_desc->dim must be 64).
  * desc->dtype is that of latent, rope and cache (bf16 or fp16); gain is device
- * float [512]; eps >= 0.  Sums in fp32, one rounding of each result.  gain
- * 16-byte, position 4-byte, freq 8-byte aligned; everything else as
- * colibri_kv_append.
+ * float [512]; eps >= 0.  Sums in fp32, one rounding of each result.  Rows from
+ * *n_valid on may be read, and are not written.  gain 16-byte, position 4-byte,
+ * freq 8-byte aligned; everything else as colibri_kv_append.
  */
 COLI_API coli_status colibri_kv_append_rope(const coli_kv_desc* desc, const coli_rope_desc* rope_desc, int n_tokens,
                                             const int32_t* n_valid, const void* latent, long long latent_stride,
@@ -764,8 +764,8 @@ COLI_API coli_status colibri_kv_gather(const coli_kv_desc* desc, int B, int n_ro
  * [q_start[0], q_start[B]) are left as they were.  Keys and values that a row
  * does not see do not reach its output, whatever values (infinities, NaN) they
  * hold; a value that is not finite reaches the rows that see its key.  Work of
- * more than 2^31 - 2 places (three and the tiles of 128 keys for every 512 rows of
- * a head: hours of it) is not computed (COLI_DEV_KV_TOKENS).  Softmax and sums in fp32; the weights are rounded to dtype for the
+ * more than 2^31 - 2^16 places (three and the tiles of 128 keys for every 512 rows
+ * of a head: hours of it) is not computed (COLI_DEV_KV_TOKENS).  Softmax and sums in fp32; the weights are rounded to dtype for the
  * product with the values.  The result does not depend on timing.
  * Asynchronous on stream, two launches.  n_tokens = 0 does nothing.  Errors:
  * COLI_EINVAL, COLI_EALIGN, COLI_EWORKSPACE, COLI_EUNSUPPORTED, COLI_ECUDA.

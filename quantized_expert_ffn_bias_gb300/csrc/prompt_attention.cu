@@ -135,7 +135,7 @@ __device__ __forceinline__ unsigned pa_before(int T, int L, int nb, int n) {
   return (unsigned)min(s, 0x7fffffffll);
 }
 
-// Borders of G <= kPaMaxCtas equal runs of the W key tiles: floor(W j / G), without leaving 32 bits.  The
+// Borders of G <= kPaMaxCtas equal runs of the W places: floor(W j / G), without leaving 32 bits.  The
 // remainder's part is below kPaMaxCtas^2, where the fp32 quotient of x + 1/2 is exact.
 struct PaCuts {
   int q, r;
@@ -276,7 +276,7 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
     total = min(total + warp_tot[w], 0x7fffffffu);
   }
   base += inc - sum;
-  wrong |= total == 0x7fffffffu;
+  wrong |= total > 0x7fff0000u;                        // (room for sums with it)
   PaRun r;
   r.status = wrong ? COLI_DEV_KV_TOKENS : 0;
   r.beg = r.end = 0;
@@ -386,8 +386,7 @@ __device__ __forceinline__ void cluster_arrive_tmem(uint32_t bar) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Wait for a phase, at most about limit_ns, suspended by the hardware meanwhile: twelve of the sixteen warps wait for most
-// of the time, and looks at the barrier would take issue slots from the softmax.  CLUSTER: for writes of either CTA.
+// Wait for a phase, at most about limit_ns, suspended by the hardware for 20 us at a time.  CLUSTER: for writes of either CTA.
 constexpr uint32_t kPaSuspendNs = 20000;
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
