@@ -59,7 +59,7 @@ constexpr int kPaSmWarps = 8;                      // softmax: warps 0..3 row ti
 constexpr int kPaLoader = 8, kPaMma = 9, kPaCheck = 10, kPaCheckWarps = 2;
 constexpr int kPaThreads = (kPaCheck + kPaCheckWarps) * 32;
 constexpr size_t kPaSmem = 2 * (size_t)kPaQBytes + (size_t)kPaStages * kPaStage + kPaSmWarps * kPaOutStage;
-static_assert(kPaSmem + 3072 <= 232448, "with the kernel's own arrays");
+static_assert(kPaSmem + 3 * 1024 <= 232448, "with the kernel's own arrays");
 constexpr int kPaMasked = 6;                       // key tiles of a unit of which some row does not see some key: 5, or 3 of two heads
 constexpr int kPaMaxCtas = 160;                    // CTAs the workspace has room for
 constexpr int kPaMaxB = 8192, kPaMaxH = 1024;
