@@ -54,12 +54,12 @@ constexpr int kPaKeys3 = 3 * kPaKeyBox;            // a CTA's K and R of a tile
 constexpr int kPaStage = kPaKeys3 + kPaValues;     // its part of a key tile
 constexpr int kPaStages = 3;
 constexpr int kPaQBytes = 3 * kPaTile * 128;       // its part of a row tile's queries
-constexpr int kPaOutStage = 8 * 128;               // a warp's place for results on their way out
+constexpr int kPaOutStage = 8 * 64;                // a warp's place for results on their way out
 constexpr int kPaSmWarps = 8;                      // softmax: warps 0..3 row tile 0, 4..7 row tile 1
 constexpr int kPaLoader = 8, kPaMma = 9, kPaCheck = 10, kPaCheckWarps = 2;
 constexpr int kPaThreads = (kPaCheck + kPaCheckWarps) * 32;
 constexpr size_t kPaSmem = 2 * (size_t)kPaQBytes + (size_t)kPaStages * kPaStage + kPaSmWarps * kPaOutStage;
-static_assert(kPaSmem + 3 * 1024 <= 232448, "with the kernel's own arrays");
+static_assert(kPaSmem + 6 * 1024 <= 232448, "with the kernel's own arrays");
 constexpr int kPaMasked = 6;                       // key tiles of a unit of which some row does not see some key: 5, or 3 of two heads
 constexpr int kPaMaxCtas = 160;                    // CTAs the workspace has room for
 constexpr int kPaMaxB = 8192, kPaMaxH = 1024;
@@ -125,7 +125,7 @@ __device__ __forceinline__ int pa_blocks(int T) { return (int)(((unsigned)T + kP
 __device__ __forceinline__ bool pa_short(int T) { return (unsigned)(T - 1) % kPaRows < (unsigned)kPaRows / 2; }
 __device__ __forceinline__ int pa_key_tiles(int keys) { return max(1, (keys + kPaTile - 1) >> 7); }
 // Places of the first n of nb blocks, saturating (a sum that does not fit 31 bits is refused).
-__device__ __forceinline__ unsigned pa_before(int T, int L, int nb, int n) {
+__device__ __noinline__ unsigned pa_before(int T, int L, int nb, int n) {
   const int a = (L - T + kPaTile - 1) >> 7;
   const int m = min(n, nb - 1);
   const int flat = a < 0 ? min(m, -a / kPaTilesPerBlock) : 0;        // blocks whose rows see nothing: one tile each
@@ -157,8 +157,27 @@ struct __align__(16) PaUnit {
 
 struct PaRun {
   int beg, end;
-  PaUnit unit0;      // that of `beg`
   int status;
+};
+
+// Where a warp is: a unit and its part [t0, t1) of the run.  In shared memory, filled by one lane; the code that fills it
+// stands once (no inlining): every role's own copy of it made the kernel 139 KB, more than the instruction cache, and a
+// unit's first tile cost 5,000 cycles in place of 1,500.
+struct __align__(16) PaAt {
+  PaUnit u;
+  int live;          // 0: behind the run's last
+  int opening;       // the run's first
+  int whole;         // all of the unit's tiles
+  int t0;
+  int two;           // row tile 1 has the rows of tile 0 and the next head
+  int heads;         // key tiles a step: 2 where there are two heads
+  int row0;          // its first row of the request
+  int shift;         // the last key that row i of the request sees: shift + i
+  int rows[2];       // rows of either row tile
+  int n[2];          // key tiles of row tile x in the part
+  int all;           // the larger
+  int masked;        // first tile of which some row does not see some key
+  __device__ __forceinline__ int first_row(int x) const { return row0 + (two ? 0 : x * 2 * kPaTile); }
 };
 
 __device__ __forceinline__ void pa_tiles(PaUnit& u) {
@@ -166,7 +185,7 @@ __device__ __forceinline__ void pa_tiles(PaUnit& u) {
   u.tiles = pa_key_tiles(rows <= kPaRows ? u.L : u.L - rows + kPaRows);
 }
 // The unit after u (of the same or a later request; the caller has not reached the end of the work).
-__device__ __forceinline__ void pa_next(const PaArgs& p, PaUnit& u) {
+__device__ __noinline__ void pa_next(const PaArgs& p, PaUnit& u) {
   u.first += kPaUnitCost + u.tiles;
   if (u.blk == u.nb) {
     u.h += 2;
@@ -194,40 +213,50 @@ __device__ __forceinline__ void pa_next(const PaArgs& p, PaUnit& u) {
   pa_tiles(u);
 }
 
-// What a part [t0, t1) of a unit is.
-struct PaPart {
-  bool two;          // row tile 1 has the rows of tile 0 and the next head
-  int heads;         // key tiles a step: 2 where there are two heads
-  int row0;          // its first row of the request
-  int rows[2];       // rows of either row tile
-  int shift;         // the last key that row i of the request sees: shift + i
-  int n[2];          // key tiles of row tile x in the part
-  int all;           // the larger
-  __device__ __forceinline__ PaPart(const PaUnit& u, int H, int t0, int t1) {
-    row0 = u.blk * kPaRows;
-    two = u.blk == u.nb;
-    shift = u.L - u.T;
-    heads = two && u.h + 1 < H ? 2 : 1;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int from = row0 + (two ? 0 : x * 2 * kPaTile);
-      rows[x] = two && x >= heads ? 0 : max(0, min(2 * kPaTile, u.T - from));
-      const int seen = rows[x] > 0 ? (shift + from + rows[x] + kPaTile - 1) >> 7 : 0;
-      n[x] = max(0, min(t1, seen) - t0);
-    }
-    all = max(n[0], n[1]);
+// a: the part that begins at place `at` (of a.u) of a run that ends at `end`.
+__device__ __noinline__ void pa_part(const PaArgs& p, PaAt& a, int at, int end) {
+  const PaUnit& u = a.u;
+  const int t0 = u.from(at), t1 = u.to(end);
+  a.live = t1 > 0;                                     // (else the border lies before its first tile)
+  a.t0 = t0;
+  a.whole = t0 == 0 && t1 == u.tiles;
+  const int row0 = u.blk * kPaRows, shift = u.L - u.T;
+  const bool two = u.blk == u.nb;
+  a.row0 = row0;
+  a.shift = shift;
+  a.two = two;
+  a.heads = two && u.h + 1 < p.H ? 2 : 1;
+  int all = 0;
+#pragma unroll 1
+  for (int x = 0; x < 2; ++x) {
+    const int from = row0 + (two ? 0 : x * 2 * kPaTile);
+    const int rows = two && x >= a.heads ? 0 : max(0, min(2 * kPaTile, u.T - from));
+    const int seen = rows > 0 ? (shift + from + rows + kPaTile - 1) >> 7 : 0;
+    const int n = max(0, min(t1, seen) - t0);
+    a.rows[x] = rows;
+    a.n[x] = n;
+    all = max(all, n);
   }
-  __device__ __forceinline__ int first_row(int x) const { return row0 + (two ? 0 : x * 2 * kPaTile); }
-  // first tile of which some row does not see some key
-  __device__ __forceinline__ int masked() const { return max(0, (shift + row0 + 1) >> 7); }
-};
+  a.all = all;
+  a.masked = max(0, (shift + row0 + 1) >> 7);
+}
+// b: the part after a.
+__device__ __noinline__ void pa_advance(const PaArgs& p, const PaAt& a, PaAt& b, int end) {
+  b = a;
+  b.opening = 0;
+  const int at = a.u.first + kPaUnitCost + a.u.tiles;
+  b.live = 0;
+  if (at >= end) return;
+  pa_next(p, b.u);
+  pa_part(p, b, at, end);
+}
 
 constexpr int kPaWhole = 4;                // units of at most so many tiles are not cut: a join costs more
 
-// Every thread of the CTA calls it.  Each thread sums a stretch of the requests.
-__device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
+// Every thread of the CTA calls it.  Each thread sums a stretch of the requests.  found: shared memory; found[0] receives
+// the unit of the run's first place.
+__device__ __forceinline__ PaRun pa_plan(const PaArgs& p, PaUnit* found) {
   __shared__ unsigned warp_tot[kPaThreads / 32];
-  __shared__ PaUnit found;
   __shared__ int s_longest;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + kPaThreads - 1) / kPaThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
@@ -291,8 +320,12 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
   const PaCuts cut(W, G);
   r.beg = cut(pair);
   r.end = cut(pair + 1);
-  // the unit of place x, found by the thread whose requests hold it
-  auto locate = [&](int x) {
+  // the units of the run's first place and, where short units are not cut, of the next run's: found by the thread whose
+  // requests hold it
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const int x = k ? r.end : r.beg;
+    if (k && (s_longest > kPaWhole || x >= W)) break;
     __syncthreads();
     if (x >= (int)base && x < (int)(base + sum)) {
       PaUnit u;
@@ -327,26 +360,22 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p) {
       }
       u.first = x - rest;
       pa_tiles(u);
-      found = u;
+      found[k] = u;
     }
-    __syncthreads();
-    return found;
-  };
-  r.unit0 = locate(r.beg);                             // (its barriers make s_longest known, too)
+    __syncthreads();                                   // (the first round's make s_longest known, too)
+    if (k && found[1].from(x) > 0) r.end = found[1].first + kPaUnitCost + found[1].tiles;
+  }
   if (s_longest <= kPaWhole) {
     // short units are not cut: a run takes those that begin in it
-    if (r.unit0.from(r.beg) > 0) {
-      r.beg = r.unit0.first + kPaUnitCost + r.unit0.tiles;
-      pa_next(p, r.unit0);
-    }
-    if (r.end < W) {
-      const PaUnit u = locate(r.end);
-      if (u.from(r.end) > 0) r.end = u.first + kPaUnitCost + u.tiles;
+    if (found[0].from(r.beg) > 0) {
+      r.beg = found[0].first + kPaUnitCost + found[0].tiles;
+      __syncthreads();
+      if (tid == 0) pa_next(p, found[0]);
     }
     return r;
   }
   // a run that begins with the first border inside its unit lists the join
-  const PaUnit& u = r.unit0;
+  const PaUnit& u = found[0];
   if ((blockIdx.x & 1) == 0 && tid == 0 && pair > 0 && u.from(r.beg) > 0 && u.from(cut(pair - 1)) == 0) {
     int m = pair;
     while (m < G && cut(m) < u.first + kPaUnitCost + u.tiles) ++m;     // runs pair - 1 .. m - 1 begin before the unit's end
@@ -387,32 +416,40 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // Wait for a phase, at most about limit_ns, suspended by the hardware for 20 us at a time.  CLUSTER: for writes of either CTA.
+// (What comes after the first look stands once: it is called from twenty places.)
 constexpr uint32_t kPaSuspendNs = 20000;
+template <bool CLUSTER>
+__device__ __forceinline__ bool pa_look(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kPaSuspendNs)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kPaSuspendNs)
+        : "memory");
+  return ok != 0;
+}
+template <bool CLUSTER>
+__device__ __noinline__ bool pa_wait_on(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
+  const unsigned long long t0 = globaltimer();
+  for (;;) {
+    if (pa_look<CLUSTER>(bar, parity)) return true;
+    if (globaltimer() - t0 > limit_ns) return false;
+  }
+}
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
-  unsigned long long t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    uint32_t ok;
-    if constexpr (CLUSTER)
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity), "r"(kPaSuspendNs)
-          : "memory");
-    else
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity), "r"(kPaSuspendNs)
-          : "memory");
-    if (ok) return true;
-    if (it == 0) t0 = globaltimer();
-    else if (globaltimer() - t0 > limit_ns) return false;
-  }
+  return pa_look<CLUSTER>(smem_u32(bar), parity) || pa_wait_on<CLUSTER>(smem_u32(bar), parity, limit_ns);
 }
 
 // TMA loads of a pair: into this CTA's shared memory, counted on a barrier of either CTA.
@@ -484,6 +521,12 @@ __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+// registers -> 8 consecutive TMEM columns
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 constexpr int kPaChunk = 16;
 __device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16_issue(taddr, r); }
@@ -566,14 +609,14 @@ __device__ __forceinline__ uint32_t pa_finite_part(uint32_t w) {
 
 template <bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
-    prompt_attention_kernel(const PaArgs p, const __grid_constant__ PaMaps maps) {
+    prompt_attention_kernel(const __grid_constant__ PaArgs p, const __grid_constant__ PaMaps maps) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // Barriers of the first CTA, for its product issuer: what is there in both CTAs.
   __shared__ uint64_t q_full[2], k_full[kPaStages], v_full[kPaStages], v_ok[kPaStages], p_ready[2];
   // Barriers of either CTA: what the products are done with; values that the check awaits.
   __shared__ uint64_t q_empty[2], k_empty[kPaStages], v_empty[kPaStages], s_full[2], o_full[2], v_here[kPaStages], drained;
   __shared__ uint32_t tmem_base;
-  __shared__ int abort_flag, cta_status;
+  __shared__ int abort_flag, cta_status, any_bad;      // any_bad: `bad` has been written
   // Keys (bits of two words, for either half) of the masked tiles whose values are not all finite in the columns of either
   // CTA, of four units, written only where there are any: the third word then is the unit's number plus one.  done: units
   // whose output each warp of either CTA has written.
@@ -601,7 +644,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
       mbar_init(&v_ok[i], 2 * kPaCheckWarps);
     }
     mbar_init(&drained, 1);
-    abort_flag = 0;
+    abort_flag = any_bad = 0;
     fence_mbar_init();
   }
   if (threadIdx.x < 2 * kPaSmWarps) (&done[0][0])[threadIdx.x] = 0;
@@ -623,20 +666,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
   griddep_wait();                                      // the launch may overlap the kernel before; its results not
-  __shared__ PaUnit units[kPaThreads / 32];            // the unit that each warp is at (out of its registers)
-  int beg, end;
+  __shared__ PaUnit found[2];
+  __shared__ PaAt places[kPaThreads / 32][2];          // where each warp is, and what comes next
+  int end;
   {
-    const PaRun run = pa_plan(p);
-    beg = run.beg;
+    const PaRun run = pa_plan(p, found);
     end = run.end;
     if (threadIdx.x == 0) cta_status = run.status;
-    if (lane == 0) units[warp] = run.unit0;
+    __syncthreads();
+    if (lane == 0) {
+      PaAt& a = places[warp][0];
+      a.live = 0;
+      if (run.beg < end) {
+        a.u = found[0];
+        pa_part(p, a, run.beg, end);
+        a.opening = 1;
+      }
+    }
   }
   __syncthreads();
-  PaUnit& u = units[warp];
-  auto next_unit = [&]() {
+  int now = 0;
+  bool looked = false;
+  auto look_ahead = [&]() {                            // once a part, where the warp waits anyway
+    if (lane == 0) pa_advance(p, places[warp][now], places[warp][now ^ 1], end);
+    looked = true;
     __syncwarp();
-    if (lane == 0) pa_next(p, u);
+  };
+  auto next_part = [&]() {
+    if (!looked) look_ahead();
+    looked = false;
+    now ^= 1;
     __syncwarp();
   };
   auto fail_wait = [&]() {
@@ -647,22 +706,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
   if (warp == kPaLoader) {
     // ---------------------------------------------------------------- loader
     bool ok = true;
-    unsigned tile = 0;                                 // key tiles begun
-    int un[2] = {0, 0};                                // units whose queries are on their way
+    unsigned tile = 0, q_used = 0, q_phase = 0;        // key tiles begun; bit x: row tile x's queries were loaded, parity
     auto wait = [&](uint64_t* bar, unsigned phase) { ok = __all_sync(0xffffffffu, pa_wait(bar, phase & 1, p.wait_ns)); };
-    for (int at = beg; ok && at < end; next_unit()) {
-      const int t0 = u.from(at), t1 = u.to(end);
-      at = u.first + kPaUnitCost + u.tiles;
-      if (t1 <= 0) break;                              // (the border lies before its first tile)
-      const PaPart part(u, p.H, t0, t1);
-      if (part.all == 0) continue;
-      const int masked = part.masked();
-      for (int i = 0; ok && i < part.all * part.heads; ++i, ++tile) {
+    for (; ok && places[warp][now].live; next_part()) {
+      const PaAt& a = places[warp][now];
+      const int steps = a.all * a.heads, heads = a.heads, masked = a.masked, k0 = a.u.k0;
+#pragma unroll 1
+      for (int i = 0; ok && i < steps; ++i, ++tile) {
         if (__any_sync(0xffffffffu, *abort_v)) { ok = false; break; }
-        const int t = t0 + (part.heads == 2 ? i >> 1 : i), head = u.h + (part.heads == 2 ? i & 1 : 0);
+        const int t = a.t0 + (heads == 2 ? i >> 1 : i), head = a.u.h + (heads == 2 ? i & 1 : 0);
         const unsigned s = tile % kPaStages, use = tile / kPaStages;
         uint8_t* dst = smem + s * kPaStage;
-        const int key = u.k0 + t * kPaTile;
+        const int key = k0 + t * kPaTile;
         if (use > 0) wait(&k_empty[s], use - 1);
         if (!ok) break;
         if (lane == 0) {
@@ -674,27 +729,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
         }
         __syncwarp();
         if (i == 0) {                                  // the queries: rows past the unit's last are other rows' or, behind
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {                // the tensor, zeros: computed, not written
-            if (!ok || part.n[x] == 0) continue;
-            if (un[x] > 0) wait(&q_empty[x], un[x] - 1);
-            if (!ok) continue;
-            if (lane == 0) {
-              if (rank == 0) mbar_arrive_expect_tx(&q_full[x], (uint32_t)(2 * kPaQBytes));
-              const uint32_t bar = cluster_addr(&q_full[x], 0);
-              for (int c = 0; c < 3; ++c)
-                tma_pair_3d(qsm + x * kPaQBytes + c * (kPaTile * 128), &maps.q, c * 64, u.h + (part.two ? x : 0),
-                            u.q0 + part.first_row(x) + rank * kPaTile, bar);
+#pragma unroll 1
+          for (int x = 0; ok && x < 2; ++x) {          // the tensor, zeros: computed, not written
+            if (a.n[x] == 0) continue;
+            if ((q_used >> x) & 1) wait(&q_empty[x], q_phase >> x);
+            if (!ok) break;
+            q_phase ^= q_used & (1u << x);
+            q_used |= 1u << x;
+            if (lane < 3) {
+              if (lane == 0 && rank == 0) mbar_arrive_expect_tx(&q_full[x], (uint32_t)(2 * kPaQBytes));
+              tma_pair_3d(qsm + x * kPaQBytes + lane * (kPaTile * 128), &maps.q, lane * 64, a.u.h + (a.two ? x : 0),
+                          a.u.q0 + a.first_row(x) + rank * kPaTile, cluster_addr(&q_full[x], 0));
             }
             __syncwarp();
-            ++un[x];
           }
-          if (ok && at < end && lane < 6) {        // and the next unit's on their way to L2
-            PaUnit w = u;
-            pa_next(p, w);
+          look_ahead();                                // and the next unit's on their way to L2
+          const PaAt& b = places[warp][now ^ 1];
+          if (ok && b.live && lane < 6) {
             const int x = lane / 3;
-            tma_prefetch_3d(&maps.q, (lane % 3) * 64, min(w.h + (w.blk == w.nb ? x : 0), p.H - 1),
-                            w.q0 + w.blk * kPaRows + ((w.blk == w.nb ? 0 : x * 2) + rank) * kPaTile);
+            tma_prefetch_3d(&maps.q, (lane % 3) * 64, min(b.u.h + (b.two ? x : 0), p.H - 1),
+                            b.u.q0 + b.first_row(x) + rank * kPaTile);
           }
           __syncwarp();
         }
@@ -715,13 +769,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
       }
     }
     // the products' last arrivals come before the CTA leaves
+#pragma unroll 1
     for (unsigned s = 0; s < kPaStages; ++s) {
       if (!ok || tile <= s) continue;
       wait(&k_empty[s], (tile - s - 1) / kPaStages);
       if (ok) wait(&v_empty[s], (tile - s - 1) / kPaStages);
     }
+#pragma unroll 1
     for (int x = 0; x < 2; ++x)
-      if (ok && un[x] > 0) wait(&q_empty[x], un[x] - 1);
+      if (ok && ((q_used >> x) & 1)) wait(&q_empty[x], q_phase >> x);
     if (!ok) fail_wait();
   } else if (warp == kPaMma) {
     // ---------------------------------------------------------------- product issuer (the warp stays converged)
@@ -731,69 +787,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
       const uint64_t kd = umma_desc_sw128(smem_u32(smem)), qd = umma_desc_sw128(smem_u32(qsm));
       const uint64_t vd = pa_desc_mn(smem_u32(smem + kPaKeys3));
       bool ok = true;
-      unsigned tile = 0, un[2] = {0, 0}, it[2] = {0, 0}, checked = 0;      // checked: bit s: parity of v_ok[s]
+      // parities, bit x or s: of q_full, p_ready, v_ok
+      unsigned tile = 0, q_phase = 0, p_phase = 0, checked = 0;
       auto wait = [&](uint64_t* bar, unsigned phase) {
         ok = __all_sync(0xffffffffu, ok && pa_wait(bar, phase & 1, p.wait_ns));
         return ok;
       };
-      for (int at = beg; ok && at < end; next_unit()) {
-        const int t0 = u.from(at), t1 = u.to(end);
-        at = u.first + kPaUnitCost + u.tiles;
-        if (t1 <= 0) break;                              // (the border lies before its first tile)
-        const PaPart part(u, p.H, t0, t1);
-        if (part.all == 0) continue;
-        const int masked = part.masked(), heads = part.heads;
-        // S of row tile x and the part's step i; its keys are the ring's tile j
-        auto scores = [&](int x, int i, unsigned j) {
-          const unsigned s = j % kPaStages;
-          if (x == 0 || heads == 2 || i >= part.n[0]) {        // (else the keys of row tile 0: awaited)
-            if (!wait(&k_full[s], j / kPaStages)) return;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < 3; ++c)
-            pa_mma_ss(tmem + x * kPaTile, qd + (uint64_t)((x * kPaQBytes + c * (kPaTile * 128)) >> 4),
-                      kd + (uint64_t)((s * kPaStage + c * kPaKeyBox) >> 4), idesc, c ? 1u : 0u);
-          pa_commit(&s_full[x]);
-          if (i + 1 == part.n[x]) pa_commit(&q_empty[x]);
-          if (heads == 2 || x == 1 || i >= part.n[1]) pa_commit(&k_empty[s]);      // (else row tile 1 is yet to read them)
-        };
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok || part.n[x] == 0 || !wait(&q_full[x], un[x])) continue;
-          scores(x, 0, tile + (heads == 2 ? x : 0));
-        }
-        for (int i = 0; ok && i < part.all; ++i, tile += heads) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || i >= part.n[x]) continue;
-            const unsigned j = tile + (heads == 2 ? x : 0), s = j % kPaStages;
-            // the values, or, where some row does not see some key, the values after their check.  (Every phase of a
-            // barrier is awaited or, v_full's of a checked tile, known to be over: a parity tells neighbours apart.)
-            if (x == 0 || heads == 2 || i >= part.n[0]) {
-              if (t0 + i >= masked) {
-                ok = __all_sync(0xffffffffu, pa_wait<true>(&v_ok[s], (checked >> s) & 1, p.wait_ns));
-                checked ^= 1u << s;
-              } else {
-                wait(&v_full[s], j / kPaStages);
+      for (; ok && places[warp][now].live; next_part()) {
+        const PaAt& a = places[warp][now];
+        const int n0 = a.n[0], n1 = a.n[1], all = a.all, heads = a.heads, masked = a.masked - a.t0;
+        // Step i: row tile by row tile, the products with the values of tile i (i = -1: none) and the scores of tile i + 1
+#pragma unroll 1
+        for (int i = -1; ok && i < all; ++i) {
+          if (i == 0) look_ahead();
+#pragma unroll 1
+          for (int x = 0; ok && x < 2; ++x) {
+            const int n = x ? n1 : n0;
+            const uint32_t sx = tmem + x * kPaTile;
+            if (i >= 0 && i < n) {
+              const unsigned j = tile + i * heads + (heads == 2 ? x : 0), s = j % kPaStages;
+              // the values, or, where some row does not see some key, the values after their check.  (Every phase of a
+              // barrier is awaited or, v_full's of a checked tile, known to be over: a parity tells neighbours apart.)
+              if (x == 0 || heads == 2 || i >= n0) {   // (else row tile 0 waited for them)
+                if (i >= masked) {
+                  ok = __all_sync(0xffffffffu, pa_wait<true>(&v_ok[s], (checked >> s) & 1, p.wait_ns));
+                  checked ^= 1u << s;
+                } else {
+                  wait(&v_full[s], j / kPaStages);
+                }
               }
+              if (!wait(&p_ready[x], p_phase >> x)) break;
+              p_phase ^= 1u << x;
+              tc_fence_after();
+              const uint64_t v = vd + (uint64_t)((s * kPaStage) >> 4);
+              pa_mma_ts(sx + kPaOCol, sx, v, idesc_v, i ? 1u : 0u);
+              pa_mma_ts(sx + kPaOCol, sx + 32, v + (uint64_t)(kPaValues / 2 >> 4), idesc_v, 1u);
+              if (heads == 2 || x == 1 || i >= n1) pa_commit(&v_empty[s]);       // (else row tile 1 is yet to read them)
+              if (i + 1 == n) pa_commit(&o_full[x]);
             }
-            if (!wait(&p_ready[x], it[x])) continue;
-            ++it[x];
-            tc_fence_after();
+            if (i + 1 < n) {
+              const unsigned j = tile + (i + 1) * heads + (heads == 2 ? x : 0), s = j % kPaStages;
+              if (i < 0) {
+                if (!wait(&q_full[x], q_phase >> x)) break;
+                q_phase ^= 1u << x;
+              }
+              if ((x == 0 || heads == 2 || i + 1 >= n0) && !wait(&k_full[s], j / kPaStages)) break;
+              tc_fence_after();
+              const uint64_t k = kd + (uint64_t)((s * kPaStage) >> 4), q = qd + (uint64_t)((x * kPaQBytes) >> 4);
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-              pa_mma_ts(tmem + kPaOCol + x * kPaTile, tmem + x * kPaTile + c * 32,
-                        vd + (uint64_t)((s * kPaStage + c * (kPaValues / 2)) >> 4), idesc_v, i || c ? 1u : 0u);
-            if (heads == 2 || x == 1 || i >= part.n[1]) pa_commit(&v_empty[s]);
-            if (i + 1 < part.n[x]) {
-              scores(x, i + 1, j + heads);
-            } else {
-              pa_commit(&o_full[x]);
-              ++un[x];
+              for (int c = 0; c < 3; ++c)
+                pa_mma_ss(sx, q + (uint64_t)(c * (kPaTile * 128) >> 4), k + (uint64_t)(c * kPaKeyBox >> 4), idesc, c ? 1u : 0u);
+              pa_commit(&s_full[x]);
+              if (i + 2 == n) pa_commit(&q_empty[x]);
+              if (heads == 2 || x == 1 || i + 1 >= n1) pa_commit(&k_empty[s]);
             }
           }
         }
+        tile += all * heads;
       }
       if (!ok && lane == 0) fail_wait();
       __syncwarp();
@@ -818,14 +868,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
     };
     bool ok = true;
     unsigned tile = 0, checked = 0, uu = 0;
-    for (int at = beg; ok && at < end; next_unit()) {
-      const int t0 = u.from(at), t1 = u.to(end);
-      at = u.first + kPaUnitCost + u.tiles;
-      if (t1 <= 0) break;                              // (the border lies before its first tile)
-      const PaPart part(u, p.H, t0, t1);
-      if (part.all == 0) continue;
-      const int masked = part.masked();
-      for (int i = max(0, masked - t0) * part.heads; ok && i < part.all * part.heads; ++i) {
+    for (; ok && places[warp][now].live; next_part()) {
+      const PaAt& a = places[warp][now];
+      if (a.all == 0) continue;
+      const int heads = a.heads, steps = a.all * heads, ahead = (a.t0 - a.masked) * heads;     // of the masked tiles
+      look_ahead();
+#pragma unroll 1
+      for (int i = max(0, -ahead); ok && i < steps; ++i) {
         const unsigned s = (tile + i) % kPaStages;
         ok = __all_sync(0xffffffffu, pa_wait(&v_here[s], (checked >> s) & 1, p.wait_ns));
         checked ^= 1u << s;
@@ -856,9 +905,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
         if (flags[0] | flags[1]) {
           ok = free_again(uu);
           if (!ok) break;
+          if (lane < 2) cluster_store(cluster_addr(&any_bad, lane), 1);
           if (lane < 6) {                              // three words into either CTA
             const int w = lane % 3;
-            cluster_store(cluster_addr(&bad[rank][uu & 3][(t0 - masked) * part.heads + i][half][w], lane / 3),
+            cluster_store(cluster_addr(&bad[rank][uu & 3][ahead + i][half][w], lane / 3),
                           w == 2 ? uu + 1 : w == 1 ? flags[1] : flags[0]);
           }
           fence_proxy_async_smem();
@@ -869,7 +919,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
           cluster_arrive_tmem(cluster_addr(&v_ok[s], 0));
         }
       }
-      tile += part.all * part.heads;
+      tile += steps;
       ++uu;
     }
     if (!ok && lane == 0) fail_wait();
@@ -882,16 +932,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
     uint8_t* stage = qsm + 2 * kPaQBytes + warp * kPaOutStage;
     unsigned it = 0, un = 0, uu = 0;
     bool ok = true;
-    for (int at = beg; ok && at < end; next_unit()) {
-      const int t0 = u.from(at), t1 = u.to(end);
-      const bool opening = at == beg, whole = t0 == 0 && t1 == u.tiles;
-      at = u.first + kPaUnitCost + u.tiles;
-      if (t1 <= 0) break;                              // (the border lies before its first tile)
-      const PaPart part(u, p.H, t0, t1);
-      const int n = part.n[x];
-      const bool mine = in_tile < part.rows[x], any = warp_row < part.rows[x];     // rows past the last are not written
-      const int lim = part.shift + min(part.first_row(x) + in_tile, u.T - 1);      // the last key this row sees
-      const int lim0 = part.shift + part.first_row(x) + warp_row;      // of the warp's first row
+    for (; ok && places[warp][now].live; next_part()) {
+      const PaAt& a = places[warp][now];
+      const int n = a.n[x], t0 = a.t0;
+      const bool mine = in_tile < a.rows[x], any = warp_row < a.rows[x];     // rows past the last are not written
+      const int lim = a.shift + min(a.first_row(x) + in_tile, a.u.T - 1);    // the last key this row sees
+      const int lim0 = a.shift + a.first_row(x) + warp_row;      // of the warp's first row
       float m = -pa_top(BF16), l = 0.f;                // reference, sum of the weights
       bool has = false;                                // the row has seen a key
 #pragma unroll 1
@@ -984,12 +1030,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
           }
           float add = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < kPaTile; c += 32) {      // (a chunk's weights take columns that are read already)
-            uint32_t r[32], w[16];
-            tmem_ld32_issue(ts + c, r);
-            tmem_ld_done<32>(r);
+          for (int c = 0; c < kPaTile; c += 16) {      // (a chunk's weights take columns that are read already)
+            uint32_t r[16], w[8];
+            tmem_ld16_issue(ts + c, r);
+            tmem_ld_done<16>(r);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
+            for (int j = 0; j < 16; j += 2) {
               float d[2];
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
@@ -998,7 +1044,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
               }
               w[j / 2] = pa_pack<BF16>(d[0], d[1]);
             }
-            tmem_st16(ts + c / 2, w);
+            tmem_st8(ts + c / 2, w);
           }
           m += by;
           has |= move;
@@ -1010,20 +1056,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
         if (lane == 0) cluster_arrive_tmem(ready);
       }
       // -------------------------------------------------------------- the unit's rows
+      look_ahead();
       if (ok && n > 0) {
         ok = __all_sync(0xffffffffu, pa_wait(&o_full[x], un & 1, p.wait_ns));
         ++un;
       }
       if (!ok) break;
       tc_fence_after();
-      const int masked = part.masked(), head = u.h + (part.two ? x : 0), row = part.first_row(x) + in_tile;
-      if (masked < t0 + n) {
+      const int masked = a.masked, head = a.u.h + (a.two ? x : 0), row = a.first_row(x) + in_tile;
+      if (masked < t0 + n && *(volatile int*)&any_bad) {
         // values that were taken out of masked tiles are added to the rows that see them (rare: small code)
-        const int e0 = max(masked, t0) - masked, e1 = t0 + n - masked, step = part.heads, mine_of = part.two ? x : 0;
-        uint32_t any_bad = 0;
+        const int e0 = max(masked, t0) - masked, e1 = t0 + n - masked, step = a.heads, mine_of = a.two ? x : 0;
+        bool here = false;
         for (int e = e0; e < e1; ++e)
-          any_bad |= bad[lane & 1][uu & 3][e * step + mine_of][lane >> 1 & 1][2] == uu + 1;
-        if (__any_sync(0xffffffffu, any_bad != 0)) {
+          here |= bad[lane & 1][uu & 3][e * step + mine_of][lane >> 1 & 1][2] == uu + 1;
+        if (__any_sync(0xffffffffu, here)) {
 #pragma unroll 1
           for (int e = e0 * 128; e < e1 * 128; ++e) {
             const int w = (e >> 7) * step + mine_of;
@@ -1034,7 +1081,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
             }
             if (!((word >> (e & 31)) & 1u)) continue;
             const int key = masked * kPaTile + e;
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + (u.k0 + (long long)key) * p.v_tok + head * p.v_head);
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v + (a.u.k0 + (long long)key) * p.v_tok + head * p.v_head);
 #pragma unroll 1
             for (int c = 0; c < kPaV; c += 16) {
               uint32_t o[16];
@@ -1054,62 +1101,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
       }
       if (any) {
         const float by = l == 0.f ? 0.f : 1.0f / l;
-        const size_t slot = pa_slot(blockIdx.x >> 1, opening ? 0 : 1, rank);
+        const bool whole = a.whole;
+        const size_t slot = pa_slot(blockIdx.x >> 1, a.opening ? 0 : 1, rank), row0 = (size_t)(a.u.q0 + row - lane) * p.H + head;
         const int in_cta = x * kPaTile + sp * 32 + lane;
-        if (whole) {
-          if (mine && p.lse)
-            p.lse[(size_t)(u.q0 + row) * p.H + head] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.693147180559945309f;
-        } else if (mine) {
-          p.part_ml[slot * kPaCtaRows + in_cta] = make_float2(has || l != 0.f ? m : -INFINITY, l);
-        }
-        const int rows = part.rows[x] - warp_row;
-        uint8_t* out = reinterpret_cast<uint8_t*>(p.out + ((size_t)(u.q0 + row - lane) * p.H + head) * kPaV);    // the warp's first row
+        if (mine && whole && p.lse)
+          p.lse[row0 + (size_t)lane * p.H] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.693147180559945309f;
+        if (mine && !whole) p.part_ml[slot * kPaCtaRows + in_cta] = make_float2(has || l != 0.f ? m : -INFINITY, l);
+        const int rows = a.rows[x] - warp_row;
+        // eight rows of 64 bytes at a time by way of shared memory, so that a store covers eight lines (a row a lane: 32)
+        const int r = lane >> 2;
+        uint8_t* out = reinterpret_cast<uint8_t*>(p.out + (row0 + (size_t)r * p.H) * kPaV) + (lane & 3) * 16;
+        const size_t row8 = (size_t)p.H * (8 * kPaV * 2);
+        uint8_t* mine8 = stage + (lane & 7) * 64;
+        const uint8_t* read8 = stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4);
         float* po = p.part + slot * kPaPart;
 #pragma unroll 1
-        for (int c = 0; c < kPaV; c += 64) {
-          uint32_t o[64];
-          if (n > 0) {
-            tmem_ld32_issue(to + c, o);
-            tmem_ld32_issue(to + c + 32, o + 32);
-            tmem_ld_done<64>(o);
-          } else {
+        for (int c = 0; c < kPaV; c += 32) {
+          uint32_t o[32];
+          tmem_ld32_issue(to + c, o);
+          tmem_ld_done<32>(o);
+          if (n == 0) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) o[j] = 0u;
+            for (int j = 0; j < 32; ++j) o[j] = 0u;
           }
           if (whole) {
-            // eight rows of 128 bytes at a time by way of shared memory, so that a store covers whole lines (a row a lane:
-            // 32 lines a store)
-            uint8_t* mine8 = stage + (lane & 7) * 128;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
               o[j] = pa_pack<BF16>(__uint_as_float(o[2 * j]) * by, __uint_as_float(o[2 * j + 1]) * by);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               if ((lane >> 3) == g) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  *reinterpret_cast<uint4*>(mine8 + ((j ^ (lane & 7)) << 4)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                for (int j = 0; j < 4; ++j)
+                  *reinterpret_cast<uint4*>(mine8 + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
               }
               __syncwarp();
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int r = (lane >> 3) + 4 * k, j = lane & 7;
-                const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((j ^ r) << 4));
-                if (g * 8 + r < rows)
-                  *reinterpret_cast<uint4*>(out + (size_t)(g * 8 + r) * p.H * (kPaV * 2) + c * 2 + j * 16) = w;
-              }
+              const uint4 w = *reinterpret_cast<const uint4*>(read8);
+              if (g * 8 + r < rows) *reinterpret_cast<uint4*>(out + g * row8 + c * 2) = w;
               __syncwarp();
             }
           } else if (n > 0 && mine) {
 #pragma unroll
-            for (int j = 0; j < 64; j += 4)
+            for (int j = 0; j < 32; j += 4)
               *reinterpret_cast<uint4*>(po + pa_part(in_cta, c + j)) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
         }
       }
       tc_fence_before();
       __syncwarp();                                    // (every lane has read `bad`)
-      uu += part.all > 0;
+      uu += a.all > 0;
       if (lane < 2) cluster_store(cluster_addr(&done[rank][warp], lane), uu);
     }
     if (!ok && lane == 0) fail_wait();
