@@ -27,15 +27,15 @@
 //
 // Work: units with their key tiles, dealt in equal runs to the pairs.  A unit is 512 rows of one head, or, for the last rows
 // of a request where they are 256 at most, those of two heads, one to either row tile: with one row tile the tensor cores
-// wait while its softmax runs (7 tokens over 20,018 keys, 16 heads: 66 us, by two heads 59).  A unit cut by a border leaves
+// wait while its softmax runs (7 tokens over 20,018 keys, 16 heads: 66 us, by two heads 59; 45 by now).  A unit cut by a border leaves
 // partial results in the workspace, which the join kernel adds up in order.
 //
-// What bounds it: a prompt of 8192 tokens and 64 heads takes 830 us on a GPU that has not been busy (1.66 PFLOP/s, 85 % of the
-// measured burst rate of bf16 products; 930 us at the power limit, where those reach 1.73): a step of both row tiles takes
-// 3,100 cycles, its products 2,560; the rest is the way from one row tile's softmax (1,050 cycles) to its next scores, a
-// chain of 3,000 cycles that two row tiles do not quite hide.  A unit costs about 9,000 cycles beside its steps (first
-// scores, last products, rows out), which is most of what a batch of short prompts pays: 12 of 209 to 1484 tokens, 32 heads,
-// 161 us of which 88 are steps.
+// What bounds it: a prompt of 8192 tokens and 64 heads takes 800 us on a GPU that has not been busy (1.72 PFLOP/s, 88 % of the
+// measured burst rate of bf16 products; 920 us at the power limit, where those reach 1.73): a step of both row tiles takes
+// 3,000 cycles, its products 2,560; the rest is the way from one row tile's softmax (1,050 cycles) to its next scores, a
+// chain of 3,000 cycles that two row tiles do not quite hide.  A unit costs about 8,000 cycles beside its steps (first
+// scores, last products, rows out, instructions that were not used for a while), which is most of what a batch of short
+// prompts pays: 12 of 209 to 1484 tokens, 32 heads, 148 us of which 88 are steps.
 #include <atomic>
 #include <type_traits>
 
@@ -251,7 +251,8 @@ __device__ __noinline__ void pa_advance(const PaArgs& p, const PaAt& a, PaAt& b,
   pa_part(p, b, at, end);
 }
 
-constexpr int kPaWhole = 4;                // units of at most so many tiles are not cut: a join costs more
+constexpr int kPaWhole = 3;                // units of at most so many tiles are not cut: a join costs more (20 requests of 100 over 400 keys,
+                                           // 32 heads: 63.6 us, with 4 66.9; 4 prompts of 300, 64 heads: 44.6, with 2 46.5)
 
 // Every thread of the CTA calls it.  Each thread sums a stretch of the requests.  found: shared memory; found[0] receives
 // the unit of the run's first place.
@@ -796,11 +797,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
       for (; ok && places[warp][now].live; next_part()) {
         const PaAt& a = places[warp][now];
         const int n0 = a.n[0], n1 = a.n[1], all = a.all, heads = a.heads, masked = a.masked - a.t0;
+        // (the row tiles' code written out: rolled up it is 9 KB less, and 8192 tokens take 852 us, not 815)
         // Step i: row tile by row tile, the products with the values of tile i (i = -1: none) and the scores of tile i + 1
 #pragma unroll 1
         for (int i = -1; ok && i < all; ++i) {
-          if (i == 0) look_ahead();
-#pragma unroll 1
+#pragma unroll
           for (int x = 0; ok && x < 2; ++x) {
             const int n = x ? n1 : n0;
             const uint32_t sx = tmem + x * kPaTile;
