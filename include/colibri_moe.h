@@ -686,8 +686,8 @@ COLI_API coli_status colibri_rope_frequencies(const coli_rope_desc* desc, uint64
  *   out          x itself with the same strides, or memory that does not
  *                overlap x; no two outputs overlap.
  * Angles are exact to 2^-24 relative; sums in fp32, each result is rounded once.
- * x and out need the alignment of their elements (16 bytes, with strides of
- * whole 16 bytes and dim a multiple of 16, are faster).  1 <= H <= 1024.
+ * x and out need the alignment of their elements (they move by 16, 8 or 4 bytes
+ * or one by one, as addresses, strides and dim, in the half layout dim / 2, allow).  1 <= H <= 1024.
  * n_tokens = 0 does nothing.  Asynchronous on stream.  Errors: COLI_EINVAL,
  * COLI_EALIGN, COLI_EUNSUPPORTED, COLI_ECUDA.
  */

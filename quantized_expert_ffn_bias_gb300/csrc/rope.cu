@@ -12,7 +12,7 @@
 
 namespace coli {
 
-constexpr int kRopeThreads = 128, kRopeItems = 4;   // items (a piece of a row) a thread, all loads in flight at once
+constexpr int kRopeThreads = 128, kRopeItems = 4;   // pieces (of a row) a thread, all loads in flight at once
 constexpr int kRopeMaxDim = 256;
 
 // (amplitude cos, amplitude sin) of position * freq
@@ -73,15 +73,32 @@ struct RopeArgs {
   long long x_tok, x_head, out_tok, out_head;    // elements
 };
 
-// A piece is 16 bytes (WIDE; in the half layout 16 of either half), or one pair.  A CTA takes some tokens and heads;
-// its threads' pieces are loaded first, the tokens' sines and cosines computed meanwhile, once for all heads.
+// BYTES of a vector, as the alignment allows: 16, 8, 4, or 0: values one by one.
+template <int BYTES>
+struct RopeVec {
+  alignas(BYTES ? BYTES : 4) uint32_t w[BYTES ? BYTES / 4 : 1];
+  __device__ __forceinline__ void load(const void* p) {
+    if constexpr (BYTES == 16) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    else if constexpr (BYTES == 8) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    else w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  __device__ __forceinline__ void store(void* p) const {
+    if constexpr (BYTES == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
+    else if constexpr (BYTES == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(w);
+    else *reinterpret_cast<uint32_t*>(p) = w[0];
+  }
+};
+
+// A piece is a vector (in the half layout one of either half), or one pair.  A CTA takes some tokens and heads; its threads'
+// pieces are loaded first, the tokens' sines and cosines computed meanwhile, once for all heads.
 // A copy in its traffic, 128 bytes a head of 64 16-bit values read and written: 8192 tokens of 64 heads take 22.0 us, 6.1 TB/s
 // (24.1 with 256 threads a CTA; with those 26.2 by two pieces a thread and 29.0 by eight).  One token: 2.3 us.
-template <typename T, bool HALF, bool WIDE>
+template <typename T, bool HALF, int BYTES>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
-  extern __shared__ float2 turn[];               // [tokens][pairs]
-  constexpr int kV = WIDE ? 16 / (int)sizeof(T) : 1;       // values of a vector
-  constexpr int kPairs = WIDE && !HALF ? kV / 2 : kV;      // pairs of a piece
+  extern __shared__ __align__(16) float2 turn[];           // [tokens][pairs]
+  constexpr int kV = BYTES ? BYTES / (int)sizeof(T) : 1;   // values of a vector
+  constexpr int kPairs = BYTES && !HALF ? kV / 2 : kV;     // pairs of a piece
+  static_assert(kPairs > 0, "whole pairs");
   const int tid = threadIdx.x;
   const int tok0 = blockIdx.x * p.tokens, head0 = blockIdx.y * p.heads;
   const int tokens = min(p.tokens, p.n - tok0), heads = min(p.heads, p.H - head0);
@@ -90,31 +107,24 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
   const T* x = reinterpret_cast<const T*>(p.x);
   T* out = reinterpret_cast<T*>(p.out);
 
-  uint4 lo[kRopeItems], hi[kRopeItems];          // WIDE
-  float a[kRopeItems], b[kRopeItems];            // else
+  RopeVec<BYTES> lo[kRopeItems], hi[kRopeItems];
+  float a[kRopeItems], b[kRopeItems];                    // BYTES = 0
   int tok[kRopeItems], pair[kRopeItems];
   long long at[kRopeItems];
-  auto find = [&](int i, int& t, int& h, int& c) {         // piece i: token, head, first pair
-    const int row = p.by_pieces(i);
-    c = (i - row * p.pieces) * kPairs;
-    t = p.by_heads(row);
-    h = row - t * p.heads;
-    return i < items && t < tokens && h < heads;
-  };
-  auto value = [&](int c) { return HALF ? c : 2 * c; };     // where pair c begins
   for (int i0 = 0; i0 < items; i0 += kRopeThreads * kRopeItems) {
 #pragma unroll
     for (int k = 0; k < kRopeItems; ++k) {
-      int t, h, c;
+      const int i = i0 + k * kRopeThreads + tid, row = p.by_pieces(i), c = (i - row * p.pieces) * kPairs;
+      const int t = p.by_heads(row), h = row - t * p.heads;
       tok[k] = -1;
-      if (!find(i0 + k * kRopeThreads + tid, t, h, c)) continue;
+      if (i >= items || t >= tokens || h >= heads) continue;
       tok[k] = t;
       pair[k] = c;
-      const T* src = x + (tok0 + t) * p.x_tok + (head0 + h) * p.x_head + value(c);
-      at[k] = (tok0 + t) * p.out_tok + (head0 + h) * p.out_head + value(c);
-      if constexpr (WIDE) {
-        lo[k] = *reinterpret_cast<const uint4*>(src);
-        if (HALF) hi[k] = *reinterpret_cast<const uint4*>(src + p.pairs);
+      const T* src = x + (tok0 + t) * p.x_tok + (head0 + h) * p.x_head + (HALF ? c : 2 * c);
+      at[k] = (tok0 + t) * p.out_tok + (head0 + h) * p.out_head + (HALF ? c : 2 * c);
+      if constexpr (BYTES) {
+        lo[k].load(src);
+        if (HALF) hi[k].load(src + p.pairs);
       } else {
         a[k] = rope_load(src);
         b[k] = rope_load(src + (HALF ? p.pairs : 1));
@@ -132,49 +142,38 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
       if (tok[k] < 0 || tok[k] >= valid) continue;
       const float2* w = turn + tok[k] * p.pairs + pair[k];
       T* dst = out + at[k];
-      if constexpr (!WIDE) {
+      if constexpr (!BYTES) {
         const float2 r = rope_rotate(a[k], b[k], w[0]);
         rope_store(dst, r.x);
         rope_store(dst + (HALF ? p.pairs : 1), r.y);
-      } else if constexpr (sizeof(T) == 4) {
-        const uint32_t* u = &lo[k].x;
-        const uint32_t* v = &hi[k].x;
-        float r[4], q[4];
-        if constexpr (HALF) {
+      } else {
+        uint32_t* u = lo[k].w;
+        uint32_t* v = hi[k].w;
+        constexpr int kWords = BYTES / 4;
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 z = rope_rotate(__uint_as_float(u[i]), __uint_as_float(v[i]), w[i]);
-            r[i] = z.x;
-            q[i] = z.y;
+          for (int i = 0; i < kPairs; ++i) {
+            uint32_t &f = HALF ? u[i] : u[2 * i], &g = HALF ? v[i] : u[2 * i + 1];
+            const float2 z = rope_rotate(__uint_as_float(f), __uint_as_float(g), w[i]);
+            f = __float_as_uint(z.x);
+            g = __float_as_uint(z.y);
           }
-          *reinterpret_cast<float4*>(dst + p.pairs) = make_float4(q[0], q[1], q[2], q[3]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 z = rope_rotate(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]), w[i]);
-            r[2 * i] = z.x;
-            r[2 * i + 1] = z.y;
+          for (int i = 0; i < kWords; ++i) {
+            if constexpr (HALF) {
+              const float2 f = rope_unpack<T>(u[i]), g = rope_unpack<T>(v[i]);
+              const float2 y = rope_rotate(f.x, g.x, w[2 * i]), z = rope_rotate(f.y, g.y, w[2 * i + 1]);
+              u[i] = rope_pack<T>(y.x, z.x);
+              v[i] = rope_pack<T>(y.y, z.y);
+            } else {
+              const float2 f = rope_unpack<T>(u[i]), z = rope_rotate(f.x, f.y, w[i]);
+              u[i] = rope_pack<T>(z.x, z.y);
+            }
           }
         }
-        *reinterpret_cast<float4*>(dst) = make_float4(r[0], r[1], r[2], r[3]);
-      } else {
-        const uint32_t* u = &lo[k].x;
-        const uint32_t* v = &hi[k].x;
-        uint32_t r[4], q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (HALF) {
-            const float2 f = rope_unpack<T>(u[i]), g = rope_unpack<T>(v[i]);
-            const float2 y = rope_rotate(f.x, g.x, w[2 * i]), z = rope_rotate(f.y, g.y, w[2 * i + 1]);
-            r[i] = rope_pack<T>(y.x, z.x);
-            q[i] = rope_pack<T>(y.y, z.y);
-          } else {
-            const float2 f = rope_unpack<T>(u[i]), z = rope_rotate(f.x, f.y, w[i]);
-            r[i] = rope_pack<T>(z.x, z.y);
-          }
-        }
-        if (HALF) *reinterpret_cast<uint4*>(dst + p.pairs) = make_uint4(q[0], q[1], q[2], q[3]);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(r[0], r[1], r[2], r[3]);
+        if (HALF) hi[k].store(dst + p.pairs);
+        lo[k].store(dst);
       }
     }
   }
@@ -275,10 +274,11 @@ static coli_status check_rope_desc(const coli_rope_desc* d, const char* who) {
   return COLI_OK;
 }
 
-template <typename T>
-static void rope_launch(const RopeArgs& a, bool half, bool wide, dim3 grid, size_t smem, cudaStream_t st) {
-  auto k = half ? (wide ? rope_kernel<T, true, true> : rope_kernel<T, true, false>)
-                : (wide ? rope_kernel<T, false, true> : rope_kernel<T, false, false>);
+template <typename T, bool HALF>
+static void rope_launch(const RopeArgs& a, int bytes, dim3 grid, size_t smem, cudaStream_t st) {
+  constexpr int kLeast = sizeof(T) == 4 && !HALF ? 8 : 4;  // bytes of the smallest vector of whole pairs
+  auto k = bytes == 16 ? rope_kernel<T, HALF, 16> : bytes == 8 ? rope_kernel<T, HALF, 8>
+                       : bytes == 4 ? rope_kernel<T, HALF, kLeast> : rope_kernel<T, HALF, 0>;
   k<<<grid, kRopeThreads, smem, st>>>(a);
 }
 
@@ -344,15 +344,20 @@ coli_status colibri_rope(const coli_rope_desc* desc, int dtype, int n_tokens, co
   if (xt < 0 || xh < 0) return fail(COLI_EINVAL, "rope: a stride of x is negative");
   if ((n_tokens > 1 && ot <= 0) || (H > 1 && oh < desc->dim)) return fail(COLI_EINVAL, "rope: outputs overlap (strides of out)");
   RopeArgs a;
-  const int per = 16 / size;
   const bool half = desc->layout == COLI_ROPE_HALF;
-  // whole 16-byte pieces, or pairs one by one
-  const bool wide = desc->dim % (half ? 2 * per : per) == 0 && aligned(x, 16) && aligned(out, 16) && xt % per == 0 &&
-                    xh % per == 0 && ot % per == 0 && oh % per == 0;
+  // the largest vector that strides, addresses and the row's pieces are whole multiples of (2763 tokens of 128 heads of 64
+  // values: by 16 bytes 16.4 us, 8 bytes 22.1, 4 bytes 24.4, value by value 58.7)
+  const unsigned long long mixed = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out) |
+                                   (unsigned long long)(xt * size) | (unsigned long long)(xh * size) |
+                                   (unsigned long long)(ot * size) | (unsigned long long)(oh * size) |
+                                   (unsigned long long)((half ? desc->dim / 2 : desc->dim) * size);
+  int bytes = mixed % 16 == 0 ? 16 : mixed % 8 == 0 ? 8 : mixed % 4 == 0 ? 4 : 0;
+  if (bytes == 4 && size == 4 && !half) bytes = 0;         // (half a pair)
+  const int values = bytes ? bytes / size : 1, pairs = bytes && !half ? values / 2 : values;     // of a piece
   a.n = n_tokens;
   a.H = H;
   a.pairs = desc->dim / 2;
-  a.pieces = !wide ? a.pairs : half ? desc->dim / (2 * per) : desc->dim / per;
+  a.pieces = a.pairs / pairs;
   const int room = kRopeThreads * kRopeItems;
   a.heads = a.pieces * H <= room ? H : room / a.pieces;      // (at most 128 pieces)
   a.tokens = room / (a.pieces * a.heads);
@@ -372,9 +377,9 @@ coli_status colibri_rope(const coli_rope_desc* desc, int dtype, int n_tokens, co
   const dim3 grid(n_tokens / a.tokens + (n_tokens % a.tokens ? 1 : 0), (H + a.heads - 1) / a.heads);
   const size_t smem = (size_t)a.tokens * a.pairs * sizeof(float2);           // (at most 32 KB)
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == COLI_X_BF16) rope_launch<__nv_bfloat16>(a, half, wide, grid, smem, st);
-  else if (dtype == COLI_X_F16) rope_launch<__half>(a, half, wide, grid, smem, st);
-  else rope_launch<float>(a, half, wide, grid, smem, st);
+  if (dtype == COLI_X_BF16) half ? rope_launch<__nv_bfloat16, true>(a, bytes, grid, smem, st) : rope_launch<__nv_bfloat16, false>(a, bytes, grid, smem, st);
+  else if (dtype == COLI_X_F16) half ? rope_launch<__half, true>(a, bytes, grid, smem, st) : rope_launch<__half, false>(a, bytes, grid, smem, st);
+  else half ? rope_launch<float, true>(a, bytes, grid, smem, st) : rope_launch<float, false>(a, bytes, grid, smem, st);
   const cudaError_t ce = cudaGetLastError();
   return ce == cudaSuccess ? COLI_OK : cuda_fail(ce, "rope");
 }

@@ -138,3 +138,33 @@ def test_one_graph_of_the_operators(torch):  # noqa: F811
         for a, b in zip(*got):
             assert torch.equal(a, b)
         assert (got[0][5][sum(new):] == 3).all()
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("dtype,N,H,dim,before,pad", [
+    ("bf16", 70, 9, 64, 128, 4), ("bf16", 70, 9, 64, 128, 2), ("f16", 33, 5, 52, 2, 0), ("f16", 33, 5, 50, 2, 0), ("f32", 20, 3, 6, 2, 2),
+    ("f32", 20, 3, 12, 0, 1), ("bf16", 1000, 1, 8, 0, 0), ("f16", 9, 128, 4, 4, 2), ("f32", 40, 2, 256, 0, 2), ("bf16", 3, 40, 254, 0, 0)])
+def test_rotation_of_rows_of_any_alignment(torch, layout, dtype, N, H, dim, before, pad):  # noqa: F811
+    """Vectors of 16, 8 and 4 bytes and single values, by what strides and the part's place allow; what lies beside is left."""
+    import quantized_expert_ffn_bias_gb300 as coli
+    from tests import prompt_ref as R
+    t = P.dt(torch, dtype)
+    d = P.rope_desc(dim, layout, "linear", 0.75)
+    freq, g = P.rope_table(torch, d), P.gen(torch, N)
+    wide = torch.randn((N, H * (before + dim) + pad), generator=g, device="cuda").to(t)
+    x = wide[:, : H * (before + dim)].unflatten(1, (H, before + dim))[..., before:]
+    pos = torch.randint(0, 100000, (N,), generator=g, device="cuda").to(torch.int32)
+    ref, size = R.rotate(x.double(), pos, R.frequencies(dim, "linear"), layout, 0.75)
+    tol = R.rotate_bound(ref, size, t) + size * (pos.double().view(-1, 1, 1) * 2.0 ** -51)
+    again = wide.clone()
+    y = again[:, : H * (before + dim)].unflatten(1, (H, before + dim))[..., before:]
+    coli.colibri_rope(d, P.TYPES[dtype], N, None, H, pos, freq, y, y.stride(0), y.stride(1), y, y.stride(0), y.stride(1))
+    torch.cuda.synchronize()
+    P.within(torch, y, ref, tol, "in place")
+    got = y.clone()
+    y.copy_(x)
+    assert torch.equal(again, wide)
+    out = torch.full((H, N, dim + 2), 5.0, dtype=t, device="cuda")[..., 2:].transpose(0, 1)          # heads first, two values off
+    coli.colibri_rope(d, P.TYPES[dtype], N, None, H, pos, freq, x, x.stride(0), x.stride(1), out, out.stride(0), out.stride(1))
+    torch.cuda.synchronize()
+    assert torch.equal(out, got)
