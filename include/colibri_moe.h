@@ -687,9 +687,9 @@ COLI_API coli_status colibri_rope_frequencies(const coli_rope_desc* desc, uint64
  *                overlap x; no two outputs overlap.
  * Angles are exact to 2^-24 relative; sums in fp32, each result is rounded once.
  * x and out need the alignment of their elements (they move by 16, 8 or 4 bytes
- * or one by one, as addresses, strides and dim, in the half layout dim / 2, allow).  1 <= H <= 1024.
- * n_tokens = 0 does nothing.  Asynchronous on stream.  Errors: COLI_EINVAL,
- * COLI_EALIGN, COLI_EUNSUPPORTED, COLI_ECUDA.
+ * or one by one, as addresses, strides and dim, in the half layout dim / 2,
+ * allow).  1 <= H <= 1024.  n_tokens = 0 does nothing.  Asynchronous on stream.
+ * Errors: COLI_EINVAL, COLI_EALIGN, COLI_EUNSUPPORTED, COLI_ECUDA.
  */
 COLI_API coli_status colibri_rope(const coli_rope_desc* desc, int dtype, int n_tokens, const int32_t* n_valid, int H,
                                   const int32_t* position, const uint64_t* freq, const void* x, long long x_token_stride,
@@ -765,8 +765,9 @@ COLI_API coli_status colibri_kv_gather(const coli_kv_desc* desc, int B, int n_ro
  * does not see do not reach its output, whatever values (infinities, NaN) they
  * hold; a value that is not finite reaches the rows that see its key.  Work of
  * more than 2^31 - 2^16 places (three and the tiles of 128 keys for every 512 rows
- * of a head: hours of it) is not computed (COLI_DEV_KV_TOKENS).  Softmax and sums in fp32; the weights are rounded to dtype for the
- * product with the values.  The result does not depend on timing.
+ * of a head: hours of it) is not computed (COLI_DEV_KV_TOKENS).  Softmax and sums
+ * in fp32; the weights are rounded to dtype for the product with the values.  The
+ * result does not depend on timing.
  * Asynchronous on stream, two launches.  n_tokens = 0 does nothing.  Errors:
  * COLI_EINVAL, COLI_EALIGN, COLI_EWORKSPACE, COLI_EUNSUPPORTED, COLI_ECUDA.
  */
