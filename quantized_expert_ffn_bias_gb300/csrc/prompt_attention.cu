@@ -408,49 +408,39 @@ __device__ __forceinline__ void cluster_store(uint32_t at, uint32_t v) {
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same where what comes before is ordered by tcgen05 fences alone (a release for the cluster waits for every store:
-// 1,000 cycles a tile).
+// The same where only tensor memory is handed over: tcgen05.wait::st and fence::before_thread_sync come before it and order it,
+// so that the arrival itself needs none (a release for the cluster waits for every store: 1,000 cycles a tile).
 __device__ __forceinline__ void cluster_arrive_tmem(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void cluster_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Wait for a phase, at most about limit_ns, suspended by the hardware for 20 us at a time.  CLUSTER: for writes of either CTA.
+// Wait for a phase, at most about limit_ns, suspended by the hardware for 20 us at a time.  For the cluster: nearly every
+// barrier counts copies, products or arrivals of either CTA.
 // (What comes after the first look stands once: it is called from twenty places.)
 constexpr uint32_t kPaSuspendNs = 20000;
-template <bool CLUSTER>
 __device__ __forceinline__ bool pa_look(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  if constexpr (CLUSTER)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(kPaSuspendNs)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(kPaSuspendNs)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kPaSuspendNs)
+      : "memory");
   return ok != 0;
 }
-template <bool CLUSTER>
 __device__ __noinline__ bool pa_wait_on(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
   const unsigned long long t0 = globaltimer();
   for (;;) {
-    if (pa_look<CLUSTER>(bar, parity)) return true;
+    if (pa_look(bar, parity)) return true;
     if (globaltimer() - t0 > limit_ns) return false;
   }
 }
-template <bool CLUSTER = false>
 __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
-  return pa_look<CLUSTER>(smem_u32(bar), parity) || pa_wait_on<CLUSTER>(smem_u32(bar), parity, limit_ns);
+  return pa_look(smem_u32(bar), parity) || pa_wait_on(smem_u32(bar), parity, limit_ns);
 }
 
 // TMA loads of a pair: into this CTA's shared memory, counted on a barrier of either CTA.
@@ -811,7 +801,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
               // barrier is awaited or, v_full's of a checked tile, known to be over: a parity tells neighbours apart.)
               if (x == 0 || heads == 2 || i >= n0) {   // (else row tile 0 waited for them)
                 if (i >= masked) {
-                  ok = __all_sync(0xffffffffu, pa_wait<true>(&v_ok[s], (checked >> s) & 1, p.wait_ns));
+                  ok = __all_sync(0xffffffffu, pa_wait(&v_ok[s], (checked >> s) & 1, p.wait_ns));
                   checked ^= 1u << s;
                 } else {
                   wait(&v_full[s], j / kPaStages);
@@ -865,6 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
       const unsigned long long from = globaltimer();
       while (__any_sync(0xffffffffu, (int)(done_v[lane & (2 * kPaSmWarps - 1)] - (uu - 3)) < 0))
         if (__any_sync(0xffffffffu, globaltimer() - from > p.wait_ns)) return false;
+      cluster_fence();                                 // (their reads come before the writes to come)
       return true;
     };
     bool ok = true;
@@ -913,12 +904,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
                           w == 2 ? uu + 1 : w == 1 ? flags[1] : flags[0]);
           }
           fence_proxy_async_smem();
-          asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          cluster_fence();
           __syncwarp();
-          if (lane == 0) cluster_arrive(cluster_addr(&v_ok[s], 0));
-        } else if (lane == 0) {                        // (nothing was written)
-          cluster_arrive_tmem(cluster_addr(&v_ok[s], 0));
         }
+        // (a release also where nothing was written: the copy that this warp waited for is handed on)
+        if (lane == 0) cluster_arrive(cluster_addr(&v_ok[s], 0));
       }
       tile += steps;
       ++uu;
@@ -1054,7 +1044,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) cluster_arrive_tmem(ready);
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(&p_ready[x]);     // (prompts of many units: 1 % over the way of the other CTA)
+          else cluster_arrive_tmem(ready);
+        }
       }
       // -------------------------------------------------------------- the unit's rows
       look_ahead();
@@ -1149,6 +1142,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
         }
       }
       tc_fence_before();
+      if (*(volatile int*)&any_bad) cluster_fence();   // (the check writes `bad` again when it knows that it has been read)
       __syncwarp();                                    // (every lane has read `bad`)
       uu += a.all > 0;
       if (lane < 2) cluster_store(cluster_addr(&done[rank][warp], lane), uu);

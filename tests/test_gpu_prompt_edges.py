@@ -168,3 +168,32 @@ def test_rotation_of_rows_of_any_alignment(torch, layout, dtype, N, H, dim, befo
     coli.colibri_rope(d, P.TYPES[dtype], N, None, H, pos, freq, x, x.stride(0), x.stride(1), out, out.stride(0), out.stride(1))
     torch.cuda.synchronize()
     assert torch.equal(out, got)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_hand_overs_between_the_ctas_of_a_pair(torch, dtype):  # noqa: F811
+    """Weights, rescaled sums and checked values of either CTA, many times over: rows within their bounds, every repetition the
+    same bits.  The scores rise along the keys (references move in every tile), most tiles cross the diagonal, and some of their
+    values are not finite."""
+    c = P.prompt_case(torch, [500, 260, 7, 130], [700, 260, 3000, 1500], 10, dtype, 21)
+    m0 = 0
+    for s in c["seq"]:
+        c["k"][m0:m0 + s, :, 0] = torch.linspace(0.0, 20.0, s, device="cuda")[:, None].to(c["k"].dtype)
+        m0 += s
+    c["q"][..., 0] = 4.0
+    out, lse = P.check_prompt(torch, c)
+    spoiled = dict(c, v=c["v"].clone())
+    spoiled["v"][[650, 900], ::3, 9] = math.inf
+    spoiled["v"][[650, 900], 1::3, 70] = -math.inf
+    odd = P.call_prompt(torch, spoiled)[0]
+    ws = torch.zeros_like(P.call_prompt(torch, c)[2])
+    for _ in range(60):
+        got = P.call_prompt(torch, c, ws=ws)[:2]
+        assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+        assert torch.equal(P.call_prompt(torch, spoiled, ws=ws)[0], odd)
+    # rows of requests 0 and 1 from the spoiled keys on (their own rows 450 and 200), in the heads and columns that were spoiled
+    want = out.clone()
+    for head, column, what in ((0, 9, math.inf), (1, 70, -math.inf)):
+        want[450:500, head::3, column] = what
+        want[700:760, head::3, column] = what
+    assert torch.equal(odd, want)
