@@ -71,6 +71,7 @@ constexpr float kPaGrow = 8.f;
 __host__ __device__ constexpr float pa_top(bool bf16) { return bf16 ? 0.f : 7.f; }
 constexpr float kPaSumLimit = 32768.f;             // a row's weights of a tile sum to at most this,
 __host__ __device__ constexpr float pa_first(bool bf16) { return bf16 ? 1.f / 64 : 32.f; }   // those of its first keys to at least this
+constexpr float kPaLowest = -3.402823466e38f;      // reference of a part in which the row has no finite score, below all others
 constexpr uint32_t kPaOCol = 256;                  // TMEM columns: S_0 0.., S_1 128.., O_0 256.., O_1 384..
 
 // A unit cut by borders: its parts are those of pairs pair, pair + 1, ...
@@ -94,7 +95,7 @@ struct PaArgs {
   int32_t* cta_status;               // [kPaMaxCtas]
   PaJoin* joins;                     // [kPaMaxCtas / 2] written by every pair (parts = 0: none)
   float* part;                       // [2 kPaMaxCtas] partial O (pa_slot, pa_part)
-  float2* part_ml;                   // [2 kPaMaxCtas][256] reference, sum
+  float2* part_ml;                   // [2 kPaMaxCtas][256] reference (-infinity: no values written), sum
   unsigned long long wait_ns;
   int withhold;                      // failure-path test: 1: no pair's first keys ever count as there
 };
@@ -1100,7 +1101,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
         const int in_cta = x * kPaTile + sp * 32 + lane;
         if (mine && whole && p.lse)
           p.lse[row0 + (size_t)lane * p.H] = l == 0.f ? -INFINITY : (log2f(l) + m) * 0.693147180559945309f;
-        if (mine && !whole) p.part_ml[slot * kPaCtaRows + in_cta] = make_float2(has || l != 0.f ? m : -INFINITY, l);
+        if (mine && !whole) p.part_ml[slot * kPaCtaRows + in_cta] = make_float2(has || l != 0.f ? m : n > 0 ? kPaLowest : -INFINITY, l);
         const int rows = a.rows[x] - warp_row;
         // eight rows of 64 bytes at a time by way of shared memory, so that a store covers eight lines (a row a lane: 32)
         const int r = lane >> 2;
@@ -1167,7 +1168,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
 
 // ------------------------------------------------------------------ join
 // Adds up the parts of every cut unit, in order.  A task is 32 rows of a unit (a row a lane, 16 values a warp).
-constexpr float kPaLowest = -3.402823466e38f;      // below every reference; a part whose row saw no key has -infinity
 constexpr int kPaJoinThreads = 256, kPaJoinCtas = 608, kPaAhead = 3;
 
 template <bool BF16>
@@ -1234,7 +1234,7 @@ __global__ void __launch_bounds__(kPaJoinThreads) prompt_attention_join_kernel(c
       for (int k = 0; k < kPaAhead; ++k) {
         const float w = pa_exp2(ml[k].x - m);
         l += w * ml[k].y;
-        if (w != 0.f) {                                // (a part without keys has written no values)
+        if (ml[k].x != -INFINITY) {                    // (else no values were written; 0 times one that is not finite stays a NaN)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             acc[c].x = fmaf(w, o[k][c].x, acc[c].x);

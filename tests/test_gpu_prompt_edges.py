@@ -197,3 +197,31 @@ def test_hand_overs_between_the_ctas_of_a_pair(torch, dtype):  # noqa: F811
         want[450:500, head::3, column] = what
         want[700:760, head::3, column] = what
     assert torch.equal(odd, want)
+
+
+@pytest.mark.parametrize("new,seq,dtype", [([3], [200], "bf16"), ([3], [20000], "bf16"), ([2, 300], [9000, 12000], "f16")])
+@pytest.mark.parametrize("far", [0.0, 0.5])
+def test_values_that_are_not_finite_behind_weights_of_nothing(torch, new, seq, dtype, far):  # noqa: F811
+    """A stretch of keys scores some 300 below the others (weights below fp32's range): its infinities and NaN still reach the rows
+    that see them, whether the keys are cut into parts or not, and nothing else changes."""
+    c = P.prompt_case(torch, new, seq, 4, dtype, 31)
+    c["q"][..., 0] = 64.0
+    c["k"][..., 0] = 0.0
+    marks, m0 = [], 0
+    for b, s in enumerate(seq):
+        first, last = int(far * s), int(far * s) + s // 4
+        c["k"][m0 + first:m0 + last, :, 0] = -64.0       # 64 * 64 / sqrt(192) = 295
+        marks.append([(m0 + (first + last) // 2, b, math.inf), (m0 + last - 1, 2, math.nan)])
+        m0 += s
+    ref, ref_lse, tol, tol_lse = P.reference(c)          # (before the values are spoiled: theirs weigh nothing)
+    odd, n0 = torch.zeros_like(ref, dtype=torch.bool), 0
+    for t, two in zip(new, marks):
+        for key, h, what in two:
+            c["v"][key, h, 11 + h] = what
+            odd[n0:n0 + t, h, 11 + h] = True             # (the stretch ends before the new tokens)
+        n0 += t
+    out, lse, ws, _ = P.call_prompt(torch, c)
+    torch.cuda.synchronize()
+    assert not torch.isfinite(out[odd]).any()
+    P.within(torch, out[~odd], ref[~odd], tol[~odd], "the others")
+    P.within(torch, lse, ref_lse, tol_lse, "lse")
