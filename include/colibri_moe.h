@@ -760,7 +760,8 @@ COLI_API coli_status colibri_kv_gather(const coli_kv_desc* desc, int B, int n_ro
  *                256-byte aligned; its first int32 is the status word
  *                (colibri_kv_check_status).  Two calls that overlap on the GPU
  *                need two workspaces.
- * A row that sees no key gets 0 and lse -infinity.  Rows outside
+ * A row that sees no key gets 0 and lse -infinity; one that sees keys which all
+ * score -infinity gets NaN and lse -infinity.  Rows outside
  * [q_start[0], q_start[B]) are left as they were.  Keys and values that a row
  * does not see do not reach its output, whatever values (infinities, NaN) they
  * hold; a value that is not finite reaches the rows that see its key.  Work of

@@ -80,7 +80,7 @@ struct __align__(16) PaJoin {
   int h, heads;     // first head; 2: two heads of the same rows
   int pair, parts;
   int which;        // of the first pair's two partial results (the others': the first)
-  int pad;
+  int first;        // rows from this one on see a key
 };
 
 struct PaArgs {
@@ -389,7 +389,7 @@ __device__ __forceinline__ PaRun pa_plan(const PaArgs& p, PaUnit* found) {
     jn.pair = pair - 1;
     jn.parts = m - (pair - 1);
     jn.which = cut(pair - 1) < u.first ? 1 : 0;
-    jn.pad = 0;
+    jn.first = u.T - u.L - u.blk * kPaRows;
     p.joins[pair] = jn;
   }
   return r;
@@ -587,6 +587,10 @@ __device__ __forceinline__ void pa_commit_here(uint64_t* bar) {
       "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
+
+// What a row's sums are multiplied by: 0 where it sees no key; NaN where every key that it sees scores -infinity, as the softmax
+// has it.
+__device__ __forceinline__ float pa_share(float l, bool sees) { return l == 0.f ? (sees ? __int_as_float(0x7fffffff) : 0.f) : 1.0f / l; }
 
 // Of a 32-bit word of two 16-bit values: whether either is an infinity or a NaN, and the word with those as 0.
 template <bool BF16>
@@ -1095,7 +1099,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
         }
       }
       if (any) {
-        const float by = l == 0.f ? 0.f : 1.0f / l;
+        const float by = pa_share(l, lim >= 0);
         const bool whole = a.whole;
         const size_t slot = pa_slot(blockIdx.x >> 1, a.opening ? 0 : 1, rank), row0 = (size_t)(a.u.q0 + row - lane) * p.H + head;
         const int in_cta = x * kPaTile + sp * 32 + lane;
@@ -1245,7 +1249,7 @@ __global__ void __launch_bounds__(kPaJoinThreads) prompt_attention_join_kernel(c
         }
       }
     }
-    const float by = l == 0.f ? 0.f : 1.0f / l;
+    const float by = pa_share(l, r >= jn.first);
     const size_t row = (size_t)(jn.row0 + r) * p.H + jn.h + second;
     if (p.lse && warp == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 #pragma unroll

@@ -225,3 +225,38 @@ def test_values_that_are_not_finite_behind_weights_of_nothing(torch, new, seq, d
     assert not torch.isfinite(out[odd]).any()
     P.within(torch, out[~odd], ref[~odd], tol[~odd], "the others")
     P.within(torch, lse, ref_lse, tol_lse, "lse")
+
+
+@pytest.mark.parametrize("new,seq", [([5], [300]), ([3], [20000]), ([10], [4]), ([600], [700]), ([2, 270], [9000, 11000])])
+def test_rows_whose_scores_are_all_minus_infinity(torch, new, seq):  # noqa: F811
+    """The softmax of minus infinities alone is NaN, its sum's log minus infinity; one finite score takes all the weight; rows
+    without keys stay 0."""
+    c = P.prompt_case(torch, new, seq, 3, "bf16", 32)
+    c["q"][..., 0] = 1.0
+    c["k"][..., 0] = -math.inf
+    alone = P.call_prompt(torch, c)[:2]
+    m0, finite = 0, []
+    for t, s in zip(new, seq):
+        finite.append(max(0, s - t // 2 - 1))            # rows before it see no finite score
+        c["k"][m0 + finite[-1], :, 0] = 0.0
+        m0 += s
+    one = P.call_prompt(torch, c)[:2]
+    torch.cuda.synchronize()
+    n0 = m0 = 0
+    for t, s, key in zip(new, seq, finite):
+        last = torch.arange(t, device="cuda") + (s - t)  # the last key that a row sees
+        for (out, lse), some in ((alone, torch.zeros_like(last, dtype=torch.bool)), (one, last >= key)):
+            o, z = out[n0:n0 + t], lse[n0:n0 + t]
+            assert (o[last < 0] == 0).all() and (z[last < 0] == -math.inf).all()
+            none = (last >= 0) & ~some
+            assert torch.isnan(o[none]).all() and (z[none] == -math.inf).all()
+            # its one weight w is rounded to the type for the product and not in the sum: w (1 + d) v / w with |d| <= eps / 2, a
+            # reciprocal and a product in fp32 (2^-22), the result's rounding: (1 + eps / 2)^2 (1 + 2^-22) - 1 < 1.01 eps
+            v = c["v"][m0 + key].double().expand(int(some.sum()), -1, -1)
+            P.within(torch, o[some], v, 1.01 * torch.finfo(torch.bfloat16).eps * v.abs() + 2.0 ** -133, "out")
+            q, k = c["q"][n0:n0 + t][some].double(), c["k"][m0 + key].double()
+            score = (torch.einsum("nhd,hd->nh", q[..., :128], k) + q[..., 128:] @ c["r"][m0 + key].double()) * c["scale"]
+            # 192 exact products summed in fp32 (2^-23 each of their magnitudes' sum), the scale and the log's few roundings
+            size = (torch.einsum("nhd,hd->nh", q[..., :128].abs(), k.abs()) + q[..., 128:].abs() @ c["r"][m0 + key].double().abs()) * c["scale"]
+            P.within(torch, z[some], score, 200 * 2.0 ** -23 * size + 2.0 ** -21 * (score.abs() + 1), "lse")
+        n0, m0 = n0 + t, m0 + s
