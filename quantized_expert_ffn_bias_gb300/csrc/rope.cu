@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
   const int tid = threadIdx.x;
   const int tok0 = blockIdx.x * p.tokens, head0 = blockIdx.y * p.heads;
   const int tokens = min(p.tokens, p.n - tok0), heads = min(p.heads, p.H - head0);
-  const int valid = p.n_valid ? *p.n_valid - tok0 : tokens;          // (awaited where the results are written)
+  const int valid = p.n_valid ? *p.n_valid : p.n;          // (awaited where the results are written)
   const int items = p.tokens * p.heads * p.pieces;
   const T* x = reinterpret_cast<const T*>(p.x);
   T* out = reinterpret_cast<T*>(p.out);
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs p) {
     }
 #pragma unroll
     for (int k = 0; k < kRopeItems; ++k) {
-      if (tok[k] < 0 || tok[k] >= valid) continue;
+      if (tok[k] < 0 || tok0 + tok[k] >= valid) continue;
       const float2* w = turn + tok[k] * p.pairs + pair[k];
       T* dst = out + at[k];
       if constexpr (!BYTES) {

@@ -260,3 +260,19 @@ def test_rows_whose_scores_are_all_minus_infinity(torch, new, seq):  # noqa: F81
             size = (torch.einsum("nhd,hd->nh", q[..., :128].abs(), k.abs()) + q[..., 128:].abs() @ c["r"][m0 + key].double().abs()) * c["scale"]
             P.within(torch, z[some], score, 200 * 2.0 ** -23 * size + 2.0 ** -21 * (score.abs() + 1), "lse")
         n0, m0 = n0 + t, m0 + s
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("count", [-2**31, -2**31 + 40, -3, 0, 2**31 - 1])
+def test_rotation_of_any_count(torch, layout, count):  # noqa: F811
+    """Rows from the count on are left, whatever the count: below 0 it leaves all of them, in every block of rows."""
+    import quantized_expert_ffn_bias_gb300 as coli
+    d = P.rope_desc(64, layout)
+    x = torch.randn((700, 2, 64), generator=P.gen(torch, 1), device="cuda").bfloat16()
+    pos, freq = torch.arange(700, dtype=torch.int32, device="cuda"), P.rope_table(torch, d)
+    want, out = torch.full_like(x, 5.0), torch.full_like(x, 5.0)
+    if count > 0:
+        coli.colibri_rope(d, 0, 700, None, 2, pos, freq, x, 128, 64, want, 128, 64)
+    coli.colibri_rope(d, 0, 700, P.ints(torch, [count]), 2, pos, freq, x, 128, 64, out, 128, 64)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and (out[600] == 5.0).all() == (count <= 0)
