@@ -228,8 +228,9 @@ __global__ void __launch_bounds__(kArWarps * 32, 12) kv_append_rope_kernel(const
     };
     float s = 1.f, mean = squares(1.f) + p.eps;
     if (!(mean > 1e-30f && mean < 1e36f)) {
-      // squares that leave fp32's range: the row times a power of two near 1 / its largest value (not so large that eps,
-      // which then decides, would overflow)
+      // squares or eps that leave fp32's range: the row times a power of two near 1 / its largest value.  Up only where squares
+      // are small, and then no further than 2^60 where there is an eps (below 1e-30; it decides); else down by 2^30 at least,
+      // so that the sum with an eps of any size is finite
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -239,7 +240,8 @@ __global__ void __launch_bounds__(kArWarps * 32, 12) kv_append_rope_kernel(const
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int e = (int)(__float_as_uint(top) >> 23) - 127;
-      s = __uint_as_float((uint32_t)(max(-126, min(-e, p.eps > 0.f ? 60 : 126)) + 127) << 23);
+      const int most = mean >= 1e36f ? -30 : p.eps > 0.f ? 60 : 126;
+      s = __uint_as_float((uint32_t)(max(-126, min(-e, most)) + 127) << 23);
       mean = squares(s) + p.eps * s * s;
     }
     const float by = 1.0f / sqrtf(mean);

@@ -276,3 +276,25 @@ def test_rotation_of_any_count(torch, layout, count):  # noqa: F811
     coli.colibri_rope(d, 0, 700, P.ints(torch, [count]), 2, pos, freq, x, 128, 64, out, 128, 64)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and (out[600] == 5.0).all() == (count <= 0)
+
+
+@pytest.mark.parametrize("eps", [1e-38, 1e30, 1e36, 3.4e38])
+def test_norm_with_any_eps(torch, eps):  # noqa: F811
+    """An eps that decides, up to fp32's largest: rows far smaller than its root stay what they are over it, rows that overflow
+    in their squares are normed."""
+    import quantized_expert_ffn_bias_gb300 as coli
+    from tests import prompt_ref as R
+    eps = float(torch.tensor(eps, dtype=torch.float32))
+    sizes = torch.tensor([1e-38, 1e-20, 1e-18, 1e-3, 1.0, 1e3, 1e15, 1e17, 5e18, 1e19, 2e25, 3e38], device="cuda", dtype=torch.float64)
+    n, t = len(sizes), torch.bfloat16
+    c = P.append_case(torch, "bf16", n, 16, "half", True, 3)
+    unit = torch.rand((n, P.V), generator=P.gen(torch, 4), device="cuda").double() * 0.9 + 0.1
+    c["latent"] = (unit * sizes[:, None]).float().to(t)
+    rd = P.rope_desc(64, "half")
+    cache = c["cache"].clone()
+    P.call_append(c, coli.coli_kv_desc(16, 1, c["n_pages"], 0, 16 * P.W), rd, P.rope_table(torch, rd), n, None, eps, cache)
+    torch.cuda.synchronize()
+    got = cache.view(-1, P.W)[c["slot"].long(), :P.V]
+    ref = R.norm(c["latent"].double(), c["gain"].double(), eps)
+    # (what is below fp32's normal range before the gain may lose all of its bits)
+    P.within(torch, got, ref, R.norm_bound(ref, t) + 2.0 ** -126 * c["gain"].double().abs(), "latent")
