@@ -684,7 +684,8 @@ COLI_API coli_status colibri_rope_frequencies(const coli_rope_desc* desc, uint64
  *   n_valid      device int32 or NULL: rows from *n_valid on are not written
  *                (q_start + B of colibri_kv_step; all n_tokens may be read).
  *   out          x itself with the same strides, or memory that does not
- *                overlap x; no two outputs overlap.
+ *                overlap x; no two outputs overlap (strides below dim, and
+ *                other strides at x's address, are refused).
  * Angles are exact to 2^-24 relative; sums in fp32, each result is rounded once.
  * x and out need the alignment of their elements (they move by 16, 8 or 4 bytes
  * or one by one, as addresses, strides and dim, in the half layout dim / 2,

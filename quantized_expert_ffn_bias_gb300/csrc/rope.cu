@@ -344,7 +344,8 @@ coli_status colibri_rope(const coli_rope_desc* desc, int dtype, int n_tokens, co
   const long long xt = n_tokens > 1 ? x_token_stride : 0, xh = H > 1 ? x_head_stride : 0;
   const long long ot = n_tokens > 1 ? out_token_stride : 0, oh = H > 1 ? out_head_stride : 0;
   if (xt < 0 || xh < 0) return fail(COLI_EINVAL, "rope: a stride of x is negative");
-  if ((n_tokens > 1 && ot <= 0) || (H > 1 && oh < desc->dim)) return fail(COLI_EINVAL, "rope: outputs overlap (strides of out)");
+  if ((n_tokens > 1 && ot < desc->dim) || (H > 1 && oh < desc->dim)) return fail(COLI_EINVAL, "rope: outputs overlap (strides of out)");
+  if (x == out && (xt != ot || xh != oh)) return fail(COLI_EINVAL, "rope: in place, but with other strides of out than of x");
   RopeArgs a;
   const bool half = desc->layout == COLI_ROPE_HALF;
   // the largest vector that strides, addresses and the row's pieces are whole multiples of (2763 tokens of 128 heads of 64

@@ -76,6 +76,13 @@ def test_rope_refuses(kw, status):
     refused(status, turn, **kw)
 
 
+@pytest.mark.parametrize("kw", [dict(ot=63), dict(ot=1, oh=512), dict(H=1, ot=40), dict(n=1, oh=32), dict(xt=512), dict(xh=128), dict(ot=320),
+                                dict(H=1, ot=64), dict(xt=0, x=P, out=P)])
+def test_rope_refuses_outputs_that_overlap(kw):
+    """Rows or heads nearer than dim, and rotation in place with other strides."""
+    refused(coli.COLI_EINVAL, turn, **kw)
+
+
 def test_rope_of_nothing():
     turn(n=0, pos=None, freq=None, x=None, out=None)
 
