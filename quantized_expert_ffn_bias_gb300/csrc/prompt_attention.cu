@@ -65,9 +65,9 @@ constexpr int kPaMaxCtas = 160;                    // CTAs the workspace has roo
 constexpr int kPaMaxB = 8192, kPaMaxH = 1024;
 constexpr int kPaMaxDevices = 64;
 constexpr int kPaPart = kPaCtaRows * kPaV;         // floats of a CTA's partial O
-// A reference is set so that the largest weight is 2^(top - 1) .. 2^top, and raised where one exceeds 2^(top + kPaGrow).
-// bf16 has fp32's range; fp16 ends at 2^16 and loses bits below 2^-14, so its weights take the upper part.
-constexpr float kPaGrow = 8.f;
+// A reference that is set by the largest weight makes that 2^(top - 1) .. 2^top.  It is set, or raised, where a tile's weights
+// against the one so far sum to more than kPaSumLimit, or those of a row's first keys to less than pa_first.  bf16 has fp32's
+// range; fp16 ends at 2^16 and loses bits below 2^-14, so its weights take the upper part.
 __host__ __device__ constexpr float pa_top(bool bf16) { return bf16 ? 0.f : 7.f; }
 constexpr float kPaSumLimit = 32768.f;             // a row's weights of a tile sum to at most this,
 __host__ __device__ constexpr float pa_first(bool bf16) { return bf16 ? 1.f / 64 : 32.f; }   // those of its first keys to at least this
@@ -93,7 +93,7 @@ struct PaArgs {
   float* lse;
   int32_t* status;
   int32_t* cta_status;               // [kPaMaxCtas]
-  PaJoin* joins;                     // [kPaMaxCtas / 2] written by every pair (parts = 0: none)
+  PaJoin* joins;                     // [kPaMaxCtas / 2] one a pair, written by it (parts = 0: none)
   float* part;                       // [2 kPaMaxCtas] partial O (pa_slot, pa_part)
   float2* part_ml;                   // [2 kPaMaxCtas][256] reference (-infinity: no values written), sum
   unsigned long long wait_ns;
@@ -520,9 +520,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
-constexpr int kPaChunk = 16;
-__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16_issue(taddr, r); }
-__device__ __forceinline__ void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32_issue(taddr, r); }
+constexpr int kPaChunk = 16;                       // columns of scores at a time (32: 2 % slower)
 // registers -> 32 consecutive TMEM columns of this warp's 32 lanes
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -949,13 +947,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPaThreads, 1)
           float2 sum = make_float2(0.f, 0.f);
           // (the next chunk of scores is on its way while one is worked on)
           uint32_t r[2][kPaChunk];
-          tmem_ld_chunk(ts, r[0]);
+          tmem_ld16_issue(ts, r[0]);
           tmem_ld_done<kPaChunk>(r[0]);
 #pragma unroll
           for (int c = 0; c < kPaTile; c += kPaChunk) {
             uint32_t(&a)[kPaChunk] = r[(c / kPaChunk) & 1];
             uint32_t(&b)[kPaChunk] = r[(c / kPaChunk + 1) & 1];
-            if (c + kPaChunk < kPaTile) tmem_ld_chunk(ts + c + kPaChunk, b);
+            if (c + kPaChunk < kPaTile) tmem_ld16_issue(ts + c + kPaChunk, b);
 #pragma unroll
             for (int j = 0; j < kPaChunk; j += 2) {
               const float2 d = ffma2(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])), by, off);
@@ -1279,7 +1277,7 @@ static PaWs pa_ws() {
     return o;
   };
   w.cta_status = take(kPaMaxCtas * sizeof(int32_t));
-  w.joins = take((size_t)kPaMaxCtas * sizeof(PaJoin));
+  w.joins = take((size_t)(kPaMaxCtas / 2) * sizeof(PaJoin));
   w.part = take((size_t)2 * kPaMaxCtas * kPaPart * sizeof(float));
   w.part_ml = take((size_t)2 * kPaMaxCtas * kPaCtaRows * sizeof(float2));
   w.total = off;
