@@ -686,7 +686,10 @@ COLI_API coli_status colibri_rope_frequencies(const coli_rope_desc* desc, uint64
  *   out          x itself with the same strides, or memory that does not
  *                overlap x; no two outputs overlap (strides below dim, and
  *                other strides at x's address, are refused).
- * Angles are exact to 2^-24 relative; sums in fp32, each result is rounded once.
+ * An angle (within half a turn) is off by 2^-24 of itself at most, beside what
+ * the table has: its step (2^-65 turns a position, which shows in pairs slower
+ * than about 3e-12 radians a position) and the 64-bit floating point that its
+ * frequencies are computed in.  Sums in fp32, each result is rounded once.
  * x and out need the alignment of their elements (they move by 16, 8 or 4 bytes
  * or one by one, as addresses, strides and dim, in the half layout dim / 2,
  * allow).  1 <= H <= 1024.  n_tokens = 0 does nothing.  Asynchronous on stream.
@@ -746,7 +749,8 @@ COLI_API coli_status colibri_kv_gather(const coli_kv_desc* desc, int B, int n_ro
  *               q[n][h][128..192) . k_rope[j])) v[j][h]
  * (scale of any sign, |scale| log2(e) finite).  A (row, key, head) costs 320
  * multiply-adds, in colibri_kv_attention 1088; that one reads 1152 bytes a key
- * for all heads, this one 512 a head.
+ * for all heads, this one 512 a head.  The widths are fixed: models whose heads
+ * have others (the cached row alone does not tell) need colibri_kv_attention.
  *   q            device [n_tokens][H][192], k and v device [n_keys][H][128],
  *                k_rope device [n_keys][64], of dtype (bf16 or fp16), 16-byte
  *                aligned, with the strides (in elements) given: positive

@@ -23,19 +23,20 @@
 // against the reference as it is, without looking for the largest score; only where a row's weights sum to more than 2^15,
 // or those of its first keys to less than 2^-6 (fp16: 32, so that weights down to 2^-29 of the sum count), are the scores
 // read again, their maximum taken and the reference (with the sum and O) moved.  Looking for the maximum first cost 8 % of a
-// prompt of 8192.
+// prompt of 8192.  That branch is written for size: with scores of normal spread hardly a tile takes it; a first key that scores
+// 12 above the rest costs 8192 tokens 2 %, the batch below 12 %, scores that rise by 20 along the keys 15 and 34 %.
 //
 // Work: units with their key tiles, dealt in equal runs to the pairs.  A unit is 512 rows of one head, or, for the last rows
 // of a request where they are 256 at most, those of two heads, one to either row tile: with one row tile the tensor cores
-// wait while its softmax runs (7 tokens over 20,018 keys, 16 heads: 66 us, by two heads 59; 45 by now).  A unit cut by a border leaves
-// partial results in the workspace, which the join kernel adds up in order.
+// wait while its softmax runs (7 tokens over 20,018 keys, 16 heads: 66 us, by two heads 59; 45 to 48 by now).  A unit cut by a
+// border leaves partial results in the workspace, which the join kernel adds up in order.
 //
-// What bounds it: a prompt of 8192 tokens and 64 heads takes 800 us on a GPU that has not been busy (1.72 PFLOP/s, 88 % of the
-// measured burst rate of bf16 products; 920 us at the power limit, where those reach 1.73): a step of both row tiles takes
+// What bounds it: a prompt of 8192 tokens and 64 heads takes 795 to 815 us on a GPU that has not been busy (1.71 PFLOP/s, 87 % of
+// the measured burst rate of bf16 products; 930 us at the power limit, where those reach 1.73): a step of both row tiles takes
 // 3,000 cycles, its products 2,560; the rest is the way from one row tile's softmax (1,050 cycles) to its next scores, a
-// chain of 3,000 cycles that two row tiles do not quite hide.  A unit costs about 8,000 cycles beside its steps (first
+// chain of 3,000 cycles that two row tiles do not quite hide.  A unit costs about 10,000 cycles beside its steps (first
 // scores, last products, rows out, instructions that were not used for a while), which is most of what a batch of short
-// prompts pays: 12 of 209 to 1484 tokens, 32 heads, 148 us of which 88 are steps.
+// prompts pays: 12 of 209 to 1484 tokens, 32 heads, 155 us: 88 for 55 steps a pair, 15 for the call, 52 for 9.3 units.
 #include <atomic>
 #include <type_traits>
 
@@ -116,7 +117,7 @@ __host__ __device__ constexpr int pa_part(int r, int c) { return ((c >> 2) * kPa
 // block j (1, 2, ...) sees keys up to its last row: max(1, a + 4 j) tiles with a = ceil((L - T) / 128), the last block all
 // of them.  Units are (request, head, block), block fastest, so that neighbouring pairs work on the same head's keys; a last
 // block of at most 256 rows comes behind them, two heads a unit.
-// What a unit costs beside its tiles (its rows' way out, the first softmax: about 9,000 cycles, a tile 3,100) is dealt with
+// What a unit costs beside its tiles (its rows' way out, the first softmax: about 10,000 cycles, a tile 3,100) is dealt with
 // them: a unit's places are kPaUnitCost and then its tiles; a border among the first is one before its first tile.
 // The code runs once a launch and what it costs is mostly fetching it: 32 bits, few divisions, each step written once.
 constexpr int kPaUnitCost = 3;
